@@ -1,4 +1,5 @@
-"""Python binding of the GB300 multi-LoRA linear library (``include/lora_linear.h``).
+"""Python binding of the GB300 multi-LoRA linear library (``include/lora_linear.h``) and of the
+paged key/value cache beside it (``include/lora_kv.h``, bound in ``kv.py``).
 
 Argument marshalling only: every step of the layer runs in the CUDA kernels
 of ``liblora_linear.so``; torch tensors are used for device memory and
@@ -31,6 +32,7 @@ STATUS_NAMES = {
 globals().update({v: k for k, v in STATUS_NAMES.items()})
 LORA_PATH_AUTO, LORA_PATH_DECODE, LORA_PATH_PREFILL = 0, 1, 2
 LORA_PREFILL_AUTO, LORA_PREFILL_SINGLE, LORA_PREFILL_PAIR = 0, 1, 2
+LORA_KV_BF16, LORA_KV_INT8 = 0, 1
 LORA_STATS_COUNT = 7
 STATS_FIELDS = ("loaded", "free_pages", "total_pages", "loads", "unloads", "calls", "bytes_held")
 
@@ -44,6 +46,8 @@ EXPORTS = (
     "lora_host_register", "lora_host_unregister", "lora_acquire", "lora_prefetch", "lora_release",
     "lora_cache_stats", "lora_pool_selftest_wait", "lora_decode_plan_info", "lora_test_delayed_copy",
     "lora_pool_set_trace", "lora_linear_q4", "lora_base_linear_q4", "lora_dequant_q4",
+    "lora_kv_create", "lora_kv_destroy", "lora_kv_reserve", "lora_kv_write", "lora_kv_read",
+    "lora_kv_attention", "lora_kv_check_errors",
 )
 PLAN_INFO_FIELDS = ("units", "G", "grid", "max_seg", "n_acc", "stages", "tmem_cols", "smem_bytes",
                     "pairs", "col_blocks", "tight", "ntok", "partials_floats", "prefetch_a")
@@ -76,6 +80,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             f"{path} is missing: build it with `python -m adapter_linear_gb300.build`")
     lib = ctypes.CDLL(path)
     vp, i32, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    i64 = ctypes.c_int64
     sig = {
         "lora_pool_create": [i32, i32, i32, i32, ctypes.POINTER(vp)],
         "lora_pool_destroy": [vp],
@@ -110,6 +115,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_linear_q4": [vp, vp, vp, vp, vp, vp, i32, vp, vp],
         "lora_base_linear_q4": [vp, vp, vp, vp, vp, i32, vp, vp],
         "lora_dequant_q4": [vp, vp, vp, i32, i32, vp, vp],
+        "lora_kv_create": [i32, i32, i32, i32, i32, vp, vp, vp, vp, ctypes.POINTER(vp)],
+        "lora_kv_destroy": [vp],
+        "lora_kv_reserve": [vp, i32, i32, i32],
+        "lora_kv_write": [vp, vp, i64, vp, i64, vp, vp],
+        "lora_kv_read": [vp, vp, i64, vp, i64, vp, vp],
+        "lora_kv_attention": [vp, vp, i64, i32, vp, f32, i32, vp, i64, vp, vp],
+        "lora_kv_check_errors": [vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -447,3 +459,6 @@ class LoraPool:
     def set_trace(self, buf, n_calls: int = 1):
         """buf: device int64/uint64 tensor of n_calls * LORA_KERNEL_SLOTS * 4 entries, or None."""
         _check(lora_pool_set_trace(self.handle, buf, n_calls), "lora_pool_set_trace")
+
+
+from .kv import KvBatch, KvCache  # noqa: E402,F401

@@ -1,0 +1,49 @@
+// kv_internal.h -- what the translation units of the paged key/value cache share: the
+// handle, the views the kernels take and the launchers (not part of the public ABI).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/lora_kv.h"
+#include "internal.h"
+
+namespace lora {
+
+// The cache as the kernels see it. Row (page, head, r) starts at ((page * H + head) * p + r)
+// * D values of k / v (bytes or bf16) and holds its scale at the same row index.
+struct KvDev {
+    void *k, *v;
+    uint16_t *ks, *vs;  // bf16 bits (int8 caches)
+    int num_pages;
+    int page_shift;     // log2 of the tokens per page
+    int H, D;
+    int *err;
+};
+
+// The batch as the kernels see it (device pointers).
+struct KvBatchDev {
+    const int32_t *table, *start, *kv_len;
+    int table_stride, n_seqs, T;
+};
+
+cudaError_t launch_kv_write(const KvDev &kv, bool int8, const KvBatchDev &b, const uint16_t *K, int64_t k_stride,
+                            const uint16_t *V, int64_t v_stride, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvDev &kv, bool int8, const KvBatchDev &b, uint16_t *K, int64_t k_stride,
+                           uint16_t *V, int64_t v_stride, int num_sms, cudaStream_t stream);
+
+// One attention call.
+struct KvAttn {
+    const uint16_t *Q;
+    uint16_t *O;
+    float *lse;          // or nullptr
+    int64_t q_stride, o_stride;
+    int Hq, G;           // query heads; query heads per kv head
+    int window;          // 0: none
+    float scale;
+};
+
+cudaError_t launch_kv_attention(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
+                                cudaStream_t stream);
+
+}  // namespace lora

@@ -1,0 +1,20 @@
+// kv_state.h -- the host-side state of a lora_kv (private to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/lora_kv.h"
+#include "kv_internal.h"
+#include "pool_state.h"
+
+struct lora_kv {
+    int device = 0, num_sms = 0;
+    int num_pages = 0, page_shift = 0, H = 0, D = 0;
+    bool int8 = false;
+    void *k = nullptr, *v = nullptr;           // the caller's arenas
+    uint16_t *ks = nullptr, *vs = nullptr;
+    int *d_err = nullptr;                      // [0] the error word, [1] its value at the last read
+    int *h_err = nullptr;                      // pinned copy of d_err[1]
+    cudaEvent_t ev_call = nullptr;             // the last call enqueued
+    cudaStream_t ctl_stream = nullptr;         // error-word reads; follows every call
+};
