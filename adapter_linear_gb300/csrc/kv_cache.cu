@@ -242,13 +242,21 @@ KvDev kv_view(const lora_kv *p)
     return v;
 }
 
-// After a call on `stream`: the error-word read waits for it. Inside a graph capture the
-// order is the caller's.
-lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
+// Calls inside a graph capture are not tracked: the order of replays is the caller's.
+lora_status is_tracked(cudaStream_t stream, bool *tracked)
 {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     CUDA_TRY(cudaStreamIsCapturing(stream, &cs));
-    if (cs != cudaStreamCaptureStatusNone) return LORA_OK;
+    *tracked = cs == cudaStreamCaptureStatusNone;
+    return LORA_OK;
+}
+
+// After a call on `stream`: the error-word read waits for it.
+lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
+{
+    bool tracked;
+    const lora_status st = is_tracked(stream, &tracked);
+    if (st != LORA_OK || !tracked) return st;
     CUDA_TRY(cudaEventRecord(p->ev_call, stream));
     CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev_call, 0));
     return LORA_OK;
@@ -293,14 +301,19 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
     p->v = v_pages;
     p->ks = static_cast<uint16_t *>(k_scales);
     p->vs = static_cast<uint16_t *>(v_scales);
+    const size_t counts = sizeof(int) * (size_t)kv_decode_grid(sms);
     if (cudaMalloc((void **)&p->d_err, 2 * sizeof(int)) != cudaSuccess ||
+        cudaMalloc((void **)&p->part, sizeof(float) * kv_decode_part_floats(head_dim, sms)) != cudaSuccess ||
+        cudaMalloc((void **)&p->count, counts) != cudaSuccess ||
         cudaHostAlloc((void **)&p->h_err, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
         cudaGetLastError();
         lora_kv_destroy(p);
         return LORA_ERR_OOM;
     }
     if (cudaMemset(p->d_err, 0, 2 * sizeof(int)) != cudaSuccess ||
+        cudaMemset(p->count, 0, counts) != cudaSuccess ||
         cudaEventCreateWithFlags(&p->ev_call, cudaEventDisableTiming) != cudaSuccess ||
+        cudaEventCreateWithFlags(&p->ev_attn, cudaEventDisableTiming) != cudaSuccess ||
         cudaStreamCreateWithFlags(&p->ctl_stream, cudaStreamNonBlocking) != cudaSuccess ||
         ensure_smem_attr((const void *)kv_read_clear_kernel, 0) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -317,6 +330,9 @@ lora_status lora_kv_destroy(lora_kv_t p)
     cudaDeviceSynchronize();
     if (p->ctl_stream) cudaStreamDestroy(p->ctl_stream);
     if (p->ev_call) cudaEventDestroy(p->ev_call);
+    if (p->ev_attn) cudaEventDestroy(p->ev_attn);
+    if (p->part) cudaFree(p->part);
+    if (p->count) cudaFree(p->count);
     if (p->d_err) cudaFree(p->d_err);
     if (p->h_err) cudaFreeHost(p->h_err);
     delete p;
@@ -379,8 +395,18 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     a.G = n_heads / p->H;
     a.window = window;
     a.scale = scale;
-    CUDA_TRY(launch_kv_attention(kv_view(p), p->int8, batch_view(batch), a, stream));
-    return note_kv_call(p, stream);
+    bool tracked;
+    if ((st = is_tracked(stream, &tracked)) != LORA_OK) return st;
+    // the scratch belongs to one call at a time: after the last one, if that ran elsewhere
+    if (tracked && p->attn_any && stream != p->attn_stream) CUDA_TRY(cudaStreamWaitEvent(stream, p->ev_attn, 0));
+    CUDA_TRY(launch_kv_decode(kv_view(p), p->int8, batch_view(batch), a, batch->max_new, INT_MAX, p->part,
+                              p->count, p->num_sms, stream));
+    if (!tracked) return LORA_OK;
+    CUDA_TRY(cudaEventRecord(p->ev_attn, stream));
+    CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev_attn, 0));
+    p->attn_stream = stream;
+    p->attn_any = true;
+    return LORA_OK;
 }
 
 lora_status lora_kv_check_errors(lora_kv_t p)

@@ -1,0 +1,669 @@
+// kv_decode.cu -- attention of short chunks (single tokens above all) over the paged cache.
+//
+// For a row at position pos and its visible keys j:
+//   z_j = scale <Q, K_j>,  m = max z_j,  l = sum exp(z_j - m),  O = sum exp(z_j - m) V_j / l,
+// in one pass with a running m (z is kept in units of log2: exp(x) = 2^(x log2 e)). Sets of
+// keys combine: (m, l, O) of two sets become M = max m, sums weighted by 2^(m - M); so the keys
+// of one head are split over warps, and over CTAs, and joined at the end.
+//
+// What bounds it: HBM. A single-token step reads every cached byte once for G = Hq / Hkv query
+// heads: 2 G flops a byte of an 8-bit cache. The products run as warp-level MMAs with the cache
+// as the 16-row operand, S^T = K Q^T and O^T = V^T P^T, so that the G heads (times the chunk's
+// tokens) fill tiles of 8 columns: half the instructions, accumulators and softmax of the other
+// way round, where 4 heads would leave 12 of 16 rows idle. What is left is issue slots for
+// turning codes into bf16, about half of all instructions with an 8-bit cache.
+//
+// Split: the work is the list of items (sequence, row tile, kv head), each a run of 64-token
+// units; the grid's CTAs take equal contiguous shares of all units together, whatever the
+// lengths, so no SM waits for the longest sequence. A CTA's share covers some whole items
+// and up to two pieces; a piece's (m, l, O) goes to scratch, and the CTA that finishes an item
+// last (a counter) joins its pieces in CTA order: the result does not depend on which one it is.
+// Inside a CTA the four warps take 16-token steps in turn, each streaming its own codes through
+// its own ring of shared memory with 16-byte asynchronous copies: no barrier until an item ends.
+#include <climits>
+
+#include "kv_device.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStep = 16;            // tokens per warp step: never crosses a page (pages hold 16 k)
+constexpr int kUnit = kWarps * kStep;
+
+// kN: tiles of 8 rows (a row: one query head of one new token) an item holds.
+template <int D, bool kInt8, int kN>
+struct Cfg {
+    static constexpr int kRows = 8 * kN;
+    static constexpr int kRowBytes = D * (kInt8 ? 1 : 2);
+    static constexpr int kTile = kStep * kRowBytes;              // K or V of a step
+    static constexpr int kStage = 2 * kTile + 4 * kStep;         // K, V, then both scales
+    static constexpr bool kWide = kRowBytes == 256;
+    // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers; rows of 256
+    // bytes: 2 of 98 KB): 100 to 150 KB in flight beside the stages in use
+    static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
+    static constexpr int kCtas = kWide ? 2 : kN == 1 ? 4 : 3;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kSmem = kWarps * kRing;
+    static constexpr int kLdO = D + 4;                           // fp32 row of O in shared memory
+    static_assert(kRing >= kRows * kLdO * 4, "O of a warp is parked in its ring");
+};
+
+// Byte offset of 16-byte chunk c of row r in a tile. The chunks of a 128-byte line are permuted
+// by the row so that the lanes of a phase of a shared load fall into different banks: for K two
+// neighbouring rows with four chunks each, for V rows 2 c with two chunks each.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t swz(int r, int c)
+{
+    if (kRowBytes == 64)  // two rows a line
+        return (uint32_t)((r >> 1) * 128 + (((((r & 1) << 2) + c) ^ (((r >> 1) & 3) << 1)) << 4));
+    // rows of 256 bytes: two halves of 128-byte rows, one after the other
+    return (uint32_t)((c >> 3) * (kStep * 128) + r * 128 + (((c & 7) ^ (((r & 1) << 2) | ((r >> 1) & 3))) << 4));
+}
+
+// V's chunk (of the 8 of a 128-byte row) that the lanes of group g read
+__device__ __forceinline__ int v_chunk(int g) { return ((g & 1) << 2) + (g >> 1); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// D += A B, 16 x 8 x 16, bf16 in, fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values, a row over four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Sequences this launch takes: those of at most max_rows rows (n G).
+struct Plan {
+    int max_rows;
+    float scale_log2;    // scale * log2(e)
+    float *part;         // [2 grid][rows][D] + [2 grid][rows][2] (m, l)
+    int *count;          // [grid] arrivals at the item that starts in that CTA and ends in another
+};
+
+struct SeqShape {
+    int row0, n, L, tiles;
+};
+
+// Visible range of a tile of R rows: tokens [lo, hi), lo rounded down to a step.
+template <int R>
+__device__ __forceinline__ void tile_range(const SeqShape &s, int tile, int G, int window, int *lo, int *hi)
+{
+    const int i0 = tile * R / G, i1 = min(s.n - 1, (tile * R + R - 1) / G);
+    const int p0 = s.L - s.n + i0, p1 = s.L - s.n + i1;
+    *hi = max(0, p1 + 1);
+    const int first = window > 0 ? max(0, p0 - window + 1) : 0;
+    *lo = min(first & ~(kStep - 1), *hi);
+}
+
+template <int R>
+__device__ __forceinline__ int tile_units(const SeqShape &s, int tile, int G, int window)
+{
+    int lo, hi;
+    tile_range<R>(s, tile, G, window, &lo, &hi);
+    return max(1, (hi - lo + kUnit - 1) / kUnit);  // rows that see nothing still write their zeros
+}
+
+template <int R>
+__device__ __forceinline__ SeqShape seq_shape(const KvDev &kv, const KvBatchDev &b, int seq, int G, int max_rows)
+{
+    const KvSeq q = kv_seq(b, kv.page_shift, seq, kv.err);
+    SeqShape s{q.row0, q.n, q.L, 0};
+    if (q.n > 0 && (int64_t)q.n * G <= max_rows) s.tiles = (q.n * G + R - 1) / R;
+    return s;
+}
+
+template <int R>
+__device__ __forceinline__ int64_t seq_units(const SeqShape &s, int H, int G, int window)
+{
+    int64_t u = 0;
+    for (int t = 0; t < s.tiles; ++t) u += tile_units<R>(s, t, G, window);
+    return u * H;
+}
+
+template <int D, bool kInt8, int kN>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
+    kv_decode_kernel(KvDev kv, KvBatchDev b, KvAttn a, Plan plan)
+{
+    using C = Cfg<D, kInt8, kN>;
+    constexpr int R = C::kRows;
+    constexpr int kM = D / 16;                    // MMAs of 16 dimensions
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_w[kWarps][R], sm_lse[R];
+    __shared__ int sm_last;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int G = a.G;
+
+    // this CTA's share of all units: every warp adds up the sequences by itself
+    int64_t total = 0;
+    for (int s = lane; s < b.n_seqs; s += 32)
+        total += seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+    const int64_t grid = min((int64_t)gridDim.x, total);
+    if ((int64_t)blockIdx.x >= grid) return;
+    int64_t u = (int64_t)blockIdx.x * total / grid;
+    const int64_t u_end = ((int64_t)blockIdx.x + 1) * total / grid;
+
+    // the sequence that holds unit u; `before`: units of the sequences ahead of it
+    int seq = 0;
+    int64_t before = 0;
+    for (int s0 = 0;; s0 += 32) {
+        const int s = s0 + lane;
+        int64_t mine =
+            s < b.n_seqs ? seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window) : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, x);
+            if (lane >= x) incl += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + incl > u);
+        if (past) {
+            const int k = __ffs(past) - 1;
+            seq = s0 + k;
+            before += __shfl_sync(0xffffffffu, incl - mine, k);
+            break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    SeqShape sh = seq_shape<R>(kv, b, seq, G, plan.max_rows);
+    int64_t seq_end = before + seq_units<R>(sh, kv.H, G, a.window);
+
+    uint8_t *const ring = smem + warp * C::kRing;
+    const uint32_t ring_addr = smem_u32(ring);
+    // this lane's part of a copy: chunks lane + 32 x of a tile
+    constexpr int kChunks = C::kRowBytes / 16, kCopies = C::kTile / 512;
+    uint32_t dst[kCopies];
+#pragma unroll
+    for (int x = 0; x < kCopies; ++x)
+        dst[x] = ring_addr + swz<C::kRowBytes>((lane + 32 * x) / kChunks, (lane + 32 * x) % kChunks);
+
+    while (u < u_end) {
+        while (u >= seq_end) {  // the next sequence with work
+            ++seq;
+            sh = seq_shape<R>(kv, b, seq, G, plan.max_rows);
+            before = seq_end;
+            seq_end = before + seq_units<R>(sh, kv.H, G, a.window);
+        }
+        // unit u of the sequence: row tile, head, unit of the item
+        int64_t item0 = before;
+        int tile = 0, nu = tile_units<R>(sh, 0, G, a.window);
+        while (u >= item0 + (int64_t)nu * kv.H) {
+            item0 += (int64_t)nu * kv.H;
+            nu = tile_units<R>(sh, ++tile, G, a.window);
+        }
+        const int head = (int)((u - item0) / nu);
+        item0 += (int64_t)head * nu;
+        const int64_t item1 = item0 + nu;
+        const int64_t seg_end = min(item1, u_end);
+        int lo, hi;
+        tile_range<R>(sh, tile, G, a.window, &lo, &hi);
+        const int tok0 = lo + (int)(u - item0) * kUnit;
+        const int tok1 = min(hi, lo + (int)(seg_end - item0) * kUnit);
+        const int rows = min(R, sh.n * G - tile * R);
+
+        // ---- this warp's steps: tokens tok0 + 16 (warp + 4 k)
+        const int nk = max(0, (tok1 - tok0 + kStep - 1) / kStep - warp + kWarps - 1) / kWarps;
+        int page_cache = 0;  // lane i: the page of step (k & ~31) + i
+        const int32_t *table = b.table + (int64_t)seq * b.table_stride;
+        int fill_k = 0, fill_stage = 0;  // the next step to copy and its stage
+        auto issue = [&]() {
+            const int k = fill_k++;
+            if (k < nk) {
+                if ((k & 31) == 0) {
+                    page_cache = 0;
+                    if (k + lane < nk) {
+                        page_cache = table[(tok0 + kStep * (warp + kWarps * (k + lane))) >> kv.page_shift];
+                        if (page_cache < 0 || page_cache >= kv.num_pages) {
+                            kv_flag_range(kv.err);
+                            page_cache = 0;
+                        }
+                    }
+                }
+                const int page = __shfl_sync(0xffffffffu, page_cache, k & 31);
+                const int tok = tok0 + kStep * (warp + kWarps * k);
+                const int64_t row = (((int64_t)page * kv.H + head) << kv.page_shift) +
+                                    (tok & ((1 << kv.page_shift) - 1));
+                const uint32_t st = fill_stage * C::kStage;
+                const uint8_t *ksrc = static_cast<const uint8_t *>(kv.k) + row * C::kRowBytes + lane * 16;
+                const uint8_t *vsrc = static_cast<const uint8_t *>(kv.v) + row * C::kRowBytes + lane * 16;
+                if (tok + kStep <= sh.L) {
+#pragma unroll
+                    for (int x = 0; x < kCopies; ++x) {
+                        cp_async16(dst[x] + st, ksrc + x * 512, 16u);
+                        cp_async16(dst[x] + st + C::kTile, vsrc + x * 512, 16u);
+                    }
+                } else {
+                    // rows past the sequence's end hold anything: zeros in their place
+#pragma unroll
+                    for (int x = 0; x < kCopies; ++x) {
+                        const uint32_t bytes = tok + (lane + 32 * x) / kChunks < sh.L ? 16u : 0u;
+                        cp_async16(dst[x] + st, ksrc + x * 512, bytes);
+                        cp_async16(dst[x] + st + C::kTile, vsrc + x * 512, bytes);
+                    }
+                }
+                if (kInt8 && lane < 4)
+                    cp_async16(ring_addr + st + 2 * C::kTile + lane * 16,
+                               reinterpret_cast<const uint8_t *>((lane < 2 ? kv.ks : kv.vs) + row) + (lane & 1) * 16,
+                               16u);
+                fill_stage = fill_stage + 1 == C::kStages ? 0 : fill_stage + 1;
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < C::kStages - 1; ++k) issue();
+
+        // Q as the 8-column operand: lane (g, c) holds row g of each tile; its dims of MMA i are
+        // those its K words hold (8-bit: 64-dim blocks of 16 dims a lane; bf16: 32-dim blocks of 8)
+        uint32_t q[kN][kM][2];
+        int pos[kN][2];  // positions of the rows this lane has scores of: 8 t + 2 c, + 1
+#pragma unroll
+        for (int t = 0; t < kN; ++t) {
+            const int row = tile * R + 8 * t + g;
+            const bool on = 8 * t + g < rows;
+            const int i = row / G;
+            const uint16_t *src = a.Q + (int64_t)(sh.row0 + i) * a.q_stride + (int64_t)(head * G + row % G) * D;
+            constexpr int kBlock = kInt8 ? 64 : 32, kLane = kBlock / 4;
+#pragma unroll
+            for (int s = 0; s < D / kBlock; ++s)
+#pragma unroll
+                for (int e = 0; e < kLane / 8; ++e) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (on) v = ldg_nc_v4(src + s * kBlock + c * kLane + e * 8);
+                    const int i0 = s * (kLane / 4) + e * 2;
+                    q[t][i0][0] = v.x;
+                    q[t][i0][1] = v.y;
+                    q[t][i0 + 1][0] = v.z;
+                    q[t][i0 + 1][1] = v.w;
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * t + 2 * c + e;  // rows beyond the tile: any position, not written
+                pos[t][e] = r < rows ? sh.L - sh.n + (tile * R + r) / G : sh.L - 1;
+            }
+        }
+        int pos_min = pos[0][0], pos_max = pos[0][0];
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                pos_min = min(pos_min, pos[t][e]);
+                pos_max = max(pos_max, pos[t][e]);
+            }
+
+        float o[kN][kM][4];
+        float m[kN][2], l[kN][2];
+#pragma unroll
+        for (int t = 0; t < kN; ++t) {
+#pragma unroll
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.0f;
+        }
+
+        int tok = tok0 + kStep * warp;
+        int stage = 0;
+        for (int k = 0; k < nk; ++k, tok += kStep * kWarps) {
+            cp_wait<C::kStages - 2>();
+            __syncwarp();
+            const uint8_t *st = ring + stage * C::kStage;
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
+            // S^T = K Q^T: rows are tokens g and g + 8, columns the query rows
+            float s[kN][4];
+#pragma unroll
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < C::kRowBytes / 64; ++x) {
+                const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g, 4 * x + c));
+                const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g + 8, 4 * x + c));
+                const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+                if constexpr (kInt8) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a0, a1, a2, a3;
+                        codes4_to_bf16(u0[j], &a0, &a2);
+                        codes4_to_bf16(u1[j], &a1, &a3);
+#pragma unroll
+                        for (int t = 0; t < kN; ++t)
+                            mma16816(s[t], a0, a1, a2, a3, q[t][4 * x + j][0], q[t][4 * x + j][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int t = 0; t < kN; ++t)
+                            mma16816(s[t], u0[2 * j], u1[2 * j], u0[2 * j + 1], u1[2 * j + 1], q[t][2 * x + j][0],
+                                     q[t][2 * x + j][1]);
+                }
+            }
+
+            // z in units of log2, masked; s[t][2 y + e]: token g + 8 y, row 8 t + 2 c + e
+            float mul[2] = {plan.scale_log2, plan.scale_log2}, vs[2] = {1.0f, 1.0f};
+            if (kInt8) {
+                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * C::kTile);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    mul[y] *= __uint_as_float((uint32_t)sc[g + 8 * y] << 16);
+                    vs[y] = __uint_as_float((uint32_t)sc[16 + g + 8 * y] << 16);
+                }
+            }
+            const bool edge = tok + kStep - 1 > pos_min || (a.window > 0 && tok <= pos_max - a.window);
+            bool grow = false;
+#pragma unroll
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        s[t][2 * y + e] *= mul[y];
+                        if (edge) {
+                            const int j = tok + g + 8 * y, p = pos[t][e];
+                            const bool see = j <= p && (a.window == 0 || j > p - a.window);
+                            s[t][2 * y + e] = see ? s[t][2 * y + e] : -INFINITY;
+                        }
+                    }
+                    grow |= fmaxf(s[t][e], s[t][2 + e]) > m[t][e] + 8.0f;
+                }
+
+            // The maximum only has to be near the true one: O and l are rescaled when a key passes
+            // it by 2^8 (weights then reach 256, which changes nothing about their precision).
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int t = 0; t < kN; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = fmaxf(s[t][e], s[t][2 + e]);
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        v = fmaxf(v, m[t][e]);
+                        const float down = m[t][e] == -INFINITY ? 0.0f : fast_exp2(m[t][e] - v);
+                        m[t][e] = v;
+                        l[t][e] *= down;
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            o[t][i][e] *= down;
+                            o[t][i][2 + e] *= down;
+                        }
+                    }
+            }
+            // Weights: summed in fp32, and for the product with V a pair of bf16, the rounded weight
+            // and the rest (together 2^-17 of it: one bf16 alone, 2^-8, shows in rows that see few
+            // keys, and HBM leaves the tensor cores the time). An 8-bit cache's V scale is
+            // multiplied in first; a masked key's weight is 0 whatever its scale is.
+            uint32_t p[kN][2], p2[kN][2];
+#pragma unroll
+            for (int t = 0; t < kN; ++t)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float w[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float z = s[t][2 * y + e];
+                        w[e] = fast_exp2(z - (m[t][e] == -INFINITY ? 0.0f : m[t][e]));
+                        l[t][e] += w[e];
+                        if (kInt8) w[e] = z == -INFINITY ? 0.0f : w[e] * vs[y];
+                    }
+                    const uint32_t top = pack_bf16x2(w[0], w[1]);
+                    p[t][y] = transpose8x8(top);
+                    p2[t][y] = transpose8x8(pack_bf16x2(w[0] - bf16_lo(top), w[1] - bf16_hi(top)));
+                }
+
+            // O^T += V^T P^T: a lane reads its dims of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9; dims
+            // 2 i and 2 i + 1 of them are rows g and g + 8 of MMA i
+            const uint8_t *vt = st + C::kTile;
+            if constexpr (kInt8) {
+                uint32_t w[4][D / 32];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                    if constexpr (D == 128) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, v_chunk(g)));
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                        w[r][2] = v.z;
+                        w[r][3] = v.w;
+                    } else {
+                        const uint2 v =
+                            *reinterpret_cast<const uint2 *>(vt + swz<C::kRowBytes>(row, g >> 1) + (g & 1) * 8);
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kM; ++i) {
+                    const int x = i >> 1, y = 2 * (i & 1);
+                    const uint32_t a0 = codes_pair_to_bf16(w[0][x], w[1][x], y);
+                    const uint32_t a1 = codes_pair_to_bf16(w[0][x], w[1][x], y + 1);
+                    const uint32_t a2 = codes_pair_to_bf16(w[2][x], w[3][x], y);
+                    const uint32_t a3 = codes_pair_to_bf16(w[2][x], w[3][x], y + 1);
+#pragma unroll
+                    for (int t = 0; t < kN; ++t) {
+                        mma16816(o[t][i], a0, a1, a2, a3, p[t][0], p[t][1]);
+                        mma16816(o[t][i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, 8 * x + v_chunk(g)));
+                        w[r][0] = v.x;
+                        w[r][1] = v.y;
+                        w[r][2] = v.z;
+                        w[r][3] = v.w;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
+                        const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
+                        const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
+                        const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+#pragma unroll
+                        for (int t = 0; t < kN; ++t) {
+                            mma16816(o[t][4 * x + i], a0, a1, a2, a3, p[t][0], p[t][1]);
+                            mma16816(o[t][4 * x + i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            issue();
+        }
+        cp_wait<0>();
+        __syncwarp();
+
+        // ---- join the warps: O in the warp's ring, (m, l) beside it
+        float *so = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int t = 0; t < kN; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * t + 2 * c + e;
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+                if (g == 0) {
+                    sm_m[warp][r] = m[t][e];
+                    sm_l[warp][r] = l[t][e];
+                }
+                // MMA i, rows g and g + 8: dims d + 2 i and d + 2 i + 1 (bf16: of each 64-dim half)
+                if (r < rows)
+#pragma unroll
+                    for (int i = 0; i < kM; i += 2) {
+                        const int d = kInt8 ? (D == 128 ? 16 * v_chunk(g) : 8 * g) + 2 * i
+                                            : 64 * (i / 4) + 8 * v_chunk(g) + 2 * (i % 4);
+                        *reinterpret_cast<float4 *>(so + r * C::kLdO + d) =
+                            make_float4(o[t][i][e], o[t][i][2 + e], o[t][i + 1][e], o[t][i + 1][2 + e]);
+                    }
+            }
+        __syncthreads();
+        const bool whole = u == item0 && seg_end == item1;
+        const int slot = 2 * blockIdx.x + (u == item0 ? 1 : 0);
+        float *part_o = plan.part + (int64_t)slot * R * D;
+        float *part_ml = plan.part + (int64_t)2 * gridDim.x * R * D + slot * 2 * R;
+        if (threadIdx.x < R) {
+            const int r = threadIdx.x;
+            float M = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
+            const float Mx = M == -INFINITY ? 0.0f : M;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float wt = fast_exp2(sm_m[w][r] - Mx);
+                sm_w[w][r] = wt;
+                sum += wt * sm_l[w][r];
+            }
+            if (whole) {
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sm_w[w][r] *= inv;
+                sm_lse[r] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+            } else {
+                part_ml[2 * r] = M;
+                part_ml[2 * r + 1] = sum;
+            }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    reinterpret_cast<const float *>(smem + w * C::kRing) + r * C::kLdO + d);
+                const float wt = sm_w[w][r];
+                acc.x = fmaf(wt, v.x, acc.x);
+                acc.y = fmaf(wt, v.y, acc.y);
+                acc.z = fmaf(wt, v.z, acc.z);
+                acc.w = fmaf(wt, v.w, acc.w);
+            }
+            if (whole) {
+                const int row = tile * R + r;
+                const int64_t t = sh.row0 + row / G;
+                const int h = head * G + row % G;
+                *reinterpret_cast<uint2 *>(a.O + t * a.o_stride + (int64_t)h * D + d) =
+                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                if (d == 0 && a.lse) a.lse[t * a.Hq + h] = sm_lse[r];
+            } else {
+                *reinterpret_cast<float4 *>(part_o + r * D + d) = acc;
+            }
+        }
+
+        // ---- a piece of an item: the last CTA to arrive joins the pieces
+        if (!whole) {
+            const int c0 = (int)(((item0 + 1) * grid - 1) / total), c1 = (int)((item1 * grid - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const int n = atomicAdd(&plan.count[c0], 1);
+                sm_last = n == c1 - c0;
+                if (sm_last) plan.count[c0] = 0;  // for the next call
+            }
+            __syncthreads();
+            if (sm_last) {
+                __threadfence();
+                const float *ml = plan.part + (int64_t)2 * gridDim.x * R * D;
+                for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
+                    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+                    float M = -INFINITY;
+                    for (int x = c0; x <= c1; ++x)
+                        M = fmaxf(M, __ldcg(ml + (2 * x + (x == c0 ? 1 : 0)) * 2 * R + 2 * r));
+                    const float Mx = M == -INFINITY ? 0.0f : M;
+                    float sum = 0.0f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int x = c0; x <= c1; ++x) {
+                        const int sl = 2 * x + (x == c0 ? 1 : 0);
+                        const float2 e = __ldcg(reinterpret_cast<const float2 *>(ml + sl * 2 * R + 2 * r));
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(plan.part + (int64_t)sl * R * D +
+                                                                                 r * D + d));
+                        const float wt = fast_exp2(e.x - Mx);
+                        sum = fmaf(wt, e.y, sum);
+                        acc.x = fmaf(wt, v.x, acc.x);
+                        acc.y = fmaf(wt, v.y, acc.y);
+                        acc.z = fmaf(wt, v.z, acc.z);
+                        acc.w = fmaf(wt, v.w, acc.w);
+                    }
+                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    const int row = tile * R + r;
+                    const int64_t t = sh.row0 + row / G;
+                    const int h = head * G + row % G;
+                    *reinterpret_cast<uint2 *>(a.O + t * a.o_stride + (int64_t)h * D + d) =
+                        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+                    if (d == 0 && a.lse)
+                        a.lse[t * a.Hq + h] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                }
+            }
+        }
+        __syncthreads();  // the rings and the small arrays are free again
+        u = seg_end;
+    }
+}
+
+}  // namespace
+
+int kv_decode_grid(int num_sms) { return 4 * num_sms; }
+
+size_t kv_decode_part_floats(int D, int num_sms) { return (size_t)2 * kv_decode_grid(num_sms) * 16 * (D + 2); }
+
+cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int max_new,
+                             int max_rows, float *part, int *count, int num_sms, cudaStream_t stream)
+{
+    auto launch = [&](auto cfg, auto *fn) {
+        using C = decltype(cfg);
+        const cudaError_t e = ensure_smem_attr((const void *)fn, C::kSmem);
+        if (e != cudaSuccess) return e;
+        const Plan plan{max_rows, a.scale * 1.4426950408889634f, part, count};
+        fn<<<C::kCtas * num_sms, kWarps * 32, C::kSmem, stream>>>(kv, b, a, plan);
+        return cudaGetLastError();
+    };
+    // one tile of 8 rows where the chunk's rows fit it, else two an item
+    const bool one = (int64_t)max_new * a.G <= 8;
+    if (kv.D == 128) {
+        if (int8)
+            return one ? launch(Cfg<128, true, 1>(), kv_decode_kernel<128, true, 1>)
+                       : launch(Cfg<128, true, 2>(), kv_decode_kernel<128, true, 2>);
+        return one ? launch(Cfg<128, false, 1>(), kv_decode_kernel<128, false, 1>)
+                   : launch(Cfg<128, false, 2>(), kv_decode_kernel<128, false, 2>);
+    }
+    if (int8)
+        return one ? launch(Cfg<64, true, 1>(), kv_decode_kernel<64, true, 1>)
+                   : launch(Cfg<64, true, 2>(), kv_decode_kernel<64, true, 2>);
+    return one ? launch(Cfg<64, false, 1>(), kv_decode_kernel<64, false, 1>)
+               : launch(Cfg<64, false, 2>(), kv_decode_kernel<64, false, 2>);
+}
+
+}  // namespace lora

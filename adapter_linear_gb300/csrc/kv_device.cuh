@@ -60,4 +60,39 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
     return (((int64_t)page * kv.H) << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
 }
 
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^x, to about 2^-22 of it; 0 for -inf
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two 8-bit codes to two bf16, exactly. x holds code a in bits 0..7 and code b in bits 16..23
+// (the other bits are ignored). A code is (low 7 bits) - (its sign bit's 128), and in bf16
+// 0x4300 | v is 128 + v for v < 128 and 0x4380 is 256: code = (128 + low) - (128 or 256).
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x)
+{
+    const uint32_t low = (x & 0x007F007Fu) | 0x43004300u;
+    const uint32_t sign = (x & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&low),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&sign));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The four codes of a word, in order, as two bf16 pairs.
+__device__ __forceinline__ void codes4_to_bf16(uint32_t w, uint32_t *lo, uint32_t *hi)
+{
+    *lo = codes_to_bf16(__byte_perm(w, 0, 0x4140));
+    *hi = codes_to_bf16(__byte_perm(w, 0, 0x4342));
+}
+
+// Code i (0..3) of word a and code i of word b as a bf16 pair.
+__device__ __forceinline__ uint32_t codes_pair_to_bf16(uint32_t a, uint32_t b, int i)
+{
+    return codes_to_bf16(__byte_perm(a, b, 0x0400u + 0x0101u * (uint32_t)i));
+}
+
 }  // namespace lora

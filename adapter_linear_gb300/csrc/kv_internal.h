@@ -43,7 +43,12 @@ struct KvAttn {
     float scale;
 };
 
-cudaError_t launch_kv_attention(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
-                                cudaStream_t stream);
+// The kernel for short chunks. It takes the sequences of at most max_rows rows (new tokens times
+// G); max_new is the caller's bound on the new tokens of one. part, count: scratch of kv_decode_part_floats floats and kv_decode_grid ints (zero
+// between calls), used by one call at a time.
+int kv_decode_grid(int num_sms);
+size_t kv_decode_part_floats(int D, int num_sms);
+cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int max_new,
+                             int max_rows, float *part, int *count, int num_sms, cudaStream_t stream);
 
 }  // namespace lora

@@ -16,5 +16,12 @@ struct lora_kv {
     int *d_err = nullptr;                      // [0] the error word, [1] its value at the last read
     int *h_err = nullptr;                      // pinned copy of d_err[1]
     cudaEvent_t ev_call = nullptr;             // the last call enqueued
+    // the attention's scratch, used by one call at a time: a call on another stream than the
+    // last one's waits for it (ev_attn)
+    float *part = nullptr;
+    int *count = nullptr;
+    cudaEvent_t ev_attn = nullptr;
+    cudaStream_t attn_stream = nullptr;
+    bool attn_any = false;
     cudaStream_t ctl_stream = nullptr;         // error-word reads; follows every call
 };
