@@ -30,6 +30,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;            // tokens per warp step: never crosses a page (pages hold 16 k)
 constexpr int kUnit = kWarps * kStep;
+#ifndef MINU
+#define MINU 2
+#endif
+constexpr int kMinUnits = MINU;
 
 // kN: tiles of 8 rows (a row: one query head of one new token) an item holds.
 template <int D, bool kInt8, int kN>
@@ -46,6 +50,7 @@ struct Cfg {
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * kRing;
     static constexpr int kLdO = D + 4;                           // fp32 row of O in shared memory
+    static constexpr int kMaxGrid = kSmem / (4 * kRows);         // pieces whose weights fit the rings
     static_assert(kRing >= kRows * kLdO * 4, "O of a warp is parked in its ring");
 };
 
@@ -75,7 +80,15 @@ __device__ __forceinline__ void cp_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// D += A B, 16 x 8 x 16, bf16 in, fp32 sums
+// D += A B, 16 x 8 x 16, fp32 sums; bf16 operands (mma16816) or f16 ones (mma16816_f16)
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1)
 {
@@ -156,13 +169,19 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     const int g = lane >> 2, c = lane & 3;
     const int G = a.G;
 
-    // this CTA's share of all units: every warp adds up the sequences by itself
-    int64_t total = 0;
-    for (int s = lane; s < b.n_seqs; s += 32)
-        total += seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window);
+    // this CTA's share of all units: every warp adds up the sequences by itself, lane i those
+    // of i, i + 32, ...
+    int64_t total = 0, first = 0;
+    for (int s = lane; s < b.n_seqs; s += 32) {
+        const int64_t v = seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window);
+        if (s == lane) first = v;
+        total += v;
+    }
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-    const int64_t grid = min((int64_t)gridDim.x, total);
+    // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
+    // they save
+    const int64_t grid = min((int64_t)gridDim.x, (total + kMinUnits - 1) / kMinUnits);
     if ((int64_t)blockIdx.x >= grid) return;
     int64_t u = (int64_t)blockIdx.x * total / grid;
     const int64_t u_end = ((int64_t)blockIdx.x + 1) * total / grid;
@@ -172,8 +191,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     int64_t before = 0;
     for (int s0 = 0;; s0 += 32) {
         const int s = s0 + lane;
-        int64_t mine =
-            s < b.n_seqs ? seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window) : 0;
+        int64_t mine = first;
+        if (s0 > 0)
+            mine = s < b.n_seqs ? seq_units<R>(seq_shape<R>(kv, b, s, G, plan.max_rows), kv.H, G, a.window) : 0;
         int64_t incl = mine;
 #pragma unroll
         for (int x = 1; x < 32; x <<= 1) {
@@ -192,6 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     SeqShape sh = seq_shape<R>(kv, b, seq, G, plan.max_rows);
     int64_t seq_end = before + seq_units<R>(sh, kv.H, G, a.window);
 
+    const uint32_t base = kv_opaque(0x43004300u);
     uint8_t *const ring = smem + warp * C::kRing;
     const uint32_t ring_addr = smem_u32(ring);
     // this lane's part of a copy: chunks lane + 32 x of a tile
@@ -279,7 +300,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         // Q as the 8-column operand: lane (g, c) holds row g of each tile; its dims of MMA i are
         // those its K words hold (8-bit: 64-dim blocks of 16 dims a lane; bf16: 32-dim blocks of 8)
         uint32_t q[kN][kM][2];
-        int pos[kN][2];  // positions of the rows this lane has scores of: 8 t + 2 c, + 1
+        float back_mul[kN][2];  // of the rows this lane has scores of: to units of log2
+        int pos[kN][2];         // and their positions of the rows this lane has scores of: 8 t + 2 c, + 1
 #pragma unroll
         for (int t = 0; t < kN; ++t) {
             const int row = tile * R + 8 * t + g;
@@ -299,6 +321,34 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                     q[t][i0 + 1][0] = v.z;
                     q[t][i0 + 1][1] = v.w;
                 }
+            // An 8-bit cache's codes become f16 in two thirds of the instructions bf16 takes, so Q
+            // becomes f16 too, its row scaled by the power of two that puts the largest magnitude
+            // into [2^14, 2^15): values down to 2^-28 of that keep all their bits, and the
+            // rest are off by at most 2^-39 of it.
+            if (kInt8) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < kM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        top = max(top, max(q[t][i][e] & 0x7FFFu, (q[t][i][e] >> 16) & 0x7FFFu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int up = min(14 + 127 - (int)(top >> 7), 126);  // bf16's exponent field
+                const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+                const float back = __uint_as_float((uint32_t)(127 - up) << 23);
+#pragma unroll
+                for (int i = 0; i < kM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __half2 h = __floats2half2_rn(bf16_lo(q[t][i][e]) * mul, bf16_hi(q[t][i][e]) * mul);
+                        q[t][i][e] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
+                back_mul[t][0] = __shfl_sync(0xffffffffu, back, 8 * c) * plan.scale_log2;
+                back_mul[t][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4) * plan.scale_log2;
+            } else {
+                back_mul[t][0] = back_mul[t][1] = plan.scale_log2;
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * t + 2 * c + e;  // rows beyond the tile: any position, not written
@@ -349,11 +399,11 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t a0, a1, a2, a3;
-                        codes4_to_bf16(u0[j], &a0, &a2);
-                        codes4_to_bf16(u1[j], &a1, &a3);
+                        codes4_to_f16(u0[j], &a0, &a2);
+                        codes4_to_f16(u1[j], &a1, &a3);
 #pragma unroll
                         for (int t = 0; t < kN; ++t)
-                            mma16816(s[t], a0, a1, a2, a3, q[t][4 * x + j][0], q[t][4 * x + j][1]);
+                            mma16816_f16(s[t], a0, a1, a2, a3, q[t][4 * x + j][0], q[t][4 * x + j][1]);
                     }
                 } else {
 #pragma unroll
@@ -366,12 +416,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             }
 
             // z in units of log2, masked; s[t][2 y + e]: token g + 8 y, row 8 t + 2 c + e
-            float mul[2] = {plan.scale_log2, plan.scale_log2}, vs[2] = {1.0f, 1.0f};
+            float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
             if (kInt8) {
                 const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * C::kTile);
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    mul[y] *= __uint_as_float((uint32_t)sc[g + 8 * y] << 16);
+                    ks[y] = __uint_as_float((uint32_t)sc[g + 8 * y] << 16);
                     vs[y] = __uint_as_float((uint32_t)sc[16 + g + 8 * y] << 16);
                 }
             }
@@ -383,7 +433,8 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 for (int e = 0; e < 2; ++e) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        s[t][2 * y + e] *= mul[y];
+                        s[t][2 * y + e] *= back_mul[t][e];
+                        if (kInt8) s[t][2 * y + e] *= ks[y];
                         if (edge) {
                             const int j = tok + g + 8 * y, p = pos[t][e];
                             const bool see = j <= p && (a.window == 0 || j > p - a.window);
@@ -461,10 +512,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 #pragma unroll
                 for (int i = 0; i < kM; ++i) {
                     const int x = i >> 1, y = 2 * (i & 1);
-                    const uint32_t a0 = codes_pair_to_bf16(w[0][x], w[1][x], y);
-                    const uint32_t a1 = codes_pair_to_bf16(w[0][x], w[1][x], y + 1);
-                    const uint32_t a2 = codes_pair_to_bf16(w[2][x], w[3][x], y);
-                    const uint32_t a3 = codes_pair_to_bf16(w[2][x], w[3][x], y + 1);
+                    const uint32_t a0 = codes_pair_to_bf16(w[0][x], w[1][x], y, base);
+                    const uint32_t a1 = codes_pair_to_bf16(w[0][x], w[1][x], y + 1, base);
+                    const uint32_t a2 = codes_pair_to_bf16(w[2][x], w[3][x], y, base);
+                    const uint32_t a3 = codes_pair_to_bf16(w[2][x], w[3][x], y + 1, base);
 #pragma unroll
                     for (int t = 0; t < kN; ++t) {
                         mma16816(o[t][i], a0, a1, a2, a3, p[t][0], p[t][1]);
@@ -595,36 +646,57 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             __syncthreads();
             if (sm_last) {
                 __threadfence();
+                // the pieces' weights first (into the rings), then their O: two rounds of
+                // independent loads, not one load after another
                 const float *ml = plan.part + (int64_t)2 * gridDim.x * R * D;
+                float *wt = reinterpret_cast<float *>(smem);  // [piece][R]
+                const int n = c1 - c0 + 1;                    // at most kMaxGrid
+                for (int i = threadIdx.x; i < n * R; i += kWarps * 32) {
+                    const int x = i / R, r = i % R;
+                    wt[i] = __ldcg(ml + (2 * (c0 + x) + (x == 0 ? 1 : 0)) * 2 * R + 2 * r);
+                }
+                __syncthreads();
+                // a row's maximum and weights by one warp: rows warp, warp + 4, ...
+                for (int r = warp; r < R; r += kWarps) {
+                    float M = -INFINITY, sum = 0.0f;
+                    for (int x = lane; x < n; x += 32) M = fmaxf(M, wt[x * R + r]);
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+                    const float Mx = M == -INFINITY ? 0.0f : M;
+                    for (int x = lane; x < n; x += 32) {
+                        const float w = fast_exp2(wt[x * R + r] - Mx);
+                        sum += w * __ldcg(ml + (2 * (c0 + x) + (x == 0 ? 1 : 0)) * 2 * R + 2 * r + 1);
+                        wt[x * R + r] = w;
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                    if (lane == 0) {
+                        sm_w[0][r] = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        sm_lse[r] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                    }
+                }
+                __syncthreads();
                 for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
                     const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-                    float M = -INFINITY;
-                    for (int x = c0; x <= c1; ++x)
-                        M = fmaxf(M, __ldcg(ml + (2 * x + (x == c0 ? 1 : 0)) * 2 * R + 2 * r));
-                    const float Mx = M == -INFINITY ? 0.0f : M;
-                    float sum = 0.0f;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int x = c0; x <= c1; ++x) {
-                        const int sl = 2 * x + (x == c0 ? 1 : 0);
-                        const float2 e = __ldcg(reinterpret_cast<const float2 *>(ml + sl * 2 * R + 2 * r));
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(plan.part + (int64_t)sl * R * D +
-                                                                                 r * D + d));
-                        const float wt = fast_exp2(e.x - Mx);
-                        sum = fmaf(wt, e.y, sum);
-                        acc.x = fmaf(wt, v.x, acc.x);
-                        acc.y = fmaf(wt, v.y, acc.y);
-                        acc.z = fmaf(wt, v.z, acc.z);
-                        acc.w = fmaf(wt, v.w, acc.w);
+                    const float *src = plan.part + r * D + d;
+#pragma unroll 8
+                    for (int x = 0; x < n; ++x) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                            src + (int64_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * R * D));
+                        const float w = wt[x * R + r];
+                        acc.x = fmaf(w, v.x, acc.x);
+                        acc.y = fmaf(w, v.y, acc.y);
+                        acc.z = fmaf(w, v.z, acc.z);
+                        acc.w = fmaf(w, v.w, acc.w);
                     }
-                    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                    const float inv = sm_w[0][r];
                     const int row = tile * R + r;
                     const int64_t t = sh.row0 + row / G;
                     const int h = head * G + row % G;
                     *reinterpret_cast<uint2 *>(a.O + t * a.o_stride + (int64_t)h * D + d) =
                         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-                    if (d == 0 && a.lse)
-                        a.lse[t * a.Hq + h] = sum == 0.0f ? -INFINITY : (M + log2f(sum)) * kLn2;
+                    if (d == 0 && a.lse) a.lse[t * a.Hq + h] = sm_lse[r];
                 }
             }
         }
@@ -647,7 +719,7 @@ cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, co
         const cudaError_t e = ensure_smem_attr((const void *)fn, C::kSmem);
         if (e != cudaSuccess) return e;
         const Plan plan{max_rows, a.scale * 1.4426950408889634f, part, count};
-        fn<<<C::kCtas * num_sms, kWarps * 32, C::kSmem, stream>>>(kv, b, a, plan);
+        fn<<<min(C::kCtas * num_sms, C::kMaxGrid), kWarps * 32, C::kSmem, stream>>>(kv, b, a, plan);
         return cudaGetLastError();
     };
     // one tile of 8 rows where the chunk's rows fit it, else two an item

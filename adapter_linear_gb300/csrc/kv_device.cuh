@@ -2,6 +2,8 @@
 // a token's cache row, and the conversions between 8-bit codes and values.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "device_common.cuh"
 #include "kv_internal.h"
 
@@ -70,29 +72,51 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
+// (x & mask) | bits in one instruction: with both constants known the compiler makes two of it,
+// so `bits` comes from a register it cannot see through (kv_opaque).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(bits));
+    return r;
+}
+__device__ __forceinline__ uint32_t kv_opaque(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("mov.b32 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // Two 8-bit codes to two bf16, exactly. x holds code a in bits 0..7 and code b in bits 16..23
 // (the other bits are ignored). A code is (low 7 bits) - (its sign bit's 128), and in bf16
 // 0x4300 | v is 128 + v for v < 128 and 0x4380 is 256: code = (128 + low) - (128 or 256).
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x)
+// base: 0x43004300 from kv_opaque.
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x, uint32_t base)
 {
-    const uint32_t low = (x & 0x007F007Fu) | 0x43004300u;
-    const uint32_t sign = (x & 0x00800080u) | 0x43004300u;
+    const uint32_t low = and_or(x, 0x007F007Fu, base);
+    const uint32_t sign = and_or(x, 0x00800080u, base);
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&low),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&sign));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// The four codes of a word, in order, as two bf16 pairs.
-__device__ __forceinline__ void codes4_to_bf16(uint32_t w, uint32_t *lo, uint32_t *hi)
+// The four codes of a word, in order, as two f16 pairs, exactly: 0x6400 | v is 1024 + v in f16,
+// v = code + 128.
+__device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t *lo, uint32_t *hi)
 {
-    *lo = codes_to_bf16(__byte_perm(w, 0, 0x4140));
-    *hi = codes_to_bf16(__byte_perm(w, 0, 0x4342));
+    w ^= 0x80808080u;
+    const uint32_t bias = 0x64806480u;  // 1024 + 128, twice
+    const uint32_t x[2] = {__byte_perm(w, 0x64646464u, 0x4140), __byte_perm(w, 0x64646464u, 0x4342)};
+    const __half2 l = __hsub2(*reinterpret_cast<const __half2 *>(&x[0]), *reinterpret_cast<const __half2 *>(&bias));
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x[1]), *reinterpret_cast<const __half2 *>(&bias));
+    *lo = *reinterpret_cast<const uint32_t *>(&l);
+    *hi = *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Code i (0..3) of word a and code i of word b as a bf16 pair.
-__device__ __forceinline__ uint32_t codes_pair_to_bf16(uint32_t a, uint32_t b, int i)
+__device__ __forceinline__ uint32_t codes_pair_to_bf16(uint32_t a, uint32_t b, int i, uint32_t base)
 {
-    return codes_to_bf16(__byte_perm(a, b, 0x0400u + 0x0101u * (uint32_t)i));
+    return codes_to_bf16(__byte_perm(a, b, 0x0400u + 0x0101u * (uint32_t)i), base);
 }
 
 }  // namespace lora
