@@ -202,8 +202,10 @@ bool tensor_ok(const void *p, int64_t stride, int64_t row)
     return p && aligned16(p) && stride >= row && stride % 8 == 0;
 }
 
+constexpr int kMaxTokens = 1 << 30;  // of a call or a sequence: positions stay clear of 32 bits
+
 // A batch the kernels can take; *empty: there is nothing to do.
-lora_status check_batch(const lora_kv_batch *b, bool *empty)
+lora_status check_batch(const lora_kv_batch *b, int page_shift, bool *empty)
 {
     *empty = false;
     if (!b || b->n_seqs < 0 || b->T < 0 || b->max_new < 0) return LORA_ERR_ARG;
@@ -212,6 +214,7 @@ lora_status check_batch(const lora_kv_batch *b, bool *empty)
         return LORA_OK;
     }
     if (!b->page_table || !b->start || !b->kv_len || b->table_stride < 1) return LORA_ERR_ARG;
+    if (b->T > kMaxTokens || ((int64_t)b->table_stride << page_shift) > kMaxTokens) return LORA_ERR_ARG;
     return LORA_OK;
 }
 
@@ -240,6 +243,21 @@ KvDev kv_view(const lora_kv *p)
     v.D = p->D;
     v.err = p->d_err;
     return v;
+}
+
+constexpr int kDecodeRows = 16;
+
+// The tcgen05 kernel's scratch (40 MB for D = 128), from the first call that needs it.
+lora_status ensure_pre_part(lora_kv *p)
+{
+    if (p->pre_part) return LORA_OK;
+    const size_t bytes = sizeof(float) * kv_prefill_part_floats(p->D, p->num_sms);
+    if (cudaMalloc((void **)&p->pre_part, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        p->pre_part = nullptr;
+        return LORA_ERR_OOM;
+    }
+    return LORA_OK;
 }
 
 // Calls inside a graph capture are not tracked: the order of replays is the caller's.
@@ -301,9 +319,9 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
     p->v = v_pages;
     p->ks = static_cast<uint16_t *>(k_scales);
     p->vs = static_cast<uint16_t *>(v_scales);
-    const size_t counts = sizeof(int) * (size_t)kv_decode_grid(sms);
+    const size_t counts = sizeof(int) * (size_t)(kv_decode_grid(sms) + 8 * kv_prefill_grid(sms));
     if (cudaMalloc((void **)&p->d_err, 2 * sizeof(int)) != cudaSuccess ||
-        cudaMalloc((void **)&p->part, sizeof(float) * kv_decode_part_floats(head_dim, sms)) != cudaSuccess ||
+        cudaMalloc((void **)&p->dec_part, sizeof(float) * kv_decode_part_floats(head_dim, sms)) != cudaSuccess ||
         cudaMalloc((void **)&p->count, counts) != cudaSuccess ||
         cudaHostAlloc((void **)&p->h_err, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
         cudaGetLastError();
@@ -331,7 +349,8 @@ lora_status lora_kv_destroy(lora_kv_t p)
     if (p->ctl_stream) cudaStreamDestroy(p->ctl_stream);
     if (p->ev_call) cudaEventDestroy(p->ev_call);
     if (p->ev_attn) cudaEventDestroy(p->ev_attn);
-    if (p->part) cudaFree(p->part);
+    if (p->dec_part) cudaFree(p->dec_part);
+    if (p->pre_part) cudaFree(p->pre_part);
     if (p->count) cudaFree(p->count);
     if (p->d_err) cudaFree(p->d_err);
     if (p->h_err) cudaFreeHost(p->h_err);
@@ -343,7 +362,7 @@ lora_status lora_kv_reserve(lora_kv_t p, int max_tokens, int n_heads, int max_se
 {
     if (!p || max_tokens < 0 || max_seqs < 0) return LORA_ERR_ARG;
     if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
-    return LORA_OK;
+    return max_tokens > max_seqs ? ensure_pre_part(p) : LORA_OK;  // single tokens never need it
 }
 
 lora_status lora_kv_write(lora_kv_t p, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
@@ -351,7 +370,7 @@ lora_status lora_kv_write(lora_kv_t p, const void *K, int64_t k_stride, const vo
 {
     if (!p) return LORA_ERR_ARG;
     bool empty;
-    lora_status st = check_batch(batch, &empty);
+    lora_status st = check_batch(batch, p->page_shift, &empty);
     if (st != LORA_OK || empty) return st;
     const int64_t row = (int64_t)p->H * p->D;
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
@@ -365,7 +384,7 @@ lora_status lora_kv_read(lora_kv_t p, void *K, int64_t k_stride, void *V, int64_
 {
     if (!p) return LORA_ERR_ARG;
     bool empty;
-    lora_status st = check_batch(batch, &empty);
+    lora_status st = check_batch(batch, p->page_shift, &empty);
     if (st != LORA_OK || empty) return st;
     const int64_t row = (int64_t)p->H * p->D;
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
@@ -381,8 +400,9 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     if (!p || window < 0) return LORA_ERR_ARG;
     if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
     bool empty;
-    lora_status st = check_batch(batch, &empty);
+    lora_status st = check_batch(batch, p->page_shift, &empty);
     if (st != LORA_OK || empty) return st;
+    if ((int64_t)batch->T * n_heads > INT_MAX) return LORA_ERR_ARG;
     const int64_t row = (int64_t)n_heads * p->D;
     if (!tensor_ok(Q, q_stride, row) || !tensor_ok(O, o_stride, row)) return LORA_ERR_ARG;
     KvAttn a;
@@ -393,14 +413,25 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     a.o_stride = o_stride;
     a.Hq = n_heads;
     a.G = n_heads / p->H;
-    a.window = window;
+    a.window = std::min(window, kMaxTokens);
     a.scale = scale;
+    // Sequences of up to kDecodeRows rows of a kv head go to the short-chunk kernel, others to
+    // the tcgen05 kernel; where max_new says that there is only one kind, one launch takes all.
+    const bool prefill = (int64_t)batch->max_new * a.G > kDecodeRows;
+    const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * batch->max_new;
+    if (prefill && (st = ensure_pre_part(p)) != LORA_OK) return st;
     bool tracked;
     if ((st = is_tracked(stream, &tracked)) != LORA_OK) return st;
     // the scratch belongs to one call at a time: after the last one, if that ran elsewhere
     if (tracked && p->attn_any && stream != p->attn_stream) CUDA_TRY(cudaStreamWaitEvent(stream, p->ev_attn, 0));
-    CUDA_TRY(launch_kv_decode(kv_view(p), p->int8, batch_view(batch), a, batch->max_new, INT_MAX, p->part,
-                              p->count, p->num_sms, stream));
+    const KvDev kv = kv_view(p);
+    const KvBatchDev bd = batch_view(batch);
+    if (decode)
+        CUDA_TRY(launch_kv_decode(kv, p->int8, bd, a, batch->max_new, prefill ? kDecodeRows : INT_MAX, p->dec_part,
+                                  p->count, p->num_sms, stream));
+    if (prefill)
+        CUDA_TRY(launch_kv_prefill(kv, p->int8, bd, a, decode ? kDecodeRows + 1 : 0, p->pre_part,
+                                   p->count + kv_decode_grid(p->num_sms), p->num_sms, stream));
     if (!tracked) return LORA_OK;
     CUDA_TRY(cudaEventRecord(p->ev_attn, stream));
     CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev_attn, 0));

@@ -62,6 +62,170 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
     return (((int64_t)page * kv.H) << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
 }
 
+// The work of an attention kernel and one CTA's share of it.
+//
+// An item is (sequence, tile of R rows, kv head); a row is one query head of one new token: row
+// r of a sequence is token r / G, head r % G of the kv head's G. An item's visible tokens [lo,
+// hi), lo rounded down to 16 (so that 16 tokens from there never cross a page), are cut into
+// units of kUnit tokens, at least one (rows that see nothing still write their zeros). Units are
+// numbered sequence by sequence, tile by tile, head by head; CTA c of `grid` takes units
+// [c total / grid, (c + 1) total / grid). Every member is called by whole warps, which all
+// compute the same. Sequences with n G outside min_rows..max_rows are left out.
+template <int R, int kUnit>
+struct KvWork {
+    const KvDev &kv;
+    const KvBatchDev &b;
+    const int G, window, min_rows, max_rows, lane;
+    int64_t total = 0;           // units of all items
+    int64_t grid = 0, u_end = 0;
+    int64_t u = 0, seg_end = 0;  // the current segment: units [u, seg_end) of one item
+    int64_t item0 = 0;           // the item's first unit
+    int64_t tile0 = 0;           // first unit of the tile's first head
+    int seq = -1, tile = 0, tiles = 0, nu = 0, head = 0, lo = 0, hi = 0;
+    KvSeq sh{0, 0, 0};
+
+    __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, int G_, int window_, int min_rows_,
+                                      int max_rows_, int lane_)
+        : kv(kv_), b(b_), G(G_), window(window_), min_rows(min_rows_), max_rows(max_rows_), lane(lane_)
+    {
+        for (int s0 = 0; s0 < b.n_seqs; s0 += 32) {
+            const int64_t v = units_of_32(s0);
+            if (s0 == 0) first_ = v;
+            total += v;
+        }
+        total = sum(total);
+    }
+
+    // Take share c of n; false: it is empty.
+    __device__ __forceinline__ bool take_share(int64_t c, int64_t n)
+    {
+        grid = n;
+        if (c >= n) return false;
+        seg_end = c * total / n;
+        u_end = (c + 1) * total / n;
+        int64_t before = 0;
+        for (int s0 = 0;; s0 += 32) {
+            const int64_t mine = s0 == 0 ? first_ : units_of_32(s0);
+            const int64_t incl = scan(mine);
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > seg_end);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                before += __shfl_sync(0xffffffffu, incl - mine, k);
+                set_seq(s0 + k);
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        for (int t0 = 0;; t0 += 32) {  // the tile, 32 at a time
+            const int64_t mine = t0 + lane < tiles ? (int64_t)units(sh, t0 + lane) * kv.H : 0;
+            const int64_t incl = scan(mine);
+            const uint32_t past = __ballot_sync(0xffffffffu, before + incl > seg_end);
+            if (past) {
+                const int k = __ffs(past) - 1;
+                tile0 = before + __shfl_sync(0xffffffffu, incl - mine, k);
+                set_tile(t0 + k);
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+
+    // The share's next segment; false at its end.
+    __device__ __forceinline__ bool next()
+    {
+        u = seg_end;
+        if (u >= u_end) return false;
+        while (u >= tile0 + (int64_t)nu * kv.H) {
+            tile0 += (int64_t)nu * kv.H;
+            if (tile + 1 < tiles) {
+                set_tile(tile + 1);
+            } else {
+                do set_seq(seq + 1);
+                while (tiles == 0);
+                set_tile(0);
+            }
+        }
+        head = (int)((u - tile0) / nu);
+        item0 = tile0 + (int64_t)head * nu;
+        seg_end = min(item0 + nu, u_end);
+        return true;
+    }
+
+    __device__ __forceinline__ bool whole() const { return u == item0 && seg_end == item0 + nu; }
+    // The CTA whose share holds unit x (total >= grid: no share is empty).
+    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * grid - 1) / total); }
+
+private:
+    int64_t first_ = 0;  // the units of sequence `lane`
+
+    __device__ __forceinline__ int tiles_of(const KvSeq &s) const
+    {
+        const int64_t rows = (int64_t)s.n * G;
+        return rows >= min_rows && rows <= max_rows ? (int)((rows + R - 1) / R) : 0;
+    }
+    __device__ __forceinline__ void range(const KvSeq &s, int t, int *lo_, int *hi_) const
+    {
+        const int i0 = (int)((int64_t)t * R / G), i1 = (int)min((int64_t)s.n - 1, ((int64_t)t * R + R - 1) / G);
+        const int p0 = s.L - s.n + i0, p1 = s.L - s.n + i1;
+        *hi_ = max(0, p1 + 1);
+        *lo_ = min((window > 0 ? max(0, p0 - window + 1) : 0) & ~15, *hi_);
+    }
+    __device__ __forceinline__ int units(const KvSeq &s, int t) const
+    {
+        int l, h;
+        range(s, t, &l, &h);
+        return max(1, (h - l + kUnit - 1) / kUnit);
+    }
+    // Units of sequence s0 + lane (0 past the last). Few tiles: a lane counts its own; a sequence
+    // of many is counted by all lanes together.
+    __device__ __forceinline__ int64_t units_of_32(int s0) const
+    {
+        KvSeq s{0, 0, 0};
+        if (s0 + lane < b.n_seqs) s = kv_seq(b, kv.page_shift, s0 + lane, kv.err);
+        const int n = tiles_of(s);
+        int64_t v = 0;
+        if (n <= 8)
+            for (int t = 0; t < n; ++t) v += units(s, t);
+        for (uint32_t todo = __ballot_sync(0xffffffffu, n > 8); todo; todo &= todo - 1) {
+            const int k = __ffs(todo) - 1;
+            const KvSeq q{0, __shfl_sync(0xffffffffu, s.n, k), __shfl_sync(0xffffffffu, s.L, k)};
+            const int m = __shfl_sync(0xffffffffu, n, k);
+            int64_t part = 0;
+            for (int t = lane; t < m; t += 32) part += units(q, t);
+            part = sum(part);
+            if (lane == k) v = part;
+        }
+        return v * kv.H;
+    }
+    __device__ __forceinline__ void set_seq(int s)
+    {
+        seq = s;
+        sh = kv_seq(b, kv.page_shift, s, kv.err);
+        tiles = tiles_of(sh);
+    }
+    __device__ __forceinline__ void set_tile(int t)
+    {
+        tile = t;
+        range(sh, t, &lo, &hi);
+        nu = units(sh, t);
+    }
+    static __device__ __forceinline__ int64_t sum(int64_t v)
+    {
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        return v;
+    }
+    __device__ __forceinline__ int64_t scan(int64_t v) const
+    {
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, v, x);
+            if (lane >= x) v += o;
+        }
+        return v;
+    }
+};
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^x, to about 2^-22 of it; 0 for -inf
@@ -111,6 +275,13 @@ __device__ __forceinline__ void codes4_to_f16(uint32_t w, uint32_t *lo, uint32_t
     const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&x[1]), *reinterpret_cast<const __half2 *>(&bias));
     *lo = *reinterpret_cast<const uint32_t *>(&l);
     *hi = *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The four codes of a word, in order, as two bf16 pairs.
+__device__ __forceinline__ void codes4_to_bf16(uint32_t w, uint32_t base, uint32_t *lo, uint32_t *hi)
+{
+    *lo = codes_to_bf16(__byte_perm(w, 0, 0x4140), base);
+    *hi = codes_to_bf16(__byte_perm(w, 0, 0x4342), base);
 }
 
 // Code i (0..3) of word a and code i of word b as a bf16 pair.

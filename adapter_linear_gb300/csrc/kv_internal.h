@@ -51,4 +51,11 @@ size_t kv_decode_part_floats(int D, int num_sms);
 cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int max_new,
                              int max_rows, float *part, int *count, int num_sms, cudaStream_t stream);
 
+// The kernel for longer chunks (tcgen05): the sequences of at least min_rows rows. part, count:
+// as above, kv_prefill_part_floats floats and 8 kv_prefill_grid ints.
+int kv_prefill_grid(int num_sms);
+size_t kv_prefill_part_floats(int D, int num_sms);
+cudaError_t launch_kv_prefill(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int min_rows,
+                              float *part, int *count, int num_sms, cudaStream_t stream);
+
 }  // namespace lora

@@ -18,8 +18,8 @@ struct lora_kv {
     cudaEvent_t ev_call = nullptr;             // the last call enqueued
     // the attention's scratch, used by one call at a time: a call on another stream than the
     // last one's waits for it (ev_attn)
-    float *part = nullptr;
-    int *count = nullptr;
+    float *dec_part = nullptr, *pre_part = nullptr;  // pre_part: from the first call or reserve
+    int *count = nullptr;                            // the short-chunk kernel's, then the other's
     cudaEvent_t ev_attn = nullptr;
     cudaStream_t attn_stream = nullptr;
     bool attn_any = false;
