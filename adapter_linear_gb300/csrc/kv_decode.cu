@@ -66,17 +66,6 @@ __device__ __forceinline__ uint32_t swz(int r, int c)
 // V's chunk (of the 8 of a 128-byte row) that the lanes of group g read
 __device__ __forceinline__ int v_chunk(int g) { return ((g & 1) << 2) + (g >> 1); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // D += A B, 16 x 8 x 16, fp32 sums; bf16 operands (mma16816) or f16 ones (mma16816_f16)
 __device__ __forceinline__ void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1)

@@ -226,6 +226,18 @@ private:
     }
 };
 
+// 16-byte asynchronous copy to shared memory; of the 16 bytes `bytes` are read, the rest are zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^x, to about 2^-22 of it; 0 for -inf

@@ -8,16 +8,24 @@
 //
 // A CTA works on 256 rows of one kv head: the G query heads that share it for 256 / G tokens, so
 // K and V are read once for all of them, as two MMA tiles of 128 rows. Warps 0-3 and 4-7 do the
-// softmax of one tile each (a thread holds a row), 8-11 bring K and V tiles into shared memory
-// (8-bit codes become bf16 on the way), warp 12 issues the MMAs:
+// softmax of one tile each (a thread holds a row), 8-15 bring K and V tiles into shared memory
+// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
 // in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): while one tile's softmax runs, the tensor cores
 // do the other tile's products. MMAs of one thread execute in order, so S_t(j+1) overwrites
 // P_t(j) only after PV_t(j) has read it, and the commit behind S_t(j+1) covers PV_t(j).
 //
-// The scales of an 8-bit cache stay outside the products: the codes are exact in bf16, a
-// key's scale multiplies its column of S, a value's its weight.
+// An 8-bit cache: the codes are exact in f16 (S) and in bf16 (O), a key's scale multiplies its
+// column of S and a value's its weight. S takes f16, because codes become f16 in two thirds of the
+// instructions bf16 takes, with Q's rows scaled by powers of two; the weights stay in bf16,
+// whose range a row's smallest weights need.
+//
+// A weight rounded to bf16 is off by up to 2^-9 of it or 2^-8 (the mantissa's place), which
+// averages out over many keys but shows where one key holds much of a row's weight. So where a
+// key may hold more than a quarter of what its row has so far, the tile's weights go to the product
+// in two bf16 parts, the second with the rest (a second product for that tile: a piece's
+// first tile, then rarely).
 //
 // Work is shared out like the short-chunk kernel's: the grid's CTAs (one an SM) take equal
 // contiguous runs of 128-token units over all items, pieces of an item go to scratch as
@@ -28,14 +36,12 @@ namespace lora {
 namespace {
 
 constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128;
-constexpr int kSoftWarps = 8, kLoadWarps = 4;
+constexpr int kSoftWarps = 8, kLoadWarps = 8;
 constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // the MMA warp's group has three idle warps
 // registers a thread of the softmax warps, the loading warps and the MMA warp's group: a block of
-// 512 threads starts with 128 each, and 2 x 168 + 104 + 72 is 4 x 128
-constexpr int kSoftRegs = 168, kLoadRegs = 104, kMmaRegs = 72;
-static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "register split");
-// rows that see fewer keys than this get weights in two bf16 parts (see below)
-constexpr int kFewKeys = 128;
+// 640 threads starts with 96 each, and 2 x 144 + 2 x 72 + 48 is 5 x 96
+constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
+static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "register split");
 
 template <int D>
 struct Cfg {
@@ -48,7 +54,8 @@ struct Cfg {
     static constexpr int kK = 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
     static constexpr int kScales = kV + kStages * kTileBytes;  // float [2][kRing][128]
-    static constexpr int kBars = kScales + 2 * kRing * 128 * 4;
+    static constexpr int kRowMul = kScales + 2 * kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
+    static constexpr int kBars = kRowMul + 2 * kBlockRows * 4;
     static constexpr int kSmem = kBars + 512 + 1024;           // and room to align to 1024
     static constexpr uint32_t kO = 256;                        // tensor memory column of O_0
 };
@@ -112,6 +119,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tmem_zero8(uint32_t taddr)
+{
+    const uint32_t z = 0;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %1, %1, %1, %1, %1, %1, %1};" ::"r"(taddr), "r"(z)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Two fp32 operations in one instruction.
@@ -131,6 +144,12 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -148,6 +167,12 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
 // A wait of a whole warp: every lane waits (and so sees what the barrier released), and all
 // agree on whether it ran out.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
@@ -155,59 +180,158 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, abort_flag, err));
 }
 
-// The scores of N keys of this thread's row: z in units of log2, -inf where the row does not see
-// the key (columns above lim or up to low).
-template <bool kInt8, int N>
-__device__ __forceinline__ void chunk_z(const uint32_t *s, const float *sc, float c, bool mask, int lim, int low,
-                                        int col0, float (&z)[N])
+// The raw scores of 32 keys of this thread's row (tensor memory columns t..t + 31) times the keys'
+// scales, in pairs; kMask: -inf where the row does not see the key (columns above lim or up to
+// low).
+template <bool kInt8, bool kMask>
+__device__ __forceinline__ void chunk_scores(uint32_t t, const float *sc, int lim, int low, int col0, uint64_t (&z)[16])
 {
+    uint32_t s[32];
+    tmem_ld32_wait(t, s);
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        uint64_t c01, c23;
-        if (kInt8) {
-            const float4 f = *reinterpret_cast<const float4 *>(sc + col0 + i);
-            c01 = pack2(f.x, f.y);
-            c23 = pack2(f.z, f.w);
-        } else {
-            c01 = c23 = pack2(c, c);
+    for (int i = 0; i < 16; ++i) z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    if (kInt8) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + col0 + 2 * i);
+            z[i] = mul2(z[i], f.x);
+            z[i + 1] = mul2(z[i + 1], f.y);
         }
-        unpack2(mul2(pack2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c01), &z[i], &z[i + 1]);
-        unpack2(mul2(pack2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c23), &z[i + 2], &z[i + 3]);
     }
-    if (mask) {
+    if (kMask) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = col0 + i <= lim && col0 + i > low ? z[i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack2(z[i], &a, &b);
+            const int c = col0 + 2 * i;
+            z[i] = pack2(c <= lim && c > low ? a : -INFINITY, c + 1 <= lim && c + 1 > low ? b : -INFINITY);
+        }
     }
 }
 
-// z becomes the weights 2^(z - m) times the values' scales (0 for a key the row does not see,
-// whatever its scale is); returns the weights' sum.
-template <bool kInt8, int N>
-__device__ __forceinline__ float chunk_w(float (&z)[N], float m, const float *vsc, bool mask, int col0)
+// The largest score of the row's 128 keys in units of log2 (mul: raw score to those; where it is
+// negative, the smallest raw score counts).
+template <bool kInt8, bool kMask>
+__device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim, int low, float mul)
 {
-    const uint64_t neg = pack2(-m, -m);
-    uint64_t sum = 0;
+    const uint64_t sign = mul < 0.0f ? pack2(-1.0f, -1.0f) : pack2(1.0f, 1.0f);
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        uint64_t z[16];
+        chunk_scores<kInt8, false>(tS + ch * 32, ksc, lim, low, ch * 32, z);
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        unpack2(add2(pack2(z[i], z[i + 1]), neg), &z[i], &z[i + 1]);
-        z[i] = fast_exp2(z[i]);
-        z[i + 1] = fast_exp2(z[i + 1]);
-        sum = add2(sum, pack2(z[i], z[i + 1]));
+        for (int i = 0; i < 16; ++i) {
+            float a, b;
+            unpack2(mul2(z[i], sign), &a, &b);
+            if (kMask) {
+                const int c = ch * 32 + 2 * i;
+                a = c <= lim && c > low ? a : -INFINITY;
+                b = c + 1 <= lim && c + 1 > low ? b : -INFINITY;
+            }
+            x[i & 3] = fmaxf(x[i & 3], fmaxf(a, b));
+        }
+        top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
     }
-    if (kInt8) {
+    return top == -INFINITY ? top : top * fabsf(mul);
+}
+
+// The row's 128 weights 2^(score - m), times the values' scales (0 for a key the row does not
+// see, whatever its scale is), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e (whose
+// scores are read by then); kRest: what rounding left of them in column 16 i + 8 + e, else
+// zeros there. Returns the weights' sum.
+template <bool kInt8, bool kMask, bool kRest>
+__device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, const float *vsc, int lim, int low,
+                                              float mul, float m)
+{
+    const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        uint64_t z[16];
+        chunk_scores<kInt8, kMask>(tS + ch * 32, ksc, lim, low, ch * 32, z);
+        uint32_t p[16], rest[16];
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 f = *reinterpret_cast<const float4 *>(vsc + col0 + i);
-            float v[4];
-            unpack2(mul2(pack2(z[i], z[i + 1]), pack2(f.x, f.y)), &v[0], &v[1]);
-            unpack2(mul2(pack2(z[i + 2], z[i + 3]), pack2(f.z, f.w)), &v[2], &v[3]);
+        for (int i = 0; i < 16; i += 2) {
+            ulonglong2 f;
+            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 32 + 2 * i);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[i + e] = mask && z[i + e] == 0.0f ? 0.0f : v[e];
+            for (int e = 0; e < 2; ++e) {
+                float a, b, wa, wb;
+                unpack2(fma2(z[i + e], mul_2, neg), &a, &b);
+                a = fast_exp2(a);
+                b = fast_exp2(b);
+                if (kMask) {
+                    float za, zb;
+                    unpack2(z[i + e], &za, &zb);
+                    a = za == -INFINITY ? 0.0f : a;
+                    b = zb == -INFINITY ? 0.0f : b;
+                }
+                const uint64_t v = pack2(a, b);
+                sum[e] = add2(sum[e], v);
+                wa = a;
+                wb = b;
+                if (kInt8) {
+                    unpack2(mul2(v, e ? f.y : f.x), &wa, &wb);
+                    if (kMask) {
+                        wa = a == 0.0f ? 0.0f : wa;
+                        wb = b == 0.0f ? 0.0f : wb;
+                    }
+                }
+                p[i + e] = pack_bf16x2(wa, wb);
+                if (kRest) rest[i + e] = pack_bf16x2(wa - bf16_lo(p[i + e]), wb - bf16_hi(p[i + e]));
+            }
+        }
+        tmem_st8(tS + ch * 32, p);
+        tmem_st8(tS + ch * 32 + 16, p + 8);
+        if (kRest) {
+            tmem_st8(tS + ch * 32 + 8, rest);
+            tmem_st8(tS + ch * 32 + 24, rest + 8);
+        } else {
+            tmem_zero8(tS + ch * 32 + 8);
+            tmem_zero8(tS + ch * 32 + 24);
         }
     }
     float a, b;
-    unpack2(sum, &a, &b);
+    unpack2(add2(sum[0], sum[1]), &a, &b);
     return a + b;
+}
+
+// Which piece of a 16-token group of an 8-bit cache lane `lane` holds: 16-byte piece `c` of rows
+// `r`, r + 32 / (D / 16), ... (so that a warp reads 512 bytes at a time, and the eight lanes of
+// a phase store to eight different chunk columns).
+template <int D>
+__device__ __forceinline__ void lane_piece(int lane, int *r, int *c)
+{
+    if (D == 128) {
+        *c = (lane & 3) | ((lane >> 1) & 4);
+        *r = ((lane >> 2) & 1) | ((lane >> 3) & 2);
+    } else {
+        *c = lane & 3;
+        *r = lane >> 2;
+    }
+}
+
+// A lane's pieces of a 16-token group as f16 or bf16 into its tile (dst: the group's first row).
+template <int D, bool kF16>
+__device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 32], int r0, int piece, uint32_t base)
+{
+#pragma unroll
+    for (int p = 0; p < D / 32; ++p) {
+        const uint32_t c[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+        uint32_t x[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (kF16)
+                codes4_to_f16(c[e], &x[2 * e], &x[2 * e + 1]);
+            else
+                codes4_to_bf16(c[e], base, &x[2 * e], &x[2 * e + 1]);
+        }
+        const int r = r0 + p * (512 / D);
+        *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * piece)) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * piece + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
 }
 
 template <int D, bool kInt8>
@@ -219,7 +343,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kBars);
     float *const kscale = reinterpret_cast<float *>(smem + C::kScales);
     float *const vscale = kscale + C::kRing * 128;
+    float *const row_mul = reinterpret_cast<float *>(smem + C::kRowMul);
     __shared__ uint32_t tmem_slot;
+    __shared__ uint32_t rest_flags[2];  // of the tiles' weights: a byte a warp, has it a second part?
     __shared__ int abort_flag;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -229,19 +355,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.q_full[i], kLoadWarps * 32);
+            mbar_init(&bars.q_full[i], kLoadWarps);
             mbar_init(&bars.q_empty[i], 1);
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], kTileRows);
             mbar_init(&bars.o_full[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars.k_full[i], kLoadWarps * 32);
+            mbar_init(&bars.k_full[i], kLoadWarps);
             mbar_init(&bars.k_empty[i], 1);
-            mbar_init(&bars.v_full[i], kLoadWarps * 32);
+            mbar_init(&bars.v_full[i], kLoadWarps);
             mbar_init(&bars.v_empty[i], 1);
         }
-        for (int i = 0; i < C::kRing; ++i) mbar_init(&bars.sc_full[i], kLoadWarps * 32);
+        for (int i = 0; i < C::kRing; ++i) mbar_init(&bars.sc_full[i], kLoadWarps);
         mbar_init(&bars.drain, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -262,9 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         const int row_in_tile = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
         const uint32_t tS = lanes + t * 128, tO = lanes + C::kO + t * D;
-        int it = 0, ns = 0, nw = 0;  // key tiles of all work, of this tile's, and its work
+        int it = 0, work = -1;  // key tiles and work of the CTA,
+        int ns = 0, nw = 0;     // and of this tile
         bool ok = true;
         while (ok && w.next()) {
+            ++work;
             const int j0 = (int)(w.u - w.item0), j1 = (int)(w.seg_end - w.item0);
             const int row_t = w.tile * kBlockRows + t * kTileRows;  // the tile's first row
             const int64_t rows = (int64_t)w.sh.n * G;
@@ -276,108 +404,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const bool on = row < rows;
             const int i = on ? row / G : w.sh.n - 1;
             const int pos = w.sh.L - w.sh.n + i;
-            // Rows that see few keys: a weight rounded to bf16 is off by up to 2^-8, which shows
-            // where few of them add up. Their weights go to the product as a rounded part and
-            // the rest.
-            const int first_pos = w.sh.L - w.sh.n + row_t / G;
-            const bool few = first_pos + 1 < kFewKeys || (a.window > 0 && a.window < kFewKeys);
             float m = -INFINITY, l = 0.0f;
+            float mul = plan.scale_log2;  // raw score -> units of log2
             for (int j = j0; j < j1; ++j, ++it, ++ns) {
                 const int tok0 = w.lo + j * kKeys;
                 const int lim = pos - tok0;
                 const int low = a.window > 0 ? pos - a.window - tok0 : -1;
                 const bool mask = __any_sync(0xffffffffu, lim < kKeys - 1 || low >= 0);
-                const float *ksc = kscale + (it % C::kRing) * 128, *vsc = vscale + (it % C::kRing) * 128;
-                if (kInt8)
-                    ok = warp_wait(&bars.sc_full[it % C::kRing], (uint32_t)(it / C::kRing) & 1u, &abort_flag,
-                                   kv.err);
+                const int ring = it % C::kRing;
+                const float *ksc = kscale + ring * 128, *vsc = vscale + ring * 128;
+                if (kInt8) {
+                    ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
+                    if (j == j0) mul = row_mul[(work & 1) * kBlockRows + t * kTileRows + row_in_tile];
+                }
                 ok = ok && warp_wait(&bars.s_full[t], (uint32_t)ns & 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 tc_fence_after_sync();
-                uint32_t p[64];
-                // the scores of the tile against m; where one passes it by 2^8 (always in a
-                // piece's first tile): m moves, O and l follow, and once more
-                bool again = j == j0 || few;
-                float top = -INFINITY;
-                if (again) {
+
+                const float top = mask ? tile_top<kInt8, true>(tS, ksc, lim, low, mul)
+                                       : tile_top<kInt8, false>(tS, ksc, lim, low, mul);
+                if (__any_sync(0xffffffffu, top > m + 8.0f)) {
+                    const float m2 = fmaxf(m, top);
+                    const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
+                    m = m2;
+                    l *= down;
+                    if (j > j0) {
 #pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t s[32];
-                        float z[32];
-                        tmem_ld32_wait(tS + ch * 32, s);
-                        chunk_z<kInt8, 32>(s, ksc, plan.scale_log2, mask, lim, low, ch * 32, z);
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32_wait(tO + x, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, z[e]);
-                    }
-                }
-                float add = 0.0f;
-#pragma unroll 1
-                for (;;) {
-                    if (again) {
-                        const float m2 = fmaxf(m, top);
-                        const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
-                        if (j > j0 && __any_sync(0xffffffffu, m2 > m)) {
-                            l *= down;
-#pragma unroll 1
-                            for (int x = 0; x < D; x += 32) {
-                                uint32_t o[32];
-                                tmem_ld32_wait(tO + x, o);
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                                tmem_st16(tO + x, o);
-                                tmem_st16(tO + x + 16, o + 16);
-                            }
-                            tmem_st_wait();
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                            tmem_st16(tO + x, o);
+                            tmem_st16(tO + x + 16, o + 16);
                         }
-                        m = m2;
-                    }
-                    if (few) break;
-                    const float mx = m == -INFINITY ? 0.0f : m;
-                    add = 0.0f;
-                    top = -INFINITY;
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t s[32];
-                        float z[32];
-                        tmem_ld32_wait(tS + ch * 32, s);
-                        chunk_z<kInt8, 32>(s, ksc, plan.scale_log2, mask, lim, low, ch * 32, z);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) top = fmaxf(top, z[e]);
-                        add += chunk_w<kInt8, 32>(z, mx, vsc, mask, ch * 32);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) p[ch * 16 + e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
-                    }
-                    again = __any_sync(0xffffffffu, top > m + 8.0f);
-                    if (!again) break;
-                }
-                if (!few) {
-#pragma unroll
-                    for (int x = 0; x < 64; x += 16) tmem_st16(tS + x, p + x);
-                } else {
-                    // the rounded parts to columns 0..63, the rests to 64..127: the scores
-                    // these overwrite are read first
-                    const float mx = m == -INFINITY ? 0.0f : m;
-                    uint32_t s[64];
-                    tmem_ld32_wait(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(s));
-                    tmem_ld32_wait(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-#pragma unroll
-                    for (int ch = 0; ch < 8; ++ch) {
-                        uint32_t x[16], hi[8], rest[8];
-                        float z[16];
-                        if (ch < 4) tmem_ld16_wait(tS + ch * 16, x);
-                        chunk_z<kInt8, 16>(ch < 4 ? x : s + (ch & 3) * 16, ksc, plan.scale_log2, mask, lim, low, ch * 16,
-                                           z);
-                        add += chunk_w<kInt8, 16>(z, mx, vsc, mask, ch * 16);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            hi[e] = pack_bf16x2(z[2 * e], z[2 * e + 1]);
-                            rest[e] = pack_bf16x2(z[2 * e] - bf16_lo(hi[e]), z[2 * e + 1] - bf16_hi(hi[e]));
-                        }
-                        tmem_st8(tS + ch * 8, hi);
-                        tmem_st8(tS + 64 + ch * 8, rest);
                     }
                 }
-                l += add;
+                const float mx = m == -INFINITY ? 0.0f : m;
+                const bool rest = __any_sync(0xffffffffu, 3.0f * fast_exp2(top - mx) > l);
+                if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t])[warp & 3] = rest;
+                if (rest)
+                    l += mask ? tile_weights<kInt8, true, true>(tS, ksc, vsc, lim, low, mul, mx)
+                              : tile_weights<kInt8, false, true>(tS, ksc, vsc, lim, low, mul, mx);
+                else
+                    l += mask ? tile_weights<kInt8, true, false>(tS, ksc, vsc, lim, low, mul, mx)
+                              : tile_weights<kInt8, false, false>(tS, ksc, vsc, lim, low, mul, mx);
                 tmem_st_wait();
                 tc_fence_before_sync();
                 mbar_arrive(&bars.p_full[t]);
@@ -479,226 +550,226 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ------------------------------------------------- Q, K and V into shared memory
         regs_down<kLoadRegs>();
+        // warp lw brings tokens 16 lw .. 16 lw + 15 of every key tile: one page lookup
         const int lw = warp - kSoftWarps;
         const int tid = threadIdx.x - kSoftWarps * 32;
         const uint32_t base = kv_opaque(0x43004300u);
-        int it = 0, nw[2] = {0, 0};
+        int it = 0, work = 0;
+        uint32_t nq[2] = {0, 0};
         bool ok = true;
-        // 8-bit: a thread holds 16 codes of a row (two chunks of bf16); bf16: one chunk
-        constexpr int kRowLanes = kInt8 ? D / 16 : D / 8;
-        constexpr int kPassRows = kLoadWarps * 32 / kRowLanes, kPasses = kKeys / kPassRows;
-        int cl, rl;  // lane -> 16-byte piece of a row, row of the warp's: a phase of eight lanes
-                     // stores to eight different chunk columns
-        if (kInt8 && D == 128) {
-            cl = (lane & 3) | ((lane >> 1) & 4);
-            rl = ((lane >> 2) & 1) | ((lane >> 3) & 2);
-        } else {
-            cl = lane % kRowLanes;
-            rl = lane / kRowLanes;
-        }
-        const int r0 = lw * (32 / kRowLanes) + rl;  // the thread's rows: r0 + kPassRows * pass
+        int pr, pc;
+        lane_piece<D>(lane, &pr, &pc);
+        auto arrive = [&](uint64_t &bar) {  // the warp's part is in shared memory
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar);
+        };
 
         while (ok && w.next()) {
             const int j0 = (int)(w.u - w.item0), j1 = (int)(w.seg_end - w.item0);
-            const int64_t rows = (int64_t)w.sh.n * G;
+            const int rows = (int)((int64_t)w.sh.n * G);
             const int32_t *table = b.table + (int64_t)w.seq * b.table_stride;
-
-            // lane i < 8: cache row of token 16 i of key tile j (head's), or -1
-            auto group_rows = [&](int j) -> int64_t {
-                const int tok = w.lo + j * kKeys + lane * 16;
-                if (lane >= 8 || tok >= w.hi) return -1;
-                const int page = table[tok >> kv.page_shift];
+            // cache row of the warp's first token of key tile j, and how many of the 16 there are
+            auto group = [&](int j, int *count) -> int64_t {
+                const int tok = w.lo + j * kKeys + lw * 16;
+                *count = j < j1 ? min(16, max(0, w.hi - tok)) : 0;
+                if (*count == 0) return 0;
+                int page = table[tok >> kv.page_shift];
                 if (page < 0 || page >= kv.num_pages) {
                     kv_flag_range(kv.err);
-                    return -1;
+                    *count = 0;
+                    page = 0;
                 }
                 return (((int64_t)page * kv.H + w.head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
             };
-            // cache row of row r of the tile, or -1 past the end
-            auto cache_row = [&](int64_t groups, int j, int r) -> int64_t {
-                const int64_t g0 = __shfl_sync(0xffffffffu, groups, r >> 4);
-                return g0 < 0 || w.lo + j * kKeys + r >= w.hi ? -1 : g0 + (r & 15);
+            // the lane's pieces of a group of codes (zeros past its end)
+            auto fetch = [&](const void *arena, int64_t row, int count, uint4 (&v)[D / 32]) {
+                const uint8_t *src = static_cast<const uint8_t *>(arena) + (row + pr) * D + pc * 16;
+#pragma unroll
+                for (int p = 0; p < D / 32; ++p) {
+                    v[p] = make_uint4(0, 0, 0, 0);
+                    if (pr + p * (512 / D) < count) v[p] = *reinterpret_cast<const uint4 *>(src + p * 512);
+                }
             };
-            int64_t groups = group_rows(j0);
+            // bf16: straight into shared memory (rows past the end hold anything: zeros)
+            auto copy = [&](const void *arena, uint8_t *dst, int64_t row, int count) {
+                constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+                const uint8_t *src = static_cast<const uint8_t *>(arena) + row * (2 * D) + lane * 16;
+#pragma unroll
+                for (int p = 0; p < 16 / kStep; ++p) {
+                    const int r = p * kStep + lane / kLanes;
+                    cp_async16(smem_u32(dst + tile_off(r, lane % kLanes)), src + p * 512, r < count ? 16u : 0u);
+                }
+                cp_commit();
+            };
+            int count, ahead_count;
+            int64_t row = group(j0, &count), ahead;
+            uint4 vk[kInt8 ? D / 32 : 1], vv[kInt8 ? D / 32 : 1];
+            if constexpr (kInt8) fetch(kv.k, row, count, vk);
 
-            // Q: the tiles' rows, 8 (D 64: 16) at a time
+            // Q: the tiles' rows, 16 (D 64: 32) at a time
+            constexpr int kLanesQ = D / 8, kRowsQ = kLoadWarps * 32 / kLanesQ;
             for (int t = 0; t < 2 && ok; ++t) {
                 const int row_t = w.tile * kBlockRows + t * kTileRows;
                 if (row_t >= rows) break;
-                ok = warp_wait(&bars.q_empty[t], ((uint32_t)nw[t] & 1u) ^ 1u, &abort_flag, kv.err);
+                ok = warp_wait(&bars.q_empty[t], (nq[t]++ & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
-                ++nw[t];
-                constexpr int kLanesQ = D / 8, kRowsQ = 128 / kLanesQ;
-#pragma unroll 8
+#pragma unroll 4
                 for (int x = 0; x < kTileRows / kRowsQ; ++x) {
                     const int r = x * kRowsQ + tid / kLanesQ, ch = tid % kLanesQ;
-                    const int row = row_t + r;
+                    const int q = row_t + r;
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < rows)
-                        v = ldg_nc_v4(a.Q + (int64_t)(w.sh.row0 + row / G) * a.q_stride +
-                                      (int64_t)(w.head * G + row % G) * D + ch * 8);
+                    if (q < rows)
+                        v = ldg_nc_v4(a.Q + (int64_t)(w.sh.row0 + q / G) * a.q_stride +
+                                      (int64_t)(w.head * G + q % G) * D + ch * 8);
+                    if (kInt8) {
+                        // to f16, the row scaled by the power of two that puts its largest magnitude
+                        // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
+                        uint32_t u[4] = {v.x, v.y, v.z, v.w}, top = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int d = kLanesQ / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const int up = min(14 + 127 - (int)(top >> 7), 126);
+                        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
+                        v = make_uint4(u[0], u[1], u[2], u[3]);
+                        if (ch == 0)
+                            row_mul[(work & 1) * kBlockRows + t * kTileRows + r] =
+                                __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
+                    }
                     *reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, ch)) = v;
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.q_full[t]);
+                arrive(bars.q_full[t]);
             }
             if (!ok) break;
+            ++work;
 
-            // one operand's tile: `rows_of` its cache rows
-            auto load_store = [&](const void *arena, uint8_t *dst, int64_t grp, int j) {
-#pragma unroll
-                for (int p0 = 0; p0 < kPasses; p0 += 8) {
-                    uint4 v[8 < kPasses ? 8 : kPasses];
-#pragma unroll
-                    for (int p = 0; p < 8 && p < kPasses; ++p) {
-                        const int64_t row = cache_row(grp, j, r0 + (p0 + p) * kPassRows);
-                        v[p] = make_uint4(0, 0, 0, 0);
-                        if (row >= 0)
-                            v[p] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(arena) +
-                                                                    row * (D * (kInt8 ? 1 : 2)) + cl * 16);
-                    }
-                    if (p0 == 0) {
-                        // the stage, once the MMAs that read it are done (the caller's barrier)
-                        ok = ok && warp_wait(dst < smem + C::kV ? &bars.k_empty[it % C::kStages]
-                                                                : &bars.v_empty[it % C::kStages],
-                                             ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
-                        if (!ok) return;
-                    }
-#pragma unroll
-                    for (int p = 0; p < 8 && p < kPasses; ++p) {
-                        const int r = r0 + (p0 + p) * kPassRows;
-                        if (kInt8) {
-                            uint4 x, y;
-                            codes4_to_bf16(v[p].x, base, &x.x, &x.y);
-                            codes4_to_bf16(v[p].y, base, &x.z, &x.w);
-                            codes4_to_bf16(v[p].z, base, &y.x, &y.y);
-                            codes4_to_bf16(v[p].w, base, &y.z, &y.w);
-                            *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * cl)) = x;
-                            *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * cl + 1)) = y;
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst + tile_off(r, cl)) = v[p];
-                        }
-                    }
-                }
-            };
-
-            for (int j = j0; j < j1 && ok; ++j, ++it) {
+            for (int j = j0; j < j1; ++j, ++it) {
                 const int s = it % C::kStages;
-                const int64_t ahead = j + 1 < j1 ? group_rows(j + 1) : -1;
-                if (kInt8) {
-                    const int64_t row = cache_row(groups, j, tid);
-                    float ks = 0.0f, vs = 0.0f;
-                    if (row >= 0) {
-                        ks = __uint_as_float((uint32_t)kv.ks[row] << 16) * plan.scale_log2;
-                        vs = __uint_as_float((uint32_t)kv.vs[row] << 16);
-                    }
-                    ok = warp_wait(&bars.k_empty[s], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
+                const uint32_t ph = ((uint32_t)(it / C::kStages) & 1u) ^ 1u;
+                uint8_t *const dk = smem + C::kK + s * C::kTileBytes + lw * 2048;
+                uint8_t *const dv = smem + C::kV + s * C::kTileBytes + lw * 2048;
+                if constexpr (kInt8) {
+                    // lanes 0-15 the keys' scales, 16-31 the values'
+                    const int ring = it % C::kRing;
+                    float sc = 0.0f;
+                    if ((lane & 15) < count)
+                        sc = __uint_as_float((uint32_t)(lane < 16 ? kv.ks : kv.vs)[row + (lane & 15)] << 16);
+                    fetch(kv.v, row, count, vv);
+                    ahead = group(j + 1, &ahead_count);
+                    ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
                     if (!ok) break;
-                    kscale[(it % C::kRing) * 128 + tid] = ks;
-                    vscale[(it % C::kRing) * 128 + tid] = vs;
-                    mbar_arrive(&bars.sc_full[it % C::kRing]);
+                    store_codes<D, true>(dk, vk, pr, pc, base);
+                    arrive(bars.k_full[s]);
+                    (lane < 16 ? kscale : vscale)[ring * 128 + lw * 16 + (lane & 15)] = sc;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
+                    fetch(kv.k, ahead, ahead_count, vk);
+                    ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
+                    if (!ok) break;
+                    store_codes<D, false>(dv, vv, pr, pc, base);
+                    arrive(bars.v_full[s]);
+                } else {
+                    ahead = group(j + 1, &ahead_count);
+                    ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
+                    if (!ok) break;
+                    copy(kv.k, dk, row, count);
+                    if (j > j0) {  // the copies of the last V have landed
+                        cp_wait<1>();
+                        arrive(bars.v_full[(it - 1) % C::kStages]);
+                    }
+                    ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
+                    if (!ok) break;
+                    copy(kv.v, dv, row, count);
+                    cp_wait<1>();
+                    arrive(bars.k_full[s]);
                 }
-                load_store(kv.k, smem + C::kK + s * C::kTileBytes, groups, j);
-                if (!ok) break;
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.k_full[s]);
-                load_store(kv.v, smem + C::kV + s * C::kTileBytes, groups, j);
-                if (!ok) break;
-                fence_proxy_async_smem();
-                mbar_arrive(&bars.v_full[s]);
-                groups = ahead;
+                row = ahead;
+                count = ahead_count;
+            }
+            if constexpr (!kInt8) {
+                cp_wait<0>();
+                if (ok) arrive(bars.v_full[(it - 1) % C::kStages]);
             }
         }
     } else {
         // -------------------------------------------------------------------- MMAs
         regs_down<kMmaRegs>();
         if (warp == kSoftWarps + kLoadWarps) {
-        const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys);
-        const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
-        const uint32_t sq = smem_u32(smem + C::kQ), sk = smem_u32(smem + C::kK), sv = smem_u32(smem + C::kV);
-        int it = 0, np[2] = {0, 0}, nw[2] = {0, 0};
-        bool ok = true;
-        while (ok && w.next()) {
-            const int n = (int)(w.seg_end - w.u);
-            const int64_t rows = (int64_t)w.sh.n * G;
-            const int nt = w.tile * (int64_t)kBlockRows + kTileRows < rows ? 2 : 1;
-            bool few[2];
-            for (int t = 0; t < 2; ++t) {
-                const int first_pos = w.sh.L - w.sh.n + (w.tile * kBlockRows + t * kTileRows) / G;
-                few[t] = first_pos + 1 < kFewKeys || (a.window > 0 && a.window < kFewKeys);
-            }
-            // S_t = Q_t K^T of key tile `at`
-            auto scores = [&](int t, int at) {
-                if (lane == 0) {
-                    const int s = at % C::kStages;
+                // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
+            const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys) - (kInt8 ? (1u << 7) | (1u << 10) : 0u);
+            const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
+            // one thread issues everything
+            if (lane == 0) {
+                const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ)), dk = sdesc_k_sw128(smem_u32(smem + C::kK));
+                const uint64_t dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
+                constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
+                int it = 0, np[2] = {0, 0}, nw[2] = {0, 0};
+                bool ok = true;
+                auto wait = [&](uint64_t &bar, uint32_t parity) {
+                    ok = ok && mbar_wait_inl(&bar, parity & 1u, &abort_flag, kv.err);
+                };
+                // S_t = Q_t K^T of the key tile in stage s
+                auto scores = [&](int t, int s) {
+                    const uint64_t q = dq + t * kTile16, k = dk + s * kTile16;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_bf16_ss(tmem + t * 128,
-                                    sdesc_k_sw128(sq + t * C::kTileBytes + (k >> 2) * 16384 + (k & 3) * 32),
-                                    sdesc_k_sw128(sk + s * C::kTileBytes + (k >> 2) * 16384 + (k & 3) * 32), id_s, k > 0);
-                    mma_commit(&bars.s_full[t]);
-                }
-                __syncwarp();
-            };
-            ok = warp_wait(&bars.k_full[it % C::kStages], (uint32_t)(it / C::kStages) & 1u, &abort_flag, kv.err);
-            for (int t = 0; t < nt && ok; ++t) {
-                ok = warp_wait(&bars.q_full[t], (uint32_t)nw[t] & 1u, &abort_flag, kv.err);
-                if (!ok) break;
-                tc_fence_after_sync();
-                scores(t, it);
-                if (n == 1 && lane == 0) mma_commit(&bars.q_empty[t]);
-            }
-            if (!ok) break;
-            if (lane == 0) mma_commit(&bars.k_empty[it % C::kStages]);
-            for (int j = 0; j < n && ok; ++j, ++it) {
-                const int s = it % C::kStages;
-                for (int t = 0; t < nt && ok; ++t) {
-                    if (t == 0)
-                        ok = warp_wait(&bars.v_full[s], (uint32_t)(it / C::kStages) & 1u, &abort_flag, kv.err);
-                    ok = ok && warp_wait(&bars.p_full[t], (uint32_t)np[t] & 1u, &abort_flag, kv.err);
-                    if (!ok) break;
-                    ++np[t];
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_bf16_ts(tmem + C::kO + t * D, tmem + t * 128 + k * 8,
-                                        sdesc_mn_sw128(sv + s * C::kTileBytes + k * 2048), id_o, (j | k) != 0);
-                        if (few[t]) {
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                mma_bf16_ts(tmem + C::kO + t * D, tmem + t * 128 + 64 + k * 8,
-                                            sdesc_mn_sw128(sv + s * C::kTileBytes + k * 2048), id_o, 1);
-                        }
-                        if (t == nt - 1) mma_commit(&bars.v_empty[s]);
-                        if (j == n - 1) mma_commit(&bars.o_full[t]);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
+                        mma_bf16_ss(tmem + t * 128, q + off, k + off, id_s, i > 0);
                     }
-                    __syncwarp();
-                    if (j + 1 < n) {
-                        const int s1 = (it + 1) % C::kStages;
-                        if (t == 0) {
-                            ok = warp_wait(&bars.k_full[s1], (uint32_t)((it + 1) / C::kStages) & 1u, &abort_flag, kv.err);
+                    mma_commit(&bars.s_full[t]);
+                };
+                while (ok && w.next()) {
+                    const int n = (int)(w.seg_end - w.u);
+                    const int64_t rows = (int64_t)w.sh.n * G;
+                    const int nt = w.tile * (int64_t)kBlockRows + kTileRows < rows ? 2 : 1;
+                    wait(bars.k_full[it % C::kStages], it / C::kStages);
+                    for (int t = 0; t < nt; ++t) {
+                        wait(bars.q_full[t], nw[t]++);
+                        if (!ok) break;
+                        scores(t, it % C::kStages);
+                        if (n == 1) mma_commit(&bars.q_empty[t]);
+                    }
+                    if (!ok) break;
+                    mma_commit(&bars.k_empty[it % C::kStages]);
+                    for (int j = 0; j < n && ok; ++j, ++it) {
+                        const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
+                        wait(bars.v_full[s], it / C::kStages);
+#pragma unroll 1
+                        for (int t = 0; t < nt && ok; ++t) {
+                            wait(bars.p_full[t], np[t]++);
                             if (!ok) break;
                             tc_fence_after_sync();
-                        }
-                        scores(t, it + 1);
-                        if (lane == 0) {
+                            const uint32_t rest = *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]);
+                            const uint64_t v = dv + s * kTile16;
+                            const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
+#pragma unroll
+                            for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
+                            if (rest) {
+#pragma unroll 1
+                                for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + 8 + i * 16, v + i * 128, id_o, 1);
+                            }
+                            if (t == nt - 1) mma_commit(&bars.v_empty[s]);
+                            if (j == n - 1) {
+                                mma_commit(&bars.o_full[t]);
+                                continue;
+                            }
+                            if (t == 0) wait(bars.k_full[s1], (it + 1) / C::kStages);
+                            if (!ok) break;
+                            scores(t, s1);
                             if (j + 2 == n) mma_commit(&bars.q_empty[t]);
                             if (t == nt - 1) mma_commit(&bars.k_empty[s1]);
                         }
-                        __syncwarp();
                     }
                 }
+                // no MMA may be in flight when the tensor memory goes
+                mma_commit(&bars.drain);
+                int unused = 0;
+                mbar_wait_inl(&bars.drain, 0, &unused, kv.err);
             }
-            for (int t = 0; t < nt; ++t) ++nw[t];
-        }
-        // no MMA may be in flight when the tensor memory goes
-        if (lane == 0) {
-            mma_commit(&bars.drain);
-            int unused = 0;
-            mbar_wait_inl(&bars.drain, 0, &unused, kv.err);
-        }
-        __syncwarp();
+            __syncwarp();
         }
     }
     tc_fence_before_sync();
