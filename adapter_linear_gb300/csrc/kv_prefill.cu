@@ -2,14 +2,14 @@
 // tensor cores.
 //
 // For a row (one query head of one new token) at position pos and its visible keys j:
-//   z_j = scale <Q, K_j>,  m >= max z_j - 8,  l = sum 2^(z_j - m),  O = sum 2^(z_j - m) V_j / l
+//   z_j = scale <Q, K_j>,  m near max z_j,  l = sum 2^(z_j - m),  O = sum 2^(z_j - m) V_j / l
 // (z in units of log2), over tiles of 128 keys in one pass. m is any number near the maximum: it
-// cancels in O / l, so it is only moved, and O rescaled, when a score passes it by 2^8.
+// cancels in O / l, so it is moved, and O rescaled, only when a score passes it by much.
 //
 // A CTA works on 256 rows of one kv head: the G query heads that share it for 256 / G tokens, so
 // K and V are read once for all of them, as two MMA tiles of 128 rows. Warps 0-3 and 4-7 do the
 // softmax of one tile each (a thread holds a row), 8-15 bring K and V tiles into shared memory
-// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs:
+// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs, warp 17 hands out the work:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
 // in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): while one tile's softmax runs, the tensor cores
@@ -30,6 +30,8 @@
 // Work is shared out like the short-chunk kernel's: the grid's CTAs (one an SM) take equal
 // contiguous runs of 128-token units over all items, pieces of an item go to scratch as
 // (m, l, O), and the warp that finishes a piece of 32 rows last joins them in CTA order.
+#include <cmath>
+
 #include "kv_device.cuh"
 
 namespace lora {
@@ -43,6 +45,8 @@ constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // the MMA warp's 
 constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "register split");
 
+constexpr int kSegments = 4;
+
 template <int D>
 struct Cfg {
     static constexpr int kTileBytes = 128 * D * 2;           // 128 rows of Q, K or V in bf16
@@ -55,20 +59,34 @@ struct Cfg {
     static constexpr int kV = kK + kStages * kTileBytes;
     static constexpr int kScales = kV + kStages * kTileBytes;  // float [2][kRing][128]
     static constexpr int kRowMul = kScales + 2 * kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
-    static constexpr int kBars = kRowMul + 2 * kBlockRows * 4;
+    static constexpr int kSegs = kRowMul + 2 * kBlockRows * 4;
+    static constexpr int kBars = kSegs + kSegments * 64;
     static constexpr int kSmem = kBars + 512 + 1024;           // and room to align to 1024
     static constexpr uint32_t kO = 256;                        // tensor memory column of O_0
 };
 
+// One segment of the CTA's share, as the warp that walks the share hands it to the others.
+struct Segment {
+    int seq, row0, n, L;    // the sequence (row0: its first row of the call's tensors)
+    int tile, head;         // block of 256 rows, kv head
+    int lo, hi;             // its visible tokens
+    int j0, j1;             // key tiles [j0, j1) of them; j1 == 0: no more segments
+    int whole, slot;        // all of the item? else the scratch slot of the piece
+    int c0, c1;             // and the CTAs that have pieces of the item
+    int pad[2];
+};
+static_assert(sizeof(Segment) == 64, "segment");
+
 struct Bars {
-    uint64_t q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], sc_full[6], s_full[2],
+    uint64_t seg_full[kSegments], seg_empty[kSegments], q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], sc_full[6], s_full[2],
         p_full[2], o_full[2], drain;
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
 struct Plan {
     int min_rows;
-    float scale_log2;
+    float scale_log2;   // |scale| log2(e)
+    uint32_t q_sign;    // 0x80008000 for a negative scale: flips the sign of a pair of Q's values
     float *part;   // [2 grid] slots of [256 / 32 warps][D / 4][32 rows][4], then [2 grid][256][2] (m, l)
     int *count;    // [grid][8] arrivals of a warp's rows at the item that starts in that CTA
 };
@@ -103,6 +121,24 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// 16 columns into registers; they are there after tmem_ld_wait on the same registers.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
@@ -180,19 +216,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, abort_flag, err));
 }
 
-// The raw scores of 32 keys of this thread's row (tensor memory columns t..t + 31) times the keys'
-// scales, in pairs; kMask: -inf where the row does not see the key (columns above lim or up to
-// low).
+// Raw scores (as loaded) of 16 keys of this thread's row times the keys' scales, in pairs; kMask:
+// -inf where the row does not see the key (columns above lim or up to low).
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ void chunk_scores(uint32_t t, const float *sc, int lim, int low, int col0, uint64_t (&z)[16])
+__device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *sc, int lim, int low, int col0,
+                                         uint64_t (&z)[8])
 {
-    uint32_t s[32];
-    tmem_ld32_wait(t, s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    for (int i = 0; i < 8; ++i) z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
     if (kInt8) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < 8; i += 2) {
             const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + col0 + 2 * i);
             z[i] = mul2(z[i], f.x);
             z[i + 1] = mul2(z[i + 1], f.y);
@@ -200,7 +234,7 @@ __device__ __forceinline__ void chunk_scores(uint32_t t, const float *sc, int li
     }
     if (kMask) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             float a, b;
             unpack2(z[i], &a, &b);
             const int c = col0 + 2 * i;
@@ -209,38 +243,33 @@ __device__ __forceinline__ void chunk_scores(uint32_t t, const float *sc, int li
     }
 }
 
-// The largest score of the row's 128 keys in units of log2 (mul: raw score to those; where it is
-// negative, the smallest raw score counts).
+// The largest score of the row's 128 keys in units of log2 (mul >= 0: raw score to those).
 template <bool kInt8, bool kMask>
 __device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim, int low, float mul)
 {
-    const uint64_t sign = mul < 0.0f ? pack2(-1.0f, -1.0f) : pack2(1.0f, 1.0f);
     float top = -INFINITY;
 #pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-        uint64_t z[16];
-        chunk_scores<kInt8, false>(tS + ch * 32, ksc, lim, low, ch * 32, z);
-        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    for (int ch = 0; ch < 8; ++ch) {
+        uint32_t s[16];
+        uint64_t z[8];
+        tmem_ld16_wait(tS + ch * 16, s);
+        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
+        float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             float a, b;
-            unpack2(mul2(z[i], sign), &a, &b);
-            if (kMask) {
-                const int c = ch * 32 + 2 * i;
-                a = c <= lim && c > low ? a : -INFINITY;
-                b = c + 1 <= lim && c + 1 > low ? b : -INFINITY;
-            }
-            x[i & 3] = fmaxf(x[i & 3], fmaxf(a, b));
+            unpack2(z[i], &a, &b);
+            x[i & 1] = fmaxf(x[i & 1], fmaxf(a, b));
         }
-        top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+        top = fmaxf(top, fmaxf(x[0], x[1]));
     }
-    return top == -INFINITY ? top : top * fabsf(mul);
+    return top == -INFINITY ? top : top * mul;
 }
 
 // The row's 128 weights 2^(score - m), times the values' scales (0 for a key the row does not
 // see, whatever its scale is), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e (whose
-// scores are read by then); kRest: what rounding left of them in column 16 i + 8 + e, else
-// zeros there. Returns the weights' sum.
+// scores are read by then), and in column 16 i + 8 + e what rounding left of them (kRest) or zeros.
+// Returns the weights' sum.
 template <bool kInt8, bool kMask, bool kRest>
 __device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, const float *vsc, int lim, int low,
                                               float mul, float m)
@@ -248,14 +277,15 @@ __device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, con
     const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-        uint64_t z[16];
-        chunk_scores<kInt8, kMask>(tS + ch * 32, ksc, lim, low, ch * 32, z);
-        uint32_t p[16], rest[16];
+    for (int ch = 0; ch < 8; ++ch) {
+        uint32_t s[16], p[8], rest[8];
+        uint64_t z[8];
+        tmem_ld16_wait(tS + ch * 16, s);
+        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < 8; i += 2) {
             ulonglong2 f;
-            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 32 + 2 * i);
+            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 16 + 2 * i);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float a, b, wa, wb;
@@ -280,19 +310,55 @@ __device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, con
                     }
                 }
                 p[i + e] = pack_bf16x2(wa, wb);
-                if (kRest) rest[i + e] = pack_bf16x2(wa - bf16_lo(p[i + e]), wb - bf16_hi(p[i + e]));
+                rest[i + e] = pack_bf16x2(wa - bf16_lo(p[i + e]), wb - bf16_hi(p[i + e]));
             }
         }
-        tmem_st8(tS + ch * 32, p);
-        tmem_st8(tS + ch * 32 + 16, p + 8);
-        if (kRest) {
-            tmem_st8(tS + ch * 32 + 8, rest);
-            tmem_st8(tS + ch * 32 + 24, rest + 8);
-        } else {
-            tmem_zero8(tS + ch * 32 + 8);
-            tmem_zero8(tS + ch * 32 + 24);
+        tmem_st8(tS + ch * 16, p);
+        if (kRest)
+            tmem_st8(tS + ch * 16 + 8, rest);
+        else
+            tmem_zero8(tS + ch * 16 + 8);
+    }
+    float a, b;
+    unpack2(add2(sum[0], sum[1]), &a, &b);
+    return a + b;
+}
+
+// The same (without masks and rests) in one pass over the scores, which stay where they are; the
+// weights in registers, and the largest score less m.
+template <bool kInt8>
+__device__ __forceinline__ float tile_guess(uint32_t tS, const float *ksc, const float *vsc, float mul, float m,
+                                            uint32_t (&p)[64], float *over)
+{
+    const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
+    uint64_t sum[2] = {0, 0};
+    float x[2] = {-INFINITY, -INFINITY};
+    uint32_t s[2][16];
+    tmem_ld16(tS, s[0]);
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        tmem_ld_wait(s[ch & 1]);
+        if (ch < 7) tmem_ld16(tS + (ch + 1) * 16, s[(ch + 1) & 1]);
+        uint64_t z[8];
+        scores16<kInt8, false>(s[ch & 1], ksc, 0, 0, ch * 16, z);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            ulonglong2 f;
+            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 16 + 2 * i);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float a, b;
+                unpack2(fma2(z[i + e], mul_2, neg), &a, &b);
+                x[e] = fmaxf(x[e], fmaxf(a, b));
+                uint64_t v = pack2(fast_exp2(a), fast_exp2(b));
+                sum[e] = add2(sum[e], v);
+                if (kInt8) v = mul2(v, e ? f.y : f.x);
+                unpack2(v, &a, &b);
+                p[ch * 8 + i + e] = pack_bf16x2(a, b);
+            }
         }
     }
+    *over = fmaxf(x[0], x[1]);
     float a, b;
     unpack2(add2(sum[0], sum[1]), &a, &b);
     return a + b;
@@ -350,15 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.G;
-    KvWork<kBlockRows, kKeys> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
-    if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total))) return;
+    Segment *const segs = reinterpret_cast<Segment *>(smem + C::kSegs);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], kLoadWarps);
             mbar_init(&bars.q_empty[i], 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], kTileRows);
+            mbar_init(&bars.p_full[i], kTileRows / 32);
             mbar_init(&bars.o_full[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
@@ -368,6 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             mbar_init(&bars.v_empty[i], 1);
         }
         for (int i = 0; i < C::kRing; ++i) mbar_init(&bars.sc_full[i], kLoadWarps);
+        for (int i = 0; i < kSegments; ++i) {
+            mbar_init(&bars.seg_full[i], 1);
+            mbar_init(&bars.seg_empty[i], kSoftWarps + kLoadWarps + 1);
+        }
         mbar_init(&bars.drain, 1);
         abort_flag = 0;
         fence_mbar_init();
@@ -381,6 +450,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
+    // segment `k` of the share once it is there (a whole warp); null: no more, or a wait ran out
+    auto segment = [&](int k) -> const Segment * {
+        if (!warp_wait(&bars.seg_full[k % kSegments], (uint32_t)(k / kSegments) & 1u, &abort_flag, kv.err)) return nullptr;
+        const Segment *g = segs + k % kSegments;
+        return g->j1 > 0 ? g : nullptr;
+    };
+    auto segment_done = [&](int k) {  // this warp has read all it needs of it
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.seg_empty[k % kSegments]);
+    };
+
     if (warp < kSoftWarps) {
         // ---------------------------------------------------------------- softmax
         regs_up<kSoftRegs>();
@@ -388,26 +468,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         const int row_in_tile = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 rows
         const uint32_t tS = lanes + t * 128, tO = lanes + C::kO + t * D;
-        int it = 0, work = -1;  // key tiles and work of the CTA,
-        int ns = 0, nw = 0;     // and of this tile
+        int it = 0;          // key tiles of the CTA,
+        int ns = 0, nw = 0;  // key tiles and segments of this tile
         bool ok = true;
-        while (ok && w.next()) {
-            ++work;
-            const int j0 = (int)(w.u - w.item0), j1 = (int)(w.seg_end - w.item0);
-            const int row_t = w.tile * kBlockRows + t * kTileRows;  // the tile's first row
-            const int64_t rows = (int64_t)w.sh.n * G;
+        for (int seg = 0; ok; ++seg) {
+            const Segment *const w = segment(seg);
+            if (!w) break;
+            const int j0 = w->j0, j1 = w->j1;
+            const int row_t = w->tile * kBlockRows + t * kTileRows;  // the tile's first row
+            const int rows = w->n * G;
             if (row_t >= rows) {
                 it += j1 - j0;
+                segment_done(seg);
                 continue;
             }
             const int row = row_t + row_in_tile;
             const bool on = row < rows;
-            const int i = on ? row / G : w.sh.n - 1;
-            const int pos = w.sh.L - w.sh.n + i;
+            const int i = on ? row / G : w->n - 1;
+            const int pos = w->L - w->n + i;
+            const int tok_lo = w->lo;
             float m = -INFINITY, l = 0.0f;
             float mul = plan.scale_log2;  // raw score -> units of log2
             for (int j = j0; j < j1; ++j, ++it, ++ns) {
-                const int tok0 = w.lo + j * kKeys;
+                const int tok0 = tok_lo + j * kKeys;
                 const int lim = pos - tok0;
                 const int low = a.window > 0 ? pos - a.window - tok0 : -1;
                 const bool mask = __any_sync(0xffffffffu, lim < kKeys - 1 || low >= 0);
@@ -415,55 +498,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const float *ksc = kscale + ring * 128, *vsc = vscale + ring * 128;
                 if (kInt8) {
                     ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
-                    if (j == j0) mul = row_mul[(work & 1) * kBlockRows + t * kTileRows + row_in_tile];
+                    if (j == j0) mul = row_mul[(seg & 1) * kBlockRows + t * kTileRows + row_in_tile];
                 }
                 ok = ok && warp_wait(&bars.s_full[t], (uint32_t)ns & 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 tc_fence_after_sync();
 
-                const float top = mask ? tile_top<kInt8, true>(tS, ksc, lim, low, mul)
-                                       : tile_top<kInt8, false>(tS, ksc, lim, low, mul);
-                if (__any_sync(0xffffffffu, top > m + 8.0f)) {
-                    const float m2 = fmaxf(m, top);
-                    const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
-                    m = m2;
-                    l *= down;
-                    if (j > j0) {
-#pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
-                            uint32_t o[32];
-                            tmem_ld32_wait(tO + x, o);
+                bool rest = j == j0, done = false;
+                const float mx = m == -INFINITY ? 0.0f : m;
+                if (!rest && !mask) {
+                    // One pass with the m there is: right unless a score passes it by so much that
+                    // the weights near fp32's range, or a key may hold much of a row's weight.
+                    uint32_t p[64];
+                    float over;
+                    const float add = tile_guess<kInt8>(tS, ksc, vsc, mul, mx, p, &over);
+                    rest = __any_sync(0xffffffffu, over > 64.0f || 3.0f * fast_exp2(over) > l);
+                    if (!rest) {
+                        l += add;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                            tmem_st16(tO + x, o);
-                            tmem_st16(tO + x + 16, o + 16);
+                        for (int x = 0; x < 8; ++x) {
+                            tmem_st8(tS + x * 16, p + x * 8);
+                            tmem_zero8(tS + x * 16 + 8);
                         }
+                        done = true;
                     }
                 }
-                const float mx = m == -INFINITY ? 0.0f : m;
-                const bool rest = __any_sync(0xffffffffu, 3.0f * fast_exp2(top - mx) > l);
+                if (!done) {
+                    const float top = mask ? tile_top<kInt8, true>(tS, ksc, lim, low, mul)
+                                           : tile_top<kInt8, false>(tS, ksc, lim, low, mul);
+                    rest = rest || __any_sync(0xffffffffu, top - mx > 64.0f || 3.0f * fast_exp2(top - mx) > l);
+                    if (!rest) {
+                        l += tile_weights<kInt8, true, false>(tS, ksc, vsc, lim, low, mul, mx);
+                    } else {
+                        const float m2 = fmaxf(m, top);
+                        const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
+                        m = m2;
+                        l *= down;
+                        if (j > j0) {
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_wait(tO + x, o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                                tmem_st16(tO + x, o);
+                            }
+                        }
+                        const float mn = m == -INFINITY ? 0.0f : m;
+                        l += mask ? tile_weights<kInt8, true, true>(tS, ksc, vsc, lim, low, mul, mn)
+                                  : tile_weights<kInt8, false, true>(tS, ksc, vsc, lim, low, mul, mn);
+                    }
+                }
                 if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t])[warp & 3] = rest;
-                if (rest)
-                    l += mask ? tile_weights<kInt8, true, true>(tS, ksc, vsc, lim, low, mul, mx)
-                              : tile_weights<kInt8, false, true>(tS, ksc, vsc, lim, low, mul, mx);
-                else
-                    l += mask ? tile_weights<kInt8, true, false>(tS, ksc, vsc, lim, low, mul, mx)
-                              : tile_weights<kInt8, false, false>(tS, ksc, vsc, lim, low, mul, mx);
                 tmem_st_wait();
                 tc_fence_before_sync();
-                mbar_arrive(&bars.p_full[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[t]);
             }
             if (!ok) break;
             ok = warp_wait(&bars.o_full[t], (uint32_t)nw & 1u, &abort_flag, kv.err);
             ++nw;
             if (!ok) break;
             tc_fence_after_sync();
-            const bool whole = w.whole();
-            const int64_t out_t = w.sh.row0 + i;
-            const int h = w.head * G + (on ? row % G : 0);
+            const bool whole = w->whole;
+            const int64_t out_t = w->row0 + i;
+            const int h = w->head * G + (on ? row % G : 0);
             uint16_t *const dst = a.O + out_t * a.o_stride + (int64_t)h * D;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            const int slot = 2 * blockIdx.x + (w.u == w.item0 ? 1 : 0);
+            const int slot = w->slot, c0 = w->c0, c1 = w->c1;
+            segment_done(seg);
             // a warp's rows of a piece: [D / 4][32][4], so that the warp writes 512 bytes at a time
             float *const part = plan.part + ((int64_t)slot * 8 + warp) * 32 * D + lane * 4;
             float2 *const part_ml =
@@ -496,7 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     a.lse[out_t * a.Hq + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             } else {
                 if (on) part_ml[slot * kBlockRows] = make_float2(m, l);
-                const int c0 = w.cta_of(w.item0), c1 = w.cta_of(w.item0 + w.nu - 1);
                 __threadfence();
                 __syncwarp();
                 int last = 0;
@@ -554,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         const int lw = warp - kSoftWarps;
         const int tid = threadIdx.x - kSoftWarps * 32;
         const uint32_t base = kv_opaque(0x43004300u);
-        int it = 0, work = 0;
+        int it = 0;
         uint32_t nq[2] = {0, 0};
         bool ok = true;
         int pr, pc;
@@ -565,14 +667,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             if (lane == 0) mbar_arrive(&bar);
         };
 
-        while (ok && w.next()) {
-            const int j0 = (int)(w.u - w.item0), j1 = (int)(w.seg_end - w.item0);
-            const int rows = (int)((int64_t)w.sh.n * G);
-            const int32_t *table = b.table + (int64_t)w.seq * b.table_stride;
+        for (int seg = 0; ok; ++seg) {
+            const Segment *const w = segment(seg);
+            if (!w) break;
+            const int j0 = w->j0, j1 = w->j1, rows = w->n * G, head = w->head, hi = w->hi, lo = w->lo + lw * 16;
+            const int32_t *table = b.table + (int64_t)w->seq * b.table_stride;
             // cache row of the warp's first token of key tile j, and how many of the 16 there are
             auto group = [&](int j, int *count) -> int64_t {
-                const int tok = w.lo + j * kKeys + lw * 16;
-                *count = j < j1 ? min(16, max(0, w.hi - tok)) : 0;
+                const int tok = lo + j * kKeys;
+                *count = j < j1 ? min(16, max(0, hi - tok)) : 0;
                 if (*count == 0) return 0;
                 int page = table[tok >> kv.page_shift];
                 if (page < 0 || page >= kv.num_pages) {
@@ -580,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     *count = 0;
                     page = 0;
                 }
-                return (((int64_t)page * kv.H + w.head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
+                return (((int64_t)page * kv.H + head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
             };
             // the lane's pieces of a group of codes (zeros past its end)
             auto fetch = [&](const void *arena, int64_t row, int count, uint4 (&v)[D / 32]) {
@@ -610,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             // Q: the tiles' rows, 16 (D 64: 32) at a time
             constexpr int kLanesQ = D / 8, kRowsQ = kLoadWarps * 32 / kLanesQ;
             for (int t = 0; t < 2 && ok; ++t) {
-                const int row_t = w.tile * kBlockRows + t * kTileRows;
+                const int row_t = w->tile * kBlockRows + t * kTileRows;
                 if (row_t >= rows) break;
                 ok = warp_wait(&bars.q_empty[t], (nq[t]++ & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
@@ -620,8 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     const int q = row_t + r;
                     uint4 v = make_uint4(0, 0, 0, 0);
                     if (q < rows)
-                        v = ldg_nc_v4(a.Q + (int64_t)(w.sh.row0 + q / G) * a.q_stride +
-                                      (int64_t)(w.head * G + q % G) * D + ch * 8);
+                        v = ldg_nc_v4(a.Q + (int64_t)(w->row0 + q / G) * a.q_stride +
+                                      (int64_t)(head * G + q % G) * D + ch * 8);
+                    v.x ^= plan.q_sign;
+                    v.y ^= plan.q_sign;
+                    v.z ^= plan.q_sign;
+                    v.w ^= plan.q_sign;
                     if (kInt8) {
                         // to f16, the row scaled by the power of two that puts its largest magnitude
                         // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
@@ -636,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                         for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
                         v = make_uint4(u[0], u[1], u[2], u[3]);
                         if (ch == 0)
-                            row_mul[(work & 1) * kBlockRows + t * kTileRows + r] =
+                            row_mul[(seg & 1) * kBlockRows + t * kTileRows + r] =
                                 __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
                     }
                     *reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, ch)) = v;
@@ -644,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 arrive(bars.q_full[t]);
             }
             if (!ok) break;
-            ++work;
+            segment_done(seg);
 
             for (int j = j0; j < j1; ++j, ++it) {
                 const int s = it % C::kStages;
@@ -721,10 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     }
                     mma_commit(&bars.s_full[t]);
                 };
-                while (ok && w.next()) {
-                    const int n = (int)(w.seg_end - w.u);
-                    const int64_t rows = (int64_t)w.sh.n * G;
-                    const int nt = w.tile * (int64_t)kBlockRows + kTileRows < rows ? 2 : 1;
+                for (int seg = 0; ok; ++seg) {
+                    wait(bars.seg_full[seg % kSegments], seg / kSegments);
+                    const Segment *const w = segs + seg % kSegments;
+                    const int n = ok ? w->j1 - w->j0 : 0;
+                    if (n <= 0) break;
+                    const int nt = w->tile * kBlockRows + kTileRows < w->n * G ? 2 : 1;
+                    mbar_arrive(&bars.seg_empty[seg % kSegments]);
                     wait(bars.k_full[it % C::kStages], it / C::kStages);
                     for (int t = 0; t < nt; ++t) {
                         wait(bars.q_full[t], nw[t]++);
@@ -770,6 +880,39 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 mbar_wait_inl(&bars.drain, 0, &unused, kv.err);
             }
             __syncwarp();
+        } else if (warp == kSoftWarps + kLoadWarps + 1) {
+            // ------------------------------------------- the share, segment by segment
+            KvWork<kBlockRows, kKeys> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
+            bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
+            for (int seg = 0;; ++seg) {
+                if (!warp_wait(&bars.seg_empty[seg % kSegments], ((uint32_t)(seg / kSegments) & 1u) ^ 1u, &abort_flag,
+                               kv.err))
+                    break;
+                more = more && w.next();
+                Segment g{};
+                if (more) {
+                    g.seq = w.seq;
+                    g.row0 = w.sh.row0;
+                    g.n = w.sh.n;
+                    g.L = w.sh.L;
+                    g.tile = w.tile;
+                    g.head = w.head;
+                    g.lo = w.lo;
+                    g.hi = w.hi;
+                    g.j0 = (int)(w.u - w.item0);
+                    g.j1 = (int)(w.seg_end - w.item0);
+                    g.whole = w.whole();
+                    g.slot = 2 * blockIdx.x + (w.u == w.item0 ? 1 : 0);
+                    g.c0 = w.cta_of(w.item0);
+                    g.c1 = w.cta_of(w.item0 + w.nu - 1);
+                }
+                if (lane == 0) {
+                    segs[seg % kSegments] = g;
+                    mbar_arrive(&bars.seg_full[seg % kSegments]);
+                }
+                __syncwarp();
+                if (!more) break;
+            }
         }
     }
     tc_fence_before_sync();
@@ -795,7 +938,8 @@ cudaError_t launch_kv_prefill(const KvDev &kv, bool int8, const KvBatchDev &b, c
     auto launch = [&](int smem, auto *fn) {
         const cudaError_t e = ensure_smem_attr((const void *)fn, smem);
         if (e != cudaSuccess) return e;
-        const Plan plan{min_rows, a.scale * 1.4426950408889634f, part, count};
+        const Plan plan{min_rows, fabsf(a.scale) * 1.4426950408889634f, signbit(a.scale) ? 0x80008000u : 0u, part,
+                        count};
         fn<<<kv_prefill_grid(num_sms), kThreads, smem, stream>>>(kv, b, a, plan);
         return cudaGetLastError();
     };
