@@ -209,11 +209,39 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// mbar_wait with one place that tries: the roles' loops run through several waits a tile, and their
+// code must stay small (a wait that is over already took 150 to 400 cycles with the larger one,
+// in instruction fetches).
+__device__ __forceinline__ bool small_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
+{
+    uint32_t n = 0;
+    uint64_t start = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if ((++n & 255u) != 0) continue;
+        const uint64_t now = global_timer_ns();
+        if (n == 256) start = now;
+        if (*abort_flag || now - start > kWaitTimeoutNs) {
+            if (!*abort_flag) atomicOr(err, kErrTimeoutBit);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // A wait of a whole warp: every lane waits (and so sees what the barrier released), and all
 // agree on whether it ran out.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
 {
-    return __all_sync(0xffffffffu, mbar_wait_inl(bar, parity, abort_flag, err));
+    return __all_sync(0xffffffffu, small_wait(bar, parity, abort_flag, err));
+}
+
+// Which of 16 columns from col0 on a row sees: a bit each.
+__device__ __forceinline__ uint32_t seen16(int lim, int low, int col0)
+{
+    const int n = min(max(lim - col0 + 1, 0), 16), skip = min(max(low - col0 + 1, 0), 16);
+    return ((1u << n) - 1u) & ~((1u << skip) - 1u);
 }
 
 // Raw scores (as loaded) of 16 keys of this thread's row times the keys' scales, in pairs; kMask:
@@ -233,12 +261,12 @@ __device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *s
         }
     }
     if (kMask) {
+        const uint32_t seen = seen16(lim, low, col0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float a, b;
             unpack2(z[i], &a, &b);
-            const int c = col0 + 2 * i;
-            z[i] = pack2(c <= lim && c > low ? a : -INFINITY, c + 1 <= lim && c + 1 > low ? b : -INFINITY);
+            z[i] = pack2(seen >> (2 * i) & 1u ? a : -INFINITY, seen >> (2 * i + 1) & 1u ? b : -INFINITY);
         }
     }
 }
@@ -717,36 +745,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 if (row_t >= rows) break;
                 ok = warp_wait(&bars.q_empty[t], (nq[t]++ & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
-#pragma unroll 4
-                for (int x = 0; x < kTileRows / kRowsQ; ++x) {
-                    const int r = x * kRowsQ + tid / kLanesQ, ch = tid % kLanesQ;
-                    const int q = row_t + r;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (q < rows)
-                        v = ldg_nc_v4(a.Q + (int64_t)(w->row0 + q / G) * a.q_stride +
-                                      (int64_t)(head * G + q % G) * D + ch * 8);
-                    v.x ^= plan.q_sign;
-                    v.y ^= plan.q_sign;
-                    v.z ^= plan.q_sign;
-                    v.w ^= plan.q_sign;
-                    if (kInt8) {
-                        // to f16, the row scaled by the power of two that puts its largest magnitude
-                        // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
-                        uint32_t u[4] = {v.x, v.y, v.z, v.w}, top = 0;
+                // all loads first: a batch costs one latency
+                constexpr int kBatch = kTileRows / kRowsQ < 4 ? kTileRows / kRowsQ : 4;
+#pragma unroll 1
+                for (int x0 = 0; x0 < kTileRows / kRowsQ; x0 += kBatch) {
+                    uint4 v[kBatch];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-#pragma unroll
-                        for (int d = kLanesQ / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        const int up = min(14 + 127 - (int)(top >> 7), 126);
-                        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
-                        v = make_uint4(u[0], u[1], u[2], u[3]);
-                        if (ch == 0)
-                            row_mul[(seg & 1) * kBlockRows + t * kTileRows + r] =
-                                __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
+                    for (int x = 0; x < kBatch; ++x) {
+                        const int q = min(row_t + (x0 + x) * kRowsQ + tid / kLanesQ, rows - 1);
+                        v[x] = *reinterpret_cast<const uint4 *>(a.Q + (int64_t)(w->row0 + q / G) * a.q_stride +
+                                                                (int64_t)(head * G + q % G) * D + (tid % kLanesQ) * 8);
                     }
-                    *reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, ch)) = v;
+#pragma unroll
+                    for (int x = 0; x < kBatch; ++x) {
+                        // (a row past the chunk's last holds that one's values: nothing reads its result)
+                        const int r = (x0 + x) * kRowsQ + tid / kLanesQ, ch = tid % kLanesQ;
+                        uint32_t u[4] = {v[x].x ^ plan.q_sign, v[x].y ^ plan.q_sign, v[x].z ^ plan.q_sign,
+                                         v[x].w ^ plan.q_sign};
+                        if (kInt8) {
+                            // to f16, the row scaled by the power of two that puts its largest magnitude
+                            // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
+                            uint32_t top = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+#pragma unroll
+                            for (int d = kLanesQ / 2; d > 0; d >>= 1)
+                                top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                            const int up = min(14 + 127 - (int)(top >> 7), 126);
+                            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
+                            if (ch == 0)
+                                row_mul[(seg & 1) * kBlockRows + t * kTileRows + r] =
+                                    __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
+                        }
+                        *reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, ch)) =
+                            make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
                 arrive(bars.q_full[t]);
             }
@@ -816,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 int it = 0, np[2] = {0, 0}, nw[2] = {0, 0};
                 bool ok = true;
                 auto wait = [&](uint64_t &bar, uint32_t parity) {
-                    ok = ok && mbar_wait_inl(&bar, parity & 1u, &abort_flag, kv.err);
+                    ok = ok && small_wait(&bar, parity & 1u, &abort_flag, kv.err);
                 };
                 // S_t = Q_t K^T of the key tile in stage s
                 auto scores = [&](int t, int s) {
@@ -877,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 // no MMA may be in flight when the tensor memory goes
                 mma_commit(&bars.drain);
                 int unused = 0;
-                mbar_wait_inl(&bars.drain, 0, &unused, kv.err);
+                small_wait(&bars.drain, 0, &unused, kv.err);
             }
             __syncwarp();
         } else if (warp == kSoftWarps + kLoadWarps + 1) {
