@@ -9,12 +9,13 @@
 // A CTA works on 256 rows of one kv head: the G query heads that share it for 256 / G tokens, so
 // K and V are read once for all of them, as two MMA tiles of 128 rows. Warps 0-3 and 4-7 do the
 // softmax of one tile each (a thread holds a row), 8-15 bring K and V tiles into shared memory
-// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs, warp 17 hands out the work:
+// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs, warp 17 hands out
+// the work:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
-// in the order PV_0(j) S_0(j+1) PV_1(j) S_1(j+1): while one tile's softmax runs, the tensor cores
-// do the other tile's products. MMAs of one thread execute in order, so S_t(j+1) overwrites
-// P_t(j) only after PV_t(j) has read it, and the commit behind S_t(j+1) covers PV_t(j).
+// in the order PV_t(j) S_t(j+1): while one tile's softmax runs, the tensor cores do the other
+// tile's products. MMAs of one thread execute in order, so S_t(j+1) overwrites P_t(j) only after
+// PV_t(j) has read it, and the commit behind S_t(j+1) covers PV_t(j).
 //
 // An 8-bit cache: the codes are exact in f16 (S) and in bf16 (O), a key's scale multiplies its
 // column of S and a value's its weight. S takes f16, because codes become f16 in two thirds of the
@@ -39,13 +40,14 @@ namespace {
 
 constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // the MMA warp's group has three idle warps
+constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // an MMA warp, one that hands out the work, two idle
 // registers a thread of the softmax warps, the loading warps and the MMA warp's group: a block of
 // 640 threads starts with 96 each, and 2 x 144 + 2 x 72 + 48 is 5 x 96
 constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
 static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "register split");
 
 constexpr int kSegments = 4;
+constexpr int kOutPitch = 80;  // bytes of a row of 32 bf16 columns: rows start 5 x 16 bytes apart
 
 template <int D>
 struct Cfg {
@@ -61,7 +63,8 @@ struct Cfg {
     static constexpr int kRowMul = kScales + 2 * kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
     static constexpr int kSegs = kRowMul + 2 * kBlockRows * 4;
     static constexpr int kBars = kSegs + kSegments * 64;
-    static constexpr int kSmem = kBars + 512 + 1024;           // and room to align to 1024
+    static constexpr int kOut = kBars + 512;                   // a softmax warp's 32 rows x 32 columns of O
+    static constexpr int kSmem = kOut + kSoftWarps * 32 * kOutPitch + 1024;           // and room to align to 1024
     static constexpr uint32_t kO = 256;                        // tensor memory column of O_0
 };
 
@@ -123,22 +126,18 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
-// 16 columns into registers; they are there after tmem_ld_wait on the same registers.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+// 8 columns into registers; they are there after tmem_ld_wait8 on the same registers (which orders
+// nothing else).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16])
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
@@ -228,6 +227,20 @@ __device__ __forceinline__ bool small_wait(uint64_t *bar, uint32_t parity, volat
         }
     }
     return true;
+}
+
+// Has the phase completed? (Does not wait.)
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 // A wait of a whole warp: every lane waits (and so sees what the barrier released), and all
@@ -361,29 +374,40 @@ __device__ __forceinline__ float tile_guess(uint32_t tS, const float *ksc, const
     const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
     float x[2] = {-INFINITY, -INFINITY};
-    uint32_t s[2][16];
-    tmem_ld16(tS, s[0]);
+    // Shared memory answers slowly while the tensor cores read their operands from it: the scales
+    // are asked for a chunk ahead.
+    uint32_t s[2][8];
+    ulonglong2 k[2][2], v[2];
+    tmem_ld8(tS, s[0]);
+    if (kInt8) {
+        k[0][0] = *reinterpret_cast<const ulonglong2 *>(ksc);
+        k[0][1] = *reinterpret_cast<const ulonglong2 *>(ksc + 4);
+    }
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
-        tmem_ld_wait(s[ch & 1]);
-        if (ch < 7) tmem_ld16(tS + (ch + 1) * 16, s[(ch + 1) & 1]);
-        uint64_t z[8];
-        scores16<kInt8, false>(s[ch & 1], ksc, 0, 0, ch * 16, z);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            ulonglong2 f;
-            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 16 + 2 * i);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float a, b;
-                unpack2(fma2(z[i + e], mul_2, neg), &a, &b);
-                x[e] = fmaxf(x[e], fmaxf(a, b));
-                uint64_t v = pack2(fast_exp2(a), fast_exp2(b));
-                sum[e] = add2(sum[e], v);
-                if (kInt8) v = mul2(v, e ? f.y : f.x);
-                unpack2(v, &a, &b);
-                p[ch * 8 + i + e] = pack_bf16x2(a, b);
+    for (int ch = 0; ch < 16; ++ch) {
+        const int b = ch & 1;
+        tmem_ld_wait8(s[b]);
+        if (ch < 15) tmem_ld8(tS + (ch + 1) * 8, s[b ^ 1]);
+        if (kInt8) {
+            v[0] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8);
+            v[1] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8 + 4);
+            if (ch < 15) {
+                k[b ^ 1][0] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 8);
+                k[b ^ 1][1] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 12);
             }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint64_t z = pack2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
+            if (kInt8) z = mul2(z, i & 1 ? k[b][i >> 1].y : k[b][i >> 1].x);
+            float e0, e1;
+            unpack2(fma2(z, mul_2, neg), &e0, &e1);
+            x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
+            uint64_t wt = pack2(fast_exp2(e0), fast_exp2(e1));
+            sum[i & 1] = add2(sum[i & 1], wt);
+            if (kInt8) wt = mul2(wt, i & 1 ? v[i >> 1].y : v[i >> 1].x);
+            unpack2(wt, &e0, &e1);
+            p[ch * 4 + i] = pack_bf16x2(e0, e1);
         }
     }
     *over = fmaxf(x[0], x[1]);
@@ -440,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     float *const row_mul = reinterpret_cast<float *>(smem + C::kRowMul);
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t rest_flags[2];  // of the tiles' weights: a byte a warp, has it a second part?
-    __shared__ int abort_flag;
+    __shared__ volatile int abort_flag;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.G;
@@ -599,22 +623,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             float *const part = plan.part + ((int64_t)slot * 8 + warp) * 32 * D + lane * 4;
             float2 *const part_ml =
                 reinterpret_cast<float2 *>(plan.part + (int64_t)2 * gridDim.x * kBlockRows * D) + warp * 32 + lane;
+            uint8_t *const out = smem + C::kOut + warp * 32 * kOutPitch;
 #pragma unroll 1
             for (int x = 0; x < D; x += 32) {
                 uint32_t o[32];
                 tmem_ld32_wait(tO + x, o);
                 if (whole) {
-                    if (on) {
+                    // through shared memory: a thread's own 16-byte stores would touch 32 rows at a
+                    // time (6300 cycles a segment), four lanes a row write 64 bytes of each
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t v[4];
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t v[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                v[y] = pack_bf16x2(__uint_as_float(o[e + 2 * y]) * inv,
-                                                   __uint_as_float(o[e + 2 * y + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(dst + x + e) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                        for (int y = 0; y < 4; ++y)
+                            v[y] = pack_bf16x2(__uint_as_float(o[e + 2 * y]) * inv, __uint_as_float(o[e + 2 * y + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + lane * kOutPitch + e * 2) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int r = y * 8 + (lane >> 2);
+                        uint16_t *const to = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, (uint64_t)dst, r));
+                        const uint4 v = *reinterpret_cast<const uint4 *>(out + r * kOutPitch + (lane & 3) * 16);
+                        if (row - lane + r < rows) *reinterpret_cast<uint4 *>(to + x + (lane & 3) * 8) = v;
+                    }
+                    __syncwarp();
                 } else if (on) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
@@ -736,32 +769,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             int count, ahead_count;
             int64_t row = group(j0, &count), ahead;
             uint4 vk[kInt8 ? D / 32 : 1], vv[kInt8 ? D / 32 : 1];
-            if constexpr (kInt8) fetch(kv.k, row, count, vk);
+            if constexpr (kInt8) {
+                fetch(kv.k, row, count, vk);
+            } else {
+                ok = warp_wait(&bars.k_empty[it % C::kStages], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag,
+                               kv.err);
+                if (!ok) break;
+                copy(kv.k, smem + C::kK + (it % C::kStages) * C::kTileBytes + lw * 2048, row, count);
+            }
 
-            // Q: the tiles' rows, 16 (D 64: 32) at a time
+            // Q: copies of both tiles' rows first, so that they cost one latency
             constexpr int kLanesQ = D / 8, kRowsQ = kLoadWarps * 32 / kLanesQ;
-            for (int t = 0; t < 2 && ok; ++t) {
-                const int row_t = w->tile * kBlockRows + t * kTileRows;
-                if (row_t >= rows) break;
+            const int qr = tid / kLanesQ, qc = tid % kLanesQ;
+            const int nt = w->tile * kBlockRows + kTileRows < rows ? 2 : 1;
+            int q = w->tile * kBlockRows + qr, qi = q / G, qg = q - qi * G;  // row, its token and head
+            const int step_i = kRowsQ / G, step_g = kRowsQ - step_i * G;
+            const uint16_t *const q_src = a.Q + (int64_t)w->row0 * a.q_stride + (int64_t)head * G * D + qc * 8;
+            for (int t = 0; t < nt && ok; ++t) {
                 ok = warp_wait(&bars.q_empty[t], (nq[t]++ & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
-                // all loads first: a batch costs one latency
-                constexpr int kBatch = kTileRows / kRowsQ < 4 ? kTileRows / kRowsQ : 4;
-#pragma unroll 1
-                for (int x0 = 0; x0 < kTileRows / kRowsQ; x0 += kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int x = 0; x < kBatch; ++x) {
-                        const int q = min(row_t + (x0 + x) * kRowsQ + tid / kLanesQ, rows - 1);
-                        v[x] = *reinterpret_cast<const uint4 *>(a.Q + (int64_t)(w->row0 + q / G) * a.q_stride +
-                                                                (int64_t)(head * G + q % G) * D + (tid % kLanesQ) * 8);
+#pragma unroll 4
+                for (int x = 0; x < kTileRows / kRowsQ; ++x) {
+                    // rows past the chunk's last become zeros
+                    const bool on = q < rows;
+                    cp_async16(smem_u32(smem + C::kQ + t * C::kTileBytes + tile_off(qr + x * kRowsQ, qc)),
+                               q_src + (on ? (int64_t)qi * a.q_stride + qg * D : 0), on ? 16u : 0u);
+                    q += kRowsQ;
+                    qi += step_i;
+                    qg += step_g;
+                    if (qg >= G) {
+                        qg -= G;
+                        ++qi;
                     }
-#pragma unroll
-                    for (int x = 0; x < kBatch; ++x) {
-                        // (a row past the chunk's last holds that one's values: nothing reads its result)
-                        const int r = (x0 + x) * kRowsQ + tid / kLanesQ, ch = tid % kLanesQ;
-                        uint32_t u[4] = {v[x].x ^ plan.q_sign, v[x].y ^ plan.q_sign, v[x].z ^ plan.q_sign,
-                                         v[x].w ^ plan.q_sign};
+                }
+            }
+            cp_commit();
+            if (!ok) {
+                cp_wait<0>();
+                break;
+            }
+            if constexpr (!kInt8) {  // the first V behind them
+                const int s = it % C::kStages;
+                ok = warp_wait(&bars.v_empty[s], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
+                if (ok) copy(kv.v, smem + C::kV + s * C::kTileBytes + lw * 2048, row, count);
+                else cp_commit();
+                cp_wait<2>();
+                arrive(bars.k_full[s]);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            for (int t = 0; t < nt; ++t) {
+                if (kInt8 || plan.q_sign) {
+#pragma unroll 2
+                    for (int r = qr; r < kTileRows; r += kRowsQ) {
+                        uint4 *const at = reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, qc));
+                        const uint4 v = *at;
+                        uint32_t u[4] = {v.x ^ plan.q_sign, v.y ^ plan.q_sign, v.z ^ plan.q_sign, v.w ^ plan.q_sign};
                         if (kInt8) {
                             // to f16, the row scaled by the power of two that puts its largest magnitude
                             // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
@@ -775,18 +839,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                             const float f = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
-                            if (ch == 0)
+                            if (qc == 0)
                                 row_mul[(seg & 1) * kBlockRows + t * kTileRows + r] =
                                     __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
                         }
-                        *reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, ch)) =
-                            make_uint4(u[0], u[1], u[2], u[3]);
+                        *at = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
                 arrive(bars.q_full[t]);
             }
-            if (!ok) break;
             segment_done(seg);
+            if (!ok) break;
 
             for (int j = j0; j < j1; ++j, ++it) {
                 const int s = it % C::kStages;
@@ -815,18 +878,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     arrive(bars.v_full[s]);
                 } else {
                     ahead = group(j + 1, &ahead_count);
-                    ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
-                    if (!ok) break;
-                    copy(kv.k, dk, row, count);
-                    if (j > j0) {  // the copies of the last V have landed
-                        cp_wait<1>();
+                    if (j > j0) {
+                        ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
+                        if (!ok) break;
+                        copy(kv.k, dk, row, count);
+                        cp_wait<1>();  // the last V has landed
                         arrive(bars.v_full[(it - 1) % C::kStages]);
+                        ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
+                        if (!ok) break;
+                        copy(kv.v, dv, row, count);
+                        cp_wait<1>();
+                        arrive(bars.k_full[s]);
                     }
-                    ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
-                    if (!ok) break;
-                    copy(kv.v, dv, row, count);
-                    cp_wait<1>();
-                    arrive(bars.k_full[s]);
                 }
                 row = ahead;
                 count = ahead_count;
@@ -836,25 +899,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 if (ok) arrive(bars.v_full[(it - 1) % C::kStages]);
             }
         }
+        cp_wait<0>();  // (a wait that ran out may leave copies behind)
     } else {
         // -------------------------------------------------------------------- MMAs
         regs_down<kMmaRegs>();
         if (warp == kSoftWarps + kLoadWarps) {
-                // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
+            // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
             const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys) - (kInt8 ? (1u << 7) | (1u << 10) : 0u);
             const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
-            // one thread issues everything
+            // One thread issues everything, PV_t(j) and S_t(j+1) of a tile together, for the tile whose
+            // weights are there first. (In a fixed order of the tiles it waits for one while the other
+            // is ready; a thread a tile interleaves the products, and both tiles' softmax then run
+            // at once and the tensor cores idle meanwhile.)
             if (lane == 0) {
                 const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ)), dk = sdesc_k_sw128(smem_u32(smem + C::kK));
                 const uint64_t dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
                 constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
-                int it = 0, np[2] = {0, 0}, nw[2] = {0, 0};
+                uint32_t it = 0, np[2] = {0, 0}, nq[2] = {0, 0};
                 bool ok = true;
                 auto wait = [&](uint64_t &bar, uint32_t parity) {
                     ok = ok && small_wait(&bar, parity & 1u, &abort_flag, kv.err);
                 };
-                // S_t = Q_t K^T of the key tile in stage s
-                auto scores = [&](int t, int s) {
+                auto scores = [&](int t, uint32_t s) {  // S_t = Q_t K^T of the key tile in stage s
                     const uint64_t q = dq + t * kTile16, k = dk + s * kTile16;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -872,42 +938,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     mbar_arrive(&bars.seg_empty[seg % kSegments]);
                     wait(bars.k_full[it % C::kStages], it / C::kStages);
                     for (int t = 0; t < nt; ++t) {
-                        wait(bars.q_full[t], nw[t]++);
+                        wait(bars.q_full[t], nq[t]++);
                         if (!ok) break;
                         scores(t, it % C::kStages);
                         if (n == 1) mma_commit(&bars.q_empty[t]);
                     }
                     if (!ok) break;
                     mma_commit(&bars.k_empty[it % C::kStages]);
-                    for (int j = 0; j < n && ok; ++j, ++it) {
-                        const int s = it % C::kStages, s1 = (it + 1) % C::kStages;
-                        wait(bars.v_full[s], it / C::kStages);
+
+                    int next[2] = {0, nt == 2 ? 0 : n};  // key tile of the tile's next PV
+                    int there = 0;                       // V of key tiles below, K of the next one: seen
+                    int t = 0;
+                    uint32_t polls = 0;
+                    uint64_t start = 0;
 #pragma unroll 1
-                        for (int t = 0; t < nt && ok; ++t) {
-                            wait(bars.p_full[t], np[t]++);
-                            if (!ok) break;
-                            tc_fence_after_sync();
-                            const uint32_t rest = *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]);
-                            const uint64_t v = dv + s * kTile16;
-                            const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
+                    while (min(next[0], next[1]) < n) {
+                        if (nt == 2) t ^= 1;
+                        const int j = t ? next[1] : next[0];
+                        const uint32_t at = it + j, s = at % C::kStages, s1 = (at + 1) % C::kStages;
+                        if (there == j && j < n && mbar_test(&bars.v_full[s], (at / C::kStages) & 1u) &&
+                            (j + 1 == n || mbar_test(&bars.k_full[s1], ((at + 1) / C::kStages) & 1u)))
+                            there = j + 1;
+                        if (there <= j || !mbar_test(&bars.p_full[t], (t ? np[1] : np[0]) & 1u)) {
+                            if ((++polls & 255u) == 0) {
+                                const uint64_t now = global_timer_ns();
+                                if (polls == 256) start = now;
+                                if (abort_flag || now - start > kWaitTimeoutNs) {
+                                    if (!abort_flag) atomicOr(kv.err, kErrTimeoutBit);
+                                    abort_flag = 1;
+                                    ok = false;
+                                    break;
+                                }
+                            }
+                            continue;
+                        }
+                        polls = 0;
+                        tc_fence_after_sync();
+                        const uint32_t rest = *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]);
+                        const uint64_t v = dv + s * kTile16;
+                        const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
 #pragma unroll
-                            for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
-                            if (rest) {
+                        for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
+                        if (rest) {
 #pragma unroll 1
-                                for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + 8 + i * 16, v + i * 128, id_o, 1);
-                            }
-                            if (t == nt - 1) mma_commit(&bars.v_empty[s]);
-                            if (j == n - 1) {
-                                mma_commit(&bars.o_full[t]);
-                                continue;
-                            }
-                            if (t == 0) wait(bars.k_full[s1], (it + 1) / C::kStages);
-                            if (!ok) break;
+                            for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + 8 + i * 16, v + i * 128, id_o, 1);
+                        }
+                        const bool both = (t ? next[0] : next[1]) > j;  // the other tile has done this key tile
+                        if (j + 1 < n) {
                             scores(t, s1);
+                            if (both) mma_commit(&bars.k_empty[s1]);
                             if (j + 2 == n) mma_commit(&bars.q_empty[t]);
-                            if (t == nt - 1) mma_commit(&bars.k_empty[s1]);
+                        } else {
+                            mma_commit(&bars.o_full[t]);
+                        }
+                        if (both) mma_commit(&bars.v_empty[s]);
+                        if (t) {
+                            ++next[1];
+                            ++np[1];
+                        } else {
+                            ++next[0];
+                            ++np[0];
                         }
                     }
+                    it += n;
                 }
                 // no MMA may be in flight when the tensor memory goes
                 mma_commit(&bars.drain);
