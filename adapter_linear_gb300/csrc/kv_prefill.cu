@@ -114,15 +114,40 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t smem_addr)
     return d;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate)
+// The MMA warp runs its loop with all lanes, so that operands stay in uniform registers (from a
+// single lane's branch each MMA took 100 cycles to issue, moving them there); `lead` is
+// non-zero in the lane that issues.
+// D[tmem] (+)= A[smem] * B[smem]
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint32_t lead, uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(lead)
         : "memory");
 }
 
@@ -479,9 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             mbar_init(&bars.o_full[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&bars.k_full[i], kLoadWarps);
+            mbar_init(&bars.k_full[i], kLoadWarps / 2);
             mbar_init(&bars.k_empty[i], 1);
-            mbar_init(&bars.v_full[i], kLoadWarps);
+            mbar_init(&bars.v_full[i], kLoadWarps / 2);
             mbar_init(&bars.v_empty[i], 1);
         }
         for (int i = 0; i < C::kRing; ++i) mbar_init(&bars.sc_full[i], kLoadWarps);
@@ -713,10 +738,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ------------------------------------------------- Q, K and V into shared memory
         regs_down<kLoadRegs>();
-        // warp lw brings tokens 16 lw .. 16 lw + 15 of every key tile: one page lookup
+        // Warps 0-3 of these bring K, 4-7 V (the stages of the two come free at different times): tokens
+        // 32 q .. 32 q + 31 of every key tile, q = warp % 4, as two 16-token groups of a page each.
         const int lw = warp - kSoftWarps;
+        const bool is_v = lw >= 4;
         const int tid = threadIdx.x - kSoftWarps * 32;
         const uint32_t base = kv_opaque(0x43004300u);
+        uint64_t *const full = is_v ? bars.v_full : bars.k_full, *const empty = is_v ? bars.v_empty : bars.k_empty;
+        const void *const arena = is_v ? kv.v : kv.k;
+        const uint16_t *const scales = is_v ? kv.vs : kv.ks;
+        float *const scale_ring = (is_v ? vscale : kscale) + (lw & 3) * 32;
+        uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 3) * 4096;
         int it = 0;
         uint32_t nq[2] = {0, 0};
         bool ok = true;
@@ -731,11 +763,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         for (int seg = 0; ok; ++seg) {
             const Segment *const w = segment(seg);
             if (!w) break;
-            const int j0 = w->j0, j1 = w->j1, rows = w->n * G, head = w->head, hi = w->hi, lo = w->lo + lw * 16;
+            const int j0 = w->j0, j1 = w->j1, rows = w->n * G, head = w->head, hi = w->hi;
+            const int lo = w->lo + (lw & 3) * 32;
             const int32_t *table = b.table + (int64_t)w->seq * b.table_stride;
-            // cache row of the warp's first token of key tile j, and how many of the 16 there are
-            auto group = [&](int j, int *count) -> int64_t {
-                const int tok = lo + j * kKeys;
+            // cache row of the first token of the warp's group x of key tile j, and how many of the 16
+            // there are
+            auto group = [&](int j, int x, int *count) -> int64_t {
+                const int tok = lo + j * kKeys + x * 16;
                 *count = j < j1 ? min(16, max(0, hi - tok)) : 0;
                 if (*count == 0) return 0;
                 int page = table[tok >> kv.page_shift];
@@ -747,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 return (((int64_t)page * kv.H + head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
             };
             // the lane's pieces of a group of codes (zeros past its end)
-            auto fetch = [&](const void *arena, int64_t row, int count, uint4 (&v)[D / 32]) {
+            auto fetch = [&](int64_t row, int count, uint4 (&v)[D / 32]) {
                 const uint8_t *src = static_cast<const uint8_t *>(arena) + (row + pr) * D + pc * 16;
 #pragma unroll
                 for (int p = 0; p < D / 32; ++p) {
@@ -756,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 }
             };
             // bf16: straight into shared memory (rows past the end hold anything: zeros)
-            auto copy = [&](const void *arena, uint8_t *dst, int64_t row, int count) {
+            auto copy = [&](uint8_t *dst, int64_t row, int count) {
                 constexpr int kLanes = D / 8, kStep = 32 / kLanes;
                 const uint8_t *src = static_cast<const uint8_t *>(arena) + row * (2 * D) + lane * 16;
 #pragma unroll
@@ -764,18 +798,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     const int r = p * kStep + lane / kLanes;
                     cp_async16(smem_u32(dst + tile_off(r, lane % kLanes)), src + p * 512, r < count ? 16u : 0u);
                 }
-                cp_commit();
             };
-            int count, ahead_count;
-            int64_t row = group(j0, &count), ahead;
-            uint4 vk[kInt8 ? D / 32 : 1], vv[kInt8 ? D / 32 : 1];
+            int count[2];
+            int64_t row[2];
+            for (int x = 0; x < 2; ++x) row[x] = group(j0, x, &count[x]);
+            uint4 v0[kInt8 ? D / 32 : 1], v1[kInt8 ? D / 32 : 1];
             if constexpr (kInt8) {
-                fetch(kv.k, row, count, vk);
+                fetch(row[0], count[0], v0);
+                fetch(row[1], count[1], v1);
             } else {
-                ok = warp_wait(&bars.k_empty[it % C::kStages], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag,
-                               kv.err);
+                ok = warp_wait(&empty[it % C::kStages], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
-                copy(kv.k, smem + C::kK + (it % C::kStages) * C::kTileBytes + lw * 2048, row, count);
+                uint8_t *const dst = stages + (it % C::kStages) * C::kTileBytes;
+                copy(dst, row[0], count[0]);
+                copy(dst + 2048, row[1], count[1]);
+                cp_commit();
             }
 
             // Q: copies of both tiles' rows first, so that they cost one latency
@@ -808,17 +845,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 cp_wait<0>();
                 break;
             }
-            if constexpr (!kInt8) {  // the first V behind them
-                const int s = it % C::kStages;
-                ok = warp_wait(&bars.v_empty[s], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
-                if (ok) copy(kv.v, smem + C::kV + s * C::kTileBytes + lw * 2048, row, count);
-                else cp_commit();
-                cp_wait<2>();
-                arrive(bars.k_full[s]);
+            if constexpr (!kInt8) {
                 cp_wait<1>();
-            } else {
-                cp_wait<0>();
+                arrive(full[it % C::kStages]);
             }
+            cp_wait<0>();
             for (int t = 0; t < nt; ++t) {
                 if (kInt8 || plan.q_sign) {
 #pragma unroll 2
@@ -854,49 +885,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             for (int j = j0; j < j1; ++j, ++it) {
                 const int s = it % C::kStages;
                 const uint32_t ph = ((uint32_t)(it / C::kStages) & 1u) ^ 1u;
-                uint8_t *const dk = smem + C::kK + s * C::kTileBytes + lw * 2048;
-                uint8_t *const dv = smem + C::kV + s * C::kTileBytes + lw * 2048;
+                uint8_t *const dst = stages + s * C::kTileBytes;
                 if constexpr (kInt8) {
-                    // lanes 0-15 the keys' scales, 16-31 the values'
-                    const int ring = it % C::kRing;
+                    const int x = lane >> 4, ring = it % C::kRing;
                     float sc = 0.0f;
-                    if ((lane & 15) < count)
-                        sc = __uint_as_float((uint32_t)(lane < 16 ? kv.ks : kv.vs)[row + (lane & 15)] << 16);
-                    fetch(kv.v, row, count, vv);
-                    ahead = group(j + 1, &ahead_count);
-                    ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
+                    if ((lane & 15) < (x ? count[1] : count[0]))
+                        sc = __uint_as_float((uint32_t)scales[(x ? row[1] : row[0]) + (lane & 15)] << 16);
+                    for (int y = 0; y < 2; ++y) row[y] = group(j + 1, y, &count[y]);
+                    ok = warp_wait(&empty[s], ph, &abort_flag, kv.err);
                     if (!ok) break;
-                    store_codes<D, true>(dk, vk, pr, pc, base);
-                    arrive(bars.k_full[s]);
-                    (lane < 16 ? kscale : vscale)[ring * 128 + lw * 16 + (lane & 15)] = sc;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
-                    fetch(kv.k, ahead, ahead_count, vk);
-                    ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
-                    if (!ok) break;
-                    store_codes<D, false>(dv, vv, pr, pc, base);
-                    arrive(bars.v_full[s]);
-                } else {
-                    ahead = group(j + 1, &ahead_count);
-                    if (j > j0) {
-                        ok = warp_wait(&bars.k_empty[s], ph, &abort_flag, kv.err);
-                        if (!ok) break;
-                        copy(kv.k, dk, row, count);
-                        cp_wait<1>();  // the last V has landed
-                        arrive(bars.v_full[(it - 1) % C::kStages]);
-                        ok = warp_wait(&bars.v_empty[s], ph, &abort_flag, kv.err);
-                        if (!ok) break;
-                        copy(kv.v, dv, row, count);
-                        cp_wait<1>();
-                        arrive(bars.k_full[s]);
+                    // K as f16, V as bf16; the next tile's codes are on their way meanwhile
+                    if (is_v) {
+                        store_codes<D, false>(dst, v0, pr, pc, base);
+                        fetch(row[0], count[0], v0);
+                        store_codes<D, false>(dst + 2048, v1, pr, pc, base);
+                        fetch(row[1], count[1], v1);
+                    } else {
+                        store_codes<D, true>(dst, v0, pr, pc, base);
+                        fetch(row[0], count[0], v0);
+                        store_codes<D, true>(dst + 2048, v1, pr, pc, base);
+                        fetch(row[1], count[1], v1);
                     }
+                    scale_ring[ring * 128 + lane] = sc;
+                    arrive(full[s]);
+                    if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
+                } else if (j > j0) {
+                    for (int y = 0; y < 2; ++y) row[y] = group(j, y, &count[y]);
+                    ok = warp_wait(&empty[s], ph, &abort_flag, kv.err);
+                    if (!ok) break;
+                    copy(dst, row[0], count[0]);
+                    copy(dst + 2048, row[1], count[1]);
+                    cp_commit();
+                    cp_wait<0>();
+                    arrive(full[s]);
                 }
-                row = ahead;
-                count = ahead_count;
-            }
-            if constexpr (!kInt8) {
-                cp_wait<0>();
-                if (ok) arrive(bars.v_full[(it - 1) % C::kStages]);
             }
         }
         cp_wait<0>();  // (a wait that ran out may leave copies behind)
@@ -907,106 +929,109 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
             const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys) - (kInt8 ? (1u << 7) | (1u << 10) : 0u);
             const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
-            // One thread issues everything, PV_t(j) and S_t(j+1) of a tile together, for the tile whose
+            // One warp issues everything, PV_t(j) and S_t(j+1) of a tile together, for the tile whose
             // weights are there first. (In a fixed order of the tiles it waits for one while the other
-            // is ready; a thread a tile interleaves the products, and both tiles' softmax then run
+            // is ready; a warp a tile interleaves the products, and both tiles' softmax then run
             // at once and the tensor cores idle meanwhile.)
-            if (lane == 0) {
-                const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ)), dk = sdesc_k_sw128(smem_u32(smem + C::kK));
-                const uint64_t dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
-                constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
-                uint32_t it = 0, np[2] = {0, 0}, nq[2] = {0, 0};
-                bool ok = true;
-                auto wait = [&](uint64_t &bar, uint32_t parity) {
-                    ok = ok && small_wait(&bar, parity & 1u, &abort_flag, kv.err);
-                };
-                auto scores = [&](int t, uint32_t s) {  // S_t = Q_t K^T of the key tile in stage s
-                    const uint64_t q = dq + t * kTile16, k = dk + s * kTile16;
+            const uint32_t lead = lane == 0;
+            const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ)), dk = sdesc_k_sw128(smem_u32(smem + C::kK));
+            const uint64_t dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
+            constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
+            uint32_t it = 0, np0 = 0, np1 = 0, nq0 = 0, nq1 = 0;
+            bool ok = true;
+            auto commit = [&](uint64_t &bar) { commit_lead(lead, smem_u32(&bar)); };
+            auto ready = [&](uint64_t &bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_test(&bar, parity & 1u)) != 0;
+            };
+            auto scores = [&](uint32_t t, uint32_t s) {  // S_t = Q_t K^T of the key tile in stage s
+                const uint64_t q = dq + t * kTile16, k = dk + s * kTile16;
+                const uint32_t d = tmem + t * 128;
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
-                        mma_bf16_ss(tmem + t * 128, q + off, k + off, id_s, i > 0);
-                    }
-                    mma_commit(&bars.s_full[t]);
-                };
-                for (int seg = 0; ok; ++seg) {
-                    wait(bars.seg_full[seg % kSegments], seg / kSegments);
-                    const Segment *const w = segs + seg % kSegments;
-                    const int n = ok ? w->j1 - w->j0 : 0;
-                    if (n <= 0) break;
-                    const int nt = w->tile * kBlockRows + kTileRows < w->n * G ? 2 : 1;
-                    mbar_arrive(&bars.seg_empty[seg % kSegments]);
-                    wait(bars.k_full[it % C::kStages], it / C::kStages);
-                    for (int t = 0; t < nt; ++t) {
-                        wait(bars.q_full[t], nq[t]++);
-                        if (!ok) break;
-                        scores(t, it % C::kStages);
-                        if (n == 1) mma_commit(&bars.q_empty[t]);
-                    }
-                    if (!ok) break;
-                    mma_commit(&bars.k_empty[it % C::kStages]);
-
-                    int next[2] = {0, nt == 2 ? 0 : n};  // key tile of the tile's next PV
-                    int there = 0;                       // V of key tiles below, K of the next one: seen
-                    int t = 0;
-                    uint32_t polls = 0;
-                    uint64_t start = 0;
-#pragma unroll 1
-                    while (min(next[0], next[1]) < n) {
-                        if (nt == 2) t ^= 1;
-                        const int j = t ? next[1] : next[0];
-                        const uint32_t at = it + j, s = at % C::kStages, s1 = (at + 1) % C::kStages;
-                        if (there == j && j < n && mbar_test(&bars.v_full[s], (at / C::kStages) & 1u) &&
-                            (j + 1 == n || mbar_test(&bars.k_full[s1], ((at + 1) / C::kStages) & 1u)))
-                            there = j + 1;
-                        if (there <= j || !mbar_test(&bars.p_full[t], (t ? np[1] : np[0]) & 1u)) {
-                            if ((++polls & 255u) == 0) {
-                                const uint64_t now = global_timer_ns();
-                                if (polls == 256) start = now;
-                                if (abort_flag || now - start > kWaitTimeoutNs) {
-                                    if (!abort_flag) atomicOr(kv.err, kErrTimeoutBit);
-                                    abort_flag = 1;
-                                    ok = false;
-                                    break;
-                                }
-                            }
-                            continue;
-                        }
-                        polls = 0;
-                        tc_fence_after_sync();
-                        const uint32_t rest = *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]);
-                        const uint64_t v = dv + s * kTile16;
-                        const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
-#pragma unroll
-                        for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
-                        if (rest) {
-#pragma unroll 1
-                            for (int i = 0; i < kKeys / 16; ++i) mma_bf16_ts(o, p + 8 + i * 16, v + i * 128, id_o, 1);
-                        }
-                        const bool both = (t ? next[0] : next[1]) > j;  // the other tile has done this key tile
-                        if (j + 1 < n) {
-                            scores(t, s1);
-                            if (both) mma_commit(&bars.k_empty[s1]);
-                            if (j + 2 == n) mma_commit(&bars.q_empty[t]);
-                        } else {
-                            mma_commit(&bars.o_full[t]);
-                        }
-                        if (both) mma_commit(&bars.v_empty[s]);
-                        if (t) {
-                            ++next[1];
-                            ++np[1];
-                        } else {
-                            ++next[0];
-                            ++np[0];
-                        }
-                    }
-                    it += n;
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
+                    mma_ss(lead, d, q + off, k + off, id_s, i > 0);
                 }
-                // no MMA may be in flight when the tensor memory goes
-                mma_commit(&bars.drain);
-                int unused = 0;
-                small_wait(&bars.drain, 0, &unused, kv.err);
+                commit(bars.s_full[t]);
+            };
+            for (int seg = 0; ok; ++seg) {
+                const Segment *const w = segment(seg);
+                if (!w) break;
+                const int n = __shfl_sync(0xffffffffu, w->j1 - w->j0, 0);
+                const int nt = __shfl_sync(0xffffffffu, w->tile * kBlockRows + kTileRows < w->n * G ? 2 : 1, 0);
+                segment_done(seg);
+                ok = warp_wait(&bars.k_full[it % C::kStages], (it / C::kStages) & 1u, &abort_flag, kv.err);
+                for (int t = 0; t < nt && ok; ++t) {
+                    ok = warp_wait(&bars.q_full[t], (t ? nq1 : nq0) & 1u, &abort_flag, kv.err);
+                    if (!ok) break;
+                    if (t)
+                        ++nq1;
+                    else
+                        ++nq0;
+                    scores(t, it % C::kStages);
+                    if (n == 1) commit(bars.q_empty[t]);
+                }
+                if (!ok) break;
+                commit(bars.k_empty[it % C::kStages]);
+
+                int next0 = 0, next1 = nt == 2 ? 0 : n;  // key tile of the tile's next PV
+                int there = 0;                           // V of key tiles below, K of the next one: seen
+                uint32_t t = 0, polls = 0;
+                uint64_t start = 0;
+#pragma unroll 1
+                while (min(next0, next1) < n) {
+                    if (nt == 2) t ^= 1;
+                    const int j = t ? next1 : next0;
+                    const uint32_t at = it + j, s = at % C::kStages, s1 = (at + 1) % C::kStages;
+                    if (there == j && j < n && ready(bars.v_full[s], at / C::kStages) &&
+                        (j + 1 == n || ready(bars.k_full[s1], (at + 1) / C::kStages)))
+                        there = j + 1;
+                    if (there <= j || !ready(bars.p_full[t], t ? np1 : np0)) {
+                        if ((++polls & 255u) == 0) {
+                            const uint64_t now = global_timer_ns();
+                            if (polls == 256) start = now;
+                            ok = __all_sync(0xffffffffu, !abort_flag && now - start <= kWaitTimeoutNs);
+                            if (!ok) {
+                                if (!abort_flag) atomicOr(kv.err, kErrTimeoutBit);
+                                abort_flag = 1;
+                                break;
+                            }
+                        }
+                        continue;
+                    }
+                    polls = 0;
+                    tc_fence_after_sync();
+                    const bool rest = __any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]) != 0);
+                    const uint64_t v = dv + s * kTile16;
+                    const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 16; ++i) mma_ts(lead, o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
+                    if (rest) {
+#pragma unroll 1
+                        for (int i = 0; i < kKeys / 16; ++i) mma_ts(lead, o, p + 8 + i * 16, v + i * 128, id_o, 1);
+                    }
+                    const bool both = (t ? next0 : next1) > j;  // the other tile has done this key tile
+                    if (j + 1 < n) {
+                        scores(t, s1);
+                        if (both) commit(bars.k_empty[s1]);
+                        if (j + 2 == n) commit(bars.q_empty[t]);
+                    } else {
+                        commit(bars.o_full[t]);
+                    }
+                    if (both) commit(bars.v_empty[s]);
+                    if (t) {
+                        ++next1;
+                        ++np1;
+                    } else {
+                        ++next0;
+                        ++np0;
+                    }
+                }
+                it += n;
             }
+            // no MMA may be in flight when the tensor memory goes
+            commit(bars.drain);
+            int unused = 0;
+            small_wait(&bars.drain, 0, &unused, kv.err);
             __syncwarp();
         } else if (warp == kSoftWarps + kLoadWarps + 1) {
             // ------------------------------------------- the share, segment by segment
