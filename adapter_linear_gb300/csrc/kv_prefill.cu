@@ -8,9 +8,9 @@
 //
 // A CTA works on 256 rows of one kv head: the G query heads that share it for 256 / G tokens, so
 // K and V are read once for all of them, as two MMA tiles of 128 rows. Warps 0-3 and 4-7 do the
-// softmax of one tile each (a thread holds a row), 8-15 bring K and V tiles into shared memory
-// (8-bit codes become 16-bit operands on the way), warp 16 issues the MMAs, warp 17 hands out
-// the work:
+// softmax of one tile each (a thread holds a row), 8-11 bring K and V tiles into shared memory
+// (8-bit codes become 16-bit operands on the way), warps 12 and 13 issue the MMAs, warp 14
+// hands out the work:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
 // in the order PV_t(j) S_t(j+1): while one tile's softmax runs, the tensor cores do the other
@@ -39,12 +39,13 @@ namespace lora {
 namespace {
 
 constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128;
-constexpr int kSoftWarps = 8, kLoadWarps = 8;
-constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // an MMA warp, one that hands out the work, two idle
-// registers a thread of the softmax warps, the loading warps and the MMA warp's group: a block of
-// 640 threads starts with 96 each, and 2 x 144 + 2 x 72 + 48 is 5 x 96
-constexpr int kSoftRegs = 144, kLoadRegs = 72, kMmaRegs = 48;
-static_assert(2 * kSoftRegs + 2 * kLoadRegs + kMmaRegs <= 5 * 96, "register split");
+constexpr int kSoftWarps = 8, kLoadWarps = 4;
+constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // two MMA warps, one that hands out the work, one idle
+// Registers a thread of the softmax warps, the loading warps and the MMA warps' group: a block of
+// 512 threads starts with 128 each, and 2 x 152 + 120 + 88 is 4 x 128. (Nothing may spill: shared
+// memory leaves L1 28 KB, and a spilled register comes back from L2.)
+constexpr int kSoftRegs = 152, kLoadRegs = 120, kMmaRegs = 88;
+static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "register split");
 
 constexpr int kSegments = 4;
 constexpr int kOutPitch = 80;  // bytes of a row of 32 bf16 columns: rows start 5 x 16 bytes apart
@@ -82,7 +83,7 @@ static_assert(sizeof(Segment) == 64, "segment");
 
 struct Bars {
     uint64_t seg_full[kSegments], seg_empty[kSegments], q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], sc_full[6], s_full[2],
-        p_full[2], o_full[2], drain;
+        p_full[2], o_full[2], turn[2], drain[2];
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
@@ -233,9 +234,23 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// mbar_wait with one place that tries: the roles' loops run through several waits a tile, and their
-// code must stay small (a wait that is over already took 150 to 400 cycles with the larger one,
-// in instruction fetches).
+// Has the phase completed? (Does not wait.)
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// mbar_wait that asks again and again instead of suspending the warp (which wakes up 1000 cycles
+// and more after the barrier), with one place that asks: the roles' loops run through several
+// waits a key tile, and their code must stay small.
 __device__ __forceinline__ bool small_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
 {
     uint32_t n = 0;
@@ -252,20 +267,6 @@ __device__ __forceinline__ bool small_wait(uint64_t *bar, uint32_t parity, volat
         }
     }
     return true;
-}
-
-// Has the phase completed? (Does not wait.)
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
 }
 
 // A wait of a whole warp: every lane waits (and so sees what the barrier released), and all
@@ -502,19 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             mbar_init(&bars.s_full[i], 1);
             mbar_init(&bars.p_full[i], kTileRows / 32);
             mbar_init(&bars.o_full[i], 1);
+            mbar_init(&bars.turn[i], 1);
+            mbar_init(&bars.drain[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars.k_full[i], kLoadWarps / 2);
-            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.k_empty[i], 2);
             mbar_init(&bars.v_full[i], kLoadWarps / 2);
-            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.v_empty[i], 2);
         }
         for (int i = 0; i < C::kRing; ++i) mbar_init(&bars.sc_full[i], kLoadWarps);
         for (int i = 0; i < kSegments; ++i) {
             mbar_init(&bars.seg_full[i], 1);
-            mbar_init(&bars.seg_empty[i], kSoftWarps + kLoadWarps + 1);
+            mbar_init(&bars.seg_empty[i], kSoftWarps + kLoadWarps + 2);
         }
-        mbar_init(&bars.drain, 1);
         abort_flag = 0;
         fence_mbar_init();
     }
@@ -738,17 +740,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ------------------------------------------------- Q, K and V into shared memory
         regs_down<kLoadRegs>();
-        // Warps 0-3 of these bring K, 4-7 V (the stages of the two come free at different times): tokens
-        // 32 q .. 32 q + 31 of every key tile, q = warp % 4, as two 16-token groups of a page each.
+        // Warps 0 and 1 of these bring K, 2 and 3 V (the stages of the two come free at different
+        // times): 64 tokens of every key tile as four 16-token groups, each of one page.
+        constexpr int kGroups = 4;
         const int lw = warp - kSoftWarps;
-        const bool is_v = lw >= 4;
+        const bool is_v = lw >= 2;
         const int tid = threadIdx.x - kSoftWarps * 32;
         const uint32_t base = kv_opaque(0x43004300u);
         uint64_t *const full = is_v ? bars.v_full : bars.k_full, *const empty = is_v ? bars.v_empty : bars.k_empty;
         const void *const arena = is_v ? kv.v : kv.k;
         const uint16_t *const scales = is_v ? kv.vs : kv.ks;
-        float *const scale_ring = (is_v ? vscale : kscale) + (lw & 3) * 32;
-        uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 3) * 4096;
+        float *const scale_ring = (is_v ? vscale : kscale) + (lw & 1) * 64;
+        uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 1) * 8192;
         int it = 0;
         uint32_t nq[2] = {0, 0};
         bool ok = true;
@@ -764,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const Segment *const w = segment(seg);
             if (!w) break;
             const int j0 = w->j0, j1 = w->j1, rows = w->n * G, head = w->head, hi = w->hi;
-            const int lo = w->lo + (lw & 3) * 32;
+            const int lo = w->lo + (lw & 1) * 64;
             const int32_t *table = b.table + (int64_t)w->seq * b.table_stride;
             // cache row of the first token of the warp's group x of key tile j, and how many of the 16
             // there are
@@ -799,19 +802,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     cp_async16(smem_u32(dst + tile_off(r, lane % kLanes)), src + p * 512, r < count ? 16u : 0u);
                 }
             };
-            int count[2];
-            int64_t row[2];
-            for (int x = 0; x < 2; ++x) row[x] = group(j0, x, &count[x]);
-            uint4 v0[kInt8 ? D / 32 : 1], v1[kInt8 ? D / 32 : 1];
+            int count[kGroups];
+            int64_t row[kGroups];
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x) row[x] = group(j0, x, &count[x]);
+            uint4 v[kInt8 ? kGroups : 1][kInt8 ? D / 32 : 1];
             if constexpr (kInt8) {
-                fetch(row[0], count[0], v0);
-                fetch(row[1], count[1], v1);
+#pragma unroll
+                for (int x = 0; x < kGroups; ++x) fetch(row[x], count[x], v[x]);
             } else {
                 ok = warp_wait(&empty[it % C::kStages], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 uint8_t *const dst = stages + (it % C::kStages) * C::kTileBytes;
-                copy(dst, row[0], count[0]);
-                copy(dst + 2048, row[1], count[1]);
+#pragma unroll
+                for (int x = 0; x < kGroups; ++x) copy(dst + x * 2048, row[x], count[x]);
                 cp_commit();
             }
 
@@ -887,34 +891,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const uint32_t ph = ((uint32_t)(it / C::kStages) & 1u) ^ 1u;
                 uint8_t *const dst = stages + s * C::kTileBytes;
                 if constexpr (kInt8) {
+                    // scales of tokens 16 x + lane % 16, two groups at a time
                     const int x = lane >> 4, ring = it % C::kRing;
-                    float sc = 0.0f;
-                    if ((lane & 15) < (x ? count[1] : count[0]))
-                        sc = __uint_as_float((uint32_t)scales[(x ? row[1] : row[0]) + (lane & 15)] << 16);
-                    for (int y = 0; y < 2; ++y) row[y] = group(j + 1, y, &count[y]);
+                    float sc[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int64_t r = x ? row[2 * y + 1] : row[2 * y];
+                        sc[y] = 0.0f;
+                        if ((lane & 15) < (x ? count[2 * y + 1] : count[2 * y]))
+                            sc[y] = __uint_as_float((uint32_t)scales[r + (lane & 15)] << 16);
+                    }
+#pragma unroll
+                    for (int y = 0; y < kGroups; ++y) row[y] = group(j + 1, y, &count[y]);
                     ok = warp_wait(&empty[s], ph, &abort_flag, kv.err);
                     if (!ok) break;
                     // K as f16, V as bf16; the next tile's codes are on their way meanwhile
-                    if (is_v) {
-                        store_codes<D, false>(dst, v0, pr, pc, base);
-                        fetch(row[0], count[0], v0);
-                        store_codes<D, false>(dst + 2048, v1, pr, pc, base);
-                        fetch(row[1], count[1], v1);
-                    } else {
-                        store_codes<D, true>(dst, v0, pr, pc, base);
-                        fetch(row[0], count[0], v0);
-                        store_codes<D, true>(dst + 2048, v1, pr, pc, base);
-                        fetch(row[1], count[1], v1);
+#pragma unroll
+                    for (int y = 0; y < kGroups; ++y) {
+                        if (is_v)
+                            store_codes<D, false>(dst + y * 2048, v[y], pr, pc, base);
+                        else
+                            store_codes<D, true>(dst + y * 2048, v[y], pr, pc, base);
+                        fetch(row[y], count[y], v[y]);
                     }
-                    scale_ring[ring * 128 + lane] = sc;
+                    scale_ring[ring * 128 + lane] = sc[0];
+                    scale_ring[ring * 128 + 32 + lane] = sc[1];
                     arrive(full[s]);
                     if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
                 } else if (j > j0) {
-                    for (int y = 0; y < 2; ++y) row[y] = group(j, y, &count[y]);
+#pragma unroll
+                    for (int y = 0; y < kGroups; ++y) row[y] = group(j, y, &count[y]);
                     ok = warp_wait(&empty[s], ph, &abort_flag, kv.err);
                     if (!ok) break;
-                    copy(dst, row[0], count[0]);
-                    copy(dst + 2048, row[1], count[1]);
+#pragma unroll
+                    for (int y = 0; y < kGroups; ++y) copy(dst + y * 2048, row[y], count[y]);
                     cp_commit();
                     cp_wait<0>();
                     arrive(full[s]);
@@ -925,33 +935,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     } else {
         // -------------------------------------------------------------------- MMAs
         regs_down<kMmaRegs>();
-        if (warp == kSoftWarps + kLoadWarps) {
+        const int t = warp - kSoftWarps - kLoadWarps;
+        if (t < 2) {
+            // Tile t's products. An MMA is issued when the one before it has started, so what a warp
+            // does between its MMAs (waiting for weights, commits: 600 cycles a key tile) idles the
+            // tensor cores unless another warp issues meanwhile: a warp a tile, in turns (without
+            // turns the two tiles' products interleave, both end late, both softmax run at once).
+            const uint32_t lead = lane == 0;
             // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
             const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys) - (kInt8 ? (1u << 7) | (1u << 10) : 0u);
             const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
-            // One warp issues everything, PV_t(j) and S_t(j+1) of a tile together, for the tile whose
-            // weights are there first. (In a fixed order of the tiles it waits for one while the other
-            // is ready; a warp a tile interleaves the products, and both tiles' softmax then run
-            // at once and the tensor cores idle meanwhile.)
-            const uint32_t lead = lane == 0;
-            const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ)), dk = sdesc_k_sw128(smem_u32(smem + C::kK));
-            const uint64_t dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
+            const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ) + t * C::kTileBytes);
+            const uint64_t dk = sdesc_k_sw128(smem_u32(smem + C::kK)), dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
             constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
-            uint32_t it = 0, np0 = 0, np1 = 0, nq0 = 0, nq1 = 0;
+            const uint32_t tS = tmem + t * 128, tO = tmem + C::kO + t * D;
+            uint32_t it = 0, np = 0, nq = 0, turns = 0;
             bool ok = true;
             auto commit = [&](uint64_t &bar) { commit_lead(lead, smem_u32(&bar)); };
-            auto ready = [&](uint64_t &bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, mbar_test(&bar, parity & 1u)) != 0;
+            auto wait = [&](uint64_t &bar, uint32_t parity) {
+                ok = ok && warp_wait(&bar, parity & 1u, &abort_flag, kv.err);
             };
-            auto scores = [&](uint32_t t, uint32_t s) {  // S_t = Q_t K^T of the key tile in stage s
-                const uint64_t q = dq + t * kTile16, k = dk + s * kTile16;
-                const uint32_t d = tmem + t * 128;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
-                    mma_ss(lead, d, q + off, k + off, id_s, i > 0);
-                }
-                commit(bars.s_full[t]);
+            auto score = [&](uint32_t s, int i) {  // step i of S = Q K^T of the key tile in stage s
+                const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
+                mma_ss(lead, tS, dq + off, dk + s * kTile16 + off, id_s, i > 0);
             };
             for (int seg = 0; ok; ++seg) {
                 const Segment *const w = segment(seg);
@@ -959,81 +965,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const int n = __shfl_sync(0xffffffffu, w->j1 - w->j0, 0);
                 const int nt = __shfl_sync(0xffffffffu, w->tile * kBlockRows + kTileRows < w->n * G ? 2 : 1, 0);
                 segment_done(seg);
-                ok = warp_wait(&bars.k_full[it % C::kStages], (it / C::kStages) & 1u, &abort_flag, kv.err);
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = warp_wait(&bars.q_full[t], (t ? nq1 : nq0) & 1u, &abort_flag, kv.err);
-                    if (!ok) break;
-                    if (t)
-                        ++nq1;
-                    else
-                        ++nq0;
-                    scores(t, it % C::kStages);
-                    if (n == 1) commit(bars.q_empty[t]);
+                if (t >= nt) {
+                    // nothing to multiply: give the stages back as they fill
+                    for (int j = 0; j < n && ok; ++j, ++it) {
+                        const uint32_t s = it % C::kStages, ph = it / C::kStages;
+                        wait(bars.k_full[s], ph);
+                        if (ok && lead) mbar_arrive(&bars.k_empty[s]);
+                        wait(bars.v_full[s], ph);
+                        if (ok && lead) mbar_arrive(&bars.v_empty[s]);
+                        __syncwarp();
+                    }
+                    continue;
                 }
+                wait(bars.k_full[it % C::kStages], it / C::kStages);
+                wait(bars.q_full[t], nq++);
                 if (!ok) break;
-                commit(bars.k_empty[it % C::kStages]);
-
-                int next0 = 0, next1 = nt == 2 ? 0 : n;  // key tile of the tile's next PV
-                int there = 0;                           // V of key tiles below, K of the next one: seen
-                uint32_t t = 0, polls = 0;
-                uint64_t start = 0;
-#pragma unroll 1
-                while (min(next0, next1) < n) {
-                    if (nt == 2) t ^= 1;
-                    const int j = t ? next1 : next0;
-                    const uint32_t at = it + j, s = at % C::kStages, s1 = (at + 1) % C::kStages;
-                    if (there == j && j < n && ready(bars.v_full[s], at / C::kStages) &&
-                        (j + 1 == n || ready(bars.k_full[s1], (at + 1) / C::kStages)))
-                        there = j + 1;
-                    if (there <= j || !ready(bars.p_full[t], t ? np1 : np0)) {
-                        if ((++polls & 255u) == 0) {
-                            const uint64_t now = global_timer_ns();
-                            if (polls == 256) start = now;
-                            ok = __all_sync(0xffffffffu, !abort_flag && now - start <= kWaitTimeoutNs);
-                            if (!ok) {
-                                if (!abort_flag) atomicOr(kv.err, kErrTimeoutBit);
-                                abort_flag = 1;
-                                break;
-                            }
-                        }
-                        continue;
-                    }
-                    polls = 0;
-                    tc_fence_after_sync();
-                    const bool rest = __any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]) != 0);
-                    const uint64_t v = dv + s * kTile16;
-                    const uint32_t p = tmem + t * 128, o = tmem + C::kO + t * D;
 #pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i) mma_ts(lead, o, p + i * 16, v + i * 128, id_o, (j | i) != 0);
-                    if (rest) {
+                for (int i = 0; i < D / 16; ++i) score(it % C::kStages, i);
+                commit(bars.s_full[t]);
+                commit(bars.k_empty[it % C::kStages]);
+                if (n == 1) commit(bars.q_empty[t]);
 #pragma unroll 1
-                        for (int i = 0; i < kKeys / 16; ++i) mma_ts(lead, o, p + 8 + i * 16, v + i * 128, id_o, 1);
+                for (int j = 0; j < n; ++j, ++it) {
+                    const uint32_t s = it % C::kStages, s1 = (it + 1) % C::kStages;
+                    wait(bars.v_full[s], it / C::kStages);
+                    if (j + 1 < n) wait(bars.k_full[s1], (it + 1) / C::kStages);
+                    wait(bars.p_full[t], np++);
+                    if (nt == 2) wait(bars.turn[t], turns++ ^ (t ^ 1));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < kKeys / 16; ++i)
+                        mma_ts(lead, tO, tS + i * 16, dv + s * kTile16 + i * 128, id_o, (j | i) != 0);
+                    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]) != 0)) {
+#pragma unroll 1
+                        for (int i = 0; i < kKeys / 16; ++i)
+                            mma_ts(lead, tO, tS + 8 + i * 16, dv + s * kTile16 + i * 128, id_o, 1);
                     }
-                    const bool both = (t ? next0 : next1) > j;  // the other tile has done this key tile
                     if (j + 1 < n) {
-                        scores(t, s1);
-                        if (both) commit(bars.k_empty[s1]);
+                        // the turn passes a little early: it takes about as long to arrive
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            if (i == D / 16 - 3 && nt == 2 && lead) mbar_arrive(&bars.turn[t ^ 1]);
+                            score(s1, i);
+                        }
+                        commit(bars.s_full[t]);
+                        commit(bars.k_empty[s1]);
                         if (j + 2 == n) commit(bars.q_empty[t]);
                     } else {
+                        if (nt == 2 && lead) mbar_arrive(&bars.turn[t ^ 1]);
                         commit(bars.o_full[t]);
                     }
-                    if (both) commit(bars.v_empty[s]);
-                    if (t) {
-                        ++next1;
-                        ++np1;
-                    } else {
-                        ++next0;
-                        ++np0;
-                    }
+                    commit(bars.v_empty[s]);
+                    __syncwarp();
                 }
-                it += n;
             }
             // no MMA may be in flight when the tensor memory goes
-            commit(bars.drain);
+            commit(bars.drain[t]);
             int unused = 0;
-            small_wait(&bars.drain, 0, &unused, kv.err);
+            small_wait(&bars.drain[t], 0, &unused, kv.err);
             __syncwarp();
-        } else if (warp == kSoftWarps + kLoadWarps + 1) {
+        } else if (t == 2) {
             // ------------------------------------------- the share, segment by segment
             KvWork<kBlockRows, kKeys> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
             bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
