@@ -30,6 +30,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;            // tokens per warp step: never crosses a page (pages hold 16 k)
 constexpr int kUnit = kWarps * kStep;
+constexpr int kHeadUnits = 3;        // an item's cost beside its units: 64 int8 requests 118 us at 0, 104 at 3, 107 at 6
 constexpr int kMinUnits = 2;         // one request, one token: 12.3 us at 1, 11.2 at 2, 11.6 at 4
 
 // kN: tiles of 8 rows (a row: one query head of one new token) an item holds.
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     const int g = lane >> 2, c = lane & 3;
     const int G = a.G;
 
-    KvWork<R, kUnit> w(kv, b, G, a.window, 0, plan.max_rows, lane);
+    KvWork<R, kUnit, kHeadUnits> w(kv, b, G, a.window, 0, plan.max_rows, lane);
     // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
     // they save
     if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits))) return;
@@ -132,9 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     while (w.next()) {
         const KvSeq &sh = w.sh;
         const int seq = w.seq, tile = w.tile, head = w.head;
-        const int64_t item0 = w.item0, item1 = w.item0 + w.nu, u = w.u, seg_end = w.seg_end;
-        const int tok0 = w.lo + (int)(u - item0) * kUnit;
-        const int tok1 = min(w.hi, w.lo + (int)(seg_end - item0) * kUnit);
+        const int tok0 = w.lo + w.j0 * kUnit, tok1 = min(w.hi, w.lo + w.j1 * kUnit);
         const int rows = min(R, sh.n * G - tile * R);
 
         // ---- this warp's steps: tokens tok0 + 16 (warp + 4 k)
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             }
         __syncthreads();
         const bool whole = w.whole();
-        const int slot = 2 * blockIdx.x + (u == item0 ? 1 : 0);
+        const int slot = 2 * blockIdx.x + (w.first() ? 1 : 0);
         float *part_o = plan.part + (int64_t)slot * R * D;
         float *part_ml = plan.part + (int64_t)2 * gridDim.x * R * D + slot * 2 * R;
         if (threadIdx.x < R) {
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 
         // ---- a piece of an item: the last CTA to arrive joins the pieces
         if (!whole) {
-            const int c0 = w.cta_of(item0), c1 = w.cta_of(item1 - 1);
+            const int c0 = w.first_cta(), c1 = w.last_cta();
             __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {

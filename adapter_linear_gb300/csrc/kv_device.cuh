@@ -67,11 +67,12 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
 // An item is (sequence, tile of R rows, kv head); a row is one query head of one new token: row
 // r of a sequence is token r / G, head r % G of the kv head's G. An item's visible tokens [lo,
 // hi), lo rounded down to 16 (so that 16 tokens from there never cross a page), are cut into
-// units of kUnit tokens, at least one (rows that see nothing still write their zeros). Units are
-// numbered sequence by sequence, tile by tile, head by head; CTA c of `grid` takes units
-// [c total / grid, (c + 1) total / grid). Every member is called by whole warps, which all
+// units of kUnit tokens, at least one (rows that see nothing still write their zeros), behind kHead
+// empty units, which stand for what an item costs beside its tokens. Units are numbered
+// sequence by sequence, tile by tile, head by head; CTA c of `grid` takes units [c total / grid,
+// (c + 1) total / grid). Every member but next() is called by whole warps, which all
 // compute the same. Sequences with n G outside min_rows..max_rows are left out.
-template <int R, int kUnit>
+template <int R, int kUnit, int kHead>
 struct KvWork {
     const KvDev &kv;
     const KvBatchDev &b;
@@ -82,6 +83,7 @@ struct KvWork {
     int64_t item0 = 0;           // the item's first unit
     int64_t tile0 = 0;           // first unit of the tile's first head
     int seq = -1, tile = 0, tiles = 0, nu = 0, head = 0, lo = 0, hi = 0;
+    int j0 = 0, j1 = 0;          // units of tokens: [j0, j1) of the item's nu - kHead
     KvSeq sh{0, 0, 0};
 
     __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, int G_, int window_, int min_rows_,
@@ -130,8 +132,29 @@ struct KvWork {
         }
     }
 
-    // The share's next segment; false at its end.
+    // The share's next segment that has tokens' units; false at its end.
     __device__ __forceinline__ bool next()
+    {
+        do {
+            if (!next_any()) return false;
+            j0 = max(0, (int)(u - item0) - kHead);
+            j1 = (int)(seg_end - item0) - kHead;
+        } while (j1 <= 0);
+        return true;
+    }
+
+    __device__ __forceinline__ bool first() const { return j0 == 0; }
+    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nu - kHead; }
+    // The CTAs that have the item's first and last tokens' units (total >= grid: no share is
+    // empty).
+    __device__ __forceinline__ int first_cta() const { return cta_of(item0 + kHead); }
+    __device__ __forceinline__ int last_cta() const { return cta_of(item0 + nu - 1); }
+
+private:
+    int64_t first_ = 0;  // the units of sequence `lane`
+
+    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * grid - 1) / total); }
+    __device__ __forceinline__ bool next_any()
     {
         u = seg_end;
         if (u >= u_end) return false;
@@ -151,13 +174,6 @@ struct KvWork {
         return true;
     }
 
-    __device__ __forceinline__ bool whole() const { return u == item0 && seg_end == item0 + nu; }
-    // The CTA whose share holds unit x (total >= grid: no share is empty).
-    __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * grid - 1) / total); }
-
-private:
-    int64_t first_ = 0;  // the units of sequence `lane`
-
     __device__ __forceinline__ int tiles_of(const KvSeq &s) const
     {
         const int64_t rows = (int64_t)s.n * G;
@@ -174,7 +190,7 @@ private:
     {
         int l, h;
         range(s, t, &l, &h);
-        return max(1, (h - l + kUnit - 1) / kUnit);
+        return kHead + max(1, (h - l + kUnit - 1) / kUnit);
     }
     // Units of sequence s0 + lane (0 past the last). Few tiles: a lane counts its own; a sequence
     // of many is counted by all lanes together.

@@ -9,7 +9,7 @@
 // A CTA works on 256 rows of one kv head: the G query heads that share it for 256 / G tokens, so
 // K and V are read once for all of them, as two MMA tiles of 128 rows. Warps 0-3 and 4-7 do the
 // softmax of one tile each (a thread holds a row), 8-11 bring K and V tiles into shared memory
-// (8-bit codes become 16-bit operands on the way), warps 12 and 13 issue the MMAs, warp 14
+// (8-bit codes become bf16 on the way), warps 12 and 13 issue the MMAs, warp 14
 // hands out the work:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
@@ -17,10 +17,8 @@
 // tile's products. MMAs of one thread execute in order, so S_t(j+1) overwrites P_t(j) only after
 // PV_t(j) has read it, and the commit behind S_t(j+1) covers PV_t(j).
 //
-// An 8-bit cache: the codes are exact in f16 (S) and in bf16 (O), a key's scale multiplies its
-// column of S and a value's its weight. S takes f16, because codes become f16 in two thirds of the
-// instructions bf16 takes, with Q's rows scaled by powers of two; the weights stay in bf16,
-// whose range a row's smallest weights need.
+// An 8-bit cache's scales stay outside the products: the codes are exact in bf16, a key's scale
+// multiplies its column of S and a value's its weight.
 //
 // A weight rounded to bf16 is off by up to 2^-9 of it or 2^-8 (the mantissa's place), which
 // averages out over many keys but shows where one key holds much of a row's weight. So where a
@@ -47,6 +45,9 @@ constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // two MMA warps, 
 constexpr int kSoftRegs = 152, kLoadRegs = 120, kMmaRegs = 88;
 static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "register split");
 
+// What an item costs beside its key tiles, in key tiles (its first tile's two parts, Q, the output):
+// 8 prompts of 2048 bf16 557 us at 0, 424 at 1, 378 at 2, 381 at 3, 406 at 6.
+constexpr int kHeadUnits = 2;
 constexpr int kSegments = 4;
 constexpr int kOutPitch = 80;  // bytes of a row of 32 bf16 columns: rows start 5 x 16 bytes apart
 
@@ -60,9 +61,8 @@ struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    static constexpr int kScales = kV + kStages * kTileBytes;  // float [2][kRing][128]
-    static constexpr int kRowMul = kScales + 2 * kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
-    static constexpr int kSegs = kRowMul + 2 * kBlockRows * 4;
+    static constexpr int kScales = kV + kStages * kTileBytes;  // float [kRing][2][128]: the keys', the values'
+    static constexpr int kSegs = kScales + kRing * 256 * 4;
     static constexpr int kBars = kSegs + kSegments * 64;
     static constexpr int kOut = kBars + 512;                   // a softmax warp's 32 rows x 32 columns of O
     static constexpr int kSmem = kOut + kSoftWarps * 32 * kOutPitch + 1024;           // and room to align to 1024
@@ -228,29 +228,8 @@ __device__ __forceinline__ void regs_down()
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Has the phase completed? (Does not wait.)
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// mbar_wait that asks again and again instead of suspending the warp (which wakes up 1000 cycles
-// and more after the barrier), with one place that asks: the roles' loops run through several
-// waits a key tile, and their code must stay small.
+// mbar_wait with one place that tries: the roles' loops run through several waits a key tile, and
+// their code must stay small.
 __device__ __forceinline__ bool small_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err)
 {
     uint32_t n = 0;
@@ -276,33 +255,23 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, small_wait(bar, parity, abort_flag, err));
 }
 
-// Which of 16 columns from col0 on a row sees: a bit each.
-__device__ __forceinline__ uint32_t seen16(int lim, int low, int col0)
+// Which of 8 columns from col0 on a row sees: a bit each.
+__device__ __forceinline__ uint32_t seen8(int lim, int low, int col0)
 {
-    const int n = min(max(lim - col0 + 1, 0), 16), skip = min(max(low - col0 + 1, 0), 16);
+    const int n = min(max(lim - col0 + 1, 0), 8), skip = min(max(low - col0 + 1, 0), 8);
     return ((1u << n) - 1u) & ~((1u << skip) - 1u);
 }
 
-// Raw scores (as loaded) of 16 keys of this thread's row times the keys' scales, in pairs; kMask:
-// -inf where the row does not see the key (columns above lim or up to low).
+// Raw scores (as loaded) of 8 keys of this thread's row times the keys' scales, in pairs; kMask:
+// -inf where the row does not see the key (a bit each in `seen`).
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *sc, int lim, int low, int col0,
-                                         uint64_t (&z)[8])
+__device__ __forceinline__ void scores8(const uint32_t (&s)[8], const ulonglong2 (&c)[2], uint32_t seen, uint64_t (&z)[4])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-    if (kInt8) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + col0 + 2 * i);
-            z[i] = mul2(z[i], f.x);
-            z[i + 1] = mul2(z[i + 1], f.y);
-        }
-    }
-    if (kMask) {
-        const uint32_t seen = seen16(lim, low, col0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        if (kInt8) z[i] = mul2(z[i], i & 1 ? c[i >> 1].y : c[i >> 1].x);
+        if (kMask) {
             float a, b;
             unpack2(z[i], &a, &b);
             z[i] = pack2(seen >> (2 * i) & 1u ? a : -INFINITY, seen >> (2 * i + 1) & 1u ? b : -INFINITY);
@@ -310,26 +279,43 @@ __device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *s
     }
 }
 
-// The largest score of the row's 128 keys in units of log2 (mul >= 0: raw score to those).
-template <bool kInt8, bool kMask>
-__device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim, int low, float mul)
+__device__ __forceinline__ void load_scales(const float *sc, ulonglong2 (&c)[2])
 {
-    float top = -INFINITY;
+    c[0] = *reinterpret_cast<const ulonglong2 *>(sc);
+    c[1] = *reinterpret_cast<const ulonglong2 *>(sc + 4);
+}
+
+// The largest score of the row's 128 keys in units of log2 (mul >= 0: raw score to those).
+// (These loops stay rolled: the roles' code together has to fit the instruction cache. Unrolled,
+// an 8-bit cache's softmax and conversions missed it in 38 % of fetches and took twice the time.)
+template <bool kInt8, bool kMask>
+__device__ __forceinline__ float tile_top(uint32_t tS, const float *sc, int lim, int low, float mul)
+{
+    float x[2] = {-INFINITY, -INFINITY};
+    uint32_t s[2][8];
+    ulonglong2 c[2][2];
+    tmem_ld8(tS, s[0]);
+    if (kInt8) load_scales(sc, c[0]);
 #pragma unroll 1
-    for (int ch = 0; ch < 8; ++ch) {
-        uint32_t s[16];
-        uint64_t z[8];
-        tmem_ld16_wait(tS + ch * 16, s);
-        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
-        float x[2] = {-INFINITY, -INFINITY};
+    for (int ch = 0; ch < 16; ch += 2)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float a, b;
-            unpack2(z[i], &a, &b);
-            x[i & 1] = fmaxf(x[i & 1], fmaxf(a, b));
+        for (int b = 0; b < 2; ++b) {
+            tmem_ld_wait8(s[b]);
+            // (the last round asks for columns it does not use)
+            const int next = ch + b + 1 < 16 ? ch + b + 1 : 0;
+            tmem_ld8(tS + next * 8, s[b ^ 1]);
+            if (kInt8) load_scales(sc + next * 8, c[b ^ 1]);
+            uint64_t z[4];
+            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, (ch + b) * 8) : 0u, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float e0, e1;
+                unpack2(z[i], &e0, &e1);
+                x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
+            }
         }
-        top = fmaxf(top, fmaxf(x[0], x[1]));
-    }
+    tmem_ld_wait8(s[0]);
+    const float top = fmaxf(x[0], x[1]);
     return top == -INFINITY ? top : top * mul;
 }
 
@@ -338,105 +324,66 @@ __device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim
 // scores are read by then), and in column 16 i + 8 + e what rounding left of them (kRest) or zeros.
 // Returns the weights' sum.
 template <bool kInt8, bool kMask, bool kRest>
-__device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, const float *vsc, int lim, int low,
-                                              float mul, float m)
+__device__ __forceinline__ float tile_weights(uint32_t tS, const float *sc, int lim, int low, float mul, float m)
 {
     const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
+    uint32_t s[2][8];
+    ulonglong2 c[2][2], v[2][2];
+    tmem_ld8(tS, s[0]);
+    if (kInt8) {
+        load_scales(sc, c[0]);
+        load_scales(sc + 128, v[0]);
+    }
 #pragma unroll 1
     for (int ch = 0; ch < 8; ++ch) {
-        uint32_t s[16], p[8], rest[8];
-        uint64_t z[8];
-        tmem_ld16_wait(tS + ch * 16, s);
-        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
+        uint32_t p[8], rest[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            ulonglong2 f;
-            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 16 + 2 * i);
+        for (int b = 0; b < 2; ++b) {
+            tmem_ld_wait8(s[b]);
+            // (the last round asks for its own columns again)
+            const int next = 2 * ch + b + 1 < 16 ? 2 * ch + b + 1 : 15;
+            tmem_ld8(tS + next * 8, s[b ^ 1]);
+            if (kInt8) {
+                load_scales(sc + next * 8, c[b ^ 1]);
+                load_scales(sc + 128 + next * 8, v[b ^ 1]);
+            }
+            uint64_t z[4];
+            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, ch * 16 + b * 8) : 0u, z);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float a, b, wa, wb;
-                unpack2(fma2(z[i + e], mul_2, neg), &a, &b);
-                a = fast_exp2(a);
-                b = fast_exp2(b);
+            for (int i = 0; i < 4; ++i) {
+                float e0, e1, w0, w1;
+                unpack2(fma2(z[i], mul_2, neg), &e0, &e1);
+                e0 = fast_exp2(e0);
+                e1 = fast_exp2(e1);
                 if (kMask) {
-                    float za, zb;
-                    unpack2(z[i + e], &za, &zb);
-                    a = za == -INFINITY ? 0.0f : a;
-                    b = zb == -INFINITY ? 0.0f : b;
+                    float z0, z1;
+                    unpack2(z[i], &z0, &z1);
+                    e0 = z0 == -INFINITY ? 0.0f : e0;
+                    e1 = z1 == -INFINITY ? 0.0f : e1;
                 }
-                const uint64_t v = pack2(a, b);
-                sum[e] = add2(sum[e], v);
-                wa = a;
-                wb = b;
+                const uint64_t e = pack2(e0, e1);
+                sum[i & 1] = add2(sum[i & 1], e);
+                w0 = e0;
+                w1 = e1;
                 if (kInt8) {
-                    unpack2(mul2(v, e ? f.y : f.x), &wa, &wb);
+                    unpack2(mul2(e, i & 1 ? v[b][i >> 1].y : v[b][i >> 1].x), &w0, &w1);
                     if (kMask) {
-                        wa = a == 0.0f ? 0.0f : wa;
-                        wb = b == 0.0f ? 0.0f : wb;
+                        w0 = e0 == 0.0f ? 0.0f : w0;
+                        w1 = e1 == 0.0f ? 0.0f : w1;
                     }
                 }
-                p[i + e] = pack_bf16x2(wa, wb);
-                rest[i + e] = pack_bf16x2(wa - bf16_lo(p[i + e]), wb - bf16_hi(p[i + e]));
+                p[b * 4 + i] = pack_bf16x2(w0, w1);
+                rest[b * 4 + i] = pack_bf16x2(w0 - bf16_lo(p[b * 4 + i]), w1 - bf16_hi(p[b * 4 + i]));
             }
         }
+        tmem_ld_wait8(s[0]);  // before its columns may be overwritten
         tmem_st8(tS + ch * 16, p);
         if (kRest)
             tmem_st8(tS + ch * 16 + 8, rest);
         else
             tmem_zero8(tS + ch * 16 + 8);
     }
-    float a, b;
-    unpack2(add2(sum[0], sum[1]), &a, &b);
-    return a + b;
-}
-
-// The same (without masks and rests) in one pass over the scores, which stay where they are; the
-// weights in registers, and the largest score less m.
-template <bool kInt8>
-__device__ __forceinline__ float tile_guess(uint32_t tS, const float *ksc, const float *vsc, float mul, float m,
-                                            uint32_t (&p)[64], float *over)
-{
-    const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
-    uint64_t sum[2] = {0, 0};
-    float x[2] = {-INFINITY, -INFINITY};
-    // Shared memory answers slowly while the tensor cores read their operands from it: the scales
-    // are asked for a chunk ahead.
-    uint32_t s[2][8];
-    ulonglong2 k[2][2], v[2];
-    tmem_ld8(tS, s[0]);
-    if (kInt8) {
-        k[0][0] = *reinterpret_cast<const ulonglong2 *>(ksc);
-        k[0][1] = *reinterpret_cast<const ulonglong2 *>(ksc + 4);
-    }
-#pragma unroll
-    for (int ch = 0; ch < 16; ++ch) {
-        const int b = ch & 1;
-        tmem_ld_wait8(s[b]);
-        if (ch < 15) tmem_ld8(tS + (ch + 1) * 8, s[b ^ 1]);
-        if (kInt8) {
-            v[0] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8);
-            v[1] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8 + 4);
-            if (ch < 15) {
-                k[b ^ 1][0] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 8);
-                k[b ^ 1][1] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 12);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t z = pack2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
-            if (kInt8) z = mul2(z, i & 1 ? k[b][i >> 1].y : k[b][i >> 1].x);
-            float e0, e1;
-            unpack2(fma2(z, mul_2, neg), &e0, &e1);
-            x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
-            uint64_t wt = pack2(fast_exp2(e0), fast_exp2(e1));
-            sum[i & 1] = add2(sum[i & 1], wt);
-            if (kInt8) wt = mul2(wt, i & 1 ? v[i >> 1].y : v[i >> 1].x);
-            unpack2(wt, &e0, &e1);
-            p[ch * 4 + i] = pack_bf16x2(e0, e1);
-        }
-    }
-    *over = fmaxf(x[0], x[1]);
     float a, b;
     unpack2(add2(sum[0], sum[1]), &a, &b);
     return a + b;
@@ -457,8 +404,8 @@ __device__ __forceinline__ void lane_piece(int lane, int *r, int *c)
     }
 }
 
-// A lane's pieces of a 16-token group as f16 or bf16 into its tile (dst: the group's first row).
-template <int D, bool kF16>
+// A lane's pieces of a 16-token group as bf16 into its tile (dst: the group's first row).
+template <int D>
 __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 32], int r0, int piece, uint32_t base)
 {
 #pragma unroll
@@ -466,12 +413,7 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 3
         const uint32_t c[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
         uint32_t x[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (kF16)
-                codes4_to_f16(c[e], &x[2 * e], &x[2 * e + 1]);
-            else
-                codes4_to_bf16(c[e], base, &x[2 * e], &x[2 * e + 1]);
-        }
+        for (int e = 0; e < 4; ++e) codes4_to_bf16(c[e], base, &x[2 * e], &x[2 * e + 1]);
         const int r = r0 + p * (512 / D);
         *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * piece)) = make_uint4(x[0], x[1], x[2], x[3]);
         *reinterpret_cast<uint4 *>(dst + tile_off(r, 2 * piece + 1)) = make_uint4(x[4], x[5], x[6], x[7]);
@@ -485,9 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kBars);
-    float *const kscale = reinterpret_cast<float *>(smem + C::kScales);
-    float *const vscale = kscale + C::kRing * 128;
-    float *const row_mul = reinterpret_cast<float *>(smem + C::kRowMul);
+    float *const scale_ring = reinterpret_cast<float *>(smem + C::kScales);
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t rest_flags[2];  // of the tiles' weights: a byte a warp, has it a second part?
     __shared__ volatile int abort_flag;
@@ -567,66 +507,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const int pos = w->L - w->n + i;
             const int tok_lo = w->lo;
             float m = -INFINITY, l = 0.0f;
-            float mul = plan.scale_log2;  // raw score -> units of log2
+            const float mul = plan.scale_log2;  // raw score -> units of log2
             for (int j = j0; j < j1; ++j, ++it, ++ns) {
                 const int tok0 = tok_lo + j * kKeys;
                 const int lim = pos - tok0;
                 const int low = a.window > 0 ? pos - a.window - tok0 : -1;
                 const bool mask = __any_sync(0xffffffffu, lim < kKeys - 1 || low >= 0);
                 const int ring = it % C::kRing;
-                const float *ksc = kscale + ring * 128, *vsc = vscale + ring * 128;
-                if (kInt8) {
+                const float *const sc = scale_ring + ring * 256;
+                if (kInt8)
                     ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
-                    if (j == j0) mul = row_mul[(seg & 1) * kBlockRows + t * kTileRows + row_in_tile];
-                }
                 ok = ok && warp_wait(&bars.s_full[t], (uint32_t)ns & 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 tc_fence_after_sync();
 
-                bool rest = j == j0, done = false;
                 const float mx = m == -INFINITY ? 0.0f : m;
-                if (!rest && !mask) {
-                    // One pass with the m there is: right unless a score passes it by so much that
-                    // the weights near fp32's range, or a key may hold much of a row's weight.
-                    uint32_t p[64];
-                    float over;
-                    const float add = tile_guess<kInt8>(tS, ksc, vsc, mul, mx, p, &over);
-                    rest = __any_sync(0xffffffffu, over > 64.0f || 3.0f * fast_exp2(over) > l);
-                    if (!rest) {
-                        l += add;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            tmem_st8(tS + x * 16, p + x * 8);
-                            tmem_zero8(tS + x * 16 + 8);
-                        }
-                        done = true;
-                    }
-                }
-                if (!done) {
-                    const float top = mask ? tile_top<kInt8, true>(tS, ksc, lim, low, mul)
-                                           : tile_top<kInt8, false>(tS, ksc, lim, low, mul);
-                    rest = rest || __any_sync(0xffffffffu, top - mx > 64.0f || 3.0f * fast_exp2(top - mx) > l);
-                    if (!rest) {
-                        l += tile_weights<kInt8, true, false>(tS, ksc, vsc, lim, low, mul, mx);
-                    } else {
-                        const float m2 = fmaxf(m, top);
-                        const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
-                        m = m2;
-                        l *= down;
-                        if (j > j0) {
+                const float top = mask ? tile_top<kInt8, true>(tS, sc, lim, low, mul)
+                                       : tile_top<kInt8, false>(tS, sc, lim, low, mul);
+                // two parts, and m moved, where a key may hold much of a row's weight
+                const bool rest =
+                    j == j0 || __any_sync(0xffffffffu, top - mx > 64.0f || 3.0f * fast_exp2(top - mx) > l);
+                if (!rest) {
+                    l += mask ? tile_weights<kInt8, true, false>(tS, sc, lim, low, mul, mx)
+                              : tile_weights<kInt8, false, false>(tS, sc, lim, low, mul, mx);
+                } else {
+                    const float m2 = fmaxf(m, top);
+                    const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
+                    m = m2;
+                    l *= down;
+                    if (j > j0) {
 #pragma unroll 1
-                            for (int x = 0; x < D; x += 16) {
-                                uint32_t o[16];
-                                tmem_ld16_wait(tO + x, o);
+                        for (int x = 0; x < D; x += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_wait(tO + x, o);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                                tmem_st16(tO + x, o);
-                            }
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+                            tmem_st16(tO + x, o);
                         }
-                        const float mn = m == -INFINITY ? 0.0f : m;
-                        l += mask ? tile_weights<kInt8, true, true>(tS, ksc, vsc, lim, low, mul, mn)
-                                  : tile_weights<kInt8, false, true>(tS, ksc, vsc, lim, low, mul, mn);
                     }
+                    const float mn = m == -INFINITY ? 0.0f : m;
+                    l += mask ? tile_weights<kInt8, true, true>(tS, sc, lim, low, mul, mn)
+                              : tile_weights<kInt8, false, true>(tS, sc, lim, low, mul, mn);
                 }
                 if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t])[warp & 3] = rest;
                 tmem_st_wait();
@@ -651,13 +572,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             float2 *const part_ml =
                 reinterpret_cast<float2 *>(plan.part + (int64_t)2 * gridDim.x * kBlockRows * D) + warp * 32 + lane;
             uint8_t *const out = smem + C::kOut + warp * 32 * kOutPitch;
-#pragma unroll 1
+            uint16_t *to[4];  // through shared memory (see below): the rows this lane writes a piece of
+            bool to_on[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = y * 8 + (lane >> 2);
+                to[y] = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, (uint64_t)dst, r)) + (lane & 3) * 8;
+                to_on[y] = row - lane + r < rows;
+            }
+#pragma unroll 2
             for (int x = 0; x < D; x += 32) {
                 uint32_t o[32];
                 tmem_ld32_wait(tO + x, o);
                 if (whole) {
-                    // through shared memory: a thread's own 16-byte stores would touch 32 rows at a
-                    // time (6300 cycles a segment), four lanes a row write 64 bytes of each
+                    // a thread's own 16-byte stores would touch 32 rows at a time (6300 cycles a
+                    // segment): four lanes a row write 64 bytes of each
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t v[4];
@@ -669,10 +598,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     __syncwarp();
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const int r = y * 8 + (lane >> 2);
-                        uint16_t *const to = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, (uint64_t)dst, r));
-                        const uint4 v = *reinterpret_cast<const uint4 *>(out + r * kOutPitch + (lane & 3) * 16);
-                        if (row - lane + r < rows) *reinterpret_cast<uint4 *>(to + x + (lane & 3) * 8) = v;
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(out + (y * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
+                        if (to_on[y]) *reinterpret_cast<uint4 *>(to[y] + x) = v;
                     }
                     __syncwarp();
                 } else if (on) {
@@ -750,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         uint64_t *const full = is_v ? bars.v_full : bars.k_full, *const empty = is_v ? bars.v_empty : bars.k_empty;
         const void *const arena = is_v ? kv.v : kv.k;
         const uint16_t *const scales = is_v ? kv.vs : kv.ks;
-        float *const scale_ring = (is_v ? vscale : kscale) + (lw & 1) * 64;
+        float *const scale_part = scale_ring + (is_v ? 128 : 0) + (lw & 1) * 64;
         uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 1) * 8192;
         int it = 0;
         uint32_t nq[2] = {0, 0};
@@ -806,10 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             int64_t row[kGroups];
 #pragma unroll
             for (int x = 0; x < kGroups; ++x) row[x] = group(j0, x, &count[x]);
-            uint4 v[kInt8 ? kGroups : 1][kInt8 ? D / 32 : 1];
+            uint4 v[kInt8 ? 2 : 1][kInt8 ? D / 32 : 1];
             if constexpr (kInt8) {
 #pragma unroll
-                for (int x = 0; x < kGroups; ++x) fetch(row[x], count[x], v[x]);
+                for (int x = 0; x < 2; ++x) fetch(row[x], count[x], v[x]);
             } else {
                 ok = warp_wait(&empty[it % C::kStages], ((uint32_t)(it / C::kStages) & 1u) ^ 1u, &abort_flag, kv.err);
                 if (!ok) break;
@@ -855,30 +783,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             }
             cp_wait<0>();
             for (int t = 0; t < nt; ++t) {
-                if (kInt8 || plan.q_sign) {
-#pragma unroll 2
+                if (plan.q_sign) {
+#pragma unroll 1
                     for (int r = qr; r < kTileRows; r += kRowsQ) {
                         uint4 *const at = reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, qc));
-                        const uint4 v = *at;
-                        uint32_t u[4] = {v.x ^ plan.q_sign, v.y ^ plan.q_sign, v.z ^ plan.q_sign, v.w ^ plan.q_sign};
-                        if (kInt8) {
-                            // to f16, the row scaled by the power of two that puts its largest magnitude
-                            // into [2^14, 2^15): values down to 2^-28 of that keep all their bits
-                            uint32_t top = 0;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
-#pragma unroll
-                            for (int d = kLanesQ / 2; d > 0; d >>= 1)
-                                top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                            const int up = min(14 + 127 - (int)(top >> 7), 126);
-                            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) u[e] = pack_f16x2(bf16_lo(u[e]) * f, bf16_hi(u[e]) * f);
-                            if (qc == 0)
-                                row_mul[(seg & 1) * kBlockRows + t * kTileRows + r] =
-                                    __uint_as_float((uint32_t)(127 - up) << 23) * plan.scale_log2;
-                        }
-                        *at = make_uint4(u[0], u[1], u[2], u[3]);
+                        const uint4 u = *at;
+                        *at = make_uint4(u.x ^ plan.q_sign, u.y ^ plan.q_sign, u.z ^ plan.q_sign, u.w ^ plan.q_sign);
                     }
                 }
                 arrive(bars.q_full[t]);
@@ -901,21 +811,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                         if ((lane & 15) < (x ? count[2 * y + 1] : count[2 * y]))
                             sc[y] = __uint_as_float((uint32_t)scales[r + (lane & 15)] << 16);
                     }
+                    // groups 0 and 1 of this tile are in registers; 2, 3 and the next tile's 0, 1
+                    // are on their way while the two before them are converted
+                    int64_t r0 = row[2], r1 = row[3];
+                    int c0 = count[2], c1 = count[3];
 #pragma unroll
                     for (int y = 0; y < kGroups; ++y) row[y] = group(j + 1, y, &count[y]);
                     ok = warp_wait(&empty[s], ph, &abort_flag, kv.err);
                     if (!ok) break;
-                    // K as f16, V as bf16; the next tile's codes are on their way meanwhile
-#pragma unroll
-                    for (int y = 0; y < kGroups; ++y) {
-                        if (is_v)
-                            store_codes<D, false>(dst + y * 2048, v[y], pr, pc, base);
-                        else
-                            store_codes<D, true>(dst + y * 2048, v[y], pr, pc, base);
-                        fetch(row[y], count[y], v[y]);
+#pragma unroll 1
+                    for (int y = 0; y < 2; ++y) {
+                        store_codes<D>(dst + y * 4096, v[0], pr, pc, base);
+                        fetch(r0, c0, v[0]);
+                        store_codes<D>(dst + y * 4096 + 2048, v[1], pr, pc, base);
+                        fetch(r1, c1, v[1]);
+                        r0 = row[0], r1 = row[1];
+                        c0 = count[0], c1 = count[1];
                     }
-                    scale_ring[ring * 128 + lane] = sc[0];
-                    scale_ring[ring * 128 + 32 + lane] = sc[1];
+                    scale_part[ring * 256 + lane] = sc[0];
+                    scale_part[ring * 256 + 32 + lane] = sc[1];
                     arrive(full[s]);
                     if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
                 } else if (j > j0) {
@@ -942,8 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             // tensor cores unless another warp issues meanwhile: a warp a tile, in turns (without
             // turns the two tiles' products interleave, both end late, both softmax run at once).
             const uint32_t lead = lane == 0;
-            // S of an 8-bit cache has f16 operands: format 0 where bf16 is 1
-            const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys) - (kInt8 ? (1u << 7) | (1u << 10) : 0u);
+            const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys);
             const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
             const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ) + t * C::kTileBytes);
             const uint64_t dk = sdesc_k_sw128(smem_u32(smem + C::kK)), dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
@@ -1027,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             __syncwarp();
         } else if (t == 2) {
             // ------------------------------------------- the share, segment by segment
-            KvWork<kBlockRows, kKeys> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
+            KvWork<kBlockRows, kKeys, kHeadUnits> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
             bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
             for (int seg = 0;; ++seg) {
                 if (!warp_wait(&bars.seg_empty[seg % kSegments], ((uint32_t)(seg / kSegments) & 1u) ^ 1u, &abort_flag,
@@ -1044,12 +957,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     g.head = w.head;
                     g.lo = w.lo;
                     g.hi = w.hi;
-                    g.j0 = (int)(w.u - w.item0);
-                    g.j1 = (int)(w.seg_end - w.item0);
+                    g.j0 = w.j0;
+                    g.j1 = w.j1;
                     g.whole = w.whole();
-                    g.slot = 2 * blockIdx.x + (w.u == w.item0 ? 1 : 0);
-                    g.c0 = w.cta_of(w.item0);
-                    g.c1 = w.cta_of(w.item0 + w.nu - 1);
+                    g.slot = 2 * blockIdx.x + (w.first() ? 1 : 0);
+                    g.c0 = w.first_cta();
+                    g.c1 = w.last_cta();
                 }
                 if (lane == 0) {
                     segs[seg % kSegments] = g;
