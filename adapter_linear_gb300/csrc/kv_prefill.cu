@@ -60,8 +60,8 @@ struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    static constexpr int kScales = kV + kStages * kTileBytes;  // float [2][kRing][128]
-    static constexpr int kRowMul = kScales + 2 * kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
+    static constexpr int kScales = kV + kStages * kTileBytes;  // [kRing][128]: value, key scale of a key (bf16)
+    static constexpr int kRowMul = kScales + kRing * 128 * 4;  // float [2][256]: of Q's rows, by work parity
     static constexpr int kSegs = kRowMul + 2 * kBlockRows * 4;
     static constexpr int kBars = kSegs + kSegments * 64;
     static constexpr int kOut = kBars + 512;                   // a softmax warp's 32 rows x 32 columns of O
@@ -276,33 +276,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, small_wait(bar, parity, abort_flag, err));
 }
 
-// Which of 16 columns from col0 on a row sees: a bit each.
-__device__ __forceinline__ uint32_t seen16(int lim, int low, int col0)
+// Which of 8 columns from col0 on a row sees: a bit each.
+__device__ __forceinline__ uint32_t seen8(int lim, int low, int col0)
 {
-    const int n = min(max(lim - col0 + 1, 0), 16), skip = min(max(low - col0 + 1, 0), 16);
+    const int n = min(max(lim - col0 + 1, 0), 8), skip = min(max(low - col0 + 1, 0), 8);
     return ((1u << n) - 1u) & ~((1u << skip) - 1u);
 }
 
-// Raw scores (as loaded) of 16 keys of this thread's row times the keys' scales, in pairs; kMask:
-// -inf where the row does not see the key (columns above lim or up to low).
+// A key's scales as they lie in the ring: the key's in the upper half, the value's in the lower.
+__device__ __forceinline__ uint64_t key_scales(uint32_t a, uint32_t b) { return pack2(bf16_hi(a), bf16_hi(b)); }
+__device__ __forceinline__ uint64_t value_scales(uint32_t a, uint32_t b) { return pack2(bf16_lo(a), bf16_lo(b)); }
+
+// Raw scores (as loaded) of 8 keys of this thread's row times the keys' scales, in pairs; kMask:
+// -inf where the row does not see the key (a bit each in `seen`).
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *sc, int lim, int low, int col0,
-                                         uint64_t (&z)[8])
+__device__ __forceinline__ void scores8(const uint32_t (&s)[8], const uint32_t (&c)[8], uint32_t seen, uint64_t (&z)[4])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-    if (kInt8) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + col0 + 2 * i);
-            z[i] = mul2(z[i], f.x);
-            z[i + 1] = mul2(z[i + 1], f.y);
-        }
-    }
-    if (kMask) {
-        const uint32_t seen = seen16(lim, low, col0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
+        z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+        if (kInt8) z[i] = mul2(z[i], key_scales(c[2 * i], c[2 * i + 1]));
+        if (kMask) {
             float a, b;
             unpack2(z[i], &a, &b);
             z[i] = pack2(seen >> (2 * i) & 1u ? a : -INFINITY, seen >> (2 * i + 1) & 1u ? b : -INFINITY);
@@ -310,26 +304,41 @@ __device__ __forceinline__ void scores16(const uint32_t (&s)[16], const float *s
     }
 }
 
+__device__ __forceinline__ void load_scales(const uint32_t *sc, uint32_t (&c)[8])
+{
+    const uint4 a = *reinterpret_cast<const uint4 *>(sc), b = *reinterpret_cast<const uint4 *>(sc + 4);
+    c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+    c[4] = b.x, c[5] = b.y, c[6] = b.z, c[7] = b.w;
+}
+
 // The largest score of the row's 128 keys in units of log2 (mul >= 0: raw score to those).
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim, int low, float mul)
+__device__ __forceinline__ float tile_top(uint32_t tS, const uint32_t *sc, int lim, int low, float mul)
 {
-    float top = -INFINITY;
+    float x[2] = {-INFINITY, -INFINITY};
+    uint32_t s[2][8], c[2][8];
+    tmem_ld8(tS, s[0]);
+    if (kInt8) load_scales(sc, c[0]);
 #pragma unroll 1
-    for (int ch = 0; ch < 8; ++ch) {
-        uint32_t s[16];
-        uint64_t z[8];
-        tmem_ld16_wait(tS + ch * 16, s);
-        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
-        float x[2] = {-INFINITY, -INFINITY};
+    for (int ch = 0; ch < 16; ch += 2)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float a, b;
-            unpack2(z[i], &a, &b);
-            x[i & 1] = fmaxf(x[i & 1], fmaxf(a, b));
+        for (int b = 0; b < 2; ++b) {
+            tmem_ld_wait8(s[b]);
+            // (the last round asks for columns past the tile's, which it does not use)
+            const int next = ch + b + 1 < 16 ? ch + b + 1 : 0;
+            tmem_ld8(tS + next * 8, s[b ^ 1]);
+            if (kInt8) load_scales(sc + next * 8, c[b ^ 1]);
+            uint64_t z[4];
+            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, (ch + b) * 8) : 0u, z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float e0, e1;
+                unpack2(z[i], &e0, &e1);
+                x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
+            }
         }
-        top = fmaxf(top, fmaxf(x[0], x[1]));
-    }
+    tmem_ld_wait8(s[0]);
+    const float top = fmaxf(x[0], x[1]);
     return top == -INFINITY ? top : top * mul;
 }
 
@@ -338,48 +347,54 @@ __device__ __forceinline__ float tile_top(uint32_t tS, const float *ksc, int lim
 // scores are read by then), and in column 16 i + 8 + e what rounding left of them (kRest) or zeros.
 // Returns the weights' sum.
 template <bool kInt8, bool kMask, bool kRest>
-__device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, const float *vsc, int lim, int low,
-                                              float mul, float m)
+__device__ __forceinline__ float tile_weights(uint32_t tS, const uint32_t *sc, int lim, int low, float mul, float m)
 {
     const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
+    uint32_t s[2][8], c[2][8];
+    tmem_ld8(tS, s[0]);
+    if (kInt8) load_scales(sc, c[0]);
 #pragma unroll 1
     for (int ch = 0; ch < 8; ++ch) {
-        uint32_t s[16], p[8], rest[8];
-        uint64_t z[8];
-        tmem_ld16_wait(tS + ch * 16, s);
-        scores16<kInt8, kMask>(s, ksc, lim, low, ch * 16, z);
+        uint32_t p[8], rest[8];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            ulonglong2 f;
-            if (kInt8) f = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 16 + 2 * i);
+        for (int b = 0; b < 2; ++b) {
+            tmem_ld_wait8(s[b]);
+            const int next = 2 * ch + b + 1 < 16 ? 2 * ch + b + 1 : 15;
+            tmem_ld8(tS + next * 8, s[b ^ 1]);
+            if (kInt8) load_scales(sc + next * 8, c[b ^ 1]);
+            uint64_t z[4];
+            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, ch * 16 + b * 8) : 0u, z);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float a, b, wa, wb;
-                unpack2(fma2(z[i + e], mul_2, neg), &a, &b);
-                a = fast_exp2(a);
-                b = fast_exp2(b);
+            for (int i = 0; i < 4; ++i) {
+                float e0, e1, w0, w1;
+                unpack2(fma2(z[i], mul_2, neg), &e0, &e1);
+                e0 = fast_exp2(e0);
+                e1 = fast_exp2(e1);
                 if (kMask) {
-                    float za, zb;
-                    unpack2(z[i + e], &za, &zb);
-                    a = za == -INFINITY ? 0.0f : a;
-                    b = zb == -INFINITY ? 0.0f : b;
+                    float z0, z1;
+                    unpack2(z[i], &z0, &z1);
+                    e0 = z0 == -INFINITY ? 0.0f : e0;
+                    e1 = z1 == -INFINITY ? 0.0f : e1;
                 }
-                const uint64_t v = pack2(a, b);
-                sum[e] = add2(sum[e], v);
-                wa = a;
-                wb = b;
+                const uint64_t v = pack2(e0, e1);
+                sum[i & 1] = add2(sum[i & 1], v);
+                w0 = e0;
+                w1 = e1;
                 if (kInt8) {
-                    unpack2(mul2(v, e ? f.y : f.x), &wa, &wb);
+                    unpack2(mul2(v, value_scales(c[b][2 * i], c[b][2 * i + 1])), &w0, &w1);
                     if (kMask) {
-                        wa = a == 0.0f ? 0.0f : wa;
-                        wb = b == 0.0f ? 0.0f : wb;
+                        w0 = e0 == 0.0f ? 0.0f : w0;
+                        w1 = e1 == 0.0f ? 0.0f : w1;
                     }
                 }
-                p[i + e] = pack_bf16x2(wa, wb);
-                rest[i + e] = pack_bf16x2(wa - bf16_lo(p[i + e]), wb - bf16_hi(p[i + e]));
+                p[b * 4 + i] = pack_bf16x2(w0, w1);
+                rest[b * 4 + i] = pack_bf16x2(w0 - bf16_lo(p[b * 4 + i]), w1 - bf16_hi(p[b * 4 + i]));
             }
         }
+        // the next 8 scores are on their way: they must have arrived before columns are overwritten
+        // that they may come from only in the last round, which asks for its own again
+        tmem_ld_wait8(s[0]);
         tmem_st8(tS + ch * 16, p);
         if (kRest)
             tmem_st8(tS + ch * 16 + 8, rest);
@@ -394,44 +409,36 @@ __device__ __forceinline__ float tile_weights(uint32_t tS, const float *ksc, con
 // The same (without masks and rests) in one pass over the scores, which stay where they are; the
 // weights in registers, and the largest score less m.
 template <bool kInt8>
-__device__ __forceinline__ float tile_guess(uint32_t tS, const float *ksc, const float *vsc, float mul, float m,
-                                            uint32_t (&p)[64], float *over)
+__device__ __forceinline__ float tile_guess(uint32_t tS, const uint32_t *sc, float mul, float m, uint32_t (&p)[64],
+                                            float *over)
 {
     const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
     float x[2] = {-INFINITY, -INFINITY};
     // Shared memory answers slowly while the tensor cores read their operands from it: the scales
-    // are asked for a chunk ahead.
-    uint32_t s[2][8];
-    ulonglong2 k[2][2], v[2];
+    // are asked for two chunks ahead.
+    uint32_t s[2][8], c[3][8];
     tmem_ld8(tS, s[0]);
     if (kInt8) {
-        k[0][0] = *reinterpret_cast<const ulonglong2 *>(ksc);
-        k[0][1] = *reinterpret_cast<const ulonglong2 *>(ksc + 4);
+        load_scales(sc, c[0]);
+        load_scales(sc + 8, c[1]);
     }
 #pragma unroll
     for (int ch = 0; ch < 16; ++ch) {
         const int b = ch & 1;
         tmem_ld_wait8(s[b]);
         if (ch < 15) tmem_ld8(tS + (ch + 1) * 8, s[b ^ 1]);
-        if (kInt8) {
-            v[0] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8);
-            v[1] = *reinterpret_cast<const ulonglong2 *>(vsc + ch * 8 + 4);
-            if (ch < 15) {
-                k[b ^ 1][0] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 8);
-                k[b ^ 1][1] = *reinterpret_cast<const ulonglong2 *>(ksc + ch * 8 + 12);
-            }
-        }
+        if (kInt8 && ch < 14) load_scales(sc + (ch + 2) * 8, c[(ch + 2) % 3]);
+        uint64_t z[4];
+        scores8<kInt8, false>(s[b], c[ch % 3], 0u, z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint64_t z = pack2(__uint_as_float(s[b][2 * i]), __uint_as_float(s[b][2 * i + 1]));
-            if (kInt8) z = mul2(z, i & 1 ? k[b][i >> 1].y : k[b][i >> 1].x);
             float e0, e1;
-            unpack2(fma2(z, mul_2, neg), &e0, &e1);
+            unpack2(fma2(z[i], mul_2, neg), &e0, &e1);
             x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
             uint64_t wt = pack2(fast_exp2(e0), fast_exp2(e1));
             sum[i & 1] = add2(sum[i & 1], wt);
-            if (kInt8) wt = mul2(wt, i & 1 ? v[i >> 1].y : v[i >> 1].x);
+            if (kInt8) wt = mul2(wt, value_scales(c[ch % 3][2 * i], c[ch % 3][2 * i + 1]));
             unpack2(wt, &e0, &e1);
             p[ch * 4 + i] = pack_bf16x2(e0, e1);
         }
@@ -485,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kBars);
-    float *const kscale = reinterpret_cast<float *>(smem + C::kScales);
-    float *const vscale = kscale + C::kRing * 128;
+    uint32_t *const scale_ring = reinterpret_cast<uint32_t *>(smem + C::kScales);
     float *const row_mul = reinterpret_cast<float *>(smem + C::kRowMul);
     __shared__ uint32_t tmem_slot;
     __shared__ uint32_t rest_flags[2];  // of the tiles' weights: a byte a warp, has it a second part?
@@ -574,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const int low = a.window > 0 ? pos - a.window - tok0 : -1;
                 const bool mask = __any_sync(0xffffffffu, lim < kKeys - 1 || low >= 0);
                 const int ring = it % C::kRing;
-                const float *ksc = kscale + ring * 128, *vsc = vscale + ring * 128;
+                const uint32_t *const sc = scale_ring + ring * 128;
                 if (kInt8) {
                     ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
                     if (j == j0) mul = row_mul[(seg & 1) * kBlockRows + t * kTileRows + row_in_tile];
@@ -590,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     // the weights near fp32's range, or a key may hold much of a row's weight.
                     uint32_t p[64];
                     float over;
-                    const float add = tile_guess<kInt8>(tS, ksc, vsc, mul, mx, p, &over);
+                    const float add = tile_guess<kInt8>(tS, sc, mul, mx, p, &over);
                     rest = __any_sync(0xffffffffu, over > 64.0f || 3.0f * fast_exp2(over) > l);
                     if (!rest) {
                         l += add;
@@ -603,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     }
                 }
                 if (!done) {
-                    const float top = mask ? tile_top<kInt8, true>(tS, ksc, lim, low, mul)
-                                           : tile_top<kInt8, false>(tS, ksc, lim, low, mul);
+                    const float top = mask ? tile_top<kInt8, true>(tS, sc, lim, low, mul)
+                                           : tile_top<kInt8, false>(tS, sc, lim, low, mul);
                     rest = rest || __any_sync(0xffffffffu, top - mx > 64.0f || 3.0f * fast_exp2(top - mx) > l);
                     if (!rest) {
-                        l += tile_weights<kInt8, true, false>(tS, ksc, vsc, lim, low, mul, mx);
+                        l += tile_weights<kInt8, true, false>(tS, sc, lim, low, mul, mx);
                     } else {
                         const float m2 = fmaxf(m, top);
                         const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
@@ -624,8 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                             }
                         }
                         const float mn = m == -INFINITY ? 0.0f : m;
-                        l += mask ? tile_weights<kInt8, true, true>(tS, ksc, vsc, lim, low, mul, mn)
-                                  : tile_weights<kInt8, false, true>(tS, ksc, vsc, lim, low, mul, mn);
+                        l += mask ? tile_weights<kInt8, true, true>(tS, sc, lim, low, mul, mn)
+                                  : tile_weights<kInt8, false, true>(tS, sc, lim, low, mul, mn);
                     }
                 }
                 if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t])[warp & 3] = rest;
@@ -651,13 +657,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             float2 *const part_ml =
                 reinterpret_cast<float2 *>(plan.part + (int64_t)2 * gridDim.x * kBlockRows * D) + warp * 32 + lane;
             uint8_t *const out = smem + C::kOut + warp * 32 * kOutPitch;
-#pragma unroll 1
+            uint16_t *to[4];  // through shared memory (see below): the rows this lane writes a piece of
+            bool to_on[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int r = y * 8 + (lane >> 2);
+                to[y] = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, (uint64_t)dst, r)) + (lane & 3) * 8;
+                to_on[y] = row - lane + r < rows;
+            }
+#pragma unroll 2
             for (int x = 0; x < D; x += 32) {
                 uint32_t o[32];
                 tmem_ld32_wait(tO + x, o);
                 if (whole) {
-                    // through shared memory: a thread's own 16-byte stores would touch 32 rows at a
-                    // time (6300 cycles a segment), four lanes a row write 64 bytes of each
+                    // a thread's own 16-byte stores would touch 32 rows at a time (6300 cycles a
+                    // segment): four lanes a row write 64 bytes of each
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         uint32_t v[4];
@@ -669,10 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     __syncwarp();
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const int r = y * 8 + (lane >> 2);
-                        uint16_t *const to = reinterpret_cast<uint16_t *>(__shfl_sync(0xffffffffu, (uint64_t)dst, r));
-                        const uint4 v = *reinterpret_cast<const uint4 *>(out + r * kOutPitch + (lane & 3) * 16);
-                        if (row - lane + r < rows) *reinterpret_cast<uint4 *>(to + x + (lane & 3) * 8) = v;
+                        const uint4 v =
+                            *reinterpret_cast<const uint4 *>(out + (y * 8 + (lane >> 2)) * kOutPitch + (lane & 3) * 16);
+                        if (to_on[y]) *reinterpret_cast<uint4 *>(to[y] + x) = v;
                     }
                     __syncwarp();
                 } else if (on) {
@@ -750,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         uint64_t *const full = is_v ? bars.v_full : bars.k_full, *const empty = is_v ? bars.v_empty : bars.k_empty;
         const void *const arena = is_v ? kv.v : kv.k;
         const uint16_t *const scales = is_v ? kv.vs : kv.ks;
-        float *const scale_ring = (is_v ? vscale : kscale) + (lw & 1) * 64;
+        uint16_t *const scale_half = reinterpret_cast<uint16_t *>(scale_ring + (lw & 1) * 64) + (is_v ? 0 : 1);
         uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 1) * 8192;
         int it = 0;
         uint32_t nq[2] = {0, 0};
@@ -893,13 +906,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 if constexpr (kInt8) {
                     // scales of tokens 16 x + lane % 16, two groups at a time
                     const int x = lane >> 4, ring = it % C::kRing;
-                    float sc[2];
+                    uint16_t sc[2];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const int64_t r = x ? row[2 * y + 1] : row[2 * y];
-                        sc[y] = 0.0f;
-                        if ((lane & 15) < (x ? count[2 * y + 1] : count[2 * y]))
-                            sc[y] = __uint_as_float((uint32_t)scales[r + (lane & 15)] << 16);
+                        sc[y] = 0;
+                        if ((lane & 15) < (x ? count[2 * y + 1] : count[2 * y])) sc[y] = scales[r + (lane & 15)];
                     }
 #pragma unroll
                     for (int y = 0; y < kGroups; ++y) row[y] = group(j + 1, y, &count[y]);
@@ -914,8 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                             store_codes<D, true>(dst + y * 2048, v[y], pr, pc, base);
                         fetch(row[y], count[y], v[y]);
                     }
-                    scale_ring[ring * 128 + lane] = sc[0];
-                    scale_ring[ring * 128 + 32 + lane] = sc[1];
+                    scale_half[2 * (ring * 128 + lane)] = sc[0];
+                    scale_half[2 * (ring * 128 + 32 + lane)] = sc[1];
                     arrive(full[s]);
                     if (lane == 0) mbar_arrive(&bars.sc_full[ring]);
                 } else if (j > j0) {
