@@ -13,73 +13,90 @@ namespace {
 
 // ------------------------------------------------------------------- kernels
 //
-// A row (one token, one head, K or V) is D values; D / 8 lanes hold it, 8 values (16 bytes) a
-// lane, so a warp holds 32 / (D / 8) rows. A token has 2 H rows (K's heads, then V's); warp w
-// takes token w / C, rows (w % C) * (rows per warp) and on, C = chunks of a token.
+// A row is one token, one head, K or V: D values. A token has 2 H rows, K's heads, then V's. A
+// warp takes a run of consecutive tokens (1 to kRun) and kRows neighbouring rows of each; a lane
+// holds 16 values of a row of an 8-bit cache (32 bytes of bf16, 16 of codes) or 8 of a bf16 one.
+//
+// HBM bounds both at thousands of tokens (write: 2 D bytes read and D + 2 written a row of an 8-bit
+// cache, read the reverse), the chain of dependent loads (sequence, length, page) at a few.
+// So a run is looked up once, a lane a token, and then copied four tokens at a time, loads
+// ahead of stores; few tokens get runs of one, so that as many warps as possible share them.
+constexpr int kRun = 16;
+constexpr int kBatch = 4;  // tokens loaded before any is stored
 
-template <int D>
+template <int D, bool kInt8>
 struct RowMap {
-    static constexpr int kLanes = D / 8;           // lanes per row
-    static constexpr int kRows = 32 / kLanes;      // rows per warp
+    static constexpr int kValues = kInt8 ? 16 : 8;   // of a lane
+    static constexpr int kLanes = D / kValues;       // of a row
+    static constexpr int kRows = 32 / kLanes;        // of a warp
+    static constexpr int kVec = kValues / 8;         // 16-byte vectors of bf16 a lane
 };
 
 __device__ __forceinline__ float bf16_bits_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
-// scale and 8 codes of this lane's 8 values; the row's kLanes lanes take part.
+// scale and 16 codes of this lane's 16 values; the row's kLanes lanes take part.
 //   s = max(bf16(amax / 127), 2^-126), code = clamp(rint(x / s), -127, 127)
 // x and s have 8 significant bits, so x / s is a tie or at least 2^-11 away from one:
 // the fp32 division decides every code as exact arithmetic would.
 template <int kLanes>
-__device__ __forceinline__ uint2 quantise8(const uint4 &x, uint16_t *scale_bits)
+__device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint16_t *scale_bits)
 {
-    const float f[8] = {bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y),
-                        bf16_lo(x.z), bf16_hi(x.z), bf16_lo(x.w), bf16_hi(x.w)};
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     // the largest magnitude as an integer: the bits of |x| order like their values, and an
     // infinity or a NaN (exponent all ones) is larger than every finite value
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool finite = top < 0x7F800000u;
-    const uint32_t sb = pack_bf16x2(__fdiv_rn(__uint_as_float(top), 127.0f), 0.0f) & 0xFFFFu;
+    const bool finite = top < 0x7F80u;
+    const uint32_t sb = pack_bf16x2(__fdiv_rn(__uint_as_float(top << 16), 127.0f), 0.0f) & 0xFFFFu;
     const float s = fmaxf(__uint_as_float(sb << 16), 1.17549435e-38f);  // 2^-126
     *scale_bits = finite ? (uint16_t)(__float_as_uint(s) >> 16) : (uint16_t)0x7FC0;
-    uint32_t w[2] = {0u, 0u};
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(rintf(__fdiv_rn(f[i], s)), -127.0f), 127.0f);
-        const int c = finite ? (int)q : 0;
-        w[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+    for (int q = 0; q < 4; ++q) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t b = w[2 * q + (e >> 1)];
+            const float f = (e & 1) ? bf16_hi(b) : bf16_lo(b);
+            const int code = (int)fminf(fmaxf(rintf(__fdiv_rn(f, s)), -127.0f), 127.0f);
+            v |= (uint32_t)((finite ? code : 0) & 0xFF) << (8 * e);
+        }
+        c[q] = v;
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
 // bf16(scale * code) of 8 codes: the product of a 7-bit code and an 8-bit scale is exact in
 // fp32, so it is rounded once.
-__device__ __forceinline__ uint4 dequantise8(uint2 c, uint16_t scale_bits)
+__device__ __forceinline__ uint4 dequantise8(uint32_t c0, uint32_t c1, float s)
 {
-    const float s = bf16_bits_f(scale_bits);
     uint32_t o[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t w = p < 2 ? c.x : c.y;
+        const uint32_t w = p < 2 ? c0 : c1;
         const int lo = (int)(int8_t)(w >> (16 * (p & 1))), hi = (int)(int8_t)(w >> (16 * (p & 1) + 8));
         o[p] = pack_bf16x2(s * (float)lo, s * (float)hi);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Where the token of row t of the call lies: its cache row for head 0; -1: a position below
-// zero; -2: nowhere (padding after the last sequence, a bad table entry or length).
-__device__ __forceinline__ int64_t token_row(const KvDev &kv, const KvBatchDev &b, int t, int lane)
+// Where the tokens of rows t0 + lane, lane < run, lie: the cache row for head 0; -1: a position
+// below zero; -2: nowhere (padding after the last sequence, a bad table entry or length).
+__device__ __forceinline__ int64_t run_rows(const KvDev &kv, const KvBatchDev &b, int t0, int run, int lane)
 {
-    const int seq = kv_find_seq(b, t, lane);
-    if (seq < 0) return -2;
-    const KvSeq s = kv_seq(b, kv.page_shift, seq, kv.err);
-    const int i = t - s.row0;
-    if (i >= s.n) return -2;
-    const int pos = s.L - s.n + i;
+    int seq = kv_find_seq(b, t0, lane);
+    const int t = t0 + lane;
+    if (seq < 0 || lane >= run) return -2;
+    KvSeq s = kv_seq(b, kv.page_shift, seq, kv.err);
+    while (t - s.row0 >= s.n) {  // a run may end in a later sequence
+        if (++seq >= b.n_seqs) return -2;
+        s = kv_seq(b, kv.page_shift, seq, kv.err);
+        if (t < s.row0) return -2;
+    }
+    const int pos = s.L - s.n + (t - s.row0);
     if (pos < 0) return -1;
     const int64_t row = kv_row(kv, b, seq, pos);
     return row < 0 ? -2 : row;
@@ -88,34 +105,50 @@ __device__ __forceinline__ int64_t token_row(const KvDev &kv, const KvBatchDev &
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(256) kv_write_kernel(KvDev kv, KvBatchDev b, const uint16_t *__restrict__ K,
                                                        int64_t k_stride, const uint16_t *__restrict__ V,
-                                                       int64_t v_stride)
+                                                       int64_t v_stride, int run_len)
 {
-    using M = RowMap<D>;
+    using M = RowMap<D, kInt8>;
     const int lane = threadIdx.x & 31;
     const int C = (2 * kv.H + M::kRows - 1) / M::kRows;
-    const int64_t items = (int64_t)b.T * C;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < items; w += warps) {
-        const int t = (int)(w / C);
-        const int r = (int)(w % C) * M::kRows + lane / M::kLanes;
-        const int d = (lane % M::kLanes) * 8;
-        const bool on = r < 2 * kv.H;
-        const bool is_v = r >= kv.H;
-        const int h = is_v ? r - kv.H : r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (on) x = ldg_nc_v4((is_v ? V + t * v_stride : K + t * k_stride) + h * D + d);
-        const int64_t row0 = token_row(kv, b, t, lane);
-        if (row0 < 0) continue;
-        const int64_t row = row0 + ((int64_t)h << kv.page_shift);
-        if (kInt8) {
-            uint16_t s;
-            const uint2 c = quantise8<M::kLanes>(x, &s);
-            if (on) {
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(is_v ? kv.v : kv.k) + row * D + d) = c;
-                if (d == 0) (is_v ? kv.vs : kv.ks)[row] = s;
+    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t0_ = w / C * run_len;
+    if (t0_ >= b.T) return;
+    const int t0 = (int)t0_, run = min(run_len, b.T - t0);
+    const int r = (int)(w % C) * M::kRows + lane / M::kLanes;
+    const int d = (lane % M::kLanes) * M::kValues;
+    const bool on = r < 2 * kv.H, is_v = r >= kv.H;
+    const int h = on ? (is_v ? r - kv.H : r) : 0;
+    const int64_t stride = is_v ? v_stride : k_stride;
+    const uint16_t *src = (is_v ? V : K) + (int64_t)t0 * stride + h * D + d;
+    const int64_t head = (int64_t)h << kv.page_shift;
+    uint4 x[kBatch][M::kVec];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int v = 0; v < M::kVec; ++v) {
+                x[i][v] = make_uint4(0, 0, 0, 0);
+                if (i0 + i < run && on) x[i][v] = ldg_nc_v4(src + (i0 + i) * stride + v * 8);
             }
-        } else if (on) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_v ? kv.v : kv.k) + row * D + d) = x;
+    };
+    load(0);  // on their way while the run is looked up
+    const int64_t rows = run_rows(kv, b, t0, run, lane);
+    for (int i0 = 0; i0 < run; i0 += kBatch) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t row = __shfl_sync(0xffffffffu, rows, min(i0 + i, 31)) + head;
+            const bool there = i0 + i < run && row >= head && on;
+            if constexpr (kInt8) {
+                uint16_t s;
+                const uint4 c = quantise16<M::kLanes>(x[i], &s);
+                if (there) {
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(is_v ? kv.v : kv.k) + row * D + d) = c;
+                    if (d == 0) (is_v ? kv.vs : kv.ks)[row] = s;
+                }
+            } else if (there) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(is_v ? kv.v : kv.k) + row * D + d) = x[i][0];
+            }
         }
     }
 }
@@ -123,41 +156,69 @@ __global__ void __launch_bounds__(256) kv_write_kernel(KvDev kv, KvBatchDev b, c
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(256) kv_read_kernel(KvDev kv, KvBatchDev b, uint16_t *__restrict__ K,
                                                       int64_t k_stride, uint16_t *__restrict__ V,
-                                                      int64_t v_stride)
+                                                      int64_t v_stride, int run_len)
 {
-    using M = RowMap<D>;
+    using M = RowMap<D, kInt8>;
     const int lane = threadIdx.x & 31;
     const int C = (2 * kv.H + M::kRows - 1) / M::kRows;
-    const int64_t items = (int64_t)b.T * C;
-    const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-    for (int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < items; w += warps) {
-        const int t = (int)(w / C);
-        const int r = (int)(w % C) * M::kRows + lane / M::kLanes;
-        const int d = (lane % M::kLanes) * 8;
-        const bool is_v = r >= kv.H;
-        const int h = is_v ? r - kv.H : r;
-        const int64_t row0 = token_row(kv, b, t, lane);
-        if (row0 == -2 || r >= 2 * kv.H) continue;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (row0 >= 0) {
-            const int64_t row = row0 + ((int64_t)h << kv.page_shift);
-            if (kInt8)
-                x = dequantise8(*reinterpret_cast<const uint2 *>(
-                                    static_cast<const uint8_t *>(is_v ? kv.v : kv.k) + row * D + d),
-                                (is_v ? kv.vs : kv.ks)[row]);
-            else
-                x = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(is_v ? kv.v : kv.k) +
-                                                     row * D + d);
+    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t0_ = w / C * run_len;
+    if (t0_ >= b.T) return;
+    const int t0 = (int)t0_, run = min(run_len, b.T - t0);
+    const int r = (int)(w % C) * M::kRows + lane / M::kLanes;
+    const int d = (lane % M::kLanes) * M::kValues;
+    const bool on = r < 2 * kv.H, is_v = r >= kv.H;
+    const int h = on ? (is_v ? r - kv.H : r) : 0;
+    const int64_t stride = is_v ? v_stride : k_stride;
+    uint16_t *dst = (is_v ? V : K) + (int64_t)t0 * stride + h * D + d;
+    const int64_t head = (int64_t)h << kv.page_shift;
+    const int64_t rows = run_rows(kv, b, t0, run, lane);
+    for (int i0 = 0; i0 < run; i0 += kBatch) {
+        uint4 x[kBatch];
+        uint16_t s[kBatch];
+        int64_t row[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            row[i] = __shfl_sync(0xffffffffu, rows, min(i0 + i, 31));
+            if (i0 + i >= run || !on) row[i] = -2;
+            x[i] = make_uint4(0, 0, 0, 0);
+            s[i] = 0;
+            if (row[i] >= 0) {
+                const int64_t at = row[i] + head;
+                x[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(is_v ? kv.v : kv.k) +
+                                                        (at * D + d) * (kInt8 ? 1 : 2));
+                if (kInt8) s[i] = (is_v ? kv.vs : kv.ks)[at];
+            }
         }
-        *reinterpret_cast<uint4 *>((is_v ? V + t * v_stride : K + t * k_stride) + h * D + d) = x;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (row[i] == -2) continue;
+            uint16_t *const to = dst + (i0 + i) * stride;
+            if constexpr (kInt8) {
+                const float f = bf16_bits_f(s[i]);
+                *reinterpret_cast<uint4 *>(to) = dequantise8(x[i].x, x[i].y, f);
+                *reinterpret_cast<uint4 *>(to + 8) = dequantise8(x[i].z, x[i].w, f);
+            } else {
+                *reinterpret_cast<uint4 *>(to) = x[i];
+            }
+        }
     }
 }
 
-int row_grid(const KvDev &kv, int T, int num_sms)
+// Run length and blocks (8 warps): runs of 1 until four warps a scheduler have one each, then
+// longer ones.
+struct RowGrid {
+    int run;
+    unsigned blocks;
+};
+RowGrid row_grid(const KvDev &kv, bool int8, int T, int num_sms)
 {
-    const int rows = 32 / (kv.D / 8);
-    const int64_t items = (int64_t)T * ((2 * kv.H + rows - 1) / rows);
-    return (int)std::min<int64_t>((items + 7) / 8, (int64_t)num_sms * 8);
+    const int rows = 32 / (kv.D / (int8 ? 16 : 8));
+    const int64_t C = (2 * kv.H + rows - 1) / rows;
+    RowGrid g;
+    g.run = (int)std::min<int64_t>(kRun, std::max<int64_t>(1, T * C / (16 * (int64_t)num_sms)));
+    g.blocks = (unsigned)(((T + g.run - 1) / g.run * C + 7) / 8);
+    return g;
 }
 
 // The error word read and cleared in one atomic step: [1] receives its value.
@@ -174,7 +235,8 @@ cudaError_t launch_kv_write(const KvDev &kv, bool int8, const KvBatchDev &b, con
                           : (int8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>);
     const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
     if (e != cudaSuccess) return e;
-    fn<<<row_grid(kv, b.T, num_sms), 256, 0, stream>>>(kv, b, K, k_stride, V, v_stride);
+    const RowGrid g = row_grid(kv, int8, b.T, num_sms);
+    fn<<<g.blocks, 256, 0, stream>>>(kv, b, K, k_stride, V, v_stride, g.run);
     return cudaGetLastError();
 }
 
@@ -185,7 +247,8 @@ cudaError_t launch_kv_read(const KvDev &kv, bool int8, const KvBatchDev &b, uint
                           : (int8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>);
     const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
     if (e != cudaSuccess) return e;
-    fn<<<row_grid(kv, b.T, num_sms), 256, 0, stream>>>(kv, b, K, k_stride, V, v_stride);
+    const RowGrid g = row_grid(kv, int8, b.T, num_sms);
+    fn<<<g.blocks, 256, 0, stream>>>(kv, b, K, k_stride, V, v_stride, g.run);
     return cudaGetLastError();
 }
 
@@ -260,23 +323,52 @@ lora_status ensure_pre_part(lora_kv *p)
     return LORA_OK;
 }
 
-// Calls inside a graph capture are not tracked: the order of replays is the caller's.
-lora_status is_tracked(cudaStream_t stream, bool *tracked)
+// After a call on `stream`: an event of that stream, for the error-word read and for attention
+// calls on other streams. Calls inside a graph capture are not tracked: the order of replays is
+// the caller's.
+lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
 {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     CUDA_TRY(cudaStreamIsCapturing(stream, &cs));
-    *tracked = cs == cudaStreamCaptureStatusNone;
+    if (cs != cudaStreamCaptureStatusNone) return LORA_OK;
+    if (!p->calls.empty() && p->calls.back().stream == stream) {
+        CUDA_TRY(cudaEventRecord(p->calls.back().ev, stream));
+        return LORA_OK;
+    }
+    // the entry of this stream, or a new one, becomes the last
+    for (size_t i = 0; i < p->calls.size(); ++i)
+        if (p->calls[i].stream == stream) {
+            std::swap(p->calls[i], p->calls.back());
+            CUDA_TRY(cudaEventRecord(p->calls.back().ev, stream));
+            return LORA_OK;
+        }
+    lora_kv::Call c{stream, nullptr};
+    CUDA_TRY(cudaEventCreateWithFlags(&c.ev, cudaEventDisableTiming));
+    if (cudaEventRecord(c.ev, stream) != cudaSuccess) {
+        cudaGetLastError();
+        cudaEventDestroy(c.ev);
+        return LORA_ERR_CUDA;
+    }
+    try {
+        p->calls.push_back(c);
+    } catch (...) {
+        cudaEventDestroy(c.ev);
+        return LORA_ERR_OOM;
+    }
     return LORA_OK;
 }
 
-// After a call on `stream`: the error-word read waits for it.
-lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
+// Before an attention call on `stream`: the scratch belongs to one call at a time, so after the
+// last attention call if that ran on another stream.
+lora_status order_attention(lora_kv *p, cudaStream_t stream)
 {
-    bool tracked;
-    const lora_status st = is_tracked(stream, &tracked);
-    if (st != LORA_OK || !tracked) return st;
-    CUDA_TRY(cudaEventRecord(p->ev_call, stream));
-    CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev_call, 0));
+    if (p->attn_stream == stream || !p->attn_any) return LORA_OK;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    CUDA_TRY(cudaStreamIsCapturing(stream, &cs));
+    if (cs != cudaStreamCaptureStatusNone) return LORA_OK;
+    for (const lora_kv::Call &c : p->calls)
+        if (c.stream == p->attn_stream) CUDA_TRY(cudaStreamWaitEvent(stream, c.ev, 0));
+    p->attn_stream = stream;
     return LORA_OK;
 }
 
@@ -330,8 +422,6 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
     }
     if (cudaMemset(p->d_err, 0, 2 * sizeof(int)) != cudaSuccess ||
         cudaMemset(p->count, 0, counts) != cudaSuccess ||
-        cudaEventCreateWithFlags(&p->ev_call, cudaEventDisableTiming) != cudaSuccess ||
-        cudaEventCreateWithFlags(&p->ev_attn, cudaEventDisableTiming) != cudaSuccess ||
         cudaStreamCreateWithFlags(&p->ctl_stream, cudaStreamNonBlocking) != cudaSuccess ||
         ensure_smem_attr((const void *)kv_read_clear_kernel, 0) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
@@ -347,8 +437,7 @@ lora_status lora_kv_destroy(lora_kv_t p)
     if (!p) return LORA_ERR_ARG;
     cudaDeviceSynchronize();
     if (p->ctl_stream) cudaStreamDestroy(p->ctl_stream);
-    if (p->ev_call) cudaEventDestroy(p->ev_call);
-    if (p->ev_attn) cudaEventDestroy(p->ev_attn);
+    for (const lora_kv::Call &c : p->calls) cudaEventDestroy(c.ev);
     if (p->dec_part) cudaFree(p->dec_part);
     if (p->pre_part) cudaFree(p->pre_part);
     if (p->count) cudaFree(p->count);
@@ -420,10 +509,7 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     const bool prefill = (int64_t)batch->max_new * a.G > kDecodeRows;
     const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * batch->max_new;
     if (prefill && (st = ensure_pre_part(p)) != LORA_OK) return st;
-    bool tracked;
-    if ((st = is_tracked(stream, &tracked)) != LORA_OK) return st;
-    // the scratch belongs to one call at a time: after the last one, if that ran elsewhere
-    if (tracked && p->attn_any && stream != p->attn_stream) CUDA_TRY(cudaStreamWaitEvent(stream, p->ev_attn, 0));
+    if ((st = order_attention(p, stream)) != LORA_OK) return st;
     const KvDev kv = kv_view(p);
     const KvBatchDev bd = batch_view(batch);
     if (decode)
@@ -432,18 +518,19 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     if (prefill)
         CUDA_TRY(launch_kv_prefill(kv, p->int8, bd, a, decode ? kDecodeRows + 1 : 0, p->pre_part,
                                    p->count + kv_decode_grid(p->num_sms), p->num_sms, stream));
-    if (!tracked) return LORA_OK;
-    CUDA_TRY(cudaEventRecord(p->ev_attn, stream));
-    CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev_attn, 0));
-    p->attn_stream = stream;
-    p->attn_any = true;
+    if ((st = note_kv_call(p, stream)) != LORA_OK) return st;
+    if (!p->attn_any) {
+        p->attn_any = true;
+        p->attn_stream = stream;
+    }
     return LORA_OK;
 }
 
 lora_status lora_kv_check_errors(lora_kv_t p)
 {
     if (!p) return LORA_ERR_ARG;
-    // on the control stream, which follows every call enqueued on the cache
+    // on the control stream, after the last call of every stream
+    for (const lora_kv::Call &c : p->calls) CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, c.ev, 0));
     kv_read_clear_kernel<<<1, 1, 0, p->ctl_stream>>>(p->d_err);
     if (cudaGetLastError() != cudaSuccess ||
         cudaMemcpyAsync(p->h_err, p->d_err + 1, sizeof(int), cudaMemcpyDeviceToHost, p->ctl_stream) !=

@@ -10,8 +10,9 @@ import ctypes
 import math
 from typing import Optional, Tuple
 
-from . import (LORA_ERR_ARG, LORA_ERR_SHAPE, LORA_KV_BF16, LORA_KV_INT8, LoraError, _check, _ptr, _stream,
-               load_library)
+import torch
+
+from . import LORA_ERR_ARG, LORA_ERR_SHAPE, LORA_KV_BF16, LORA_KV_INT8, LoraError, _check, _ptr, load_library
 
 
 class _BatchStruct(ctypes.Structure):
@@ -29,7 +30,6 @@ class KvBatch:
     the step's tensors and max_new a bound on the rows of one sequence."""
 
     def __init__(self, page_table, start, kv_len, T: int, max_new: int):
-        import torch
         for t, nd in ((page_table, 2), (start, 1), (kv_len, 1)):
             if t.dtype != torch.int32 or t.dim() != nd or not t.is_contiguous():
                 raise LoraError(LORA_ERR_ARG, "KvBatch: page_table, start and kv_len are contiguous int32")
@@ -49,7 +49,6 @@ class KvCache:
 
     def __init__(self, num_pages: int, page_tokens: int, kv_heads: int, head_dim: int, fmt: int = LORA_KV_INT8,
                  device="cuda", arenas: Optional[Tuple] = None):
-        import torch
         self.handle = None
         self.num_pages, self.page_tokens = num_pages, page_tokens
         self.kv_heads, self.head_dim, self.fmt = kv_heads, head_dim, fmt
@@ -69,6 +68,7 @@ class KvCache:
                                   not t.is_contiguous()):
                 raise LoraError(LORA_ERR_SHAPE, f"KvCache: scales are contiguous {shape[:3]} of bfloat16")
         self.k, self.v, self.k_scales, self.v_scales = k, v, ks, vs
+        self._device = k.device.index or 0
         h = ctypes.c_void_p()
         _check(load_library().lora_kv_create(num_pages, page_tokens, kv_heads, head_dim, fmt, _ptr(k), _ptr(v),
                                              _ptr(ks), _ptr(vs), ctypes.byref(h)), "lora_kv_create")
@@ -92,9 +92,13 @@ class KvCache:
         except Exception:  # noqa: BLE001
             pass
 
+    def _stream(self, stream) -> int:
+        if stream is None:  # (torch.cuda.current_stream() builds an object: 3 us of a call's 10)
+            return torch._C._cuda_getCurrentRawStream(self._device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
     def _rows(self, x, heads: int, batch: KvBatch, what: str) -> int:
         """The token stride of x, a bf16 [T, heads, head_dim] tensor with contiguous heads."""
-        import torch
         T, D = batch.T, self.head_dim
         if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[0] != T or x.shape[1] != heads or x.shape[2] != D:
             raise LoraError(LORA_ERR_SHAPE, f"{what}: bfloat16 [{T}, {heads}, {D}] expected")
@@ -111,11 +115,10 @@ class KvCache:
         ks = self._rows(K, self.kv_heads, batch, "lora_kv_write K")
         vs = self._rows(V, self.kv_heads, batch, "lora_kv_write V")
         _check(self._lib.lora_kv_write(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                       _stream(stream)), "lora_kv_write")
+                                       self._stream(stream)), "lora_kv_write")
 
     def read(self, batch: KvBatch, K=None, V=None, stream=None):
         """The batch's tokens as bf16 [T, kv_heads, head_dim] keys and values."""
-        import torch
         shape = (batch.T, self.kv_heads, self.head_dim)
         if K is None:
             K = torch.empty(shape, dtype=torch.bfloat16, device=self.k.device)
@@ -124,14 +127,13 @@ class KvCache:
         ks = self._rows(K, self.kv_heads, batch, "lora_kv_read K")
         vs = self._rows(V, self.kv_heads, batch, "lora_kv_read V")
         _check(self._lib.lora_kv_read(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                      _stream(stream)), "lora_kv_read")
+                                      self._stream(stream)), "lora_kv_read")
         return K, V
 
     def attention(self, Q, batch: KvBatch, scale: Optional[float] = None, window: int = 0, O=None, lse=None,
                   stream=None):
         """Attention of the batch's tokens over the cache, which already holds them.
         Q bf16 [T, n_heads, head_dim]; returns O (as Q) and lse fp32 [T, n_heads]."""
-        import torch
         if Q.dim() != 3:
             raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention: Q is [T, n_heads, head_dim]")
         T, Hq = Q.shape[0], Q.shape[1]
@@ -146,7 +148,7 @@ class KvCache:
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
         _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, window,
-                                           O.data_ptr(), os_, lse.data_ptr(), _stream(stream)),
+                                           O.data_ptr(), os_, lse.data_ptr(), self._stream(stream)),
                "lora_kv_attention")
         return O, lse
 
