@@ -32,12 +32,13 @@ struct RowMap {
     static constexpr int kVec = kValues / 8;         // 16-byte vectors of bf16 a lane
 };
 
-__device__ __forceinline__ float bf16_bits_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-
 // scale and 16 codes of this lane's 16 values; the row's kLanes lanes take part.
-//   s = max(bf16(amax / 127), 2^-126), code = clamp(rint(x / s), -127, 127)
-// x and s have 8 significant bits, so x / s is a tie or at least 2^-11 away from one:
-// the fp32 division decides every code as exact arithmetic would.
+//   s = max(bf16(amax / 127), 2^-126), code = rint(x / s), ties to even
+// (at most 127: s is at least amax / 127.499). x and s have 8 significant bits, so x / s is either a
+// tie or more than 2^-10 away from one. y = x * (1 / s) is off by less than 2^-15, so rounding it
+// to a multiple of 2^-11 first gives the ties exactly and moves nothing else across one: the codes
+// are those of exact arithmetic without a division each (a division each: 16384 tokens written
+// and read back 76 us, so 57).
 template <int kLanes>
 __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint16_t *scale_bits)
 {
@@ -53,32 +54,37 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint16_t *scale
     const uint32_t sb = pack_bf16x2(__fdiv_rn(__uint_as_float(top << 16), 127.0f), 0.0f) & 0xFFFFu;
     const float s = fmaxf(__uint_as_float(sb << 16), 1.17549435e-38f);  // 2^-126
     *scale_bits = finite ? (uint16_t)(__float_as_uint(s) >> 16) : (uint16_t)0x7FC0;
+    const float inv = __frcp_rn(s);
+    const uint64_t inv2 = pack2(inv, inv);
+    const uint64_t grid = pack2(6144.0f, 6144.0f), back = pack2(-6144.0f, -6144.0f);  // 1.5 2^12: multiples of 2^-11
+    const uint64_t whole = pack2(12582912.0f, 12582912.0f);  // 1.5 2^23: the code in the low byte
     uint32_t c[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        uint32_t v = 0;
+        uint32_t v[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t b = w[2 * q + (e >> 1)];
-            const float f = (e & 1) ? bf16_hi(b) : bf16_lo(b);
-            const int code = (int)fminf(fmaxf(rintf(__fdiv_rn(f, s)), -127.0f), 127.0f);
-            v |= (uint32_t)((finite ? code : 0) & 0xFF) << (8 * e);
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t b = w[2 * q + e];
+            float lo, hi;
+            unpack2(add2(add2(fma2(pack2(bf16_lo(b), bf16_hi(b)), inv2, grid), back), whole), &lo, &hi);
+            v[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
         }
-        c[q] = v;
+        c[q] = finite ? __byte_perm(v[0], v[1], 0x5410) : 0u;
     }
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// bf16(scale * code) of 8 codes: the product of a 7-bit code and an 8-bit scale is exact in
-// fp32, so it is rounded once.
-__device__ __forceinline__ uint4 dequantise8(uint32_t c0, uint32_t c1, float s)
+// bf16(scale * code) of 8 codes: codes are exact in bf16, and a bf16 product rounds the exact one
+// once. s: the scale, twice.
+__device__ __forceinline__ uint4 dequantise8(uint32_t c0, uint32_t c1, __nv_bfloat162 s, uint32_t base)
 {
     uint32_t o[4];
+    codes4_to_bf16(c0, base, &o[0], &o[1]);
+    codes4_to_bf16(c1, base, &o[2], &o[3]);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        const uint32_t w = p < 2 ? c0 : c1;
-        const int lo = (int)(int8_t)(w >> (16 * (p & 1))), hi = (int)(int8_t)(w >> (16 * (p & 1) + 8));
-        o[p] = pack_bf16x2(s * (float)lo, s * (float)hi);
+        const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o[p]), s);
+        o[p] = *reinterpret_cast<const uint32_t *>(&v);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -171,6 +177,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvDev kv, KvBatchDev b, ui
     const int h = on ? (is_v ? r - kv.H : r) : 0;
     const int64_t stride = is_v ? v_stride : k_stride;
     uint16_t *dst = (is_v ? V : K) + (int64_t)t0 * stride + h * D + d;
+    const uint32_t base = kv_opaque(0x43004300u);
     const int64_t head = (int64_t)h << kv.page_shift;
     const int64_t rows = run_rows(kv, b, t0, run, lane);
     for (int i0 = 0; i0 < run; i0 += kBatch) {
@@ -195,9 +202,9 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvDev kv, KvBatchDev b, ui
             if (row[i] == -2) continue;
             uint16_t *const to = dst + (i0 + i) * stride;
             if constexpr (kInt8) {
-                const float f = bf16_bits_f(s[i]);
-                *reinterpret_cast<uint4 *>(to) = dequantise8(x[i].x, x[i].y, f);
-                *reinterpret_cast<uint4 *>(to + 8) = dequantise8(x[i].z, x[i].w, f);
+                const __nv_bfloat162 f = q4_scale_pair(s[i]);
+                *reinterpret_cast<uint4 *>(to) = dequantise8(x[i].x, x[i].y, f, base);
+                *reinterpret_cast<uint4 *>(to + 8) = dequantise8(x[i].z, x[i].w, f, base);
             } else {
                 *reinterpret_cast<uint4 *>(to) = x[i];
             }
