@@ -315,7 +315,7 @@ KvDev kv_view(const lora_kv *p)
     return v;
 }
 
-constexpr int kDecodeRows = 16;
+constexpr int kDecodeRows = 24;
 
 // The tcgen05 kernel's scratch (40 MB for D = 128), from the first call that needs it.
 lora_status ensure_pre_part(lora_kv *p)

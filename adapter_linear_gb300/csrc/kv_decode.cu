@@ -21,6 +21,7 @@
 // Inside a CTA the four warps take 16-token steps in turn, each streaming its own codes through
 // its own ring of shared memory with 16-byte asynchronous copies: no barrier until an item ends.
 #include <climits>
+#include <type_traits>
 
 #include "kv_device.cuh"
 
@@ -43,8 +44,8 @@ struct Cfg {
     static constexpr bool kWide = kRowBytes == 256;
     // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers; rows of 256
     // bytes: 2 of 98 KB): 100 to 150 KB in flight beside the stages in use
-    static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
-    static constexpr int kCtas = kWide ? 2 : kN == 1 ? 4 : 3;
+    static constexpr int kStages = kWide || kN == 1 ? 3 : kN == 2 ? 4 : 6;
+    static constexpr int kCtas = kWide || kN > 2 ? 2 : kN == 1 ? 4 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * kRing;
     static constexpr int kLdO = D + 4;                           // fp32 row of O in shared memory
@@ -611,20 +612,20 @@ cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, co
         fn<<<min(C::kCtas * num_sms, C::kMaxGrid), kWarps * 32, C::kSmem, stream>>>(kv, b, a, plan);
         return cudaGetLastError();
     };
-    // one tile of 8 rows where the chunk's rows fit it, else two an item
-    const bool one = (int64_t)max_new * a.G <= 8;
-    if (kv.D == 128) {
-        if (int8)
-            return one ? launch(Cfg<128, true, 1>(), kv_decode_kernel<128, true, 1>)
-                       : launch(Cfg<128, true, 2>(), kv_decode_kernel<128, true, 2>);
-        return one ? launch(Cfg<128, false, 1>(), kv_decode_kernel<128, false, 1>)
-                   : launch(Cfg<128, false, 2>(), kv_decode_kernel<128, false, 2>);
-    }
-    if (int8)
-        return one ? launch(Cfg<64, true, 1>(), kv_decode_kernel<64, true, 1>)
-                   : launch(Cfg<64, true, 2>(), kv_decode_kernel<64, true, 2>);
-    return one ? launch(Cfg<64, false, 1>(), kv_decode_kernel<64, false, 1>)
-               : launch(Cfg<64, false, 2>(), kv_decode_kernel<64, false, 2>);
+    const int64_t rows = (int64_t)max_new * a.G;
+    auto pick = [&](auto d, auto i8) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool kInt8 = decltype(i8)::value;
+        if (rows <= 8) return launch(Cfg<D, kInt8, 1>(), kv_decode_kernel<D, kInt8, 1>);
+        if (rows <= 16) return launch(Cfg<D, kInt8, 2>(), kv_decode_kernel<D, kInt8, 2>);
+        return launch(Cfg<D, kInt8, 3>(), kv_decode_kernel<D, kInt8, 3>);
+    };
+    using std::integral_constant;
+    if (kv.D == 128)
+        return int8 ? pick(integral_constant<int, 128>(), std::true_type())
+                    : pick(integral_constant<int, 128>(), std::false_type());
+    return int8 ? pick(integral_constant<int, 64>(), std::true_type())
+                : pick(integral_constant<int, 64>(), std::false_type());
 }
 
 }  // namespace lora
