@@ -34,6 +34,9 @@ constexpr int kUnit = kWarps * kStep;
 constexpr int kHeadUnits = 3;        // an item's cost beside its units: 64 int8 requests 118 us at 0, 104 at 3, 107 at 6
 constexpr int kMinUnits = 2;         // one request, one token: 12.3 us at 1, 11.2 at 2, 11.6 at 4
 
+constexpr int kMaxCtas = 4;    // CTAs an SM, of any variant
+constexpr int kPartRows = 48;  // and the rows that those of one SM hold
+
 // kN: tiles of 8 rows (a row: one query head of one new token) an item holds.
 template <int D, bool kInt8, int kN>
 struct Cfg {
@@ -44,13 +47,14 @@ struct Cfg {
     static constexpr bool kWide = kRowBytes == 256;
     // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers; rows of 256
     // bytes: 2 of 98 KB): 100 to 150 KB in flight beside the stages in use
-    static constexpr int kStages = kWide || kN == 1 ? 3 : kN == 2 ? 4 : 6;
-    static constexpr int kCtas = kWide || kN > 2 ? 2 : kN == 1 ? 4 : 3;
+    static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
+    static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 ? 4 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * kRing;
     static constexpr int kLdO = D + 4;                           // fp32 row of O in shared memory
     static constexpr int kMaxGrid = kSmem / (4 * kRows);         // pieces whose weights fit the rings
     static_assert(kRing >= kRows * kLdO * 4, "O of a warp is parked in its ring");
+    static_assert(kCtas * kRows <= kPartRows && kCtas <= kMaxCtas, "scratch of an SM's CTAs");
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile. The chunks of a 128-byte line are permuted
@@ -110,6 +114,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     constexpr int kM = D / 16;                    // MMAs of 16 dimensions
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_w[kWarps][R], sm_lse[R];
+    __shared__ float sm_back[R];
+    __shared__ int sm_pos[R];
+    __shared__ uint4 sm_q[kN][kM / 2][32];  // [tile][pair of MMAs][lane]: the same for all warps
     __shared__ int sm_last;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,72 +195,63 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 #pragma unroll
         for (int k = 0; k < C::kStages - 1; ++k) issue();
 
-        // Q as the 8-column operand: lane (g, c) holds row g of each tile; its dims of MMA i are
-        // those its K words hold (8-bit: 64-dim blocks of 16 dims a lane; bf16: 32-dim blocks of 8)
-        uint32_t q[kN][kM][2];
-        float back_mul[kN][2];  // of the rows this lane has scores of: to units of log2
-        int pos[kN][2];         // and their positions of the rows this lane has scores of: 8 t + 2 c, + 1
-#pragma unroll
-        for (int t = 0; t < kN; ++t) {
-            const int row = tile * R + 8 * t + g;
-            const bool on = 8 * t + g < rows;
+        // Q as the 8-column operand, a tile a warp: lane (g, c) holds row g of it; its dims of MMA i
+        // are those its K words hold (8-bit: 64-dim blocks of 16 dims a lane; bf16: 32-dim blocks of 8)
+        static_assert(kN <= kWarps, "a tile a warp");
+        if (warp < kN) {
+            const int row = tile * R + 8 * warp + g;
+            const bool on = 8 * warp + g < rows;
             const int i = row / G;
             const uint16_t *src = a.Q + (int64_t)(sh.row0 + i) * a.q_stride + (int64_t)(head * G + row % G) * D;
             constexpr int kBlock = kInt8 ? 64 : 32, kLane = kBlock / 4;
+            uint4 q[kM / 2];
 #pragma unroll
-            for (int s = 0; s < D / kBlock; ++s)
-#pragma unroll
-                for (int e = 0; e < kLane / 8; ++e) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (on) v = ldg_nc_v4(src + s * kBlock + c * kLane + e * 8);
-                    const int i0 = s * (kLane / 4) + e * 2;
-                    q[t][i0][0] = v.x;
-                    q[t][i0][1] = v.y;
-                    q[t][i0 + 1][0] = v.z;
-                    q[t][i0 + 1][1] = v.w;
-                }
+            for (int x = 0; x < kM / 2; ++x) {
+                q[x] = make_uint4(0, 0, 0, 0);
+                if (on) q[x] = ldg_nc_v4(src + (x / (kLane / 8)) * kBlock + c * kLane + (x % (kLane / 8)) * 8);
+            }
             // An 8-bit cache's codes become f16 in two thirds of the instructions bf16 takes, so Q
             // becomes f16 too, its row scaled by the power of two that puts the largest magnitude
             // into [2^14, 2^15): values down to 2^-28 of that keep all their bits, and the
             // rest are off by at most 2^-39 of it.
+            float back = 1.0f;
             if (kInt8) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < kM; ++i)
+                for (int x = 0; x < kM / 2; ++x) {
+                    const uint32_t v[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        top = max(top, max(q[t][i][e] & 0x7FFFu, (q[t][i][e] >> 16) & 0x7FFFu));
+                    for (int e = 0; e < 4; ++e) top = max(top, max(v[e] & 0x7FFFu, (v[e] >> 16) & 0x7FFFu));
+                }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const int up = min(14 + 127 - (int)(top >> 7), 126);  // bf16's exponent field
                 const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-                const float back = __uint_as_float((uint32_t)(127 - up) << 23);
+                back = __uint_as_float((uint32_t)(127 - up) << 23);
+                auto f16 = [&](uint32_t v) {
+                    const __half2 h = __floats2half2_rn(bf16_lo(v) * mul, bf16_hi(v) * mul);
+                    return *reinterpret_cast<const uint32_t *>(&h);
+                };
 #pragma unroll
-                for (int i = 0; i < kM; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const __half2 h = __floats2half2_rn(bf16_lo(q[t][i][e]) * mul, bf16_hi(q[t][i][e]) * mul);
-                        q[t][i][e] = *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                back_mul[t][0] = __shfl_sync(0xffffffffu, back, 8 * c) * plan.scale_log2;
-                back_mul[t][1] = __shfl_sync(0xffffffffu, back, 8 * c + 4) * plan.scale_log2;
-            } else {
-                back_mul[t][0] = back_mul[t][1] = plan.scale_log2;
+                for (int x = 0; x < kM / 2; ++x) q[x] = make_uint4(f16(q[x].x), f16(q[x].y), f16(q[x].z), f16(q[x].w));
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * t + 2 * c + e;  // rows beyond the tile: any position, not written
-                pos[t][e] = r < rows ? sh.L - sh.n + (tile * R + r) / G : sh.L - 1;
+            for (int x = 0; x < kM / 2; ++x) sm_q[warp][x][lane] = q[x];
+            if (c == 0) {
+                sm_back[8 * warp + g] = back * plan.scale_log2;  // to units of log2
+                // rows beyond the tile: any position, not written
+                sm_pos[8 * warp + g] = on ? sh.L - sh.n + i : sh.L - 1;
             }
         }
-        int pos_min = pos[0][0], pos_max = pos[0][0];
+        __syncthreads();
+        // of the rows this lane has scores of: 8 t + 2 c, + 1
+        float back_mul[kN][2];
 #pragma unroll
-        for (int t = 0; t < kN; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                pos_min = min(pos_min, pos[t][e]);
-                pos_max = max(pos_max, pos[t][e]);
-            }
+        for (int t = 0; t < kN; ++t) {
+            back_mul[t][0] = sm_back[8 * t + 2 * c];
+            back_mul[t][1] = sm_back[8 * t + 2 * c + 1];
+        }
+        const int pos_min = sh.L - sh.n + tile * R / G, pos_max = sh.L - sh.n + (tile * R + rows - 1) / G;
 
         float o[kN][kM][4];
         float m[kN][2], l[kN][2];
@@ -288,21 +286,27 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
                 if constexpr (kInt8) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t a0, a1, a2, a3;
-                        codes4_to_f16(u0[j], &a0, &a2);
-                        codes4_to_f16(u1[j], &a1, &a3);
+                    for (int j = 0; j < 4; j += 2) {
+                        uint32_t u[2][4];
 #pragma unroll
-                        for (int t = 0; t < kN; ++t)
-                            mma16816_f16(s[t], a0, a1, a2, a3, q[t][4 * x + j][0], q[t][4 * x + j][1]);
+                        for (int y = 0; y < 2; ++y) {
+                            codes4_to_f16(u0[j + y], &u[y][0], &u[y][2]);
+                            codes4_to_f16(u1[j + y], &u[y][1], &u[y][3]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < kN; ++t) {
+                            const uint4 q = sm_q[t][2 * x + j / 2][lane];
+                            mma16816_f16(s[t], u[0][0], u[0][1], u[0][2], u[0][3], q.x, q.y);
+                            mma16816_f16(s[t], u[1][0], u[1][1], u[1][2], u[1][3], q.z, q.w);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int t = 0; t < kN; ++t)
-                            mma16816(s[t], u0[2 * j], u1[2 * j], u0[2 * j + 1], u1[2 * j + 1], q[t][2 * x + j][0],
-                                     q[t][2 * x + j][1]);
+                    for (int t = 0; t < kN; ++t) {
+                        const uint4 q = sm_q[t][x][lane];
+                        mma16816(s[t], u0[0], u1[0], u0[1], u1[1], q.x, q.y);
+                        mma16816(s[t], u0[2], u1[2], u0[3], u1[3], q.z, q.w);
+                    }
                 }
             }
 
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                         s[t][2 * y + e] *= back_mul[t][e];
                         if (kInt8) s[t][2 * y + e] *= ks[y];
                         if (edge) {
-                            const int j = tok + g + 8 * y, p = pos[t][e];
+                            const int j = tok + g + 8 * y, p = sm_pos[8 * t + 2 * c + e];
                             const bool see = j <= p && (a.window == 0 || j > p - a.window);
                             s[t][2 * y + e] = see ? s[t][2 * y + e] : -INFINITY;
                         }
@@ -597,9 +601,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 
 }  // namespace
 
-int kv_decode_grid(int num_sms) { return 4 * num_sms; }
+int kv_decode_grid(int num_sms) { return kMaxCtas * num_sms; }
 
-size_t kv_decode_part_floats(int D, int num_sms) { return (size_t)2 * kv_decode_grid(num_sms) * 16 * (D + 2); }
+// two pieces a CTA
+size_t kv_decode_part_floats(int D, int num_sms) { return (size_t)2 * kPartRows * num_sms * (D + 2); }
 
 cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int max_new,
                              int max_rows, float *part, int *count, int num_sms, cudaStream_t stream)
