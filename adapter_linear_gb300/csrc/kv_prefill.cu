@@ -13,18 +13,28 @@
 // hands out the work:
 //   S_t = Q_t K^T  (both operands in shared memory, S in tensor memory, 128 columns a tile)
 //   O_t += P_t V   (P, the bf16 weights, written by the softmax over S; O in tensor memory)
-// in the order PV_t(j) S_t(j+1): while one tile's softmax runs, the tensor cores do the other
-// tile's products. MMAs of one thread execute in order, so S_t(j+1) overwrites P_t(j) only after
-// PV_t(j) has read it, and the commit behind S_t(j+1) covers PV_t(j).
+// in two halves of 64 keys: PV_t(j, h) follows as soon as that half's weights are there, and behind it
+// S_t(j + 1, h) over the same columns, so that the next tile's scores of one half are made
+// while the softmax works on the other half. MMAs of one thread execute in order, so S_t(j + 1, h)
+// overwrites P_t(j, h) only after PV_t(j, h) has read it, and the commit behind S_t(j + 1, h) covers
+// PV_t(j, h). (A product a tile, in turns of the two tiles: 8 prompts of 2048 bf16 379 us,
+// halves 373; 512 tokens over 32000 int8 398, so 377. S with N = 64 reads Q twice, which costs
+// 24 % of the products' time at D = 128.)
+//
+// The softmax of a row, a thread: 32 scores at a time from tensor memory into registers, the next
+// 32 on their way while these become weights.
+//
+// What bounds it: the tensor cores take 2900 cycles of the 3500 that a key tile of 2 x 128 rows
+// takes at D = 128, bf16; with an 8-bit cache (6000 cycles) they share shared memory's bandwidth
+// with the conversion of the codes, and the softmax's two multiplications by scales come on top.
 //
 // An 8-bit cache's scales stay outside the products: the codes are exact in bf16, a key's scale
 // multiplies its column of S and a value's its weight.
 //
-// A weight rounded to bf16 is off by up to 2^-9 of it or 2^-8 (the mantissa's place), which
-// averages out over many keys but shows where one key holds much of a row's weight. So where a
-// key may hold more than a quarter of what its row has so far, the tile's weights go to the product
-// in two bf16 parts, the second with the rest (a second product for that tile: a piece's
-// first tile, then rarely).
+// A weight rounded to bf16 is off by up to 2^-8 of it, which averages out over many keys but shows
+// where one key holds much of a row's weight. So where a key may hold more than a quarter of
+// what its row has so far, the half's weights go to the product in two bf16 parts, the second with
+// the rest (a second product for that half: a piece's first keys, then rarely).
 //
 // Work is shared out like the short-chunk kernel's: the grid's CTAs (one an SM) take equal
 // contiguous runs of 128-token units over all items, pieces of an item go to scratch as
@@ -36,7 +46,7 @@
 namespace lora {
 namespace {
 
-constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128;
+constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128, kHalf = 64, kPart = 32;
 constexpr int kSoftWarps = 8, kLoadWarps = 4;
 constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // two MMA warps, one that hands out the work, one idle
 // Registers a thread of the softmax warps, the loading warps and the MMA warps' group: a block of
@@ -82,8 +92,8 @@ struct Segment {
 static_assert(sizeof(Segment) == 64, "segment");
 
 struct Bars {
-    uint64_t seg_full[kSegments], seg_empty[kSegments], q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4], v_empty[4], sc_full[6], s_full[2],
-        p_full[2], o_full[2], turn[2], drain[2];
+    uint64_t seg_full[kSegments], seg_empty[kSegments], q_full[2], q_empty[2], k_full[4], k_empty[4], v_full[4],
+        v_empty[4], sc_full[6], s_full[2][2], p_full[2][2], pv_half[2], o_full[2], drain[2];
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
 
@@ -152,28 +162,37 @@ __device__ __forceinline__ void commit_lead(uint32_t lead, uint32_t bar)
         : "memory");
 }
 
-// 8 columns into registers; they are there after tmem_ld_wait8 on the same registers (which orders
+// 32 columns into registers; they are there after tmem_wait32 on the same registers (which orders
 // nothing else).
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[kPart])
 {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+                 "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8])
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[kPart])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
                  : "memory");
 }
+
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t *r)
 {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
@@ -226,138 +245,101 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, small_wait(bar, parity, abort_flag, err));
 }
 
-// Which of 8 columns from col0 on a row sees: a bit each.
-__device__ __forceinline__ uint32_t seen8(int lim, int low, int col0)
-{
-    const int n = min(max(lim - col0 + 1, 0), 8), skip = min(max(low - col0 + 1, 0), 8);
-    return ((1u << n) - 1u) & ~((1u << skip) - 1u);
-}
-
-// Raw scores (as loaded) of 8 keys of this thread's row times the keys' scales, in pairs; kMask:
-// -inf where the row does not see the key (a bit each in `seen`).
+// The row's scores of 32 keys in units of log2, in pairs: raw ones (as loaded) times mul and the
+// keys' scales, -inf where the row does not see the key (kMask); returns the largest.
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ void scores8(const uint32_t (&s)[8], const ulonglong2 (&c)[2], uint32_t seen, uint64_t (&z)[4])
+__device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, int lim, int low, uint64_t mul,
+                                             uint64_t (&z)[kPart / 2])
 {
+    float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-        if (kInt8) z[i] = mul2(z[i], i & 1 ? c[i >> 1].y : c[i >> 1].x);
+    for (int i = 0; i < kPart / 2; ++i) {
+        z[i] = mul2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul);
+        if (kInt8) {
+            const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(sc + 2 * (i & ~1));
+            z[i] = mul2(z[i], i & 1 ? c.y : c.x);
+        }
+        float a, b;
+        unpack2(z[i], &a, &b);
         if (kMask) {
-            float a, b;
-            unpack2(z[i], &a, &b);
-            z[i] = pack2(seen >> (2 * i) & 1u ? a : -INFINITY, seen >> (2 * i + 1) & 1u ? b : -INFINITY);
+            a = 2 * i <= lim && 2 * i > low ? a : -INFINITY;
+            b = 2 * i + 1 <= lim && 2 * i + 1 > low ? b : -INFINITY;
+            z[i] = pack2(a, b);
         }
+        top[i & 1] = fmaxf(top[i & 1], fmaxf(a, b));
     }
+    return fmaxf(top[0], top[1]);
 }
 
-__device__ __forceinline__ void load_scales(const float *sc, ulonglong2 (&c)[2])
-{
-    c[0] = *reinterpret_cast<const ulonglong2 *>(sc);
-    c[1] = *reinterpret_cast<const ulonglong2 *>(sc + 4);
-}
-
-// The largest score of the row's 128 keys in units of log2 (mul >= 0: raw score to those).
-// (These loops stay rolled: the roles' code together has to fit the instruction cache. Unrolled,
-// an 8-bit cache's softmax and conversions missed it in 38 % of fetches and took twice the time.)
+// The row's 32 weights 2^(z - m), times the values' scales (0 for a key the row does not see,
+// whatever its scale is), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e, and in column
+// 16 i + 8 + e what rounding left of them (rest) or zeros. Returns the weights' sum.
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ float tile_top(uint32_t tS, const float *sc, int lim, int low, float mul)
+__device__ __forceinline__ float part_weights(const uint64_t (&z)[kPart / 2], uint32_t tS, const float *sc, float m,
+                                              bool rest)
 {
-    float x[2] = {-INFINITY, -INFINITY};
-    uint32_t s[2][8];
-    ulonglong2 c[2][2];
-    tmem_ld8(tS, s[0]);
-    if (kInt8) load_scales(sc, c[0]);
-#pragma unroll 1
-    for (int ch = 0; ch < 16; ch += 2)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            tmem_ld_wait8(s[b]);
-            // (the last round asks for columns it does not use)
-            const int next = ch + b + 1 < 16 ? ch + b + 1 : 0;
-            tmem_ld8(tS + next * 8, s[b ^ 1]);
-            if (kInt8) load_scales(sc + next * 8, c[b ^ 1]);
-            uint64_t z[4];
-            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, (ch + b) * 8) : 0u, z);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float e0, e1;
-                unpack2(z[i], &e0, &e1);
-                x[i & 1] = fmaxf(x[i & 1], fmaxf(e0, e1));
-            }
-        }
-    tmem_ld_wait8(s[0]);
-    const float top = fmaxf(x[0], x[1]);
-    return top == -INFINITY ? top : top * mul;
-}
-
-// The row's 128 weights 2^(score - m), times the values' scales (0 for a key the row does not
-// see, whatever its scale is), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e (whose
-// scores are read by then), and in column 16 i + 8 + e what rounding left of them (kRest) or zeros.
-// Returns the weights' sum.
-template <bool kInt8, bool kMask, bool kRest>
-__device__ __forceinline__ float tile_weights(uint32_t tS, const float *sc, int lim, int low, float mul, float m)
-{
-    const uint64_t mul_2 = pack2(mul, mul), neg = pack2(-m, -m);
+    const uint64_t neg = pack2(-m, -m);
     uint64_t sum[2] = {0, 0};
-    uint32_t s[2][8];
-    ulonglong2 c[2][2], v[2][2];
-    tmem_ld8(tS, s[0]);
-    if (kInt8) {
-        load_scales(sc, c[0]);
-        load_scales(sc + 128, v[0]);
-    }
-#pragma unroll 1
-    for (int ch = 0; ch < 8; ++ch) {
-        uint32_t p[8], rest[8];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            tmem_ld_wait8(s[b]);
-            // (the last round asks for its own columns again)
-            const int next = 2 * ch + b + 1 < 16 ? 2 * ch + b + 1 : 15;
-            tmem_ld8(tS + next * 8, s[b ^ 1]);
+    for (int ch = 0; ch < kPart / 16; ++ch) {
+        uint64_t w[8];
+        uint32_t p[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            float e0, e1, z0, z1;
+            unpack2(z[8 * ch + e], &z0, &z1);
+            unpack2(add2(z[8 * ch + e], neg), &e0, &e1);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            w[e] = pack2(e0, e1);
+            sum[e & 1] = add2(sum[e & 1], w[e]);
             if (kInt8) {
-                load_scales(sc + next * 8, c[b ^ 1]);
-                load_scales(sc + 128 + next * 8, v[b ^ 1]);
+                const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(sc + 128 + 16 * ch + 2 * (e & ~1));
+                w[e] = mul2(w[e], e & 1 ? v.y : v.x);
             }
-            uint64_t z[4];
-            scores8<kInt8, kMask>(s[b], c[b], kMask ? seen8(lim, low, ch * 16 + b * 8) : 0u, z);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float e0, e1, w0, w1;
-                unpack2(fma2(z[i], mul_2, neg), &e0, &e1);
-                e0 = fast_exp2(e0);
-                e1 = fast_exp2(e1);
-                if (kMask) {
-                    float z0, z1;
-                    unpack2(z[i], &z0, &z1);
-                    e0 = z0 == -INFINITY ? 0.0f : e0;
-                    e1 = z1 == -INFINITY ? 0.0f : e1;
-                }
-                const uint64_t e = pack2(e0, e1);
-                sum[i & 1] = add2(sum[i & 1], e);
-                w0 = e0;
-                w1 = e1;
-                if (kInt8) {
-                    unpack2(mul2(e, i & 1 ? v[b][i >> 1].y : v[b][i >> 1].x), &w0, &w1);
-                    if (kMask) {
-                        w0 = e0 == 0.0f ? 0.0f : w0;
-                        w1 = e1 == 0.0f ? 0.0f : w1;
-                    }
-                }
-                p[b * 4 + i] = pack_bf16x2(w0, w1);
-                rest[b * 4 + i] = pack_bf16x2(w0 - bf16_lo(p[b * 4 + i]), w1 - bf16_hi(p[b * 4 + i]));
+            unpack2(w[e], &e0, &e1);
+            if (kInt8 && kMask) {
+                e0 = z0 == -INFINITY ? 0.0f : e0;
+                e1 = z1 == -INFINITY ? 0.0f : e1;
+                w[e] = pack2(e0, e1);
             }
+            p[e] = pack_bf16x2(e0, e1);
         }
-        tmem_ld_wait8(s[0]);  // before its columns may be overwritten
         tmem_st8(tS + ch * 16, p);
-        if (kRest)
-            tmem_st8(tS + ch * 16 + 8, rest);
-        else
+        if (rest) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float w0, w1;
+                unpack2(w[e], &w0, &w1);
+                p[e] = pack_bf16x2(w0 - bf16_lo(p[e]), w1 - bf16_hi(p[e]));
+            }
+            tmem_st8(tS + ch * 16 + 8, p);
+        } else {
             tmem_zero8(tS + ch * 16 + 8);
+        }
     }
     float a, b;
     unpack2(add2(sum[0], sum[1]), &a, &b);
     return a + b;
+}
+
+// A row's 8 columns of O, or of pairs of weights, times `down`.
+__device__ __forceinline__ void scale_o(uint32_t tO, float down)
+{
+    uint32_t o[8];
+    tmem_ld8_wait(tO, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
+    tmem_st8(tO, o);
+}
+__device__ __forceinline__ void scale_p(uint32_t tP, float down)
+{
+    uint32_t p[8];
+    tmem_st_wait();
+    tmem_ld8_wait(tP, p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = pack_bf16x2(bf16_lo(p[e]) * down, bf16_hi(p[e]) * down);
+    tmem_st8(tP, p);
 }
 
 // Which piece of a 16-token group of an 8-bit cache lane `lane` holds: 16-byte piece `c` of rows
@@ -400,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
     Bars &bars = *reinterpret_cast<Bars *>(smem + C::kBars);
     float *const scale_ring = reinterpret_cast<float *>(smem + C::kScales);
     __shared__ uint32_t tmem_slot;
-    __shared__ uint32_t rest_flags[2];  // of the tiles' weights: a byte a warp, has it a second part?
+    __shared__ uint32_t rest_flags[2][2];  // of the tiles' weights: a byte a warp, has it a second part?
     __shared__ volatile int abort_flag;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -411,10 +393,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.q_full[i], kLoadWarps);
             mbar_init(&bars.q_empty[i], 1);
-            mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_full[i], kTileRows / 32);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&bars.s_full[i][h], 1);
+                mbar_init(&bars.p_full[i][h], kTileRows / 32);
+            }
             mbar_init(&bars.o_full[i], 1);
-            mbar_init(&bars.turn[i], 1);
+            mbar_init(&bars.pv_half[i], 1);
             mbar_init(&bars.drain[i], 1);
         }
         for (int i = 0; i < C::kStages; ++i) {
@@ -478,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const int pos = w->L - w->n + i;
             const int tok_lo = w->lo;
             float m = -INFINITY, l = 0.0f;
-            const float mul = plan.scale_log2;  // raw score -> units of log2
+            const uint64_t mul_2 = pack2(plan.scale_log2, plan.scale_log2);  // raw score -> units of log2
             for (int j = j0; j < j1; ++j, ++it, ++ns) {
                 const int tok0 = tok_lo + j * kKeys;
                 const int lim = pos - tok0;
@@ -488,43 +472,64 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const float *const sc = scale_ring + ring * 256;
                 if (kInt8)
                     ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
-                ok = ok && warp_wait(&bars.s_full[t], (uint32_t)ns & 1u, &abort_flag, kv.err);
+                ok = ok && warp_wait(&bars.s_full[t][0], (uint32_t)ns & 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 tc_fence_after_sync();
-
-                const float mx = m == -INFINITY ? 0.0f : m;
-                const float top = mask ? tile_top<kInt8, true>(tS, sc, lim, low, mul)
-                                       : tile_top<kInt8, false>(tS, sc, lim, low, mul);
-                // two parts, and m moved, where a key may hold much of a row's weight
-                const bool rest =
-                    j == j0 || __any_sync(0xffffffffu, top - mx > 64.0f || 3.0f * fast_exp2(top - mx) > l);
-                if (!rest) {
-                    l += mask ? tile_weights<kInt8, true, false>(tS, sc, lim, low, mul, mx)
-                              : tile_weights<kInt8, false, false>(tS, sc, lim, low, mul, mx);
-                } else {
-                    const float m2 = fmaxf(m, top);
-                    const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
-                    m = m2;
-                    l *= down;
-                    if (j > j0) {
+                uint32_t s[kPart];
+                tmem_ld32(tS, s);
+                bool rest_half = false;
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_wait(tO + x, o);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * down);
-                            tmem_st16(tO + x, o);
-                        }
+                for (int x = 0; x < 4; ++x) {  // 32 keys at a time
+                    const int k0 = x * kPart;
+                    uint64_t z[kPart / 2];
+                    tmem_wait32(s);
+                    const float top = mask ? part_scores<kInt8, true>(s, sc + k0, lim - k0, low - k0, mul_2, z)
+                                           : part_scores<kInt8, false>(s, sc + k0, 0, 0, mul_2, z);
+                    if (x == 1) {
+                        ok = warp_wait(&bars.s_full[t][1], (uint32_t)ns & 1u, &abort_flag, kv.err);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                    }
+                    tmem_ld32(tS + (k0 + kPart) % kKeys, s);  // (the last one's is not used)
+                    // two parts where a key may hold much of a row's weight; m is moved with the tile's
+                    // first keys, and where it is far off
+                    const float mx = m == -INFINITY ? 0.0f : m;
+                    const bool far = top > mx + 16.0f || (m == -INFINITY && top > m);
+                    const bool rest = __any_sync(0xffffffffu, far || 3.0f * fast_exp2(top - mx) > l);
+                    if (rest && (x == 0 || __any_sync(0xffffffffu, far))) {
+                        const float m2 = x == 0 || far ? fmaxf(m, top) : m;
+                        const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
+                        m = m2;
+                        l *= down;
+                        // the product before these keys' is done
+                        ok = x < 2 ? warp_wait(&bars.s_full[t][1], (uint32_t)ns & 1u, &abort_flag, kv.err)
+                                   : warp_wait(&bars.pv_half[t], (uint32_t)ns & 1u, &abort_flag, kv.err);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        if (j > j0 || x > 1)
+#pragma unroll 1
+                            for (int y = 0; y < D; y += 8) scale_o(tO + y, down);
+                        // weights of this half that no product has had: what another rounding takes
+                        // from them is 2^-16 of less than 2^-8
+                        if (x & 1)
+#pragma unroll 1
+                            for (int y = 0; y < kPart; y += 8) scale_p(tS + k0 - kPart + y, down);
                     }
                     const float mn = m == -INFINITY ? 0.0f : m;
-                    l += mask ? tile_weights<kInt8, true, true>(tS, sc, lim, low, mul, mn)
-                              : tile_weights<kInt8, false, true>(tS, sc, lim, low, mul, mn);
+                    l += mask ? part_weights<kInt8, true>(z, tS + k0, sc + k0, mn, rest)
+                              : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, rest);
+                    rest_half |= rest;
+                    if (x & 1) {
+                        if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t][x >> 1])[warp & 3] = rest_half;
+                        rest_half = false;
+                        tmem_st_wait();
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.p_full[t][x >> 1]);
+                    }
                 }
-                if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t])[warp & 3] = rest;
-                tmem_st_wait();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[t]);
+                tmem_wait32(s);
+                if (!ok) break;
             }
             if (!ok) break;
             ok = warp_wait(&bars.o_full[t], (uint32_t)nw & 1u, &abort_flag, kv.err);
@@ -824,24 +829,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         if (t < 2) {
             // Tile t's products. An MMA is issued when the one before it has started, so what a warp
             // does between its MMAs (waiting for weights, commits: 600 cycles a key tile) idles the
-            // tensor cores unless another warp issues meanwhile: a warp a tile, in turns (without
-            // turns the two tiles' products interleave, both end late, both softmax run at once).
+            // tensor cores unless another warp issues meanwhile: a warp a tile.
             const uint32_t lead = lane == 0;
-            const uint32_t id_s = idesc_bf16_f32(kTileRows, kKeys);
+            const uint32_t id_s = idesc_bf16_f32(kTileRows, kHalf);
             const uint32_t id_o = idesc_bf16_f32(kTileRows, D) | (1u << 16);  // B: N along the row
             const uint64_t dq = sdesc_k_sw128(smem_u32(smem + C::kQ) + t * C::kTileBytes);
             const uint64_t dk = sdesc_k_sw128(smem_u32(smem + C::kK)), dv = sdesc_mn_sw128(smem_u32(smem + C::kV));
             constexpr uint32_t kTile16 = C::kTileBytes / 16;  // descriptors count 16-byte units
             const uint32_t tS = tmem + t * 128, tO = tmem + C::kO + t * D;
-            uint32_t it = 0, np = 0, nq = 0, turns = 0;
+            uint32_t it = 0, np = 0, nq = 0;
             bool ok = true;
             auto commit = [&](uint64_t &bar) { commit_lead(lead, smem_u32(&bar)); };
             auto wait = [&](uint64_t &bar, uint32_t parity) {
                 ok = ok && warp_wait(&bar, parity & 1u, &abort_flag, kv.err);
             };
-            auto score = [&](uint32_t s, int i) {  // step i of S = Q K^T of the key tile in stage s
-                const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
-                mma_ss(lead, tS, dq + off, dk + s * kTile16 + off, id_s, i > 0);
+            auto score = [&](uint32_t s, int h) {  // S = Q K^T of half h of the key tile in stage s
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t off = (i >> 2) * 1024 + (i & 3) * 2;
+                    mma_ss(lead, tS + h * kHalf, dq + off, dk + s * kTile16 + h * (kHalf * 8) + off, id_s, i > 0);
+                }
+                commit(bars.s_full[t][h]);
             };
             for (int seg = 0; ok; ++seg) {
                 const Segment *const w = segment(seg);
@@ -864,40 +872,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 wait(bars.k_full[it % C::kStages], it / C::kStages);
                 wait(bars.q_full[t], nq++);
                 if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) score(it % C::kStages, i);
-                commit(bars.s_full[t]);
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) score(it % C::kStages, h);
                 commit(bars.k_empty[it % C::kStages]);
                 if (n == 1) commit(bars.q_empty[t]);
 #pragma unroll 1
-                for (int j = 0; j < n; ++j, ++it) {
+                for (int j = 0; j < n; ++j, ++it, ++np) {
                     const uint32_t s = it % C::kStages, s1 = (it + 1) % C::kStages;
                     wait(bars.v_full[s], it / C::kStages);
                     if (j + 1 < n) wait(bars.k_full[s1], (it + 1) / C::kStages);
-                    wait(bars.p_full[t], np++);
-                    if (nt == 2) wait(bars.turn[t], turns++ ^ (t ^ 1));
-                    if (!ok) break;
-                    tc_fence_after_sync();
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts(lead, tO, tS + i * 16, dv + s * kTile16 + i * 128, id_o, (j | i) != 0);
-                    if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&rest_flags[t]) != 0)) {
 #pragma unroll 1
-                        for (int i = 0; i < kKeys / 16; ++i)
-                            mma_ts(lead, tO, tS + 8 + i * 16, dv + s * kTile16 + i * 128, id_o, 1);
-                    }
-                    if (j + 1 < n) {
-                        // the turn passes a little early: it takes about as long to arrive
+                    for (int h = 0; h < 2; ++h) {
+                        wait(bars.p_full[t][h], np);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        const uint32_t a = tS + h * kHalf;
+                        const uint64_t b = dv + s * kTile16 + h * (kHalf * 8);
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            if (i == D / 16 - 3 && nt == 2 && lead) mbar_arrive(&bars.turn[t ^ 1]);
-                            score(s1, i);
+                        for (int i = 0; i < kHalf / 16; ++i) mma_ts(lead, tO, a + i * 16, b + i * 128, id_o, (j | h | i) != 0);
+                        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(&rest_flags[t][h]) != 0)) {
+#pragma unroll 1
+                            for (int i = 0; i < kHalf / 16; ++i)
+                                mma_ts(lead, tO, a + 8 + i * 16, b + i * 128, id_o, 1);
                         }
-                        commit(bars.s_full[t]);
+                        if (h == 0) commit(bars.pv_half[t]);
+                        if (j + 1 < n) score(s1, h);
+                    }
+                    if (!ok) break;
+                    if (j + 1 < n) {
                         commit(bars.k_empty[s1]);
                         if (j + 2 == n) commit(bars.q_empty[t]);
                     } else {
-                        if (nt == 2 && lead) mbar_arrive(&bars.turn[t ^ 1]);
                         commit(bars.o_full[t]);
                     }
                     commit(bars.v_empty[s]);
