@@ -21,7 +21,7 @@ namespace {
 // cache, read the reverse), the chain of dependent loads (sequence, length, page) at a few.
 // So a run is looked up once, a lane a token, and then copied four tokens at a time, loads
 // ahead of stores; few tokens get runs of one, so that as many warps as possible share them.
-constexpr int kRun = 16;
+constexpr int kRun = 8;
 constexpr int kBatch = 4;  // tokens loaded before any is stored
 
 template <int D, bool kInt8>
@@ -87,6 +87,12 @@ __device__ __forceinline__ uint4 dequantise8(uint32_t c0, uint32_t c1, __nv_bflo
         o[p] = *reinterpret_cast<const uint32_t *>(&v);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ uint4 shfl_xor_v4(uint4 v, int d)
+{
+    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d),
+                      __shfl_xor_sync(0xffffffffu, v.z, d), __shfl_xor_sync(0xffffffffu, v.w, d));
 }
 
 // Where the tokens of rows t0 + lane, lane < run, lie: the cache row for head 0; -1: a position
@@ -178,6 +184,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvDev kv, KvBatchDev b, ui
     const int64_t stride = is_v ? v_stride : k_stride;
     uint16_t *dst = (is_v ? V : K) + (int64_t)t0 * stride + h * D + d;
     const uint32_t base = kv_opaque(0x43004300u);
+    const bool odd = lane & 1;
     const int64_t head = (int64_t)h << kv.page_shift;
     const int64_t rows = run_rows(kv, b, t0, run, lane);
     for (int i0 = 0; i0 < run; i0 += kBatch) {
@@ -199,13 +206,18 @@ __global__ void __launch_bounds__(256) kv_read_kernel(KvDev kv, KvBatchDev b, ui
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (row[i] == -2) continue;
             uint16_t *const to = dst + (i0 + i) * stride;
             if constexpr (kInt8) {
+                // two neighbouring lanes swap halves, so that each store fills 32-byte sectors
+                // (141741 tokens read: 175 us without, so 165), and what is written makes room
+                // in L2 first (157)
                 const __nv_bfloat162 f = q4_scale_pair(s[i]);
-                *reinterpret_cast<uint4 *>(to) = dequantise8(x[i].x, x[i].y, f, base);
-                *reinterpret_cast<uint4 *>(to + 8) = dequantise8(x[i].z, x[i].w, f, base);
-            } else {
+                const uint4 lo = dequantise8(x[i].x, x[i].y, f, base), hi = dequantise8(x[i].z, x[i].w, f, base);
+                const uint4 got = shfl_xor_v4(odd ? lo : hi, 1);
+                if (row[i] == -2) continue;
+                __stcs(reinterpret_cast<uint4 *>(odd ? to - 8 : to), odd ? got : lo);
+                __stcs(reinterpret_cast<uint4 *>(odd ? to + 8 : to + 16), odd ? hi : got);
+            } else if (row[i] != -2) {
                 *reinterpret_cast<uint4 *>(to) = x[i];
             }
         }
