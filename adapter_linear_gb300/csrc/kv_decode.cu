@@ -431,6 +431,40 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                         w[r][2] = v.z;
                         w[r][3] = v.w;
                     }
+                    if (edge) {
+                        // A weight of 0 does not keep an infinity or a NaN out of a product: where not
+                        // all rows see all tokens, they are taken out and added to the rows that do.
+                        bool bad = false;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t f = finite_part(w[r][i]);
+                                bad |= f != w[r][i];
+                                w[r][i] = f;
+                            }
+                        if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                            for (int y = 0; y < kStep; ++y) {
+                                const uint4 v =
+                                    *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(y, 8 * x + v_chunk(g)));
+                                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int t = 0; t < kN; ++t)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int p = sm_pos[8 * t + 2 * c + e];
+                                        if (tok + y > p || (a.window > 0 && tok + y <= p - a.window)) continue;
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const uint32_t f = u[i] ^ finite_part(u[i]);
+                                            o[t][4 * x + i][e] += bf16_lo(f);
+                                            o[t][4 * x + i][2 + e] += bf16_hi(f);
+                                        }
+                                    }
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);

@@ -283,6 +283,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// Of a pair of bf16: the infinities and NaN become zeros (finite_part), or all but them do
+// (the other half of the same xor).
+__device__ __forceinline__ uint32_t finite_part(uint32_t v)
+{
+    const uint32_t lo = (v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu;
+    const uint32_t hi = (v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u;
+    return lo | hi;
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^x, to about 2^-22 of it; 0 for -inf

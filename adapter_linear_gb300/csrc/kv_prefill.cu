@@ -87,7 +87,8 @@ struct Segment {
     int j0, j1;             // key tiles [j0, j1) of them; j1 == 0: no more segments
     int whole, slot;        // all of the item? else the scratch slot of the piece
     int c0, c1;             // and the CTAs that have pieces of the item
-    int pad[2];
+    int bad;                // V had an infinity or a NaN in a tile that not all rows see (unquantised cache)
+    int pad;
 };
 static_assert(sizeof(Segment) == 64, "segment");
 
@@ -96,6 +97,15 @@ struct Bars {
         v_empty[4], sc_full[6], s_full[2][2], p_full[2][2], pv_half[2], o_full[2], drain[2];
 };
 static_assert(sizeof(Bars) <= 512, "barriers");
+
+// The positions [x, y] that all rows of a segment's block see.
+__device__ __forceinline__ int2 seen_by_all(const Segment *w, int G, int window)
+{
+    const int first = w->tile * kBlockRows, p0 = w->L - w->n;
+    return make_int2(window > 0 ? p0 + (min(first + kBlockRows, w->n * G) - 1) / G - window + 1 : 0, p0 + first / G);
+}
+// Of 16 tokens from tok0, does some row not see one?
+__device__ __forceinline__ bool edge_group(int tok0, int2 seen) { return tok0 + 15 > seen.y || tok0 < seen.x; }
 
 struct Plan {
     int min_rows;
@@ -373,6 +383,40 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 3
     }
 }
 
+// The infinities and NaN of V that the loading warps took out of the segment's tiles, to the
+// rows that see them (whatever the weight: it is positive). pos: the row's position, -1: no row.
+template <int D>
+__device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const Segment *w, int G, int window, int pos,
+                                     uint32_t tO)
+{
+    const int32_t *const table = b.table + (int64_t)w->seq * b.table_stride;
+    const int2 seen = seen_by_all(w, G, window);
+#pragma unroll 1
+    for (int x = 0; x < D; x += 8) {
+        uint32_t o[8];
+        tmem_ld8_wait(tO + x, o);
+#pragma unroll 1
+        for (int tok = w->lo + w->j0 * kKeys; tok < min(w->hi, w->lo + w->j1 * kKeys); ++tok) {
+            if (tok > pos || (window > 0 && tok <= pos - window)) continue;
+            if (!edge_group(tok - ((tok - w->lo) & 15), seen)) continue;
+            const int page = table[tok >> kv.page_shift];
+            if (page < 0 || page >= kv.num_pages) continue;
+            const int64_t row = (((int64_t)page * kv.H + w->head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
+            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(kv.v) + row * D + x);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t f = u[e] ^ finite_part(u[e]);
+                o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16_lo(f));
+                o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16_hi(f));
+            }
+        }
+        __syncwarp();
+        tmem_st8(tO + x, o);
+    }
+    tmem_st_wait();
+}
+
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBatchDev b, KvAttn a, Plan plan)
 {
@@ -542,6 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             uint16_t *const dst = a.O + out_t * a.o_stride + (int64_t)h * D;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const int slot = w->slot, c0 = w->c0, c1 = w->c1;
+            if constexpr (!kInt8) {
+                if (*const_cast<const volatile int *>(&w->bad)) add_bad<D>(kv, b, w, G, a.window, on ? pos : -1, tO);
+            }
             segment_done(seg);
             // a warp's rows of a piece: [D / 4][32][4], so that the warp writes 512 bytes at a time
             float *const part = plan.part + ((int64_t)slot * 8 + warp) * 32 * D + lane * 4;
@@ -706,6 +753,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     cp_async16(smem_u32(dst + tile_off(r, lane % kLanes)), src + p * 512, r < count ? 16u : 0u);
                 }
             };
+            // A weight of 0 does not keep an infinity or a NaN of V out of a product: where not all
+            // rows see all tokens (bf16) they become zeros, and the softmax adds them to the rows
+            // that do.
+            const int2 seen = is_v ? seen_by_all(w, G, a.window) : make_int2(0, INT32_MAX);
+            auto drop_bad = [&](uint8_t *dst, int j) {
+                constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+#pragma unroll 1
+                for (int x = 0; x < kGroups; ++x) {
+                    const int tok0 = lo + j * kKeys + x * 16;
+                    if (!edge_group(tok0, seen) || tok0 >= hi) continue;
+                    auto at = [&](int p) {  // what this lane copied
+                        return reinterpret_cast<uint4 *>(dst + x * 2048 + tile_off(p * kStep + lane / kLanes, lane % kLanes));
+                    };
+                    uint32_t top = 0;  // a carry into a half's highest bit: an exponent of all ones
+#pragma unroll
+                    for (int p = 0; p < 16 / kStep; ++p) {
+                        const uint4 u = *at(p);
+                        top |= (u.x & 0x7F807F80u) + 0x00800080u;
+                        top |= (u.y & 0x7F807F80u) + 0x00800080u;
+                        top |= (u.z & 0x7F807F80u) + 0x00800080u;
+                        top |= (u.w & 0x7F807F80u) + 0x00800080u;
+                    }
+                    if ((top & 0x80008000u) == 0) continue;
+#pragma unroll 1
+                    for (int p = 0; p < 16 / kStep; ++p) {
+                        const uint4 u = *at(p);
+                        *at(p) = make_uint4(finite_part(u.x), finite_part(u.y), finite_part(u.z), finite_part(u.w));
+                    }
+                    *const_cast<volatile int *>(&w->bad) = 1;
+                }
+            };
             int count[kGroups];
             int64_t row[kGroups];
 #pragma unroll
@@ -755,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             }
             if constexpr (!kInt8) {
                 cp_wait<1>();
+                drop_bad(stages + (it % C::kStages) * C::kTileBytes, j0);
                 arrive(full[it % C::kStages]);
             }
             cp_wait<0>();
@@ -817,6 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     for (int y = 0; y < kGroups; ++y) copy(dst + y * 2048, row[y], count[y]);
                     cp_commit();
                     cp_wait<0>();
+                    drop_bad(dst, j);
                     arrive(full[s]);
                 }
             }

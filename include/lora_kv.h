@@ -28,7 +28,9 @@
  *    sets the cache's error word and is not followed; lora_kv_check_errors then returns
  *    LORA_ERR_RANGE, the rows of that sequence are unspecified, other rows stay correct.
  *    Table entries past a sequence's last page are not read.
- *  - Cache rows that hold no token of a sequence may hold anything (inf and NaN included).
+ *  - Cache rows that hold no token of a sequence may hold anything (inf and NaN included). An
+ *    infinity or a NaN in a token's K or V reaches the rows that see that token, no others.
+ *  - T and table_stride * p are at most 2^30, T * n_heads below 2^31 (else LORA_ERR_ARG).
  *  - A cache is not thread-safe: use it from one host thread at a time. Calls on several
  *    streams are allowed: attention calls (which share scratch) are ordered by the library;
  *    the order of a write and the calls that use what it wrote is the caller's, as for any
