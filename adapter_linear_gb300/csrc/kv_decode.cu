@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     const int g = lane >> 2, c = lane & 3;
     const int G = a.G;
 
-    KvWork<R, kUnit, kHeadUnits> w(kv, b, G, a.window, 0, plan.max_rows, lane);
+    KvWork<R, kUnit, kHeadUnits> w(kv, b, a, 0, plan.max_rows, lane);
     // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
     // they save
     if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits))) return;

@@ -62,6 +62,12 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
     return (((int64_t)page * kv.H) << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
 }
 
+// x / G for 0 <= x < 2^31 (KvAttn::g_mul, g_shift).
+__device__ __forceinline__ int div_g(const KvAttn &a, int x)
+{
+    return a.G == 1 ? x : (int)(__umulhi((uint32_t)x, a.g_mul) >> a.g_shift);
+}
+
 // The work of an attention kernel and one CTA's share of it.
 //
 // An item is (sequence, tile of R rows, kv head); a row is one query head of one new token: row
@@ -76,6 +82,7 @@ template <int R, int kUnit, int kHead>
 struct KvWork {
     const KvDev &kv;
     const KvBatchDev &b;
+    const KvAttn &a;
     const int G, window, min_rows, max_rows, lane;
     int64_t total = 0;           // units of all items
     int64_t grid = 0, u_end = 0;
@@ -86,9 +93,9 @@ struct KvWork {
     int j0 = 0, j1 = 0;          // units of tokens: [j0, j1) of the item's nu - kHead
     KvSeq sh{0, 0, 0};
 
-    __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, int G_, int window_, int min_rows_,
+    __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, const KvAttn &a_, int min_rows_,
                                       int max_rows_, int lane_)
-        : kv(kv_), b(b_), G(G_), window(window_), min_rows(min_rows_), max_rows(max_rows_), lane(lane_)
+        : kv(kv_), b(b_), a(a_), G(a_.G), window(a_.window), min_rows(min_rows_), max_rows(max_rows_), lane(lane_)
     {
         for (int s0 = 0; s0 < b.n_seqs; s0 += 32) {
             const int64_t v = units_of_32(s0);
@@ -181,7 +188,9 @@ private:
     }
     __device__ __forceinline__ void range(const KvSeq &s, int t, int *lo_, int *hi_) const
     {
-        const int i0 = (int)((int64_t)t * R / G), i1 = (int)min((int64_t)s.n - 1, ((int64_t)t * R + R - 1) / G);
+        // (n G < 2^31, and the last tile's last row may pass it)
+        const int r1 = min(t * R + (R - 1u), s.n * (uint32_t)G - 1u);
+        const int i0 = div_g(a, t * R), i1 = div_g(a, r1);
         const int p0 = s.L - s.n + i0, p1 = s.L - s.n + i1;
         *hi_ = max(0, p1 + 1);
         *lo_ = min((window > 0 ? max(0, p0 - window + 1) : 0) & ~15, *hi_);
@@ -299,6 +308,13 @@ __device__ __forceinline__ float fast_exp2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fast_log2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 

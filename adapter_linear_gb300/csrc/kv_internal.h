@@ -39,13 +39,16 @@ struct KvAttn {
     float *lse;          // or nullptr
     int64_t q_stride, o_stride;
     int Hq, G;           // query heads; query heads per kv head
+    uint32_t g_mul;      // x / G = x g_mul >> (32 + g_shift) for 0 <= x < 2^31, G > 1
+    int g_shift;
     int window;          // 0: none
     float scale;
 };
 
 // The kernel for short chunks. It takes the sequences of at most max_rows rows (new tokens times
-// G); max_new is the caller's bound on the new tokens of one. part, count: scratch of kv_decode_part_floats floats and kv_decode_grid ints (zero
-// between calls), used by one call at a time.
+// G); max_new is the caller's bound on the new tokens of one. part, count: scratch of
+// kv_decode_part_floats floats and kv_decode_grid ints (zero between calls), used by one call at a
+// time.
 int kv_decode_grid(int num_sms);
 size_t kv_decode_part_floats(int D, int num_sms);
 cudaError_t launch_kv_decode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int max_new,

@@ -71,7 +71,8 @@ struct Cfg {
     static constexpr int kQ = 0;
     static constexpr int kK = 2 * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    static constexpr int kScales = kV + kStages * kTileBytes;  // float [kRing][2][128]: the keys', the values'
+    static constexpr int kScales = kV + kStages * kTileBytes;  // float [kRing][2][128]: the keys' (times the
+                                                               // score's), the values'
     static constexpr int kSegs = kScales + kRing * 256 * 4;
     static constexpr int kBars = kSegs + kSegments * 64;
     static constexpr int kOut = kBars + 512;                   // a softmax warp's 32 rows x 32 columns of O
@@ -255,7 +256,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, small_wait(bar, parity, abort_flag, err));
 }
 
-// The row's scores of 32 keys in units of log2, in pairs: raw ones (as loaded) times mul and the
+// The row's scores of 32 keys in units of log2, in pairs: raw ones (as loaded) times mul or the
 // keys' scales, -inf where the row does not see the key (kMask); returns the largest.
 template <bool kInt8, bool kMask>
 __device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, int lim, int low, uint64_t mul,
@@ -264,10 +265,12 @@ __device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const f
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < kPart / 2; ++i) {
-        z[i] = mul2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), mul);
+        z[i] = pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
         if (kInt8) {
             const ulonglong2 c = *reinterpret_cast<const ulonglong2 *>(sc + 2 * (i & ~1));
             z[i] = mul2(z[i], i & 1 ? c.y : c.x);
+        } else {
+            z[i] = mul2(z[i], mul);
         }
         float a, b;
         unpack2(z[i], &a, &b);
@@ -506,7 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const int pos = w->L - w->n + i;
             const int tok_lo = w->lo;
             float m = -INFINITY, l = 0.0f;
-            const uint64_t mul_2 = pack2(plan.scale_log2, plan.scale_log2);  // raw score -> units of log2
+            // raw score -> units of log2 (an 8-bit cache's keys' scales have that factor already)
+            const uint64_t mul_2 = pack2(plan.scale_log2, plan.scale_log2);
+            float thr = -INFINITY;  // a key above this may hold much of the row's weight so far
             for (int j = j0; j < j1; ++j, ++it, ++ns) {
                 const int tok0 = tok_lo + j * kKeys;
                 const int lim = pos - tok0;
@@ -537,9 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     tmem_ld32(tS + (k0 + kPart) % kKeys, s);  // (the last one's is not used)
                     // two parts where a key may hold much of a row's weight; m is moved with the tile's
                     // first keys, and where it is far off
-                    const float mx = m == -INFINITY ? 0.0f : m;
-                    const bool far = top > mx + 16.0f || (m == -INFINITY && top > m);
-                    const bool rest = __any_sync(0xffffffffu, far || 3.0f * fast_exp2(top - mx) > l);
+                    const bool rest = __any_sync(0xffffffffu, top > thr);
+                    const bool far = top > m + 16.0f;
                     if (rest && (x == 0 || __any_sync(0xffffffffu, far))) {
                         const float m2 = x == 0 || far ? fmaxf(m, top) : m;
                         const float down = m == -INFINITY ? 0.0f : fast_exp2(m - m2);
@@ -562,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     const float mn = m == -INFINITY ? 0.0f : m;
                     l += mask ? part_weights<kInt8, true>(z, tS + k0, sc + k0, mn, rest)
                               : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, rest);
+                    thr = mn + fminf(fast_log2(l) - 1.58496f, 16.0f);  // a third of what the row has
                     rest_half |= rest;
                     if (x & 1) {
                         if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t][x >> 1])[warp & 3] = rest_half;
@@ -701,6 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
         uint64_t *const full = is_v ? bars.v_full : bars.k_full, *const empty = is_v ? bars.v_empty : bars.k_empty;
         const void *const arena = is_v ? kv.v : kv.k;
         const uint16_t *const scales = is_v ? kv.vs : kv.ks;
+        const float scale_mul = is_v ? 1.0f : plan.scale_log2;
         float *const scale_part = scale_ring + (is_v ? 128 : 0) + (lw & 1) * 64;
         uint8_t *const stages = smem + (is_v ? C::kV : C::kK) + (lw & 1) * 8192;
         int it = 0;
@@ -864,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                         const int64_t r = x ? row[2 * y + 1] : row[2 * y];
                         sc[y] = 0.0f;
                         if ((lane & 15) < (x ? count[2 * y + 1] : count[2 * y]))
-                            sc[y] = __uint_as_float((uint32_t)scales[r + (lane & 15)] << 16);
+                            sc[y] = __uint_as_float((uint32_t)scales[r + (lane & 15)] << 16) * scale_mul;
                     }
                     // groups 0 and 1 of this tile are in registers; 2, 3 and the next tile's 0, 1
                     // are on their way while the two before them are converted
@@ -996,7 +1002,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             __syncwarp();
         } else if (t == 2) {
             // ------------------------------------------- the share, segment by segment
-            KvWork<kBlockRows, kKeys, kHeadUnits> w(kv, b, G, a.window, plan.min_rows, INT32_MAX, lane);
+            KvWork<kBlockRows, kKeys, kHeadUnits> w(kv, b, a, plan.min_rows, INT32_MAX, lane);
             bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
             for (int seg = 0;; ++seg) {
                 if (!warp_wait(&bars.seg_empty[seg % kSegments], ((uint32_t)(seg / kSegments) & 1u) ^ 1u, &abort_flag,
