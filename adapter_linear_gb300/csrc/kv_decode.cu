@@ -20,6 +20,12 @@
 // last (a counter) joins its pieces in CTA order: the result does not depend on which one it is.
 // Inside a CTA the four warps take 16-token steps in turn, each streaming its own codes through
 // its own ring of shared memory with 16-byte asynchronous copies: no barrier until an item ends.
+//
+// Measured, 32 query heads on 8 kv heads of 128 values: 64 requests of one token over 17 to 8191
+// tokens, 8-bit, 98 us (5.6 TB/s); 256 requests over 500 to 4095, bf16, 361 us (6.7 TB/s, the copy
+// bandwidth); 32 requests of 3 to 6 tokens over 300 to 6000, 8-bit, 81 us (2.7 TB/s: three row
+// tiles' accumulators leave 8 warps an SM, which wait for their own arithmetic); one request over
+// 2047 tokens 11 us (loads that depend on one another: lengths, pages, codes, then the join).
 #include <climits>
 #include <type_traits>
 
@@ -45,8 +51,9 @@ struct Cfg {
     static constexpr int kTile = kStep * kRowBytes;              // K or V of a step
     static constexpr int kStage = 2 * kTile + 4 * kStep;         // K, V, then both scales
     static constexpr bool kWide = kRowBytes == 256;
-    // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers; rows of 256
-    // bytes: 2 of 98 KB): 100 to 150 KB in flight beside the stages in use
+    // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers, 2 for three, which
+    // spill at 3: 104 us against 81 for 32 drafts; rows of 256 bytes: 2 of 98 KB): 100 to
+    // 150 KB in flight beside the stages in use
     static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
     static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 ? 4 : 3;
     static constexpr int kRing = kStages * kStage;
@@ -104,6 +111,280 @@ struct Plan {
     float *part;         // [2 grid][rows][D] + [2 grid][rows][2] (m, l)
     int *count;          // [grid] arrivals at the item that starts in that CTA and ends in another
 };
+
+// A warp's steps of an item, nk of them from token `tok`, for the first kT tiles of its rows, and
+// then their O into the ring and (m, l) into sm_m and sm_l. issue() starts the copy of the next step.
+template <int D, bool kInt8, int kN, int kT, class Issue>
+__device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int window, int rows, int pos_min, int pos_max,
+                                          uint32_t base, uint8_t *ring, const uint4 (&sm_q)[kN][D / 32][32],
+                                          const float *sm_back, const int *sm_pos, float *sm_m, float *sm_l)
+{
+    using C = Cfg<D, kInt8, kN>;
+    constexpr int kM = D / 16;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // of the rows this lane has scores of: 8 t + 2 c, + 1
+    float back_mul[kT][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+        back_mul[t][0] = sm_back[8 * t + 2 * c];
+        back_mul[t][1] = sm_back[8 * t + 2 * c + 1];
+    }
+    float o[kT][kM][4];
+    float m[kT][2], l[kT][2];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
+        m[t][0] = m[t][1] = -INFINITY;
+        l[t][0] = l[t][1] = 0.0f;
+    }
+
+    int stage = 0;
+    for (int k = 0; k < nk; ++k, tok += kStep * kWarps) {
+        cp_wait<C::kStages - 2>();
+        __syncwarp();
+        const uint8_t *st = ring + stage * C::kStage;
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+
+        // S^T = K Q^T: rows are tokens g and g + 8, columns the query rows
+        float s[kT][4];
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < C::kRowBytes / 64; ++x) {
+            const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g, 4 * x + c));
+            const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g + 8, 4 * x + c));
+            const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
+            if constexpr (kInt8) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    uint32_t u[2][4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        codes4_to_f16(u0[j + y], &u[y][0], &u[y][2]);
+                        codes4_to_f16(u1[j + y], &u[y][1], &u[y][3]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < kT; ++t) {
+                        const uint4 q = sm_q[t][2 * x + j / 2][lane];
+                        mma16816_f16(s[t], u[0][0], u[0][1], u[0][2], u[0][3], q.x, q.y);
+                        mma16816_f16(s[t], u[1][0], u[1][1], u[1][2], u[1][3], q.z, q.w);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < kT; ++t) {
+                    const uint4 q = sm_q[t][x][lane];
+                    mma16816(s[t], u0[0], u1[0], u0[1], u1[1], q.x, q.y);
+                    mma16816(s[t], u0[2], u1[2], u0[3], u1[3], q.z, q.w);
+                }
+            }
+        }
+
+        // z in units of log2, masked; s[t][2 y + e]: token g + 8 y, row 8 t + 2 c + e
+        float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
+        if (kInt8) {
+            const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * C::kTile);
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                ks[y] = __uint_as_float((uint32_t)sc[g + 8 * y] << 16);
+                vs[y] = __uint_as_float((uint32_t)sc[16 + g + 8 * y] << 16);
+            }
+        }
+        const bool edge = tok + kStep - 1 > pos_min || (window > 0 && tok <= pos_max - window);
+        bool grow = false;
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    s[t][2 * y + e] *= back_mul[t][e];
+                    if (kInt8) s[t][2 * y + e] *= ks[y];
+                    if (edge) {
+                        const int j = tok + g + 8 * y, p = sm_pos[8 * t + 2 * c + e];
+                        const bool see = j <= p && (window == 0 || j > p - window);
+                        s[t][2 * y + e] = see ? s[t][2 * y + e] : -INFINITY;
+                    }
+                }
+                grow |= fmaxf(s[t][e], s[t][2 + e]) > m[t][e] + 8.0f;
+            }
+
+        // The maximum only has to be near the true one: O and l are rescaled when a key passes
+        // it by 2^8 (weights then reach 256, which changes nothing about their precision).
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float v = fmaxf(s[t][e], s[t][2 + e]);
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    v = fmaxf(v, m[t][e]);
+                    const float down = m[t][e] == -INFINITY ? 0.0f : fast_exp2(m[t][e] - v);
+                    m[t][e] = v;
+                    l[t][e] *= down;
+#pragma unroll
+                    for (int i = 0; i < kM; ++i) {
+                        o[t][i][e] *= down;
+                        o[t][i][2 + e] *= down;
+                    }
+                }
+        }
+        // Weights: summed in fp32, and for the product with V a pair of bf16, the rounded weight
+        // and the rest (together 2^-17 of it: one bf16 alone, 2^-8, shows in rows that see few
+        // keys, and HBM leaves the tensor cores the time). An 8-bit cache's V scale is
+        // multiplied in first; a masked key's weight is 0 whatever its scale is.
+        uint32_t p[kT][2], p2[kT][2];
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                float w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float z = s[t][2 * y + e];
+                    w[e] = fast_exp2(z - (m[t][e] == -INFINITY ? 0.0f : m[t][e]));
+                    l[t][e] += w[e];
+                    if (kInt8) w[e] = z == -INFINITY ? 0.0f : w[e] * vs[y];
+                }
+                const uint32_t top = pack_bf16x2(w[0], w[1]);
+                p[t][y] = transpose8x8(top);
+                p2[t][y] = transpose8x8(pack_bf16x2(w[0] - bf16_lo(top), w[1] - bf16_hi(top)));
+            }
+
+        // O^T += V^T P^T: a lane reads its dims of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9; dims
+        // 2 i and 2 i + 1 of them are rows g and g + 8 of MMA i
+        const uint8_t *vt = st + C::kTile;
+        if constexpr (kInt8) {
+            uint32_t w[4][D / 32];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                if constexpr (D == 128) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, v_chunk(g)));
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    w[r][2] = v.z;
+                    w[r][3] = v.w;
+                } else {
+                    const uint2 v =
+                        *reinterpret_cast<const uint2 *>(vt + swz<C::kRowBytes>(row, g >> 1) + (g & 1) * 8);
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kM; ++i) {
+                const int x = i >> 1, y = 2 * (i & 1);
+                const uint32_t a0 = codes_pair_to_bf16(w[0][x], w[1][x], y, base);
+                const uint32_t a1 = codes_pair_to_bf16(w[0][x], w[1][x], y + 1, base);
+                const uint32_t a2 = codes_pair_to_bf16(w[2][x], w[3][x], y, base);
+                const uint32_t a3 = codes_pair_to_bf16(w[2][x], w[3][x], y + 1, base);
+#pragma unroll
+                for (int t = 0; t < kT; ++t) {
+                    mma16816(o[t][i], a0, a1, a2, a3, p[t][0], p[t][1]);
+                    mma16816(o[t][i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) {
+                uint32_t w[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                    const uint4 v =
+                        *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, 8 * x + v_chunk(g)));
+                    w[r][0] = v.x;
+                    w[r][1] = v.y;
+                    w[r][2] = v.z;
+                    w[r][3] = v.w;
+                }
+                if (edge) {
+                    // A weight of 0 does not keep an infinity or a NaN out of a product: where not
+                    // all rows see all tokens, they are taken out and added to the rows that do.
+                    bool bad = false;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t f = finite_part(w[r][i]);
+                            bad |= f != w[r][i];
+                            w[r][i] = f;
+                        }
+                    if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                        for (int y = 0; y < kStep; ++y) {
+                            const uint4 v =
+                                *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(y, 8 * x + v_chunk(g)));
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int t = 0; t < kT; ++t)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int p = sm_pos[8 * t + 2 * c + e];
+                                    if (tok + y > p || (window > 0 && tok + y <= p - window)) continue;
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint32_t f = u[i] ^ finite_part(u[i]);
+                                        o[t][4 * x + i][e] += bf16_lo(f);
+                                        o[t][4 * x + i][2 + e] += bf16_hi(f);
+                                    }
+                                }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
+                    const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
+                    const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
+                    const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+#pragma unroll
+                    for (int t = 0; t < kT; ++t) {
+                        mma16816(o[t][4 * x + i], a0, a1, a2, a3, p[t][0], p[t][1]);
+                        mma16816(o[t][4 * x + i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        issue();
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // ---- join the warps: O in the warp's ring, (m, l) beside it
+    float *so = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 8 * t + 2 * c + e;
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+            if (g == 0) {
+                sm_m[r] = m[t][e];
+                sm_l[r] = l[t][e];
+            }
+            // MMA i, rows g and g + 8: dims d + 2 i and d + 2 i + 1 (bf16: of each 64-dim half)
+            if (r < rows)
+#pragma unroll
+                for (int i = 0; i < kM; i += 2) {
+                    const int d = kInt8 ? (D == 128 ? 16 * v_chunk(g) : 8 * g) + 2 * i
+                                        : 64 * (i / 4) + 8 * v_chunk(g) + 2 * (i % 4);
+                    *reinterpret_cast<float4 *>(so + r * C::kLdO + d) =
+                        make_float4(o[t][i][e], o[t][i][2 + e], o[t][i + 1][e], o[t][i + 1][2 + e]);
+                }
+        }
+}
 
 template <int D, bool kInt8, int kN>
 __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
@@ -244,271 +525,18 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             }
         }
         __syncthreads();
-        // of the rows this lane has scores of: 8 t + 2 c, + 1
-        float back_mul[kN][2];
-#pragma unroll
-        for (int t = 0; t < kN; ++t) {
-            back_mul[t][0] = sm_back[8 * t + 2 * c];
-            back_mul[t][1] = sm_back[8 * t + 2 * c + 1];
-        }
         const int pos_min = sh.L - sh.n + tile * R / G, pos_max = sh.L - sh.n + (tile * R + rows - 1) / G;
-
-        float o[kN][kM][4];
-        float m[kN][2], l[kN][2];
-#pragma unroll
-        for (int t = 0; t < kN; ++t) {
-#pragma unroll
-            for (int i = 0; i < kM; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[t][i][e] = 0.0f;
-            m[t][0] = m[t][1] = -INFINITY;
-            l[t][0] = l[t][1] = 0.0f;
-        }
-
-        int tok = tok0 + kStep * warp;
-        int stage = 0;
-        for (int k = 0; k < nk; ++k, tok += kStep * kWarps) {
-            cp_wait<C::kStages - 2>();
-            __syncwarp();
-            const uint8_t *st = ring + stage * C::kStage;
-            stage = stage + 1 == C::kStages ? 0 : stage + 1;
-
-            // S^T = K Q^T: rows are tokens g and g + 8, columns the query rows
-            float s[kN][4];
-#pragma unroll
-            for (int t = 0; t < kN; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
-#pragma unroll
-            for (int x = 0; x < C::kRowBytes / 64; ++x) {
-                const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g, 4 * x + c));
-                const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz<C::kRowBytes>(g + 8, 4 * x + c));
-                const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
-                if constexpr (kInt8) {
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        uint32_t u[2][4];
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            codes4_to_f16(u0[j + y], &u[y][0], &u[y][2]);
-                            codes4_to_f16(u1[j + y], &u[y][1], &u[y][3]);
-                        }
-#pragma unroll
-                        for (int t = 0; t < kN; ++t) {
-                            const uint4 q = sm_q[t][2 * x + j / 2][lane];
-                            mma16816_f16(s[t], u[0][0], u[0][1], u[0][2], u[0][3], q.x, q.y);
-                            mma16816_f16(s[t], u[1][0], u[1][1], u[1][2], u[1][3], q.z, q.w);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int t = 0; t < kN; ++t) {
-                        const uint4 q = sm_q[t][x][lane];
-                        mma16816(s[t], u0[0], u1[0], u0[1], u1[1], q.x, q.y);
-                        mma16816(s[t], u0[2], u1[2], u0[3], u1[3], q.z, q.w);
-                    }
-                }
-            }
-
-            // z in units of log2, masked; s[t][2 y + e]: token g + 8 y, row 8 t + 2 c + e
-            float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
-            if (kInt8) {
-                const uint16_t *sc = reinterpret_cast<const uint16_t *>(st + 2 * C::kTile);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    ks[y] = __uint_as_float((uint32_t)sc[g + 8 * y] << 16);
-                    vs[y] = __uint_as_float((uint32_t)sc[16 + g + 8 * y] << 16);
-                }
-            }
-            const bool edge = tok + kStep - 1 > pos_min || (a.window > 0 && tok <= pos_max - a.window);
-            bool grow = false;
-#pragma unroll
-            for (int t = 0; t < kN; ++t)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        s[t][2 * y + e] *= back_mul[t][e];
-                        if (kInt8) s[t][2 * y + e] *= ks[y];
-                        if (edge) {
-                            const int j = tok + g + 8 * y, p = sm_pos[8 * t + 2 * c + e];
-                            const bool see = j <= p && (a.window == 0 || j > p - a.window);
-                            s[t][2 * y + e] = see ? s[t][2 * y + e] : -INFINITY;
-                        }
-                    }
-                    grow |= fmaxf(s[t][e], s[t][2 + e]) > m[t][e] + 8.0f;
-                }
-
-            // The maximum only has to be near the true one: O and l are rescaled when a key passes
-            // it by 2^8 (weights then reach 256, which changes nothing about their precision).
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int t = 0; t < kN; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v = fmaxf(s[t][e], s[t][2 + e]);
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        v = fmaxf(v, m[t][e]);
-                        const float down = m[t][e] == -INFINITY ? 0.0f : fast_exp2(m[t][e] - v);
-                        m[t][e] = v;
-                        l[t][e] *= down;
-#pragma unroll
-                        for (int i = 0; i < kM; ++i) {
-                            o[t][i][e] *= down;
-                            o[t][i][2 + e] *= down;
-                        }
-                    }
-            }
-            // Weights: summed in fp32, and for the product with V a pair of bf16, the rounded weight
-            // and the rest (together 2^-17 of it: one bf16 alone, 2^-8, shows in rows that see few
-            // keys, and HBM leaves the tensor cores the time). An 8-bit cache's V scale is
-            // multiplied in first; a masked key's weight is 0 whatever its scale is.
-            uint32_t p[kN][2], p2[kN][2];
-#pragma unroll
-            for (int t = 0; t < kN; ++t)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float w[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float z = s[t][2 * y + e];
-                        w[e] = fast_exp2(z - (m[t][e] == -INFINITY ? 0.0f : m[t][e]));
-                        l[t][e] += w[e];
-                        if (kInt8) w[e] = z == -INFINITY ? 0.0f : w[e] * vs[y];
-                    }
-                    const uint32_t top = pack_bf16x2(w[0], w[1]);
-                    p[t][y] = transpose8x8(top);
-                    p2[t][y] = transpose8x8(pack_bf16x2(w[0] - bf16_lo(top), w[1] - bf16_hi(top)));
-                }
-
-            // O^T += V^T P^T: a lane reads its dims of tokens 2 c, 2 c + 1, 2 c + 8, 2 c + 9; dims
-            // 2 i and 2 i + 1 of them are rows g and g + 8 of MMA i
-            const uint8_t *vt = st + C::kTile;
-            if constexpr (kInt8) {
-                uint32_t w[4][D / 32];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                    if constexpr (D == 128) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, v_chunk(g)));
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        w[r][2] = v.z;
-                        w[r][3] = v.w;
-                    } else {
-                        const uint2 v =
-                            *reinterpret_cast<const uint2 *>(vt + swz<C::kRowBytes>(row, g >> 1) + (g & 1) * 8);
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kM; ++i) {
-                    const int x = i >> 1, y = 2 * (i & 1);
-                    const uint32_t a0 = codes_pair_to_bf16(w[0][x], w[1][x], y, base);
-                    const uint32_t a1 = codes_pair_to_bf16(w[0][x], w[1][x], y + 1, base);
-                    const uint32_t a2 = codes_pair_to_bf16(w[2][x], w[3][x], y, base);
-                    const uint32_t a3 = codes_pair_to_bf16(w[2][x], w[3][x], y + 1, base);
-#pragma unroll
-                    for (int t = 0; t < kN; ++t) {
-                        mma16816(o[t][i], a0, a1, a2, a3, p[t][0], p[t][1]);
-                        mma16816(o[t][i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    uint32_t w[4][4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                        const uint4 v =
-                            *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(row, 8 * x + v_chunk(g)));
-                        w[r][0] = v.x;
-                        w[r][1] = v.y;
-                        w[r][2] = v.z;
-                        w[r][3] = v.w;
-                    }
-                    if (edge) {
-                        // A weight of 0 does not keep an infinity or a NaN out of a product: where not
-                        // all rows see all tokens, they are taken out and added to the rows that do.
-                        bool bad = false;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t f = finite_part(w[r][i]);
-                                bad |= f != w[r][i];
-                                w[r][i] = f;
-                            }
-                        if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll 1
-                            for (int y = 0; y < kStep; ++y) {
-                                const uint4 v =
-                                    *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(y, 8 * x + v_chunk(g)));
-                                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                                for (int t = 0; t < kN; ++t)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int p = sm_pos[8 * t + 2 * c + e];
-                                        if (tok + y > p || (a.window > 0 && tok + y <= p - a.window)) continue;
-#pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const uint32_t f = u[i] ^ finite_part(u[i]);
-                                            o[t][4 * x + i][e] += bf16_lo(f);
-                                            o[t][4 * x + i][2 + e] += bf16_hi(f);
-                                        }
-                                    }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410);
-                        const uint32_t a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
-                        const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410);
-                        const uint32_t a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
-#pragma unroll
-                        for (int t = 0; t < kN; ++t) {
-                            mma16816(o[t][4 * x + i], a0, a1, a2, a3, p[t][0], p[t][1]);
-                            mma16816(o[t][4 * x + i], a0, a1, a2, a3, p2[t][0], p2[t][1]);
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-            issue();
-        }
-        cp_wait<0>();
-        __syncwarp();
-
-        // ---- join the warps: O in the warp's ring, (m, l) beside it
-        float *so = reinterpret_cast<float *>(ring);
-#pragma unroll
-        for (int t = 0; t < kN; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * t + 2 * c + e;
-                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
-                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
-                l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
-                if (g == 0) {
-                    sm_m[warp][r] = m[t][e];
-                    sm_l[warp][r] = l[t][e];
-                }
-                // MMA i, rows g and g + 8: dims d + 2 i and d + 2 i + 1 (bf16: of each 64-dim half)
-                if (r < rows)
-#pragma unroll
-                    for (int i = 0; i < kM; i += 2) {
-                        const int d = kInt8 ? (D == 128 ? 16 * v_chunk(g) : 8 * g) + 2 * i
-                                            : 64 * (i / 4) + 8 * v_chunk(g) + 2 * (i % 4);
-                        *reinterpret_cast<float4 *>(so + r * C::kLdO + d) =
-                            make_float4(o[t][i][e], o[t][i][2 + e], o[t][i + 1][e], o[t][i + 1][2 + e]);
-                    }
-            }
+        // one tile where the item's rows fit it (40 requests of 7 heads, 37 of them of one token: 99 us
+        // with all tiles, 93 with one)
+        auto run = [&](auto tiles) {
+            run_steps<D, kInt8, kN, decltype(tiles)::value>(issue, nk, tok0 + kStep * warp, a.window, rows, pos_min,
+                                                            pos_max, base, ring, sm_q, sm_back, sm_pos, sm_m[warp],
+                                                            sm_l[warp]);
+        };
+        if (rows <= 8)
+            run(std::integral_constant<int, 1>());
+        else
+            run(std::integral_constant<int, kN>());
         __syncthreads();
         const bool whole = w.whole();
         const int slot = 2 * blockIdx.x + (w.first() ? 1 : 0);
