@@ -22,8 +22,8 @@
 // its own ring of shared memory with 16-byte asynchronous copies: no barrier until an item ends.
 //
 // Measured, 32 query heads on 8 kv heads of 128 values: 64 requests of one token over 17 to 8191
-// tokens, 8-bit, 98 us (5.6 TB/s); 256 requests over 500 to 4095, bf16, 361 us (6.7 TB/s, the copy
-// bandwidth); 32 requests of 3 to 6 tokens over 300 to 6000, 8-bit, 81 us (2.7 TB/s: three row
+// tokens, 8-bit, 99 us (5.6 TB/s); 256 requests over 500 to 4095, bf16, 361 us (6.7 TB/s, the copy
+// bandwidth); 32 requests of 3 to 6 tokens over 300 to 6000, 8-bit, 79 us (2.8 TB/s: three row
 // tiles' accumulators leave 8 warps an SM, which wait for their own arithmetic); one request over
 // 2047 tokens 11 us (loads that depend on one another: lengths, pages, codes, then the join).
 #include <climits>
@@ -37,8 +37,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;            // tokens per warp step: never crosses a page (pages hold 16 k)
 constexpr int kUnit = kWarps * kStep;
-constexpr int kHeadUnits = 3;        // an item's cost beside its units: 64 int8 requests 118 us at 0, 104 at 3, 107 at 6
-constexpr int kMinUnits = 2;         // one request, one token: 12.3 us at 1, 11.2 at 2, 11.6 at 4
+// An item's cost beside its units, in units: 32 8-bit drafts 85 us at 2, 81 at 3, 79 at 4, 64 requests of
+// one token 99 at each.
+constexpr int kHeadUnits = 4;
+constexpr int kMinUnits = 2;         // one request, one token: 11.2 us at 1, 11.0 at 2, 11.6 at 4
 
 constexpr int kMaxCtas = 4;    // CTAs an SM, of any variant
 constexpr int kPartRows = 48;  // and the rows that those of one SM hold

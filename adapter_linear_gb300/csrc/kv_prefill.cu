@@ -24,9 +24,13 @@
 // The softmax of a row, a thread: 32 scores at a time from tensor memory into registers, the next
 // 32 on their way while these become weights.
 //
-// What bounds it: the tensor cores take 2900 cycles of the 3500 that a key tile of 2 x 128 rows
-// takes at D = 128, bf16; with an 8-bit cache (6000 cycles) they share shared memory's bandwidth
-// with the conversion of the codes, and the softmax's two multiplications by scales come on top.
+// What bounds it: the softmax. Of the 3500 cycles that a key tile of 2 x 128 rows takes at D = 128,
+// bf16, it takes 2900 in each row's thread (41 % of the issue slots are used, the rest is
+// latency between dependent instructions, two softmax warps a scheduler); with an 8-bit cache 6000 of
+// 6200 (51 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
+// the loads of scales and the MMAs' operands use 80 % of shared memory's bandwidth. The tensor cores
+// are active 46 and 42 % of the time. 32 query heads on 8 kv heads of 128 values: 8 prompts of
+// 2048 tokens bf16 381 us (0.72 PFLOP/s), 512 tokens over 32000 8-bit 365 us (0.74).
 //
 // An 8-bit cache's scales stay outside the products: the codes are exact in bf16, a key's scale
 // multiplies its column of S and a value's its weight.
@@ -56,8 +60,8 @@ constexpr int kSoftRegs = 152, kLoadRegs = 120, kMmaRegs = 88;
 static_assert(2 * kSoftRegs + kLoadRegs + kMmaRegs <= 4 * 128, "register split");
 
 // What an item costs beside its key tiles, in key tiles (its first tile's two parts, Q, the output):
-// 8 prompts of 2048 bf16 557 us at 0, 424 at 1, 378 at 2, 381 at 3, 406 at 6.
-constexpr int kHeadUnits = 2;
+// 8 prompts of 2048 bf16 442 us at 1, 388 at 2, 381 at 3; 40 mixed 8-bit requests 94, 94 and 95.
+constexpr int kHeadUnits = 3;
 constexpr int kSegments = 4;
 constexpr int kOutPitch = 80;  // bytes of a row of 32 bf16 columns: rows start 5 x 16 bytes apart
 
