@@ -27,8 +27,8 @@
 // What bounds it: the softmax. Of the 3500 cycles that a key tile of 2 x 128 rows takes at D = 128,
 // bf16, it takes 2900 in each row's thread (41 % of the issue slots are used, the rest is
 // latency between dependent instructions, two softmax warps a scheduler); with an 8-bit cache 6000 of
-// 6200 (51 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
-// the loads of scales and the MMAs' operands use 80 % of shared memory's bandwidth. The tensor cores
+// 6200 (47 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
+// the loads of scales and the MMAs' operands use 84 % of shared memory's bandwidth. The tensor cores
 // are active 46 and 42 % of the time. 32 query heads on 8 kv heads of 128 values: 8 prompts of
 // 2048 tokens bf16 381 us (0.72 PFLOP/s), 512 tokens over 32000 8-bit 365 us (0.74).
 //
@@ -185,18 +185,24 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[kPart])
                  "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
                  "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+                   "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
                  : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[kPart])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                   "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                   "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
 __device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8])
@@ -263,8 +269,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // The row's scores of 32 keys in units of log2, in pairs: raw ones (as loaded) times mul or the
 // keys' scales, -inf where the row does not see the key (kMask); returns the largest.
 template <bool kInt8, bool kMask>
-__device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, int lim, int low, uint64_t mul,
-                                             uint64_t (&z)[kPart / 2])
+__device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, int lim, int low,
+                                             uint64_t mul, uint64_t (&z)[kPart / 2])
 {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -393,8 +399,8 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 3
 // The infinities and NaN of V that the loading warps took out of the segment's tiles, to the
 // rows that see them (whatever the weight: it is positive). pos: the row's position, -1: no row.
 template <int D>
-__device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const Segment *w, int G, int window, int pos,
-                                     uint32_t tO)
+__device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const Segment *w, int G, int window,
+                                        int pos, uint32_t tO)
 {
     const int32_t *const table = b.table + (int64_t)w->seq * b.table_stride;
     const int2 seen = seen_by_all(w, G, window);
@@ -408,7 +414,8 @@ __device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, co
             if (!edge_group(tok - ((tok - w->lo) & 15), seen)) continue;
             const int page = table[tok >> kv.page_shift];
             if (page < 0 || page >= kv.num_pages) continue;
-            const int64_t row = (((int64_t)page * kv.H + w->head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
+            const int64_t row =
+                (((int64_t)page * kv.H + w->head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
             const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(kv.v) + row * D + x);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -477,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
 
     // segment `k` of the share once it is there (a whole warp); null: no more, or a wait ran out
     auto segment = [&](int k) -> const Segment * {
-        if (!warp_wait(&bars.seg_full[k % kSegments], (uint32_t)(k / kSegments) & 1u, &abort_flag, kv.err)) return nullptr;
+        if (!warp_wait(&bars.seg_full[k % kSegments], (uint32_t)(k / kSegments) & 1u, &abort_flag, kv.err))
+            return nullptr;
         const Segment *g = segs + k % kSegments;
         return g->j1 > 0 ? g : nullptr;
     };
@@ -573,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     thr = mn + fminf(fast_log2(l) - 1.58496f, 16.0f);  // a third of what the row has
                     rest_half |= rest;
                     if (x & 1) {
-                        if (lane == 0) reinterpret_cast<volatile uint8_t *>(&rest_flags[t][x >> 1])[warp & 3] = rest_half;
+                        if (lane == 0)
+                            reinterpret_cast<volatile uint8_t *>(&rest_flags[t][x >> 1])[warp & 3] = rest_half;
                         rest_half = false;
                         tmem_st_wait();
                         tc_fence_before_sync();
@@ -774,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     const int tok0 = lo + j * kKeys + x * 16;
                     if (!edge_group(tok0, seen) || tok0 >= hi) continue;
                     auto at = [&](int p) {  // what this lane copied
-                        return reinterpret_cast<uint4 *>(dst + x * 2048 + tile_off(p * kStep + lane / kLanes, lane % kLanes));
+                        return reinterpret_cast<uint4 *>(dst + x * 2048 +
+                                                         tile_off(p * kStep + lane / kLanes, lane % kLanes));
                     };
                     uint32_t top = 0;  // a carry into a half's highest bit: an exponent of all ones
 #pragma unroll
