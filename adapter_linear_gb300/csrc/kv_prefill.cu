@@ -30,7 +30,7 @@
 // 6200 (47 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
 // the loads of scales and the MMAs' operands use 84 % of shared memory's bandwidth. The tensor cores
 // are active 46 and 42 % of the time. 32 query heads on 8 kv heads of 128 values: 8 prompts of
-// 2048 tokens bf16 381 us (0.72 PFLOP/s), 512 tokens over 32000 8-bit 365 us (0.74).
+// 2048 tokens bf16 381 us (0.72 PFLOP/s), 512 tokens over 32000 8-bit 358 us (0.76).
 //
 // An 8-bit cache's scales stay outside the products: the codes are exact in bf16, a key's scale
 // multiplies its column of S and a value's its weight.
@@ -267,10 +267,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 }
 
 // The row's scores of 32 keys in units of log2, in pairs: raw ones (as loaded) times mul or the
-// keys' scales, -inf where the row does not see the key (kMask); returns the largest.
-template <bool kInt8, bool kMask>
-__device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, int lim, int low,
-                                             uint64_t mul, uint64_t (&z)[kPart / 2])
+// keys' scales; returns the largest.
+template <bool kInt8>
+__device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const float *sc, uint64_t mul,
+                                             uint64_t (&z)[kPart / 2])
 {
     float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -284,18 +284,30 @@ __device__ __forceinline__ float part_scores(const uint32_t (&s)[kPart], const f
         }
         float a, b;
         unpack2(z[i], &a, &b);
-        if (kMask) {
-            a = 2 * i <= lim && 2 * i > low ? a : -INFINITY;
-            b = 2 * i + 1 <= lim && 2 * i + 1 > low ? b : -INFINITY;
-            z[i] = pack2(a, b);
-        }
         top[i & 1] = fmaxf(top[i & 1], fmaxf(a, b));
     }
     return fmaxf(top[0], top[1]);
 }
 
+// -inf for the keys that the row does not see: it sees columns above `low` up to `lim`; returns the
+// largest score that is left.
+__device__ __forceinline__ float mask_scores(uint64_t (&z)[kPart / 2], int lim, int low)
+{
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPart / 2; ++i) {
+        float a, b;
+        unpack2(z[i], &a, &b);
+        a = 2 * i <= lim && 2 * i > low ? a : -INFINITY;
+        b = 2 * i + 1 <= lim && 2 * i + 1 > low ? b : -INFINITY;
+        z[i] = pack2(a, b);
+        top = fmaxf(top, fmaxf(a, b));
+    }
+    return top;
+}
+
 // The row's 32 weights 2^(z - m), times the values' scales (0 for a key the row does not see,
-// whatever its scale is), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e, and in column
+// whatever its scale is: kMask, 8-bit), as bf16 pairs: keys 16 i + 2 e, + 1 in column 16 i + e, and in column
 // 16 i + 8 + e what rounding left of them (rest) or zeros. Returns the weights' sum.
 template <bool kInt8, bool kMask>
 __device__ __forceinline__ float part_weights(const uint64_t (&z)[kPart / 2], uint32_t tS, const float *sc, float m,
@@ -321,7 +333,7 @@ __device__ __forceinline__ float part_weights(const uint64_t (&z)[kPart / 2], ui
                 w[e] = mul2(w[e], e & 1 ? v.y : v.x);
             }
             unpack2(w[e], &e0, &e1);
-            if (kInt8 && kMask) {
+            if (kMask) {
                 e0 = z0 == -INFINITY ? 0.0f : e0;
                 e1 = z1 == -INFINITY ? 0.0f : e1;
                 w[e] = pack2(e0, e1);
@@ -544,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     const int k0 = x * kPart;
                     uint64_t z[kPart / 2];
                     tmem_wait32(s);
-                    const float top = mask ? part_scores<kInt8, true>(s, sc + k0, lim - k0, low - k0, mul_2, z)
-                                           : part_scores<kInt8, false>(s, sc + k0, 0, 0, mul_2, z);
+                    float top = part_scores<kInt8>(s, sc + k0, mul_2, z);
+                    if (mask) top = mask_scores(z, lim - k0, low - k0);
                     if (x == 1) {
                         ok = warp_wait(&bars.s_full[t][1], (uint32_t)ns & 1u, &abort_flag, kv.err);
                         if (!ok) break;
@@ -576,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                             for (int y = 0; y < kPart; y += 8) scale_p(tS + k0 - kPart + y, down);
                     }
                     const float mn = m == -INFINITY ? 0.0f : m;
-                    l += mask ? part_weights<kInt8, true>(z, tS + k0, sc + k0, mn, rest)
-                              : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, rest);
+                    l += kInt8 && mask ? part_weights<kInt8, kInt8>(z, tS + k0, sc + k0, mn, rest)
+                                       : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, rest);
                     thr = mn + fminf(fast_log2(l) - 1.58496f, 16.0f);  // a third of what the row has
                     rest_half |= rest;
                     if (x & 1) {
