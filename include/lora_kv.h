@@ -32,9 +32,10 @@
  *    infinity or a NaN in a token's K or V reaches the rows that see that token, no others.
  *  - T and table_stride * p are at most 2^30, T * n_heads below 2^31 (else LORA_ERR_ARG).
  *  - A cache is not thread-safe: use it from one host thread at a time. Calls on several
- *    streams are allowed: attention calls (which share scratch) are ordered by the library;
- *    the order of a write and the calls that use what it wrote is the caller's, as for any
- *    two kernels.
+ *    streams are allowed: attention calls (which share scratch) are ordered by the library,
+ *    those captured in a graph by whoever replays it (no other attention call of the cache beside
+ *    the replay); the order of a write and the calls that use what it wrote is the caller's, as
+ *    for any two kernels.
  */
 #ifndef LORA_KV_H
 #define LORA_KV_H

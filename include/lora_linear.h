@@ -75,7 +75,8 @@ typedef enum {
     LORA_ERR_IN_USE = 12,         /* unload of an adapter a chain still lists  */
     LORA_ERR_RANGE = 13           /* a kernel of the checked build (LORA_CHECK)
                                      met an index outside its table or buffer
-                                     (reported by lora_pool_check_errors)      */
+                                     (reported by lora_pool_check_errors), or
+                                     a paged cache's call did (lora_kv.h)      */
 } lora_status;
 
 /* Limits. */
