@@ -68,7 +68,7 @@ class KvCache:
                                   not t.is_contiguous()):
                 raise LoraError(LORA_ERR_SHAPE, f"KvCache: scales are contiguous {shape[:3]} of bfloat16")
         self.k, self.v, self.k_scales, self.v_scales = k, v, ks, vs
-        self._device = k.device.index or 0
+        self._torch_device, self._device = k.device, k.device.index or 0
         h = ctypes.c_void_p()
         _check(load_library().lora_kv_create(num_pages, page_tokens, kv_heads, head_dim, fmt, _ptr(k), _ptr(v),
                                              _ptr(ks), _ptr(vs), ctypes.byref(h)), "lora_kv_create")
@@ -120,12 +120,15 @@ class KvCache:
     def read(self, batch: KvBatch, K=None, V=None, stream=None):
         """The batch's tokens as bf16 [T, kv_heads, head_dim] keys and values."""
         shape = (batch.T, self.kv_heads, self.head_dim)
+        ks = vs = self.kv_heads * self.head_dim
         if K is None:
-            K = torch.empty(shape, dtype=torch.bfloat16, device=self.k.device)
+            K = torch.empty(shape, dtype=torch.bfloat16, device=self._torch_device)
+        else:
+            ks = self._rows(K, self.kv_heads, batch, "lora_kv_read K")
         if V is None:
-            V = torch.empty(shape, dtype=torch.bfloat16, device=self.k.device)
-        ks = self._rows(K, self.kv_heads, batch, "lora_kv_read K")
-        vs = self._rows(V, self.kv_heads, batch, "lora_kv_read V")
+            V = torch.empty(shape, dtype=torch.bfloat16, device=self._torch_device)
+        else:
+            vs = self._rows(V, self.kv_heads, batch, "lora_kv_read V")
         _check(self._lib.lora_kv_read(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
                                       self._stream(stream)), "lora_kv_read")
         return K, V
@@ -136,15 +139,17 @@ class KvCache:
         Q bf16 [T, n_heads, head_dim]; returns O (as Q) and lse fp32 [T, n_heads]."""
         if Q.dim() != 3:
             raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention: Q is [T, n_heads, head_dim]")
-        T, Hq = Q.shape[0], Q.shape[1]
+        T, Hq, _ = Q.shape
+        qs = self._rows(Q, Hq, batch, "lora_kv_attention Q")
         if O is None:
-            O = torch.empty((T, Hq, self.head_dim), dtype=torch.bfloat16, device=self.k.device)
+            O = torch.empty((T, Hq, self.head_dim), dtype=torch.bfloat16, device=self._torch_device)
+            os_ = Hq * self.head_dim
+        else:
+            os_ = self._rows(O, Hq, batch, "lora_kv_attention O")
         if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=self.k.device)
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=self._torch_device)
         elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention lse: contiguous float32 [T, n_heads] expected")
-        qs = self._rows(Q, Hq, batch, "lora_kv_attention Q")
-        os_ = self._rows(O, Hq, batch, "lora_kv_attention O")
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
         _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, window,

@@ -111,8 +111,6 @@ lora_status lora_kv_read(lora_kv_t kv, void *K, int64_t k_stride, void *V, int64
  *     lse[t,h] = log sum_j exp(z_j),   O[t,h] = sum_j exp(z_j - lse) V_j
  * and O = 0, lse = -inf for a row that sees no token. Scores, softmax and sums are held in
  * fp32; O is rounded to bf16 once. lse (fp32 [T][n_heads]) may be NULL.
- * In a bf16 cache a token of the sequence that a row does not see must still be finite (0
- * times inf in the product with V); an int8 cache has no such condition.
  *   n_heads: a multiple of H_kv, at most 1024. O must not alias Q or the cache.
  * Asynchronous on `stream`. Errors: ARG, SHAPE (n_heads), OOM (scratch), CUDA.
  */
