@@ -21,6 +21,9 @@ namespace {
 // cache, read the reverse), the chain of dependent loads (sequence, length, page) at a few.
 // So a run is looked up once, a lane a token, and then copied four tokens at a time, loads
 // ahead of stores; few tokens get runs of one, so that as many warps as possible share them.
+// Measured, 8 kv heads of 128 values, 8-bit: 141741 tokens read 153 us (5.7 TB/s; runs of 16 157, of
+// 4 160), 16384 written and read 47 us (two kernels of 100 MB). More resident warps do not help: with
+// 48 registers a thread the copies in flight spill (177 and 63 us).
 constexpr int kRun = 8;
 constexpr int kBatch = 4;  // tokens loaded before any is stored
 
@@ -38,7 +41,7 @@ struct RowMap {
 // tie or more than 2^-10 away from one. y = x * (1 / s) is off by less than 2^-15, so rounding it
 // to a multiple of 2^-11 first gives the ties exactly and moves nothing else across one: the codes
 // are those of exact arithmetic without a division each (a division each: 16384 tokens written
-// and read back 76 us, so 57).
+// and read back 76 us, so 56).
 template <int kLanes>
 __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint16_t *scale_bits)
 {
