@@ -543,9 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                 const bool mask = __any_sync(0xffffffffu, lim < kKeys - 1 || low >= 0);
                 const int ring = it % C::kRing;
                 const float *const sc = scale_ring + ring * 256;
+                ok = warp_wait(&bars.s_full[t][0], (uint32_t)ns & 1u, &abort_flag, kv.err);
+                // The scales second: a tile that skipped a segment has not followed sc_full, and a parity
+                // tells a phase only from its neighbours. The MMA warp that made S of tile `it` has seen
+                // v_full of tile it - 1, and a loading warp arrives at a tile's sc_full before it loads the
+                // next: sc_full of every tile up to it - 2 is complete here.
                 if (kInt8)
-                    ok = warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
-                ok = ok && warp_wait(&bars.s_full[t][0], (uint32_t)ns & 1u, &abort_flag, kv.err);
+                    ok = ok && warp_wait(&bars.sc_full[ring], (uint32_t)(it / C::kRing) & 1u, &abort_flag, kv.err);
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint32_t s[kPart];
