@@ -102,14 +102,15 @@ __device__ __forceinline__ uint4 shfl_xor_v4(uint4 v, int d)
 // below zero; -2: nowhere (padding after the last sequence, a bad table entry or length).
 __device__ __forceinline__ int64_t run_rows(const KvDev &kv, const KvBatchDev &b, int t0, int run, int lane)
 {
-    int seq = kv_find_seq(b, t0, lane);
+    int seq = max(0, kv_find_seq(b, t0, lane));
     const int t = t0 + lane;
-    if (seq < 0 || lane >= run) return -2;
-    KvSeq s = kv_seq(b, kv.page_shift, seq, kv.err);
-    while (t - s.row0 >= s.n) {  // a run may end in a later sequence
-        if (++seq >= b.n_seqs) return -2;
+    if (lane >= run) return -2;
+    KvSeq s;
+    for (;; ++seq) {  // a run may end in a later sequence
+        if (seq >= b.n_seqs) return -2;
         s = kv_seq(b, kv.page_shift, seq, kv.err);
         if (t < s.row0) return -2;
+        if (t - s.row0 < s.n) break;
     }
     const int pos = s.L - s.n + (t - s.row0);
     if (pos < 0) return -1;

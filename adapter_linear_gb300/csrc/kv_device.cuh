@@ -11,31 +11,27 @@ namespace lora {
 
 __device__ __forceinline__ void kv_flag_range(int *err) { atomicOr(err, kErrRangeBit); }
 
-// Sequence b's rows [row0, row0 + n) and length L, checked: a start outside 0..T or a length
-// beyond the table flags the error word and reads as an empty sequence.
+// Sequence b's rows [row0, row0 + n) and length L, checked: a start outside 0..T, starts that
+// decrease or a length beyond the table flag the error word and read as an empty sequence.
 struct KvSeq {
     int row0, n, L;
 };
 
 __device__ __forceinline__ KvSeq kv_seq(const KvBatchDev &b, int page_shift, int seq, int *err)
 {
-    KvSeq s;
-    s.row0 = b.start[seq];
-    const int end = b.start[seq + 1];
-    s.n = end - s.row0;
-    s.L = b.kv_len[seq];
-    if (s.row0 < 0 || end > b.T || s.n < 0 || s.L < 0 ||
-        (int64_t)s.L > ((int64_t)b.table_stride << page_shift)) {
+    const int row0 = b.start[seq], end = b.start[seq + 1], L = b.kv_len[seq];
+    // (compared before they are subtracted: the difference of two bad starts may wrap round)
+    if (row0 < 0 || end < row0 || end > b.T || L < 0 || (int64_t)L > ((int64_t)b.table_stride << page_shift)) {
         kv_flag_range(err);
-        s.n = 0;
-        s.L = 0;
+        return KvSeq{0, 0, 0};
     }
-    return s;
+    return KvSeq{row0, end - row0, L};
 }
 
 // The sequence whose rows hold row t (called by a whole warp, the same t in every lane): the
 // last b with start[b] <= t, by a 32-way search: a round narrows the range to a 32nd, so 1024
-// sequences take two dependent loads. -1: before the first row.
+// sequences take two dependent loads. -1: before the first row. Among bad starts the search stops
+// at the first that is above t, so it finds t's sequence or one before it.
 __device__ __forceinline__ int kv_find_seq(const KvBatchDev &b, int t, int lane)
 {
     int lo = 0, len = b.n_seqs;  // the answer is lo - 1 + (number of starts <= t in [lo, lo + len))
@@ -43,7 +39,8 @@ __device__ __forceinline__ int kv_find_seq(const KvBatchDev &b, int t, int lane)
         const int step = (len + 31) >> 5;
         const int at = lo + (lane + 1) * step - 1;  // the last entry of this lane's part
         const bool le = at < lo + len && b.start[at] <= t;
-        const int full = __popc(__ballot_sync(0xffffffffu, le));  // parts that lie wholly below
+        // parts that lie wholly below, up to the first that does not
+        const int full = __clz(__brev(~__ballot_sync(0xffffffffu, le)));
         const int end = lo + len;
         lo += full * step;
         len = min(step - 1, end - lo);
