@@ -478,7 +478,8 @@ lora_status lora_kv_reserve(lora_kv_t p, int max_tokens, int n_heads, int max_se
 {
     if (!p || max_tokens < 0 || max_seqs < 0) return LORA_ERR_ARG;
     if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
-    return max_tokens > max_seqs ? ensure_pre_part(p) : LORA_OK;  // single tokens never need it
+    // all of them may be one sequence's
+    return (int64_t)max_tokens * (n_heads / p->H) > kDecodeRows ? ensure_pre_part(p) : LORA_OK;
 }
 
 lora_status lora_kv_write(lora_kv_t p, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
@@ -535,15 +536,17 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     a.window = std::min(window, kMaxTokens);
     a.scale = scale;
     // Sequences of up to kDecodeRows rows of a kv head go to the short-chunk kernel, others to
-    // the tcgen05 kernel; where max_new says that there is only one kind, one launch takes all.
-    const bool prefill = (int64_t)batch->max_new * a.G > kDecodeRows;
-    const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * batch->max_new;
+    // the tcgen05 kernel; where max_new says that there is only one kind, one launch takes all. (No
+    // sequence has more than T rows, so that a loose bound needs no scratch that lora_kv_reserve leaves out.)
+    const int max_new = std::min(batch->max_new, batch->T);
+    const bool prefill = (int64_t)max_new * a.G > kDecodeRows;
+    const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
     if (prefill && (st = ensure_pre_part(p)) != LORA_OK) return st;
     if ((st = order_attention(p, stream)) != LORA_OK) return st;
     const KvDev kv = kv_view(p);
     const KvBatchDev bd = batch_view(batch);
     if (decode)
-        CUDA_TRY(launch_kv_decode(kv, p->int8, bd, a, batch->max_new, prefill ? kDecodeRows : INT_MAX, p->dec_part,
+        CUDA_TRY(launch_kv_decode(kv, p->int8, bd, a, max_new, prefill ? kDecodeRows : INT_MAX, p->dec_part,
                                   p->count, p->num_sms, stream));
     if (prefill)
         CUDA_TRY(launch_kv_prefill(kv, p->int8, bd, a, decode ? kDecodeRows + 1 : 0, p->pre_part,

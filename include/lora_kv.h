@@ -77,9 +77,10 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
 /* Wait for the device, then free the handle and its scratch (not the arenas). */
 lora_status lora_kv_destroy(lora_kv_t kv);
 
-/* Size the attention's scratch for calls of up to max_tokens rows, n_heads query heads and
- * max_seqs sequences. A larger call grows it, which allocates and synchronises the device:
- * call this first when lora_kv_attention will run inside a CUDA graph capture. */
+/* Make sure of the attention's scratch for calls of up to max_tokens rows, n_heads query heads
+ * and max_seqs sequences, whatever rows each has and whatever max_new they give. The first call
+ * that needs scratch beyond the handle's own allocates it (40 MB): call this first when
+ * lora_kv_attention will run inside a CUDA graph capture. */
 lora_status lora_kv_reserve(lora_kv_t kv, int max_tokens, int n_heads, int max_seqs);
 
 /*
