@@ -47,7 +47,7 @@ EXPORTS = (
     "lora_cache_stats", "lora_pool_selftest_wait", "lora_decode_plan_info", "lora_test_delayed_copy",
     "lora_pool_set_trace", "lora_linear_q4", "lora_base_linear_q4", "lora_dequant_q4",
     "lora_kv_create", "lora_kv_destroy", "lora_kv_reserve", "lora_kv_write", "lora_kv_read",
-    "lora_kv_attention", "lora_kv_check_errors",
+    "lora_kv_attention", "lora_kv_check_errors", "lora_kv_selftest_timeout",
 )
 PLAN_INFO_FIELDS = ("units", "G", "grid", "max_seg", "n_acc", "stages", "tmem_cols", "smem_bytes",
                     "pairs", "col_blocks", "tight", "ntok", "partials_floats", "prefetch_a")
@@ -122,6 +122,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_kv_read": [vp, vp, i64, vp, i64, vp, vp],
         "lora_kv_attention": [vp, vp, i64, i32, vp, f32, i32, vp, i64, vp, vp],
         "lora_kv_check_errors": [vp],
+        "lora_kv_selftest_timeout": [vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)

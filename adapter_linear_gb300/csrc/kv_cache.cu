@@ -247,6 +247,13 @@ RowGrid row_grid(const KvDev &kv, bool int8, int T, int num_sms)
 // The error word read and cleared in one atomic step: [1] receives its value.
 __global__ void kv_read_clear_kernel(int *err) { err[1] = atomicExch(err, 0); }
 
+// What calls leave behind whose waits ran out (lora_kv_selftest_timeout).
+__global__ void kv_abandon_kernel(int *err, int *count, int n)
+{
+    for (int i = threadIdx.x; i < n; i += blockDim.x) count[i] = 1 + i % 3;
+    if (threadIdx.x == 0) atomicOr(err, kErrTimeoutBit);
+}
+
 }  // namespace
 
 namespace lora {
@@ -330,6 +337,9 @@ KvDev kv_view(const lora_kv *p)
     v.err = p->d_err;
     return v;
 }
+
+// Arrival counters of both attention kernels.
+int count_ints(const lora_kv *p) { return kv_decode_grid(p->num_sms) + 8 * kv_prefill_grid(p->num_sms); }
 
 // Rows (query heads of new tokens) of a kv head up to which the short-chunk kernel takes a sequence: 32
 // requests of 6 tokens on 4 query heads (24 rows) take 82 us there, 161 on the tcgen05 kernel, of
@@ -438,7 +448,7 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
     p->v = v_pages;
     p->ks = static_cast<uint16_t *>(k_scales);
     p->vs = static_cast<uint16_t *>(v_scales);
-    const size_t counts = sizeof(int) * (size_t)(kv_decode_grid(sms) + 8 * kv_prefill_grid(sms));
+    const size_t counts = sizeof(int) * (size_t)count_ints(p);
     if (cudaMalloc((void **)&p->d_err, 2 * sizeof(int)) != cudaSuccess ||
         cudaMalloc((void **)&p->dec_part, sizeof(float) * kv_decode_part_floats(head_dim, sms)) != cudaSuccess ||
         cudaMalloc((void **)&p->count, counts) != cudaSuccess ||
@@ -570,9 +580,22 @@ lora_status lora_kv_check_errors(lora_kv_t p)
             cudaSuccess ||
         cudaStreamSynchronize(p->ctl_stream) != cudaSuccess)
         return LORA_ERR_CUDA;
-    if (*p->h_err & kErrTimeoutBit) return LORA_ERR_TIMEOUT;
+    if (*p->h_err & kErrTimeoutBit) {
+        // pieces of that call never arrived: the counters start from zero again
+        CUDA_TRY(cudaMemsetAsync(p->count, 0, sizeof(int) * (size_t)count_ints(p), p->ctl_stream));
+        CUDA_TRY(cudaStreamSynchronize(p->ctl_stream));
+        return LORA_ERR_TIMEOUT;
+    }
     if (*p->h_err & kErrRangeBit) return LORA_ERR_RANGE;
     return LORA_OK;
+}
+
+lora_status lora_kv_selftest_timeout(lora_kv_t p, lora_stream_t stream)
+{
+    if (!p) return LORA_ERR_ARG;
+    kv_abandon_kernel<<<1, 256, 0, stream>>>(p->d_err, p->count, count_ints(p));
+    CUDA_TRY(cudaGetLastError());
+    return note_kv_call(p, stream);
 }
 
 }  // extern "C"

@@ -159,3 +159,7 @@ class KvCache:
 
     def check_errors(self) -> int:
         return self._lib.lora_kv_check_errors(self.handle)
+
+    def selftest_timeout(self, stream=None):
+        """Test hook: leaves the cache as calls do whose bounded waits ran out."""
+        _check(self._lib.lora_kv_selftest_timeout(self.handle, self._stream(stream)), "lora_kv_selftest_timeout")

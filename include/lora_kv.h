@@ -120,9 +120,15 @@ lora_status lora_kv_attention(lora_kv_t kv, const void *Q, int64_t q_stride, int
                               int64_t o_stride, float *lse, lora_stream_t stream);
 
 /* Wait for the calls enqueued on the cache, then read and clear its error word: LORA_OK,
- * LORA_ERR_RANGE or LORA_ERR_TIMEOUT, LORA_ERR_CUDA if the device reported an error. (Graph
- * replays are not tracked: synchronise their stream first.) */
+ * LORA_ERR_RANGE or LORA_ERR_TIMEOUT, LORA_ERR_CUDA if the device reported an error. After
+ * LORA_ERR_TIMEOUT (a kernel's bounded wait ran out) the outputs of the attention calls since the
+ * last check are unspecified; the cache is ready for new calls. (Graph replays are not tracked:
+ * synchronise their stream first.) */
 lora_status lora_kv_check_errors(lora_kv_t kv);
+
+/* Test hook: leave the cache as attention calls do whose bounded waits ran out (the error word, and
+ * pieces of a split sequence that others wait to join). Nothing waits or fails on the device. */
+lora_status lora_kv_selftest_timeout(lora_kv_t kv, lora_stream_t stream);
 
 #ifdef __cplusplus
 }
