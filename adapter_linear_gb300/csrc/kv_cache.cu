@@ -360,24 +360,35 @@ lora_status ensure_pre_part(lora_kv *p)
     return LORA_OK;
 }
 
-// After a call on `stream`: an event of that stream, for the error-word read and for attention
-// calls on other streams. Calls inside a graph capture are not tracked: the order of replays is
-// the caller's.
-lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
+bool capturing(cudaStream_t stream, lora_status *st)
 {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    CUDA_TRY(cudaStreamIsCapturing(stream, &cs));
-    if (cs != cudaStreamCaptureStatusNone) return LORA_OK;
-    if (!p->calls.empty() && p->calls.back().stream == stream) {
-        CUDA_TRY(cudaEventRecord(p->calls.back().ev, stream));
-        return LORA_OK;
-    }
+    *st = cudaStreamIsCapturing(stream, &cs) == cudaSuccess ? LORA_OK : LORA_ERR_CUDA;
+    if (*st != LORA_OK) cudaGetLastError();
+    return cs != cudaStreamCaptureStatusNone;
+}
+
+// `ev` now stands for what it stood for and for the work of `stream` so far. Two streams may have
+// one handle (the per-thread stream of two threads, a stream made after another was destroyed), so the
+// old record is waited for before it is replaced; on one stream that is nothing.
+lora_status extend_event(cudaEvent_t ev, cudaStream_t stream)
+{
+    CUDA_TRY(cudaStreamWaitEvent(stream, ev, 0));
+    CUDA_TRY(cudaEventRecord(ev, stream));
+    return LORA_OK;
+}
+
+// After a write or a read on `stream`: an event of that stream, for the error-word read. Calls inside a
+// graph capture are not tracked: the order of replays is the caller's.
+lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
+{
+    lora_status st;
+    if (capturing(stream, &st) || st != LORA_OK) return st;
     // the entry of this stream, or a new one, becomes the last
-    for (size_t i = 0; i < p->calls.size(); ++i)
+    for (size_t i = p->calls.size(); i-- > 0;)
         if (p->calls[i].stream == stream) {
             std::swap(p->calls[i], p->calls.back());
-            CUDA_TRY(cudaEventRecord(p->calls.back().ev, stream));
-            return LORA_OK;
+            return extend_event(p->calls.back().ev, stream);
         }
     lora_kv::Call c{stream, nullptr};
     CUDA_TRY(cudaEventCreateWithFlags(&c.ev, cudaEventDisableTiming));
@@ -392,20 +403,6 @@ lora_status note_kv_call(lora_kv *p, cudaStream_t stream)
         cudaEventDestroy(c.ev);
         return LORA_ERR_OOM;
     }
-    return LORA_OK;
-}
-
-// Before an attention call on `stream`: the scratch belongs to one call at a time, so after the
-// last attention call if that ran on another stream.
-lora_status order_attention(lora_kv *p, cudaStream_t stream)
-{
-    if (p->attn_stream == stream || !p->attn_any) return LORA_OK;
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    CUDA_TRY(cudaStreamIsCapturing(stream, &cs));
-    if (cs != cudaStreamCaptureStatusNone) return LORA_OK;
-    for (const lora_kv::Call &c : p->calls)
-        if (c.stream == p->attn_stream) CUDA_TRY(cudaStreamWaitEvent(stream, c.ev, 0));
-    p->attn_stream = stream;
     return LORA_OK;
 }
 
@@ -460,6 +457,7 @@ lora_status lora_kv_create(int num_pages, int page_tokens, int n_kv_heads, int h
     if (cudaMemset(p->d_err, 0, 2 * sizeof(int)) != cudaSuccess ||
         cudaMemset(p->count, 0, counts) != cudaSuccess ||
         cudaStreamCreateWithFlags(&p->ctl_stream, cudaStreamNonBlocking) != cudaSuccess ||
+        cudaEventCreateWithFlags(&p->attn_ev, cudaEventDisableTiming) != cudaSuccess ||
         ensure_smem_attr((const void *)kv_read_clear_kernel, 0) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         lora_kv_destroy(p);
@@ -475,6 +473,7 @@ lora_status lora_kv_destroy(lora_kv_t p)
     cudaDeviceSynchronize();
     if (p->ctl_stream) cudaStreamDestroy(p->ctl_stream);
     for (const lora_kv::Call &c : p->calls) cudaEventDestroy(c.ev);
+    if (p->attn_ev) cudaEventDestroy(p->attn_ev);
     if (p->dec_part) cudaFree(p->dec_part);
     if (p->pre_part) cudaFree(p->pre_part);
     if (p->count) cudaFree(p->count);
@@ -552,19 +551,26 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     const bool prefill = (int64_t)max_new * a.G > kDecodeRows;
     const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
     if (prefill && (st = ensure_pre_part(p)) != LORA_OK) return st;
-    if ((st = order_attention(p, stream)) != LORA_OK) return st;
+    // The scratch belongs to one call at a time: after the last attention call, whatever stream that
+    // ran on (captured calls: the order of replays is the caller's).
+    const bool tracked = !capturing(stream, &st);
+    if (st != LORA_OK) return st;
+    if (tracked) CUDA_TRY(cudaStreamWaitEvent(stream, p->attn_ev, 0));
     const KvDev kv = kv_view(p);
     const KvBatchDev bd = batch_view(batch);
+    cudaError_t e = cudaSuccess;
     if (decode)
-        CUDA_TRY(launch_kv_decode(kv, p->int8, bd, a, max_new, prefill ? kDecodeRows : INT_MAX, p->dec_part,
-                                  p->count, p->num_sms, stream));
-    if (prefill)
-        CUDA_TRY(launch_kv_prefill(kv, p->int8, bd, a, decode ? kDecodeRows + 1 : 0, p->pre_part,
-                                   p->count + kv_decode_grid(p->num_sms), p->num_sms, stream));
-    if ((st = note_kv_call(p, stream)) != LORA_OK) return st;
-    if (!p->attn_any) {
-        p->attn_any = true;
-        p->attn_stream = stream;
+        e = launch_kv_decode(kv, p->int8, bd, a, max_new, prefill ? kDecodeRows : INT_MAX, p->dec_part, p->count,
+                             p->num_sms, stream);
+    if (prefill && e == cudaSuccess)
+        e = launch_kv_prefill(kv, p->int8, bd, a, decode ? kDecodeRows + 1 : 0, p->pre_part,
+                              p->count + kv_decode_grid(p->num_sms), p->num_sms, stream);
+    // (the first launch may have run when the second failed; the event stands for all calls so far,
+    // each having waited for the one before)
+    if (tracked && cudaEventRecord(p->attn_ev, stream) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return LORA_ERR_CUDA;
     }
     return LORA_OK;
 }
@@ -572,7 +578,8 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
 lora_status lora_kv_check_errors(lora_kv_t p)
 {
     if (!p) return LORA_ERR_ARG;
-    // on the control stream, after the last call of every stream
+    // on the control stream, after every call
+    CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->attn_ev, 0));
     for (const lora_kv::Call &c : p->calls) CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, c.ev, 0));
     kv_read_clear_kernel<<<1, 1, 0, p->ctl_stream>>>(p->d_err);
     if (cudaGetLastError() != cudaSuccess ||

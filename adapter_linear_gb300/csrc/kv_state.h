@@ -17,17 +17,15 @@ struct lora_kv {
     uint16_t *ks = nullptr, *vs = nullptr;
     int *d_err = nullptr;                      // [0] the error word, [1] its value at the last read
     int *h_err = nullptr;                      // pinned copy of d_err[1]
-    // the last call on each stream that has been used, the most recent stream's at the end
+    // the writes and reads so far on each stream that has been used, the most recent stream's at the end
     struct Call {
         cudaStream_t stream;
         cudaEvent_t ev;
     };
     std::vector<Call> calls;
-    // the attention's scratch, used by one call at a time: a call on another stream than the
-    // last one's waits for that stream's last call
+    // the attention's scratch, used by one call at a time; attn_ev: the attention calls so far
+    cudaEvent_t attn_ev = nullptr;
     float *dec_part = nullptr, *pre_part = nullptr;  // pre_part: from the first call or reserve
     int *count = nullptr;                            // the short-chunk kernel's, then the other's
-    cudaStream_t attn_stream = nullptr;
-    bool attn_any = false;
     cudaStream_t ctl_stream = nullptr;         // error-word reads
 };
