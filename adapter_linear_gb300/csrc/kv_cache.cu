@@ -297,17 +297,20 @@ bool tensor_ok(const void *p, int64_t stride, int64_t row)
 
 constexpr int kMaxTokens = 1 << 30;  // of a call or a sequence: positions stay clear of 32 bits
 
-// A batch the kernels can take; *empty: there is nothing to do.
-lora_status check_batch(const lora_kv_batch *b, int page_shift, bool *empty)
+// A batch the kernels can take, with the cache's device current; *empty: there is nothing to do.
+lora_status check_batch(const lora_kv *p, const lora_kv_batch *b, bool *empty)
 {
     *empty = false;
+    int dev = -1;
+    CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return LORA_ERR_ARG;
     if (!b || b->n_seqs < 0 || b->T < 0 || b->max_new < 0) return LORA_ERR_ARG;
     if (b->n_seqs == 0 || b->T == 0) {
         *empty = true;
         return LORA_OK;
     }
     if (!b->page_table || !b->start || !b->kv_len || b->table_stride < 1) return LORA_ERR_ARG;
-    if (b->T > kMaxTokens || ((int64_t)b->table_stride << page_shift) > kMaxTokens) return LORA_ERR_ARG;
+    if (b->T > kMaxTokens || ((int64_t)b->table_stride << p->page_shift) > kMaxTokens) return LORA_ERR_ARG;
     return LORA_OK;
 }
 
@@ -496,7 +499,7 @@ lora_status lora_kv_write(lora_kv_t p, const void *K, int64_t k_stride, const vo
 {
     if (!p) return LORA_ERR_ARG;
     bool empty;
-    lora_status st = check_batch(batch, p->page_shift, &empty);
+    lora_status st = check_batch(p, batch, &empty);
     if (st != LORA_OK || empty) return st;
     const int64_t row = (int64_t)p->H * p->D;
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
@@ -510,7 +513,7 @@ lora_status lora_kv_read(lora_kv_t p, void *K, int64_t k_stride, void *V, int64_
 {
     if (!p) return LORA_ERR_ARG;
     bool empty;
-    lora_status st = check_batch(batch, p->page_shift, &empty);
+    lora_status st = check_batch(p, batch, &empty);
     if (st != LORA_OK || empty) return st;
     const int64_t row = (int64_t)p->H * p->D;
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
@@ -526,7 +529,7 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     if (!p || window < 0) return LORA_ERR_ARG;
     if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
     bool empty;
-    lora_status st = check_batch(batch, p->page_shift, &empty);
+    lora_status st = check_batch(p, batch, &empty);
     if (st != LORA_OK || empty) return st;
     if ((int64_t)batch->T * n_heads > INT_MAX) return LORA_ERR_ARG;
     const int64_t row = (int64_t)n_heads * p->D;

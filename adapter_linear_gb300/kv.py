@@ -33,6 +33,9 @@ class KvBatch:
         for t, nd in ((page_table, 2), (start, 1), (kv_len, 1)):
             if t.dtype != torch.int32 or t.dim() != nd or not t.is_contiguous():
                 raise LoraError(LORA_ERR_ARG, "KvBatch: page_table, start and kv_len are contiguous int32")
+        self.device = page_table.get_device()
+        if self.device < 0 or start.get_device() != self.device or kv_len.get_device() != self.device:
+            raise LoraError(LORA_ERR_ARG, "KvBatch: page_table, start and kv_len are on one GPU")
         n = page_table.shape[0]
         if start.shape[0] != n + 1 or kv_len.shape[0] != n:
             raise LoraError(LORA_ERR_SHAPE, "KvBatch: start has n_seqs + 1 entries, kv_len n_seqs")
@@ -67,8 +70,10 @@ class KvCache:
             if t is not None and (tuple(t.shape) != shape[:3] or t.dtype != torch.bfloat16 or
                                   not t.is_contiguous()):
                 raise LoraError(LORA_ERR_SHAPE, f"KvCache: scales are contiguous {shape[:3]} of bfloat16")
+        self._torch_device, self._device = k.device, k.get_device()
+        if self._device < 0 or any(t is not None and t.get_device() != self._device for t in (v, ks, vs)):
+            raise LoraError(LORA_ERR_ARG, "KvCache: the arenas are on one GPU")
         self.k, self.v, self.k_scales, self.v_scales = k, v, ks, vs
-        self._torch_device, self._device = k.device, k.device.index or 0
         h = ctypes.c_void_p()
         _check(load_library().lora_kv_create(num_pages, page_tokens, kv_heads, head_dim, fmt, _ptr(k), _ptr(v),
                                              _ptr(ks), _ptr(vs), ctypes.byref(h)), "lora_kv_create")
@@ -102,6 +107,8 @@ class KvCache:
         T, D = batch.T, self.head_dim
         if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[0] != T or x.shape[1] != heads or x.shape[2] != D:
             raise LoraError(LORA_ERR_SHAPE, f"{what}: bfloat16 [{T}, {heads}, {D}] expected")
+        if x.get_device() != self._device or batch.device != self._device:
+            raise LoraError(LORA_ERR_ARG, f"{what}: the tensors of a call are on the cache's GPU")
         s = x.stride()
         if (s[2] != 1 and D > 1) or (s[1] != D and heads > 1):
             raise LoraError(LORA_ERR_ARG, f"{what}: the heads of a token must be contiguous")
@@ -115,11 +122,14 @@ class KvCache:
         ks = self._rows(K, self.kv_heads, batch, "lora_kv_write K")
         vs = self._rows(V, self.kv_heads, batch, "lora_kv_write V")
         _check(self._lib.lora_kv_write(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                       self._stream(stream)), "lora_kv_write")
+                                       self._stream(stream)),
+               "lora_kv_write")
 
     def read(self, batch: KvBatch, K=None, V=None, stream=None):
         """The batch's tokens as bf16 [T, kv_heads, head_dim] keys and values."""
         shape = (batch.T, self.kv_heads, self.head_dim)
+        if batch.device != self._device:
+            raise LoraError(LORA_ERR_ARG, "lora_kv_read: the tensors of a call are on the cache's GPU")
         ks = vs = self.kv_heads * self.head_dim
         if K is None:
             K = torch.empty(shape, dtype=torch.bfloat16, device=self._torch_device)
@@ -130,7 +140,8 @@ class KvCache:
         else:
             vs = self._rows(V, self.kv_heads, batch, "lora_kv_read V")
         _check(self._lib.lora_kv_read(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                      self._stream(stream)), "lora_kv_read")
+                                       self._stream(stream)),
+               "lora_kv_read")
         return K, V
 
     def attention(self, Q, batch: KvBatch, scale: Optional[float] = None, window: int = 0, O=None, lse=None,
@@ -150,11 +161,12 @@ class KvCache:
             lse = torch.empty((T, Hq), dtype=torch.float32, device=self._torch_device)
         elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention lse: contiguous float32 [T, n_heads] expected")
+        elif lse.get_device() != self._device:
+            raise LoraError(LORA_ERR_ARG, "lora_kv_attention lse: the tensors of a call are on the cache's GPU")
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
         _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, window,
-                                           O.data_ptr(), os_, lse.data_ptr(), self._stream(stream)),
-               "lora_kv_attention")
+                                           O.data_ptr(), os_, lse.data_ptr(), self._stream(stream)), "lora_kv_attention")
         return O, lse
 
     def check_errors(self) -> int:

@@ -31,6 +31,7 @@
  *  - Cache rows that hold no token of a sequence may hold anything (inf and NaN included). An
  *    infinity or a NaN in a token's K or V reaches the rows that see that token, no others.
  *  - T and table_stride * p are at most 2^30, T * n_heads below 2^31 (else LORA_ERR_ARG).
+ *  - Calls are made with the device current that the cache was created on (else LORA_ERR_ARG).
  *  - A cache is not thread-safe: use it from one host thread at a time. Calls on several
  *    streams are allowed: attention calls (which share scratch) are ordered by the library,
  *    those captured in a graph by whoever replays it (no other attention call of the cache beside
