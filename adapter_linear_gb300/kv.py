@@ -40,6 +40,7 @@ class KvBatch:
         if start.shape[0] != n + 1 or kv_len.shape[0] != n:
             raise LoraError(LORA_ERR_SHAPE, "KvBatch: start has n_seqs + 1 entries, kv_len n_seqs")
         self.page_table, self.start, self.kv_len, self.T = page_table, start, kv_len, T
+        self.tensors = (page_table, start, kv_len)
         self.struct = _BatchStruct(page_table.data_ptr(), start.data_ptr(), kv_len.data_ptr(),
                                    page_table.shape[1], n, T, max_new)
         self.ref = ctypes.byref(self.struct)
@@ -48,7 +49,10 @@ class KvBatch:
 class KvCache:
     """A paged cache of num_pages pages of page_tokens tokens for kv_heads heads of head_dim
     values, bf16 or int8 with a bf16 scale per row. arenas: the tensors (k, v, k_scales,
-    v_scales; the scales None for bf16) to use in place of newly allocated ones."""
+    v_scales; the scales None for bf16) to use in place of newly allocated ones.
+
+    Calls run on the current stream or on `stream` (a torch stream or a handle), which then has to
+    follow what filled their inputs; outputs that a call allocates belong to the stream it runs on."""
 
     def __init__(self, num_pages: int, page_tokens: int, kv_heads: int, head_dim: int, fmt: int = LORA_KV_INT8,
                  device="cuda", arenas: Optional[Tuple] = None):
@@ -97,10 +101,29 @@ class KvCache:
         except Exception:  # noqa: BLE001
             pass
 
-    def _stream(self, stream) -> int:
-        if stream is None:  # (torch.cuda.current_stream() builds an object: 3 us of a call's 10)
-            return torch._C._cuda_getCurrentRawStream(self._device)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+    def _stream(self, stream, batch=None, *tensors) -> int:
+        """The handle to launch on. On a stream other than the current one the allocator learns that
+        it uses the call's tensors."""
+        current = torch._C._cuda_getCurrentRawStream(self._device)  # (current_stream() builds an object: 3 us)
+        if stream is None:
+            return current
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle != current and batch is not None:
+            stream = self._stream_object(stream)
+            for t in tensors + batch.tensors + (self.k, self.v, self.k_scales, self.v_scales):
+                if t is not None:
+                    t.record_stream(stream)
+        return handle
+
+    def _stream_object(self, stream):
+        return torch.cuda.ExternalStream(stream, self._torch_device) if isinstance(stream, int) else stream
+
+    def _empty(self, shape, dtype, stream):
+        """An output, allocated for the stream that will write it."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self._torch_device)
+        with torch.cuda.stream(self._stream_object(stream)):
+            return torch.empty(shape, dtype=dtype, device=self._torch_device)
 
     def _rows(self, x, heads: int, batch: KvBatch, what: str) -> int:
         """The token stride of x, a bf16 [T, heads, head_dim] tensor with contiguous heads."""
@@ -121,8 +144,8 @@ class KvCache:
         """Write the batch's keys and values (bf16 [T, kv_heads, head_dim]) into their pages."""
         ks = self._rows(K, self.kv_heads, batch, "lora_kv_write K")
         vs = self._rows(V, self.kv_heads, batch, "lora_kv_write V")
-        _check(self._lib.lora_kv_write(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                       self._stream(stream)),
+        st = self._stream(stream, batch, K, V)
+        _check(self._lib.lora_kv_write(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref, st),
                "lora_kv_write")
 
     def read(self, batch: KvBatch, K=None, V=None, stream=None):
@@ -132,15 +155,15 @@ class KvCache:
             raise LoraError(LORA_ERR_ARG, "lora_kv_read: the tensors of a call are on the cache's GPU")
         ks = vs = self.kv_heads * self.head_dim
         if K is None:
-            K = torch.empty(shape, dtype=torch.bfloat16, device=self._torch_device)
+            K = self._empty(shape, torch.bfloat16, stream)
         else:
             ks = self._rows(K, self.kv_heads, batch, "lora_kv_read K")
         if V is None:
-            V = torch.empty(shape, dtype=torch.bfloat16, device=self._torch_device)
+            V = self._empty(shape, torch.bfloat16, stream)
         else:
             vs = self._rows(V, self.kv_heads, batch, "lora_kv_read V")
-        _check(self._lib.lora_kv_read(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref,
-                                       self._stream(stream)),
+        st = self._stream(stream, batch, K, V)
+        _check(self._lib.lora_kv_read(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref, st),
                "lora_kv_read")
         return K, V
 
@@ -153,20 +176,21 @@ class KvCache:
         T, Hq, _ = Q.shape
         qs = self._rows(Q, Hq, batch, "lora_kv_attention Q")
         if O is None:
-            O = torch.empty((T, Hq, self.head_dim), dtype=torch.bfloat16, device=self._torch_device)
+            O = self._empty((T, Hq, self.head_dim), torch.bfloat16, stream)
             os_ = Hq * self.head_dim
         else:
             os_ = self._rows(O, Hq, batch, "lora_kv_attention O")
         if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=self._torch_device)
+            lse = self._empty((T, Hq), torch.float32, stream)
         elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
             raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention lse: contiguous float32 [T, n_heads] expected")
         elif lse.get_device() != self._device:
             raise LoraError(LORA_ERR_ARG, "lora_kv_attention lse: the tensors of a call are on the cache's GPU")
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
+        st = self._stream(stream, batch, Q, O, lse)
         _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, window,
-                                           O.data_ptr(), os_, lse.data_ptr(), self._stream(stream)), "lora_kv_attention")
+                                           O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention")
         return O, lse
 
     def check_errors(self) -> int:

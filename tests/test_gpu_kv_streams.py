@@ -53,3 +53,28 @@ def test_check_errors_waits_for_writes_on_per_thread_streams():
             b.submit(p.cache.write, K[:1], V[:1], small, PER_THREAD).result()
             assert p.cache.check_errors() == al.LORA_ERR_RANGE
             assert p.cache.check_errors() == al.LORA_OK
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_memory_of_a_call_on_another_stream(as_handle):
+    """Outputs belong to the stream that writes them, and inputs dropped after the call are not handed
+    out again while it runs."""
+    p = R.Paged(al, al.LORA_KV_INT8, [300, 200], [50, 30], 2, 128, 16, seed=250)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if as_handle else side
+    rows = [torch.randn(p.T, h, 128, device="cuda").to(torch.bfloat16) for h in (8, 2, 2)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                       # some 50 ms
+    O, lse = p.cache.attention(rows[0], p.batch, stream=stream)
+    p.cache.write(rows[1], rows[2], p.batch, stream=stream)
+    K, V = p.cache.read(p.batch, stream=stream)
+    outputs, inputs = [O, lse, K, V], rows
+    used = {x.data_ptr() for x in outputs + inputs}
+    like = [(x.shape, x.dtype) for x in outputs + inputs]
+    del O, lse, K, V, rows, outputs, inputs
+    assert not side.query()                                  # still asleep
+    fresh = [torch.empty(s, dtype=d, device="cuda") for s, d in like]
+    assert not used & {x.data_ptr() for x in fresh}
+    side.synchronize()
+    assert p.cache.check_errors() == al.LORA_OK
