@@ -21,6 +21,12 @@ class _BatchStruct(ctypes.Structure):
                 ("max_new", ctypes.c_int32)]
 
 
+def _clamped(x: int) -> int:
+    """x as the library's int takes it: ctypes would drop high bits; above 2^30 nothing differs, and
+    any negative number is refused."""
+    return max(-1, min(x, 1 << 30))
+
+
 class KvBatch:
     """The tokens of one step: rows start[b]..start[b+1] of the step's tensors are the last
     tokens of sequence b, whose kv_len[b] tokens lie in the pages page_table[b] names.
@@ -42,7 +48,7 @@ class KvBatch:
         self.page_table, self.start, self.kv_len, self.T = page_table, start, kv_len, T
         self.tensors = (page_table, start, kv_len)
         self.struct = _BatchStruct(page_table.data_ptr(), start.data_ptr(), kv_len.data_ptr(),
-                                   page_table.shape[1], n, T, max_new)
+                                   page_table.shape[1], n, T, _clamped(max_new))
         self.ref = ctypes.byref(self.struct)
 
 
@@ -189,7 +195,7 @@ class KvCache:
         if scale is None:
             scale = 1.0 / math.sqrt(self.head_dim)
         st = self._stream(stream, batch, Q, O, lse)
-        _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, window,
+        _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, _clamped(window),
                                            O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention")
         return O, lse
 

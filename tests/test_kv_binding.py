@@ -1,9 +1,11 @@
 """What the binding of the paged cache refuses or hands on by itself (no GPU)."""
+import math
+
 import pytest
 import torch
 
 import adapter_linear_gb300 as al
-from adapter_linear_gb300.kv import KvBatch, KvCache
+from adapter_linear_gb300.kv import KvBatch, KvCache, _BatchStruct
 
 
 def refused(status, call):
@@ -60,3 +62,20 @@ def test_tensors_of_another_device_are_refused():
     refused(al.LORA_ERR_ARG, lambda: c.read(b))
     refused(al.LORA_ERR_ARG, lambda: c.attention(Q, b))
     assert c._lib.calls == []
+
+
+@pytest.mark.parametrize("window,given", [(0, 0), (5, 5), (2 ** 31, 2 ** 30), (2 ** 32 + 5, 2 ** 30), (-1, -1),
+                                          (-2 ** 32, -1)])
+def test_no_window_loses_its_high_bits(window, given, monkeypatch):
+    c, b = a_cache_on(-1), a_batch_on(-1, 3)
+    monkeypatch.setattr(KvCache, "_stream", lambda self, stream, *args: 0)
+    Q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    c.attention(Q, b, window=window, O=torch.zeros_like(Q), lse=torch.zeros(3, 4))
+    (name, args), = c._lib.calls
+    assert name == "lora_kv_attention" and args[6] == given and args[5] == 1 / math.sqrt(64)
+
+
+def test_a_bound_on_the_rows_loses_no_high_bits():
+    from adapter_linear_gb300.kv import _clamped
+    for max_new, kept in ((3, 3), (2 ** 32, 2 ** 30), (-2 ** 32 + 1, -1)):
+        assert _BatchStruct(0, 0, 0, 1, 1, 1, _clamped(max_new)).max_new == kept
