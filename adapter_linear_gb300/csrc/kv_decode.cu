@@ -116,10 +116,12 @@ struct Plan {
 
 // A warp's steps of an item, nk of them from token `tok`, for the first kT tiles of its rows, and
 // then their O into the ring and (m, l) into sm_m and sm_l. issue() starts the copy of the next step.
-template <int D, bool kInt8, int kN, int kT, class Issue>
-__device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int window, int rows, int pos_min, int pos_max,
-                                          uint32_t base, uint8_t *ring, const uint4 (&sm_q)[kN][D / 32][32],
-                                          const float *sm_back, const int *sm_pos, float *sm_m, float *sm_l)
+// v_row(j): V of token j < tok_end, which the table names (for an unquantised cache's bad values).
+template <int D, bool kInt8, int kN, int kT, class Issue, class Row>
+__device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int tok, int tok_end, int window, int rows,
+                                          int pos_min, int pos_max, uint32_t base, uint8_t *ring,
+                                          const uint4 (&sm_q)[kN][D / 32][32], const float *sm_back, const int *sm_pos,
+                                          float *sm_m, float *sm_l)
 {
     using C = Cfg<D, kInt8, kN>;
     constexpr int kM = D / 16;
@@ -143,7 +145,9 @@ __device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int win
         l[t][0] = l[t][1] = 0.0f;
     }
 
+    bool bad = false;  // V had an infinity or a NaN that was left out of the product
     int stage = 0;
+    const int tok_first = tok;
     for (int k = 0; k < nk; ++k, tok += kStep * kWarps) {
         cp_wait<C::kStages - 2>();
         __syncwarp();
@@ -308,10 +312,7 @@ __device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int win
                     w[r][2] = v.z;
                     w[r][3] = v.w;
                 }
-                if (edge) {
-                    // A weight of 0 does not keep an infinity or a NaN out of a product: where not
-                    // all rows see all tokens, they are taken out and added to the rows that do.
-                    bool bad = false;
+                if (edge) {  // not all rows see all of these tokens
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -320,27 +321,6 @@ __device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int win
                             bad |= f != w[r][i];
                             w[r][i] = f;
                         }
-                    if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll 1
-                        for (int y = 0; y < kStep; ++y) {
-                            const uint4 v =
-                                *reinterpret_cast<const uint4 *>(vt + swz<C::kRowBytes>(y, 8 * x + v_chunk(g)));
-                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int t = 0; t < kT; ++t)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    const int p = sm_pos[8 * t + 2 * c + e];
-                                    if (tok + y > p || (window > 0 && tok + y <= p - window)) continue;
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint32_t f = u[i] ^ finite_part(u[i]);
-                                        o[t][4 * x + i][e] += bf16_lo(f);
-                                        o[t][4 * x + i][2 + e] += bf16_hi(f);
-                                    }
-                                }
-                        }
-                    }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -362,6 +342,57 @@ __device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int win
     cp_wait<0>();
     __syncwarp();
 
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
+            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
+        }
+    if constexpr (!kInt8) {
+        // 0 O is 0 for a finite O; a row whose weights are NaN is NaN as it is
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float zero = 0.0f;
+#pragma unroll
+                for (int i = 0; i < kM; ++i) zero = fmaf(o[t][i][e], 0.0f, fmaf(o[t][i][2 + e], 0.0f, zero));
+                bad |= zero != 0.0f && l[t][e] == l[t][e];
+            }
+        if (__any_sync(0xffffffffu, bad)) {
+            // once to clear what the product made of them, once to add them up
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+                for (int y = 0; y < nk * kStep; ++y) {
+                    const int j = tok_first + y % kStep + y / kStep * (kStep * kWarps);
+                    if (j >= tok_end) break;
+                    const uint16_t *const row = v_row(j);
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(row + 64 * x + 8 * v_chunk(g));
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int t = 0; t < kT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int p = sm_pos[8 * t + 2 * c + e];
+                                if (j > p || (window > 0 && j <= p - window)) continue;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t f = u[i] ^ finite_part(u[i]);
+                                    float &lo = o[t][4 * x + i][e], &hi = o[t][4 * x + i][2 + e];
+                                    if (f & 0xFFFFu) lo = pass == 0 ? 0.0f : lo + bf16_lo(f);
+                                    if (f >> 16) hi = pass == 0 ? 0.0f : hi + bf16_hi(f);
+                                }
+                            }
+                    }
+                }
+        }
+    }
+
     // ---- join the warps: O in the warp's ring, (m, l) beside it
     float *so = reinterpret_cast<float *>(ring);
 #pragma unroll
@@ -369,9 +400,6 @@ __device__ __forceinline__ void run_steps(Issue &issue, int nk, int tok, int win
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int r = 8 * t + 2 * c + e;
-            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 4);
-            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 8);
-            l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], 16);
             if (g == 0) {
                 sm_m[r] = m[t][e];
                 sm_l[r] = l[t][e];
@@ -475,6 +503,12 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             }
             cp_commit();
         };
+        auto v_row = [&](int j) {  // (a bad page: the same stand-in as above)
+            int page = table[j >> kv.page_shift];
+            if (page < 0 || page >= kv.num_pages) page = 0;
+            return static_cast<const uint16_t *>(kv.v) +
+                   ((((int64_t)page * kv.H + head) << kv.page_shift) + (j & ((1 << kv.page_shift) - 1))) * D;
+        };
 #pragma unroll
         for (int k = 0; k < C::kStages - 1; ++k) issue();
 
@@ -531,9 +565,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         // one tile where the item's rows fit it (40 requests of 7 heads, 37 of them of one token: 99 us
         // with all tiles, 93 with one)
         auto run = [&](auto tiles) {
-            run_steps<D, kInt8, kN, decltype(tiles)::value>(issue, nk, tok0 + kStep * warp, a.window, rows, pos_min,
-                                                            pos_max, base, ring, sm_q, sm_back, sm_pos, sm_m[warp],
-                                                            sm_l[warp]);
+            run_steps<D, kInt8, kN, decltype(tiles)::value>(issue, v_row, nk, tok0 + kStep * warp, tok1, a.window, rows,
+                                                            pos_min, pos_max, base, ring, sm_q, sm_back, sm_pos,
+                                                            sm_m[warp], sm_l[warp]);
         };
         if (rows <= 8)
             run(std::integral_constant<int, 1>());
@@ -575,10 +609,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 const float4 v = *reinterpret_cast<const float4 *>(
                     reinterpret_cast<const float *>(smem + x * C::kRing) + r * C::kLdO + d);
                 const float wt = sm_w[x][r];
-                acc.x = fmaf(wt, v.x, acc.x);
-                acc.y = fmaf(wt, v.y, acc.y);
-                acc.z = fmaf(wt, v.z, acc.z);
-                acc.w = fmaf(wt, v.w, acc.w);
+                acc.x = add_piece<kInt8>(wt, v.x, acc.x);
+                acc.y = add_piece<kInt8>(wt, v.y, acc.y);
+                acc.z = add_piece<kInt8>(wt, v.z, acc.z);
+                acc.w = add_piece<kInt8>(wt, v.w, acc.w);
             }
             if (whole) {
                 const int row = tile * R + r;
@@ -644,10 +678,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                         const float4 v = __ldcg(reinterpret_cast<const float4 *>(
                             src + (int64_t)(2 * (c0 + x) + (x == 0 ? 1 : 0)) * R * D));
                         const float w = wt[x * R + r];
-                        acc.x = fmaf(w, v.x, acc.x);
-                        acc.y = fmaf(w, v.y, acc.y);
-                        acc.z = fmaf(w, v.z, acc.z);
-                        acc.w = fmaf(w, v.w, acc.w);
+                        acc.x = add_piece<kInt8>(w, v.x, acc.x);
+                        acc.y = add_piece<kInt8>(w, v.y, acc.y);
+                        acc.z = add_piece<kInt8>(w, v.z, acc.z);
+                        acc.w = add_piece<kInt8>(w, v.w, acc.w);
                     }
                     const float inv = sm_w[0][r];
                     const int row = tile * R + r;

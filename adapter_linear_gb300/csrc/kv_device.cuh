@@ -289,6 +289,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// An infinity or a NaN of V in an unquantised cache belongs to every row that sees its token, whatever
+// weight it has there: the row's value is NaN with a NaN or infinities of both signs, else that
+// infinity. The products do not give that (0 or a negative second part of a weight times an
+// infinity is NaN or the other infinity), so the kernels look for values of O that are not finite and
+// work those out from V again; where some rows do not see all tokens, the bad values stay out of the
+// product.
+//
 // Of a pair of bf16: the infinities and NaN become zeros (finite_part), or all but them do
 // (the other half of the same xor).
 __device__ __forceinline__ uint32_t finite_part(uint32_t v)
@@ -296,6 +303,13 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t v)
     const uint32_t lo = (v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu;
     const uint32_t hi = (v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u;
     return lo | hi;
+}
+
+// acc + wt v for a piece's weight, which may be 0 where its O is an infinity.
+template <bool kInt8>
+__device__ __forceinline__ float add_piece(float wt, float v, float acc)
+{
+    return fmaf(!kInt8 && wt == 0.0f && fabsf(v) == INFINITY ? 1.0f : wt, v, acc);
 }
 
 constexpr float kLn2 = 0.6931471805599453f;

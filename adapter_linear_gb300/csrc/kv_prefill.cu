@@ -408,35 +408,60 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 3
     }
 }
 
-// The infinities and NaN of V that the loading warps took out of the segment's tiles, to the
-// rows that see them (whatever the weight: it is positive). pos: the row's position, -1: no row.
+// The infinities and NaN of V among a segment's tokens, to the rows that see them. pos: the row's
+// position, -1: no row; finite: the row's weights are. A block of 8 columns where O is finite lacks
+// what the loading warps took out; one where it is not is worked out from all tokens again.
 template <int D>
 __device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const Segment *w, int G, int window,
-                                        int pos, uint32_t tO)
+                                        int pos, bool finite, uint32_t tO)
 {
+    const int lane = threadIdx.x & 31;
     const int32_t *const table = b.table + (int64_t)w->seq * b.table_stride;
     const int2 seen = seen_by_all(w, G, window);
+    const int end = min(w->hi, w->lo + w->j1 * kKeys);
 #pragma unroll 1
     for (int x = 0; x < D; x += 8) {
         uint32_t o[8];
         tmem_ld8_wait(tO + x, o);
-#pragma unroll 1
-        for (int tok = w->lo + w->j0 * kKeys; tok < min(w->hi, w->lo + w->j1 * kKeys); ++tok) {
-            if (tok > pos || (window > 0 && tok <= pos - window)) continue;
-            if (!edge_group(tok - ((tok - w->lo) & 15), seen)) continue;
-            const int page = table[tok >> kv.page_shift];
-            if (page < 0 || page >= kv.num_pages) continue;
-            const int64_t row =
-                (((int64_t)page * kv.H + w->head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
-            const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(kv.v) + row * D + x);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        float zero = 0.0f, sum[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t f = u[e] ^ finite_part(u[e]);
-                o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + bf16_lo(f));
-                o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + bf16_hi(f));
+        for (int e = 0; e < 8; ++e) {
+            zero = fmaf(__uint_as_float(o[e]), 0.0f, zero);
+            sum[e] = 0.0f;
+        }
+        const bool all = __any_sync(0xffffffffu, finite && zero != 0.0f);
+#pragma unroll 1
+        for (int tok0 = w->lo + w->j0 * kKeys; tok0 < end; tok0 += 32) {  // a token a lane
+            const int tok = tok0 + lane;
+            uint32_t f[4] = {0, 0, 0, 0};
+            if (tok < end && (all || edge_group(tok & ~15, seen))) {
+                const int page = table[tok >> kv.page_shift];
+                if (page >= 0 && page < kv.num_pages) {
+                    const int64_t row =
+                        (((int64_t)page * kv.H + w->head) << kv.page_shift) + (tok & ((1 << kv.page_shift) - 1));
+                    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(kv.v) + row * D + x);
+                    f[0] = v.x ^ finite_part(v.x);
+                    f[1] = v.y ^ finite_part(v.y);
+                    f[2] = v.z ^ finite_part(v.z);
+                    f[3] = v.w ^ finite_part(v.w);
+                }
+            }
+#pragma unroll 1
+            for (uint32_t left = __ballot_sync(0xffffffffu, (f[0] | f[1] | f[2] | f[3]) != 0); left; left &= left - 1) {
+                const int from = __ffs(left) - 1;
+                const bool sees = tok0 + from <= pos && (window == 0 || tok0 + from > pos - window);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t u = __shfl_sync(0xffffffffu, f[e], from);
+                    if (sees) {
+                        sum[2 * e] += bf16_lo(u);
+                        sum[2 * e + 1] += bf16_hi(u);
+                    }
+                }
             }
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = sum[e] == 0.0f ? o[e] : __float_as_uint(sum[e]);
         __syncwarp();
         tmem_st8(tO + x, o);
     }
@@ -621,7 +646,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             const int slot = w->slot, c0 = w->c0, c1 = w->c1;
             if constexpr (!kInt8) {
-                if (*const_cast<const volatile int *>(&w->bad)) add_bad<D>(kv, b, w, G, a.window, on ? pos : -1, tO);
+                // bad values of V: known from the loading warps, or seen in O, of which 0 O is then not 0
+                // (looked for while O is written: 8 prompts of 2048 bf16 412 us, not 390)
+                float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                for (int x = 0; x < D; x += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_wait(tO + x, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) zero[e & 3] = fmaf(__uint_as_float(o[e]), 0.0f, zero[e & 3]);
+                }
+                const bool odd = on && l == l && (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f;
+                if (__any_sync(0xffffffffu, odd || *const_cast<const volatile int *>(&w->bad)))
+                    add_bad<D>(kv, b, w, G, a.window, on ? pos : -1, on && l == l, tO);
             }
             segment_done(seg);
             // a warp's rows of a piece: [D / 4][32][4], so that the warp writes 512 bytes at a time
@@ -704,14 +741,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                             const float *src = plan.part + ((int64_t)sl * 8 + warp) * 32 * D + lane * 4 + d * 32;
                             const float4 v0 = __ldcg(reinterpret_cast<const float4 *>(src));
                             const float4 v1 = __ldcg(reinterpret_cast<const float4 *>(src + 128));
-                            acc[0] = fmaf(wt, v0.x, acc[0]);
-                            acc[1] = fmaf(wt, v0.y, acc[1]);
-                            acc[2] = fmaf(wt, v0.z, acc[2]);
-                            acc[3] = fmaf(wt, v0.w, acc[3]);
-                            acc[4] = fmaf(wt, v1.x, acc[4]);
-                            acc[5] = fmaf(wt, v1.y, acc[5]);
-                            acc[6] = fmaf(wt, v1.z, acc[6]);
-                            acc[7] = fmaf(wt, v1.w, acc[7]);
+                            acc[0] = add_piece<kInt8>(wt, v0.x, acc[0]);
+                            acc[1] = add_piece<kInt8>(wt, v0.y, acc[1]);
+                            acc[2] = add_piece<kInt8>(wt, v0.z, acc[2]);
+                            acc[3] = add_piece<kInt8>(wt, v0.w, acc[3]);
+                            acc[4] = add_piece<kInt8>(wt, v1.x, acc[4]);
+                            acc[5] = add_piece<kInt8>(wt, v1.y, acc[5]);
+                            acc[6] = add_piece<kInt8>(wt, v1.z, acc[6]);
+                            acc[7] = add_piece<kInt8>(wt, v1.w, acc[7]);
                         }
                         *reinterpret_cast<uint4 *>(dst + d) =
                             make_uint4(pack_bf16x2(acc[0] * back, acc[1] * back), pack_bf16x2(acc[2] * back, acc[3] * back),
@@ -788,9 +825,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     cp_async16(smem_u32(dst + tile_off(r, lane % kLanes)), src + p * 512, r < count ? 16u : 0u);
                 }
             };
-            // A weight of 0 does not keep an infinity or a NaN of V out of a product: where not all
-            // rows see all tokens (bf16) they become zeros, and the softmax adds them to the rows
-            // that do.
+            // Where not all rows see all tokens the infinities and NaN of V (bf16) become zeros: a weight
+            // of 0 does not keep them out of a product.
             const int2 seen = is_v ? seen_by_all(w, G, a.window) : make_int2(0, INT32_MAX);
             auto drop_bad = [&](uint8_t *dst, int j) {
                 constexpr int kLanes = D / 8, kStep = 32 / kLanes;

@@ -29,7 +29,9 @@
  *    LORA_ERR_RANGE, the rows of that sequence are unspecified, other rows stay correct.
  *    Table entries past a sequence's last page are not read.
  *  - Cache rows that hold no token of a sequence may hold anything (inf and NaN included). An
- *    infinity or a NaN in a token's K or V reaches the rows that see that token, no others.
+ *    infinity or a NaN in a token's K or V reaches the rows that see that token, no others. One of
+ *    V in a bf16 cache makes that value of O that infinity, whatever weight the token has, and NaN
+ *    where the row also sees a NaN or the other infinity there.
  *  - T and table_stride * p are at most 2^30, T * n_heads below 2^31 (else LORA_ERR_ARG).
  *  - Calls are made with the device current that the cache was created on (else LORA_ERR_ARG).
  *  - A cache is not thread-safe: use it from one host thread at a time. Calls on several
