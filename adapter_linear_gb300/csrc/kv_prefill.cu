@@ -702,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prefill_kernel(KvDev kv, KvBat
                     for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<uint4 *>(part + (x + e) * 32) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
+                __syncwarp();  // the next load is the whole warp's
             }
             tc_fence_before_sync();
             if (whole) {
