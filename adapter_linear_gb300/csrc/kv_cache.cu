@@ -542,7 +542,9 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     a.o_stride = o_stride;
     a.Hq = n_heads;
     a.G = n_heads / p->H;
-    a.g_shift = 0;  // 2^s >= G: the multiplier, 2^(31 + s) / G rounded up, is off by less than 2^s / 2^31 of it
+    // 2^(s + 1) >= G > 2^s: the multiplier, 2^(32 + s) / G rounded up, times G is off from 2^(32 + s) by less than
+    // G, which shows from x = 2^31 on
+    a.g_shift = 0;
     while ((2 << a.g_shift) < a.G) ++a.g_shift;
     a.g_mul = a.G > 1 ? (uint32_t)(((1ull << (32 + a.g_shift)) + a.G - 1) / a.G) : 0;
     a.window = std::min(window, kMaxTokens);

@@ -55,7 +55,8 @@ struct Cfg {
     static constexpr bool kWide = kRowBytes == 256;
     // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers, 2 for three, which
     // spill at 3: 104 us against 81 for 32 drafts; rows of 256 bytes: 2 of 98 KB): 100 to
-    // 150 KB in flight beside the stages in use
+    // 150 KB in flight beside the stages in use. (Two row tiles of an 8-bit cache, D = 128: 16 bytes a thread
+    // spill; the others none.)
     static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
     static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 ? 4 : 3;
     static constexpr int kRing = kStages * kStage;
@@ -243,7 +244,7 @@ __device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int 
                 }
         }
         // Weights: summed in fp32, and for the product with V a pair of bf16, the rounded weight
-        // and the rest (together 2^-17 of it: one bf16 alone, 2^-8, shows in rows that see few
+        // and the rest (together off by 2^-16 of it: one bf16 alone, 2^-8, shows in rows that see few
         // keys, and HBM leaves the tensor cores the time). An 8-bit cache's V scale is
         // multiplied in first; a masked key's weight is 0 whatever its scale is.
         uint32_t p[kT][2], p2[kT][2];

@@ -23,7 +23,8 @@
  *  - Token tensors (K, V, Q, O) are bf16, [T][heads][D] with the heads of a token contiguous
  *    and token_stride elements from one token to the next (slices of a fused projection's
  *    output are fine): token_stride a multiple of 8 and at least heads * D, pointers 16-byte
- *    aligned. Rows at and after start[n_seqs] are neither read nor written.
+ *    aligned. Rows at and after start[n_seqs] are not written, and what they hold does not matter
+ *    (they have to exist: the write loads all T rows).
  *  - A table entry outside 0..P-1, a kv_len beyond table_stride * p or a start outside 0..T
  *    sets the cache's error word and is not followed; lora_kv_check_errors then returns
  *    LORA_ERR_RANGE, the rows of that sequence are unspecified, other rows stay correct.
@@ -113,8 +114,11 @@ lora_status lora_kv_read(lora_kv_t kv, void *K, int64_t k_stride, void *V, int64
  * position pos of sequence b, query head h and kv head h / (n_heads / H_kv),
  *     z_j = scale * <Q[t,h], K_j>,  j <= pos, and j > pos - window if window > 0,
  *     lse[t,h] = log sum_j exp(z_j),   O[t,h] = sum_j exp(z_j - lse) V_j
- * and O = 0, lse = -inf for a row that sees no token. Scores, softmax and sums are held in
- * fp32; O is rounded to bf16 once. lse (fp32 [T][n_heads]) may be NULL.
+ * and O = 0, lse = -inf for a row that sees no token. Scores, maxima, sums and O are held in
+ * fp32, and O is rounded to bf16 once. On its way into the product with V a weight is the sum of
+ * two bf16 numbers (off by 2^-16 of it) in sequences of up to 24 rows of a kv head (n_b * n_heads /
+ * H_kv) and, in longer ones, where a key may hold more than a quarter of what its row has so far;
+ * elsewhere it is rounded to bf16 (2^-8 of it). lse (fp32 [T][n_heads]) may be NULL.
  *   n_heads: a multiple of H_kv, at most 1024. O must not alias Q or the cache.
  * Asynchronous on `stream`. Errors: ARG, SHAPE (n_heads), OOM (scratch), CUDA.
  */
