@@ -21,11 +21,12 @@
 // Inside a CTA the four warps take 16-token steps in turn, each streaming its own codes through
 // its own ring of shared memory with 16-byte asynchronous copies: no barrier until an item ends.
 //
-// Measured, 32 query heads on 8 kv heads of 128 values: 64 requests of one token over 17 to 8191
-// tokens, 8-bit, 99 us (5.6 TB/s); 256 requests over 500 to 4095, bf16, 361 us (6.7 TB/s, the copy
-// bandwidth); 32 requests of 3 to 6 tokens over 300 to 6000, 8-bit, 79 us (2.8 TB/s: three row
-// tiles' accumulators leave 8 warps an SM, which wait for their own arithmetic); one request over
-// 2047 tokens 11 us (loads that depend on one another: lengths, pages, codes, then the join).
+// Measured, calls one after another, 32 query heads on 8 kv heads of 128 values: 64 requests of one
+// token over 17 to 8191 tokens, 8-bit, 100 us (5.5 TB/s); 256 requests over 500 to 4095, bf16, 366 us
+// (6.6 TB/s, 98 % of the copy bandwidth); 32 requests of 3 to 6 tokens over 300 to 6000, 8-bit, 82 us
+// (2.7 TB/s: three row tiles' accumulators leave 8 warps an SM, which wait for their own arithmetic); one
+// request over 2047 tokens 11 us on the GPU (loads that depend on one another: lengths, pages, codes, then the
+// join).
 #include <climits>
 #include <type_traits>
 

@@ -25,12 +25,12 @@
 // 32 on their way while these become weights.
 //
 // What bounds it: the softmax. Of the 3500 cycles that a key tile of 2 x 128 rows takes at D = 128,
-// bf16, it takes 2900 in each row's thread (41 % of the issue slots are used, the rest is
+// bf16, it takes 2900 in each row's thread (44 % of the issue slots are used, the rest is
 // latency between dependent instructions, two softmax warps a scheduler); with an 8-bit cache 6000 of
-// 6200 (47 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
-// the loads of scales and the MMAs' operands use 84 % of shared memory's bandwidth. The tensor cores
-// are active 46 and 42 % of the time. 32 query heads on 8 kv heads of 128 values: 8 prompts of
-// 2048 tokens bf16 381 us (0.72 PFLOP/s), 512 tokens over 32000 8-bit 358 us (0.76).
+// 6200 (49 %), the multiplications by scales on top and, beside it, the codes' conversion: their stores,
+// the loads of scales and the MMAs' operands use 86 % of shared memory's bandwidth. The tensor cores
+// are active 47 and 45 % of the time. 32 query heads on 8 kv heads of 128 values: 8 prompts of
+// 2048 tokens bf16 391 us (0.70 PFLOP/s), 512 tokens over 32000 8-bit 359 us (0.75), call included.
 //
 // An 8-bit cache's scales stay outside the products: the codes are exact in bf16, a key's scale
 // multiplies its column of S and a value's its weight.
