@@ -63,9 +63,12 @@ def test_memory_of_a_call_on_another_stream(as_handle):
     side = torch.cuda.Stream()
     stream = side.cuda_stream if as_handle else side
     rows = [torch.randn(p.T, h, 128, device="cuda").to(torch.bfloat16) for h in (8, 2, 2)]
+    p.cache.write(rows[1], rows[2], p.batch)                 # (kernels loaded, scratch there)
+    p.cache.attention(rows[0], p.batch)
+    p.cache.read(p.batch)
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(100_000_000)                       # some 50 ms
+        torch.cuda._sleep(400_000_000)                       # some 200 ms
     O, lse = p.cache.attention(rows[0], p.batch, stream=stream)
     p.cache.write(rows[1], rows[2], p.batch, stream=stream)
     K, V = p.cache.read(p.batch, stream=stream)
