@@ -48,6 +48,7 @@ EXPORTS = (
     "lora_pool_set_trace", "lora_linear_q4", "lora_base_linear_q4", "lora_dequant_q4",
     "lora_kv_create", "lora_kv_destroy", "lora_kv_reserve", "lora_kv_write", "lora_kv_read",
     "lora_kv_attention", "lora_kv_check_errors", "lora_kv_selftest_timeout",
+    "lora_rotary_frequencies", "lora_rotary_init", "lora_rotary_apply", "lora_kv_write_rotary",
 )
 PLAN_INFO_FIELDS = ("units", "G", "grid", "max_seg", "n_acc", "stages", "tmem_cols", "smem_bytes",
                     "pairs", "col_blocks", "tight", "ntok", "partials_floats", "prefetch_a")
@@ -80,7 +81,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             f"{path} is missing: build it with `python -m adapter_linear_gb300.build`")
     lib = ctypes.CDLL(path)
     vp, i32, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
-    i64 = ctypes.c_int64
+    i64, f64 = ctypes.c_int64, ctypes.c_double
     sig = {
         "lora_pool_create": [i32, i32, i32, i32, ctypes.POINTER(vp)],
         "lora_pool_destroy": [vp],
@@ -123,6 +124,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_kv_attention": [vp, vp, i64, i32, vp, f32, i32, vp, i64, vp, vp],
         "lora_kv_check_errors": [vp],
         "lora_kv_selftest_timeout": [vp, vp],
+        "lora_rotary_frequencies": [i32, f64, i32, f64, f64, vp, vp, vp],
+        "lora_rotary_init": [i32, i32, vp, f64, vp],
+        "lora_rotary_apply": [vp, i32, vp, i32, vp, i32, i32, vp],
+        "lora_kv_write_rotary": [vp, vp, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -462,4 +467,5 @@ class LoraPool:
         _check(lora_pool_set_trace(self.handle, buf, n_calls), "lora_pool_set_trace")
 
 
+from .rotary import Rotary  # noqa: E402,F401
 from .kv import KvBatch, KvCache  # noqa: E402,F401

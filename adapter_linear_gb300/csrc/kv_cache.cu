@@ -6,6 +6,7 @@
 
 #include "kv_device.cuh"
 #include "kv_state.h"
+#include "rotary_device.cuh"
 
 using namespace lora;
 
@@ -505,6 +506,35 @@ lora_status lora_kv_write(lora_kv_t p, const void *K, int64_t k_stride, const vo
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
     CUDA_TRY(launch_kv_write(kv_view(p), p->int8, batch_view(batch), static_cast<const uint16_t *>(K), k_stride,
                              static_cast<const uint16_t *>(V), v_stride, p->num_sms, stream));
+    return note_kv_call(p, stream);
+}
+
+lora_status lora_kv_write_rotary(lora_kv_t p, const lora_rotary *rotary, const void *K, int64_t k_stride,
+                                 const void *V, int64_t v_stride, const void *Q, int64_t q_stride, int n_heads,
+                                 void *Q_out, int64_t qo_stride, const lora_kv_batch *batch, lora_stream_t stream)
+{
+    if (!p || !rotary_ok(rotary)) return LORA_ERR_ARG;
+    if (rotary->rotary_dim > p->D || n_heads < 0 || n_heads > 1024) return LORA_ERR_SHAPE;
+    bool empty;
+    lora_status st = check_batch(p, batch, &empty);
+    if (st != LORA_OK || empty) return st;
+    if ((int64_t)batch->T * (n_heads + 2 * p->H) > INT_MAX) return LORA_ERR_ARG;
+    const int64_t row = (int64_t)p->H * p->D, q_row = (int64_t)n_heads * p->D;
+    if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
+    if (n_heads > 0 && (!tensor_ok(Q, q_stride, q_row) || !tensor_ok(Q_out, qo_stride, q_row) ||
+                        (Q == Q_out && q_stride != qo_stride)))
+        return LORA_ERR_ARG;
+    KvRotaryArgs a;
+    a.K = static_cast<const uint16_t *>(K);
+    a.V = static_cast<const uint16_t *>(V);
+    a.Q = static_cast<const uint16_t *>(Q);
+    a.Q_out = static_cast<uint16_t *>(Q_out);
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.qo_stride = qo_stride;
+    a.Hq = n_heads;
+    CUDA_TRY(launch_kv_write_rotary(kv_view(p), p->int8, batch_view(batch), rotary, a, p->num_sms, stream));
     return note_kv_call(p, stream);
 }
 

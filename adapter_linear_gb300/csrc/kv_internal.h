@@ -32,6 +32,16 @@ cudaError_t launch_kv_write(const KvDev &kv, bool int8, const KvBatchDev &b, con
 cudaError_t launch_kv_read(const KvDev &kv, bool int8, const KvBatchDev &b, uint16_t *K, int64_t k_stride,
                            uint16_t *V, int64_t v_stride, int num_sms, cudaStream_t stream);
 
+// The write with rotary positions: K, V as for the write; Q (Hq heads, 0: none) rotated into Q_out.
+struct KvRotaryArgs {
+    const uint16_t *K, *V, *Q;
+    uint16_t *Q_out;
+    int64_t k_stride, v_stride, q_stride, qo_stride;
+    int Hq;
+};
+cudaError_t launch_kv_write_rotary(const KvDev &kv, bool int8, const KvBatchDev &b, const lora_rotary *rotary,
+                                   const KvRotaryArgs &a, int num_sms, cudaStream_t stream);
+
 // One attention call.
 struct KvAttn {
     const uint16_t *Q;

@@ -1,0 +1,205 @@
+// rotary.cu -- rotary positions: frequencies (host), and the kernel that rotates tensors of tokens.
+#include <algorithm>
+#include <cmath>
+
+#include "pool_state.h"
+#include "rotary_device.cuh"
+
+using namespace lora;
+
+namespace {
+
+struct Tensors {
+    const uint16_t *in[LORA_ROTARY_MAX_TENSORS];
+    uint16_t *out[LORA_ROTARY_MAX_TENSORS];
+    int64_t in_stride[LORA_ROTARY_MAX_TENSORS], out_stride[LORA_ROTARY_MAX_TENSORS];
+    int end[LORA_ROTARY_MAX_TENSORS];  // heads of the tensors up to this one (those past the last: the same)
+};
+
+constexpr int kBatch = 4;  // blocks of rows loaded before any is stored
+
+// A row is one head of one token, of any tensor; head_dim / 16 lanes hold one. A warp takes `blocks`
+// blocks of 32 / (head_dim / 16) rows of one token, so that its lanes' eight angles each serve all of them.
+__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryDev rot, Tensors x, int head_dim,
+                                                     const int32_t *__restrict__ positions, int T, int inverse,
+                                                     int parts, int blocks)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const int64_t t64 = w / parts;
+    if (t64 >= T) return;
+    const int t = (int)t64;
+    const int lanes = head_dim / 16, per = 32 / lanes;  // lanes of a row, rows of a block
+    const int sub = lane / lanes, c = lane - sub * lanes;
+    const int rows = x.end[LORA_ROTARY_MAX_TENSORS - 1];
+    const int first = (int)(w - t64 * parts) * blocks * per + sub;
+    const int last = sub < per ? min(rows, first - sub + blocks * per) : 0;
+    int d0, d1;
+    rotary_runs(rot, c, &d0, &d1);
+    const bool turns = 16 * c < rot.dim;
+    Turn8 turn;
+    if (turns) turn = rotary_turn(rot, c, positions[t], inverse);
+    for (int r0 = first; r0 < last; r0 += kBatch * per) {
+        uint4 v[kBatch][2];
+        uint16_t *to[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = r0 + i * per;
+            to[i] = nullptr;
+            if (r >= last) continue;
+            int k = 0, begin = 0;
+#pragma unroll
+            for (int y = 0; y < LORA_ROTARY_MAX_TENSORS - 1; ++y)
+                if (r >= x.end[y]) {
+                    k = y + 1;
+                    begin = x.end[y];
+                }
+            const uint16_t *const src = x.in[k] + (int64_t)t * x.in_stride[k] + (int64_t)(r - begin) * head_dim;
+            to[i] = x.out[k] + (int64_t)t * x.out_stride[k] + (int64_t)(r - begin) * head_dim;
+            if (!turns && to[i] == src) {  // in place: what is not rotated is there
+                to[i] = nullptr;
+                continue;
+            }
+            v[i][0] = *reinterpret_cast<const uint4 *>(src + d0);
+            v[i][1] = *reinterpret_cast<const uint4 *>(src + d1);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (!to[i]) continue;
+            if (turns) {
+                float f[16];
+                unpack8(v[i][0], f);
+                unpack8(v[i][1], f + 8);
+                rotary_pairs(rot.half, turn, f);
+                v[i][0] = pack8(f);
+                v[i][1] = pack8(f + 8);
+            }
+            *reinterpret_cast<uint4 *>(to[i] + d0) = v[i][0];
+            *reinterpret_cast<uint4 *>(to[i] + d1) = v[i][1];
+        }
+    }
+}
+
+bool positive(double x) { return std::isfinite(x) && x > 0.0; }
+
+constexpr double kTwoPi = 6.283185307179586476925;
+
+}  // namespace
+
+extern "C" {
+
+lora_status lora_rotary_frequencies(int rotary_dim, double base, int scaling, double scale, double trained,
+                                    const double *options, double *freq, double *factor)
+{
+    if (!freq || !factor || !positive(base)) return LORA_ERR_ARG;
+    if (scaling < LORA_ROTARY_PLAIN || scaling > LORA_ROTARY_BANDS) return LORA_ERR_ARG;
+    if (rotary_dim < 16 || rotary_dim > LORA_ROTARY_MAX_DIM || rotary_dim % 16 != 0) return LORA_ERR_SHAPE;
+    if (scaling != LORA_ROTARY_PLAIN && !positive(scale)) return LORA_ERR_ARG;
+    const bool yarn = scaling == LORA_ROTARY_YARN, bands = scaling == LORA_ROTARY_BANDS;
+    double o0 = yarn ? 32.0 : 1.0, o1 = yarn ? 1.0 : 4.0;
+    if (yarn || bands) {
+        if (!positive(trained)) return LORA_ERR_ARG;
+        if (options) {
+            o0 = options[0];
+            o1 = options[1];
+        }
+        if (!positive(o0) || !positive(o1) || (yarn ? o0 <= o1 : o0 >= o1)) return LORA_ERR_ARG;
+        if (yarn && base <= 1.0) return LORA_ERR_ARG;
+    }
+    const int R = rotary_dim;
+    if (scaling == LORA_ROTARY_NTK) base *= std::pow(scale, (double)R / (R - 2));
+    // pair at which a model of this base turns `turns` times over the trained context
+    auto pair_of = [&](double turns) { return R * std::log(trained / (kTwoPi * turns)) / (2.0 * std::log(base)); };
+    double low = 0.0, high = 0.0;
+    if (yarn) {
+        low = std::fmax(std::floor(pair_of(o0)), 0.0);
+        high = std::fmin(std::ceil(pair_of(o1)), R - 1.0);
+        if (high <= low) high = low + 0.001;
+    }
+    *factor = yarn && scale > 1.0 ? 0.1 * std::log(scale) + 1.0 : 1.0;
+    for (int i = 0; i < R / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / R);
+        if (scaling == LORA_ROTARY_LINEAR) f /= scale;
+        if (yarn) {
+            const double far = std::fmin(std::fmax((i - low) / (high - low), 0.0), 1.0);
+            f = f / scale * far + f * (1.0 - far);
+        }
+        if (bands) {
+            const double turns = trained * f / kTwoPi;
+            const double near = std::fmin(std::fmax((turns - o0) / (o1 - o0), 0.0), 1.0);
+            f = f / scale * (1.0 - near) + f * near;
+        }
+        freq[i] = f;
+    }
+    return LORA_OK;
+}
+
+lora_status lora_rotary_init(int rotary_dim, int layout, const double *freq, double factor, lora_rotary *out)
+{
+    if (!freq || !out || !std::isfinite(factor) || !std::isfinite((float)factor)) return LORA_ERR_ARG;
+    if (layout != LORA_ROTARY_HALF && layout != LORA_ROTARY_INTERLEAVED) return LORA_ERR_ARG;
+    if (rotary_dim < 16 || rotary_dim > LORA_ROTARY_MAX_DIM || rotary_dim % 16 != 0) return LORA_ERR_SHAPE;
+    for (int i = 0; i < rotary_dim / 2; ++i)
+        if (!std::isfinite(freq[i])) return LORA_ERR_ARG;
+    lora_rotary r = {};
+    r.rotary_dim = rotary_dim;
+    r.layout = layout;
+    r.factor = (float)factor;
+    for (int i = 0; i < rotary_dim / 2; ++i) {
+        double turns = freq[i] / kTwoPi;
+        turns -= std::floor(turns);                       // in [0, 1], 1 by rounding
+        r.step[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
+    }
+    *out = r;
+    return LORA_OK;
+}
+
+lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotary_tensor *tensors, int head_dim,
+                              const int32_t *positions, int T, int inverse, lora_stream_t stream)
+{
+    if (!rotary_ok(rotary) || !tensors || n < 1 || n > LORA_ROTARY_MAX_TENSORS || T < 0 || T > (1 << 30))
+        return LORA_ERR_ARG;
+    if (head_dim < rotary->rotary_dim || head_dim > LORA_ROTARY_MAX_DIM || head_dim % 16 != 0) return LORA_ERR_SHAPE;
+    Tensors x = {};
+    int64_t rows = 0;
+    for (int i = 0; i < LORA_ROTARY_MAX_TENSORS; ++i) {
+        if (i < n) {
+            const lora_rotary_tensor &a = tensors[i];
+            if (a.heads < 1 || a.heads > 65536) return LORA_ERR_ARG;
+            const int64_t row = (int64_t)a.heads * head_dim;
+            if (T > 0 && (!a.in || !a.out)) return LORA_ERR_ARG;
+            if ((reinterpret_cast<uintptr_t>(a.in) | reinterpret_cast<uintptr_t>(a.out)) & 15) return LORA_ERR_ARG;
+            if (a.in_stride < row || a.out_stride < row || a.in_stride % 8 != 0 || a.out_stride % 8 != 0)
+                return LORA_ERR_ARG;
+            if (a.in == a.out && a.in_stride != a.out_stride) return LORA_ERR_ARG;
+            x.in[i] = static_cast<const uint16_t *>(a.in);
+            x.out[i] = static_cast<uint16_t *>(a.out);
+            x.in_stride[i] = a.in_stride;
+            x.out_stride[i] = a.out_stride;
+            rows += a.heads;
+        }
+        x.end[i] = (int)rows;
+    }
+    if (T == 0) return LORA_OK;
+    if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3)) return LORA_ERR_ARG;
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    CUDA_TRY(cudaGetDevice(&dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (major != 10 || minor != 3) return LORA_ERR_UNSUPPORTED;
+    CUDA_TRY(ensure_smem_attr((const void *)rotary_kernel, 0));
+    const int per = 32 / (head_dim / 16);
+    const int64_t all = (rows + per - 1) / per;  // blocks of a token
+    // one block a warp until four warps a scheduler have one, then up to all of a token's
+    const int64_t blocks = std::min(all, std::max<int64_t>(1, (int64_t)T * all / (16 * (int64_t)sms)));
+    const int64_t parts = (all + blocks - 1) / blocks;
+    const int64_t ctas = ((int64_t)T * parts + 7) / 8;
+    if (ctas > 0x7FFFFFFF) return LORA_ERR_ARG;
+    rotary_kernel<<<(unsigned)ctas, 256, 0, stream>>>(rotary_view(rotary), x, head_dim, positions, T, inverse != 0,
+                                                      (int)parts, (int)blocks);
+    CUDA_TRY(cudaGetLastError());
+    return LORA_OK;
+}
+
+}  // extern "C"

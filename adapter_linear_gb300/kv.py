@@ -13,6 +13,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import LORA_ERR_ARG, LORA_ERR_SHAPE, LORA_KV_BF16, LORA_KV_INT8, LoraError, _check, _ptr, load_library
+from .rotary import Rotary
 
 
 class _BatchStruct(ctypes.Structure):
@@ -153,6 +154,30 @@ class KvCache:
         st = self._stream(stream, batch, K, V)
         _check(self._lib.lora_kv_write(self.handle, K.data_ptr(), ks, V.data_ptr(), vs, batch.ref, st),
                "lora_kv_write")
+
+    def write_rotary(self, rotary: Rotary, K, V, batch: KvBatch, Q=None, Q_out=None, stream=None):
+        """Write the batch's keys, rotated by their positions, and its values (as they are) into their pages. Q
+        (bf16 [T, heads, head_dim]): rotated beside them into Q_out (Q itself: in place; by default a new
+        tensor), which is returned."""
+        what = "lora_kv_write_rotary"
+        ks, vs = self._rows(K, self.kv_heads, batch, what + " K"), self._rows(V, self.kv_heads, batch, what + " V")
+        qs = os_ = heads = 0
+        if Q is not None:
+            if Q.dim() != 3:
+                raise LoraError(LORA_ERR_SHAPE, what + ": Q is [T, heads, head_dim]")
+            heads = Q.shape[1]
+            qs = self._rows(Q, heads, batch, what + " Q")
+            if Q_out is None:
+                Q_out = self._empty((batch.T, heads, self.head_dim), torch.bfloat16, stream)
+                os_ = heads * self.head_dim
+            else:
+                os_ = self._rows(Q_out, heads, batch, what + " Q_out")
+        elif Q_out is not None:
+            raise LoraError(LORA_ERR_ARG, what + ": Q_out without Q")
+        st = self._stream(stream, batch, K, V, Q, Q_out)
+        _check(self._lib.lora_kv_write_rotary(self.handle, rotary.ref, K.data_ptr(), ks, V.data_ptr(), vs, _ptr(Q), qs,
+                                              heads, _ptr(Q_out), os_, batch.ref, st), what)
+        return Q_out
 
     def read(self, batch: KvBatch, K=None, V=None, stream=None):
         """The batch's tokens as bf16 [T, kv_heads, head_dim] keys and values."""

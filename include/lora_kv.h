@@ -45,6 +45,7 @@
 #define LORA_KV_H
 
 #include "lora_linear.h"
+#include "lora_rotary.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -100,6 +101,22 @@ lora_status lora_kv_reserve(lora_kv_t kv, int max_tokens, int n_heads, int max_s
  */
 lora_status lora_kv_write(lora_kv_t kv, const void *K, int64_t k_stride, const void *V, int64_t v_stride,
                           const lora_kv_batch *batch, lora_stream_t stream);
+
+/*
+ * The write with rotary positions (lora_rotary.h) on the way: K's rows are rotated by their tokens' positions
+ * in fp32 and written (rounded once to bf16, or quantised from fp32 as above), V's are written as they are,
+ * and, where n_heads > 0, Q ([T][n_heads][D]) is rotated into Q_out (rounded once), in one pass.
+ * Scales and codes of V are those of lora_kv_write. K's come from fp32 values that are off by their
+ * arithmetic (2^-21 of the pair's length): a code is within 1/2 + 2^-10 of a step of the exact
+ * value; a rotated value beyond the largest bf16 counts as an infinity. Q_out == Q (and its stride) rotates in
+ * place; otherwise the two do not overlap. Rows of Q_out at positions below zero become zeros; those at
+ * and after start[n_seqs] and those of a bad sequence are not written (Q's and K's are loaded).
+ * rotary: HOST, rotary_dim at most the cache's head_dim. n_heads: 0..1024.
+ * Asynchronous on `stream`. Errors: ARG, SHAPE (rotary_dim, n_heads), CUDA.
+ */
+lora_status lora_kv_write_rotary(lora_kv_t kv, const lora_rotary *rotary, const void *K, int64_t k_stride,
+                                 const void *V, int64_t v_stride, const void *Q, int64_t q_stride, int n_heads,
+                                 void *Q_out, int64_t qo_stride, const lora_kv_batch *batch, lora_stream_t stream);
 
 /*
  * Read the batch's tokens back: K and V [T][H_kv][D] bf16, an int8 cache's values as
