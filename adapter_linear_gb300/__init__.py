@@ -49,6 +49,8 @@ EXPORTS = (
     "lora_kv_create", "lora_kv_destroy", "lora_kv_reserve", "lora_kv_write", "lora_kv_read",
     "lora_kv_attention", "lora_kv_check_errors", "lora_kv_selftest_timeout",
     "lora_rotary_frequencies", "lora_rotary_init", "lora_rotary_apply", "lora_kv_write_rotary",
+    "lora_kv_pages_create", "lora_kv_pages_destroy", "lora_kv_pages_update", "lora_kv_pages_compact",
+    "lora_kv_pages_used", "lora_kv_pages_check_errors", "lora_kv_copy", "lora_kv_copy_pages",
 )
 PLAN_INFO_FIELDS = ("units", "G", "grid", "max_seg", "n_acc", "stages", "tmem_cols", "smem_bytes",
                     "pairs", "col_blocks", "tight", "ntok", "partials_floats", "prefetch_a")
@@ -127,6 +129,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_rotary_frequencies": [i32, f64, i32, f64, f64, vp, vp, vp],
         "lora_rotary_init": [i32, i32, vp, f64, vp],
         "lora_rotary_apply": [vp, i32, vp, i32, vp, i32, i32, vp],
+        "lora_kv_pages_create": [i32, i32, i32, i32, vp, vp, vp, ctypes.POINTER(vp)],
+        "lora_kv_pages_destroy": [vp],
+        "lora_kv_pages_update": [vp, vp, vp, vp, vp],
+        "lora_kv_pages_compact": [vp, vp, vp, vp],
+        "lora_kv_pages_used": [vp, ctypes.POINTER(i32)],
+        "lora_kv_pages_check_errors": [vp],
+        "lora_kv_copy": [vp, vp, vp],
+        "lora_kv_copy_pages": [vp, vp, vp, vp, i32, vp],
         "lora_kv_write_rotary": [vp, vp, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, vp],
     }
     for name, args in sig.items():
@@ -468,4 +478,4 @@ class LoraPool:
 
 
 from .rotary import Rotary  # noqa: E402,F401
-from .kv import KvBatch, KvCache  # noqa: E402,F401
+from .kv import KvBatch, KvCache, KvPages  # noqa: E402,F401

@@ -5,6 +5,7 @@
 #include <new>
 
 #include "kv_device.cuh"
+#include "kv_pages_state.h"
 #include "kv_state.h"
 #include "rotary_device.cuh"
 
@@ -549,6 +550,35 @@ lora_status lora_kv_read(lora_kv_t p, void *K, int64_t k_stride, void *V, int64_
     if (!tensor_ok(K, k_stride, row) || !tensor_ok(V, v_stride, row)) return LORA_ERR_ARG;
     CUDA_TRY(launch_kv_read(kv_view(p), p->int8, batch_view(batch), static_cast<uint16_t *>(K), k_stride,
                             static_cast<uint16_t *>(V), v_stride, p->num_sms, stream));
+    return note_kv_call(p, stream);
+}
+
+lora_status lora_kv_copy(lora_kv_t p, lora_kv_pages_t pages, lora_stream_t stream)
+{
+    if (!p || !pages || pages->device != p->device) return LORA_ERR_ARG;
+    if (pages->page_shift != p->page_shift || pages->num_pages > p->num_pages) return LORA_ERR_ARG;
+    int dev = -1;
+    CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return LORA_ERR_ARG;
+    bool tracked;
+    lora_status st = kv_pages_begin(pages, stream, &tracked);
+    if (st != LORA_OK) return st;
+    st = kv_pages_end(pages, stream, tracked, launch_kv_copy_moves(kv_view(p), p->int8, pages, p->num_sms, stream));
+    return st == LORA_OK ? note_kv_call(p, stream) : st;
+}
+
+lora_status lora_kv_copy_pages(lora_kv_t p, const int32_t *src, const int32_t *dst, const int32_t *rows, int n,
+                               lora_stream_t stream)
+{
+    if (!p || n < 0) return LORA_ERR_ARG;
+    int dev = -1;
+    CUDA_TRY(cudaGetDevice(&dev));
+    if (dev != p->device) return LORA_ERR_ARG;
+    if (n == 0) return LORA_OK;
+    if (!src || !dst) return LORA_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | reinterpret_cast<uintptr_t>(rows)) & 3)
+        return LORA_ERR_ARG;
+    CUDA_TRY(launch_kv_copy(kv_view(p), p->int8, src, dst, rows, nullptr, n, p->num_sms, stream));
     return note_kv_call(p, stream);
 }
 

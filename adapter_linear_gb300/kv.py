@@ -224,9 +224,139 @@ class KvCache:
                                            O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention")
         return O, lse
 
+    def copy(self, pages: "KvPages", stream=None):
+        """Make the copies that the last update or compaction of `pages` asks for."""
+        if pages._device != self._device:
+            raise LoraError(LORA_ERR_ARG, "lora_kv_copy: the page tables are on the cache's GPU")
+        st = self._stream(stream, pages)
+        _check(self._lib.lora_kv_copy(self.handle, pages.handle, st), "lora_kv_copy")
+
+    def copy_pages(self, src, dst, rows=None, stream=None):
+        """Copy the first rows[i] (all) tokens of page src[i] to page dst[i] (int32 [n] tensors)."""
+        lists = tuple(t for t in (src, dst, rows) if t is not None)
+        for t in lists:
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.shape != src.shape:
+                raise LoraError(LORA_ERR_SHAPE, "lora_kv_copy_pages: src, dst and rows are contiguous int32 [n]")
+            if t.get_device() != self._device:
+                raise LoraError(LORA_ERR_ARG, "lora_kv_copy_pages: the tensors of a call are on the cache's GPU")
+        st = self._stream(stream, _Tensors(lists))
+        _check(self._lib.lora_kv_copy_pages(self.handle, src.data_ptr(), dst.data_ptr(), _ptr(rows), src.shape[0], st),
+               "lora_kv_copy_pages")
+
     def check_errors(self) -> int:
         return self._lib.lora_kv_check_errors(self.handle)
 
     def selftest_timeout(self, stream=None):
         """Test hook: leaves the cache as calls do whose bounded waits ran out."""
         _check(self._lib.lora_kv_selftest_timeout(self.handle, self._stream(stream)), "lora_kv_selftest_timeout")
+
+
+class _Tensors:
+    """Tensors a call uses, where a KvBatch stands otherwise."""
+
+    def __init__(self, tensors):
+        self.tensors = tensors
+
+
+class KvPages:
+    """The page tables of max_seqs sequences over num_pages pages of page_tokens tokens: `table` int32 [max_seqs,
+    max_entries], `kv_len` int32 [max_seqs] and `refs` int32 [num_pages] (table entries that name a page),
+    device tensors that a KvBatch may name. tensors: (table, kv_len, refs) to use in place of new, empty ones.
+
+    Calls run on the current stream or on `stream`. They change the tables; KvCache.copy then makes the copies
+    they ask for, in each cache."""
+
+    def __init__(self, num_pages: int, page_tokens: int, max_seqs: int, max_entries: int, device="cuda",
+                 tensors: Optional[Tuple] = None):
+        self.handle = None
+        self.num_pages, self.page_tokens, self.max_seqs, self.max_entries = num_pages, page_tokens, max_seqs, max_entries
+        if tensors is None:
+            if min(num_pages, max_seqs, max_entries) < 1:
+                raise LoraError(LORA_ERR_SHAPE, "KvPages: num_pages, max_seqs and max_entries are positive")
+            table = torch.full((max_seqs, max_entries), -1, dtype=torch.int32, device=device)
+            kv_len, refs = (torch.zeros(n, dtype=torch.int32, device=device) for n in (max_seqs, num_pages))
+        else:
+            table, kv_len, refs = tensors
+        self._device = table.get_device()
+        self._state(table, refs, "KvPages")
+        self._slots(kv_len, "KvPages: kv_len")
+        self.table, self.kv_len, self.refs = table, kv_len, refs
+        self.tensors = (table, kv_len, refs)
+        h = ctypes.c_void_p()
+        self._lib = load_library()
+        _check(self._lib.lora_kv_pages_create(num_pages, page_tokens, max_seqs, max_entries, table.data_ptr(),
+                                              kv_len.data_ptr(), refs.data_ptr(), ctypes.byref(h)),
+               "lora_kv_pages_create")
+        self.handle = h.value
+
+    def close(self):
+        if self.handle:
+            self._lib.lora_kv_pages_destroy(self.handle)
+            self.handle = None
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001
+            pass
+
+    def _state(self, table, refs, what):
+        for t, shape in ((table, (self.max_seqs, self.max_entries)), (refs, (self.num_pages,))):
+            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise LoraError(LORA_ERR_SHAPE, f"{what}: contiguous int32 {shape} expected")
+            if self._device < 0 or t.get_device() != self._device:
+                raise LoraError(LORA_ERR_ARG, f"{what}: the tensors are on one GPU")
+
+    def _slots(self, t, what):
+        if t.dtype != torch.int32 or tuple(t.shape) != (self.max_seqs,) or not t.is_contiguous():
+            raise LoraError(LORA_ERR_SHAPE, f"{what} is contiguous int32 [{self.max_seqs}]")
+        if self._device < 0 or t.get_device() != self._device:
+            raise LoraError(LORA_ERR_ARG, f"{what} is on the tables' GPU")
+
+    def _stream(self, stream, *tensors) -> int:
+        current = torch._C._cuda_getCurrentRawStream(self._device)
+        if stream is None:
+            return current
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        if handle != current:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, self.table.device)
+            for t in tensors + self.tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        return handle
+
+    def update(self, parent=None, keep=None, room=None, stream=None):
+        """Slot i becomes the first keep[i] tokens (all) of what slot parent[i] (itself) holds, -1: nothing, and
+        room[i] (0) tokens behind them; int32 [max_seqs] tensors. Follow it with KvCache.copy in each cache
+        unless every slot keeps its own tokens."""
+        for t, name in ((parent, "parent"), (keep, "keep"), (room, "room")):
+            if t is not None:
+                self._slots(t, f"lora_kv_pages_update: {name}")
+        st = self._stream(stream, parent, keep, room)
+        _check(self._lib.lora_kv_pages_update(self.handle, _ptr(parent), _ptr(keep), _ptr(room), st),
+               "lora_kv_pages_update")
+
+    def compact(self, out: Optional[Tuple] = None, stream=None):
+        """Number the used pages from 0. out: (table, refs) for the new state, by default this object's own. Follow
+        it with KvCache.copy in each cache."""
+        table, refs = out if out is not None else (None, None)
+        if out is not None:
+            self._state(table, refs, "lora_kv_pages_compact")
+        st = self._stream(stream, table, refs)
+        _check(self._lib.lora_kv_pages_compact(self.handle, _ptr(table), _ptr(refs), st), "lora_kv_pages_compact")
+
+    def used(self) -> int:
+        """Pages in use, once the calls so far are done."""
+        n = ctypes.c_int(0)
+        _check(self._lib.lora_kv_pages_used(self.handle, ctypes.byref(n)), "lora_kv_pages_used")
+        return n.value
+
+    def check_errors(self) -> int:
+        return self._lib.lora_kv_pages_check_errors(self.handle)

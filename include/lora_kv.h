@@ -127,6 +127,80 @@ lora_status lora_kv_read(lora_kv_t kv, void *K, int64_t k_stride, void *V, int64
                          const lora_kv_batch *batch, lora_stream_t stream);
 
 /*
+ * The page tables of sequences that come, fork, grow, shrink and go. A lora_kv_pages keeps, over the caller's
+ * device arrays (valid until it is destroyed; a lora_kv_batch may name them),
+ *   page_table [max_seqs][table_stride], kv_len [max_seqs]    as a batch has them, a row a slot
+ *   refs [num_pages]                                           table entries that name each page
+ * where slot s holds kv_len[s] tokens (0: it is empty) in its first ceil(kv_len[s] / p) entries. A new
+ * one: lengths and refs 0. Only these calls change the arrays, or the caller, who keeps refs true. The
+ * tables serve any number of caches (one a layer) of num_pages pages or more: the calls below change the
+ * tables, and lora_kv_copy makes the copies of pages that the last of them asks for in one cache.
+ * Calls are ordered by the library, on whatever streams (captured ones by whoever replays the graph); nothing is
+ * allocated after the creation. Not thread-safe. Limits: max_seqs 65536, max_seqs * table_stride below 2^31,
+ * table_stride * p at most 2^30.
+ */
+typedef struct lora_kv_pages lora_kv_pages;
+typedef lora_kv_pages *lora_kv_pages_t;
+
+/* Create on the current device; nothing is written to the arrays. Errors: SHAPE (num_pages outside 1..2^27,
+ * page_tokens, max_seqs, table_stride), ARG (null or misaligned (4 bytes) arrays, out == NULL), UNSUPPORTED,
+ * OOM, CUDA. */
+lora_status lora_kv_pages_create(int num_pages, int page_tokens, int max_seqs, int table_stride,
+                                 int32_t *page_table, int32_t *kv_len, int32_t *refs, lora_kv_pages_t *out);
+
+/* Wait for the device, then free the handle and its scratch (not the arrays). */
+lora_status lora_kv_pages_destroy(lora_kv_pages_t pages);
+
+/*
+ * Every slot i becomes the first n_i = min(keep[i], kv_len[parent[i]]) tokens of what slot parent[i] holds now
+ * (parent -1: nothing), and room[i] tokens behind them: kv_len[i] = n_i + room[i]. parent, keep, room: device
+ * int32 [max_seqs]; NULL: the slot itself, all its tokens, 0. So a step that extends its sequences
+ * gives room; parent copies, reorders (all at once: beams) and frees; keep trims.
+ *
+ * Pages that n_i fills are shared. The page that n_i ends inside belongs to one slot alone, which may write
+ * its other rows: it stays with the slot that ends inside it (first those with parent[i] = i, then the
+ * lowest i) if no slot has all of it; the others get a page of their own and a copy of its rows (lora_kv_copy).
+ * New pages are the lowest that no slot names afterwards, slot by slot, entry by entry. Entries that a slot no
+ * longer uses become -1.
+ *
+ * Where the pages do not suffice (LORA_ERR_OOM from lora_kv_pages_check_errors), or a parent, a room, a length or
+ * an entry is out of range (LORA_ERR_RANGE), nothing changes and nothing is to be copied.
+ * Asynchronous on `stream`. Errors: ARG, CUDA.
+ */
+lora_status lora_kv_pages_update(lora_kv_pages_t pages, const int32_t *parent, const int32_t *keep, const int32_t *room,
+                                 lora_stream_t stream);
+
+/*
+ * With n pages in use, moves those numbered n and above, in order, to the free pages below n, in order: afterwards
+ * pages 0..n-1 are used, and the arenas' rest may serve others. table_out, refs_out: device arrays like
+ * page_table and refs that get the new state (the handle's own keep the old one, for steps that still run on
+ * it); both NULL: in place. kv_len does not change. lora_kv_copy then moves the pages, in each cache.
+ * Entries out of range are left as they are (LORA_ERR_RANGE).
+ * Asynchronous on `stream`. Errors: ARG, CUDA.
+ */
+lora_status lora_kv_pages_compact(lora_kv_pages_t pages, int32_t *table_out, int32_t *refs_out, lora_stream_t stream);
+
+/* Wait for the calls enqueued on the handle, then HOST *used = pages that refs names. Errors: ARG, CUDA. */
+lora_status lora_kv_pages_used(lora_kv_pages_t pages, int *used);
+
+/* Wait for the calls enqueued on the handle, then read and clear its error word: LORA_OK, LORA_ERR_OOM,
+ * LORA_ERR_RANGE, LORA_ERR_CUDA. (Graph replays are not tracked: synchronise their stream first.) */
+lora_status lora_kv_pages_check_errors(lora_kv_pages_t pages);
+
+/* Make the copies that the last update or compaction of `pages` asks for in the cache (K, V and scales; the rows
+ * in use of an update's pages, whole pages of a compaction's). Follows that call; a later call on `pages` follows
+ * this one. Asynchronous on `stream`. Errors: ARG (null, another device, page_tokens that differ, a cache of
+ * fewer pages), CUDA. */
+lora_status lora_kv_copy(lora_kv_t kv, lora_kv_pages_t pages, lora_stream_t stream);
+
+/* Copy the first rows[i] (NULL: all) tokens of page src[i] to page dst[i], i < n (device int32 arrays). Pairs with a
+ * negative page are left out; one with a page or a row count out of range sets the error word (LORA_ERR_RANGE).
+ * No page is a destination twice, or a destination and a source (of another pair).
+ * Asynchronous on `stream`. Errors: ARG (also n < 0), CUDA. */
+lora_status lora_kv_copy_pages(lora_kv_t kv, const int32_t *src, const int32_t *dst, const int32_t *rows, int n,
+                               lora_stream_t stream);
+
+/*
  * Attention of the batch's tokens over the cache (which already holds them): for row t at
  * position pos of sequence b, query head h and kv head h / (n_heads / H_kv),
  *     z_j = scale * <Q[t,h], K_j>,  j <= pos, and j > pos - window if window > 0,
