@@ -51,6 +51,7 @@ EXPORTS = (
     "lora_rotary_frequencies", "lora_rotary_init", "lora_rotary_apply", "lora_kv_write_rotary",
     "lora_kv_pages_create", "lora_kv_pages_destroy", "lora_kv_pages_update", "lora_kv_pages_compact",
     "lora_kv_pages_used", "lora_kv_pages_check_errors", "lora_kv_copy", "lora_kv_copy_pages",
+    "lora_kv_reserve_shared", "lora_kv_attention_shared",
 )
 PLAN_INFO_FIELDS = ("units", "G", "grid", "max_seg", "n_acc", "stages", "tmem_cols", "smem_bytes",
                     "pairs", "col_blocks", "tight", "ntok", "partials_floats", "prefetch_a")
@@ -129,6 +130,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "lora_rotary_frequencies": [i32, f64, i32, f64, f64, vp, vp, vp],
         "lora_rotary_init": [i32, i32, vp, f64, vp],
         "lora_rotary_apply": [vp, i32, vp, i32, vp, i32, i32, vp],
+        "lora_kv_reserve_shared": [vp, i32, i32, i32],
+        "lora_kv_attention_shared": [vp, vp, i64, i32, vp, vp, f32, vp, i64, vp, vp],
         "lora_kv_pages_create": [i32, i32, i32, i32, vp, vp, vp, ctypes.POINTER(vp)],
         "lora_kv_pages_destroy": [vp],
         "lora_kv_pages_update": [vp, vp, vp, vp, vp],
@@ -478,4 +481,4 @@ class LoraPool:
 
 
 from .rotary import Rotary  # noqa: E402,F401
-from .kv import KvBatch, KvCache, KvPages  # noqa: E402,F401
+from .kv import KvBatch, KvCache, KvGroups, KvPages  # noqa: E402,F401

@@ -365,6 +365,60 @@ lora_status ensure_pre_part(lora_kv *p)
     return LORA_OK;
 }
 
+// The attention over shared prefixes keeps between its kernels, one behind the other (16-byte pieces): O and lse
+// of the prefixes, the groups, and where each sequence's own tokens begin.
+struct ShareSizes {
+    size_t O, lse2, groups, total;
+    ShareSizes(const lora_kv *p, int64_t T, int n_heads, int64_t n_seqs)
+    {
+        auto up = [](size_t n) { return (n + 15) / 16 * 16; };
+        O = 0;
+        lse2 = up((size_t)T * n_heads * p->D * sizeof(float));
+        groups = lse2 + up((size_t)T * n_heads * sizeof(float));
+        total = groups + (size_t)n_seqs * (sizeof(int4) + sizeof(int32_t));
+    }
+};
+lora_status ensure_share(lora_kv *p, size_t bytes)
+{
+    if (bytes <= p->share_bytes) return LORA_OK;
+    bytes = std::max(bytes, 2 * p->share_bytes);
+    try {
+        p->share_old.reserve(p->share_old.size() + 1);
+    } catch (...) {
+        return LORA_ERR_OOM;
+    }
+    void *block = nullptr;
+    if (cudaMalloc(&block, bytes) != cudaSuccess) {
+        cudaGetLastError();
+        return LORA_ERR_OOM;
+    }
+    if (p->share) p->share_old.push_back(p->share);
+    p->share = block;
+    p->share_bytes = bytes;
+    return LORA_OK;
+}
+
+KvAttn attention_view(const lora_kv *p, const void *Q, int64_t q_stride, int n_heads, float scale, int window, void *O,
+                      int64_t o_stride, float *lse)
+{
+    KvAttn a;
+    a.Q = static_cast<const uint16_t *>(Q);
+    a.O = static_cast<uint16_t *>(O);
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.o_stride = o_stride;
+    a.Hq = n_heads;
+    a.G = n_heads / p->H;
+    // 2^(s + 1) >= G > 2^s: the multiplier, 2^(32 + s) / G rounded up, times G is off from 2^(32 + s) by less than
+    // G, which shows from x = 2^31 on
+    a.g_shift = 0;
+    while ((2 << a.g_shift) < a.G) ++a.g_shift;
+    a.g_mul = a.G > 1 ? (uint32_t)(((1ull << (32 + a.g_shift)) + a.G - 1) / a.G) : 0;
+    a.window = std::min(window, kMaxTokens);
+    a.scale = scale;
+    return a;
+}
+
 bool capturing(cudaStream_t stream, lora_status *st)
 {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -481,6 +535,8 @@ lora_status lora_kv_destroy(lora_kv_t p)
     if (p->attn_ev) cudaEventDestroy(p->attn_ev);
     if (p->dec_part) cudaFree(p->dec_part);
     if (p->pre_part) cudaFree(p->pre_part);
+    if (p->share) cudaFree(p->share);
+    for (void *block : p->share_old) cudaFree(block);
     if (p->count) cudaFree(p->count);
     if (p->d_err) cudaFree(p->d_err);
     if (p->h_err) cudaFreeHost(p->h_err);
@@ -594,21 +650,7 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
     if ((int64_t)batch->T * n_heads > INT_MAX) return LORA_ERR_ARG;
     const int64_t row = (int64_t)n_heads * p->D;
     if (!tensor_ok(Q, q_stride, row) || !tensor_ok(O, o_stride, row)) return LORA_ERR_ARG;
-    KvAttn a;
-    a.Q = static_cast<const uint16_t *>(Q);
-    a.O = static_cast<uint16_t *>(O);
-    a.lse = lse;
-    a.q_stride = q_stride;
-    a.o_stride = o_stride;
-    a.Hq = n_heads;
-    a.G = n_heads / p->H;
-    // 2^(s + 1) >= G > 2^s: the multiplier, 2^(32 + s) / G rounded up, times G is off from 2^(32 + s) by less than
-    // G, which shows from x = 2^31 on
-    a.g_shift = 0;
-    while ((2 << a.g_shift) < a.G) ++a.g_shift;
-    a.g_mul = a.G > 1 ? (uint32_t)(((1ull << (32 + a.g_shift)) + a.G - 1) / a.G) : 0;
-    a.window = std::min(window, kMaxTokens);
-    a.scale = scale;
+    const KvAttn a = attention_view(p, Q, q_stride, n_heads, scale, window, O, o_stride, lse);
     // Sequences of up to kDecodeRows rows of a kv head go to the short-chunk kernel, others to
     // the tcgen05 kernel; where max_new says that there is only one kind, one launch takes all. (No
     // sequence has more than T rows, so that a loose bound needs no scratch that lora_kv_reserve leaves out.)
@@ -632,6 +674,76 @@ lora_status lora_kv_attention(lora_kv_t p, const void *Q, int64_t q_stride, int 
                               p->count + kv_decode_grid(p->num_sms), p->num_sms, stream);
     // (the first launch may have run when the second failed; the event stands for all calls so far,
     // each having waited for the one before)
+    if (tracked && cudaEventRecord(p->attn_ev, stream) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return LORA_ERR_CUDA;
+    }
+    return LORA_OK;
+}
+
+lora_status lora_kv_reserve_shared(lora_kv_t p, int max_tokens, int n_heads, int max_seqs)
+{
+    if (!p || max_tokens < 0 || max_seqs < 0) return LORA_ERR_ARG;
+    if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
+    if ((int64_t)max_tokens * n_heads > INT_MAX) return LORA_ERR_ARG;
+    const lora_status st = lora_kv_reserve(p, max_tokens, n_heads, max_seqs);
+    return st == LORA_OK ? ensure_share(p, ShareSizes(p, max_tokens, n_heads, max_seqs).total) : st;
+}
+
+lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_stride, int n_heads,
+                                     const lora_kv_batch *batch, const lora_kv_groups *groups, float scale, void *O,
+                                     int64_t o_stride, float *lse, lora_stream_t stream)
+{
+    if (!p) return LORA_ERR_ARG;
+    if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
+    bool empty;
+    lora_status st = check_batch(p, batch, &empty);
+    if (st != LORA_OK) return st;
+    if (groups && (groups->n_groups < 0 || groups->n_groups > batch->n_seqs || groups->max_tokens < 0))
+        return LORA_ERR_ARG;
+    if (groups && groups->n_groups > 0 && (!groups->seq_start || !groups->prefix_len)) return LORA_ERR_ARG;
+    if (empty || !groups || groups->n_groups == 0)
+        return lora_kv_attention(p, Q, q_stride, n_heads, batch, scale, 0, O, o_stride, lse, stream);
+    if ((int64_t)batch->T * n_heads > INT_MAX) return LORA_ERR_ARG;
+    const int64_t row = (int64_t)n_heads * p->D;
+    if (!tensor_ok(Q, q_stride, row) || !tensor_ok(O, o_stride, row)) return LORA_ERR_ARG;
+    const KvAttn a = attention_view(p, Q, q_stride, n_heads, scale, 0, O, o_stride, lse);
+    // the kernels of the sequences' own tokens: as for lora_kv_attention; of the prefixes: the short-chunk one
+    // where no group has more rows than it takes
+    const int max_new = std::min(batch->max_new, batch->T), max_tokens = std::min(groups->max_tokens, batch->T);
+    const bool prefill = (int64_t)max_new * a.G > kDecodeRows;
+    const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
+    const bool wide = (int64_t)max_tokens * a.G > kDecodeRows;
+    const ShareSizes sizes(p, batch->T, n_heads, batch->n_seqs);
+    if ((prefill || wide) && (st = ensure_pre_part(p)) != LORA_OK) return st;
+    if ((st = ensure_share(p, sizes.total)) != LORA_OK) return st;
+    char *const block = static_cast<char *>(p->share);
+    KvShareDev share;
+    share.O = reinterpret_cast<float *>(block + sizes.O);
+    share.lse2 = reinterpret_cast<float *>(block + sizes.lse2);
+    share.groups = reinterpret_cast<int4 *>(block + sizes.groups);
+    share.lo = reinterpret_cast<int32_t *>(share.groups + batch->n_seqs);
+    const bool tracked = !capturing(stream, &st);  // the scratch belongs to one call at a time
+    if (st != LORA_OK) return st;
+    if (tracked) CUDA_TRY(cudaStreamWaitEvent(stream, p->attn_ev, 0));
+    const KvDev kv = kv_view(p);
+    const KvBatchDev bd = batch_view(batch);
+    KvBatchDev bg = bd;
+    bg.n_seqs = groups->n_groups;
+    int *const pre_count = p->count + kv_decode_grid(p->num_sms);
+    cudaError_t e = launch_kv_share_plan(kv, bd, groups->seq_start, groups->prefix_len, groups->n_groups, share, stream);
+    if (e == cudaSuccess)
+        e = wide ? launch_kv_prefill_shared(kPrefix, kv, p->int8, bg, a, share, 0, p->pre_part, pre_count, p->num_sms,
+                                            stream)
+                 : launch_kv_decode_shared(kPrefix, kv, p->int8, bg, a, share, max_tokens, INT_MAX, p->dec_part,
+                                           p->count, p->num_sms, stream);
+    if (decode && e == cudaSuccess)
+        e = launch_kv_decode_shared(kOwn, kv, p->int8, bd, a, share, max_new, prefill ? kDecodeRows : INT_MAX,
+                                    p->dec_part, p->count, p->num_sms, stream);
+    if (prefill && e == cudaSuccess)
+        e = launch_kv_prefill_shared(kOwn, kv, p->int8, bd, a, share, decode ? kDecodeRows + 1 : 0, p->pre_part,
+                                     pre_count, p->num_sms, stream);
     if (tracked && cudaEventRecord(p->attn_ev, stream) != cudaSuccess && e == cudaSuccess) e = cudaErrorUnknown;
     if (e != cudaSuccess) {
         cudaGetLastError();

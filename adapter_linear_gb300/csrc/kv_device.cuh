@@ -15,6 +15,7 @@ __device__ __forceinline__ void kv_flag_range(int *err) { atomicOr(err, kErrRang
 // decrease or a length beyond the table flag the error word and read as an empty sequence.
 struct KvSeq {
     int row0, n, L;
+    int lo = 0;  // the first token of its own (kOwn)
 };
 
 __device__ __forceinline__ KvSeq kv_seq(const KvBatchDev &b, int page_shift, int seq, int *err)
@@ -23,9 +24,9 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatchDev &b, int page_shift, int
     // (compared before they are subtracted: the difference of two bad starts may wrap round)
     if (row0 < 0 || end < row0 || end > b.T || L < 0 || (int64_t)L > ((int64_t)b.table_stride << page_shift)) {
         kv_flag_range(err);
-        return KvSeq{0, 0, 0};
+        return KvSeq{0, 0, 0, 0};
     }
-    return KvSeq{row0, end - row0, L};
+    return KvSeq{row0, end - row0, L, 0};
 }
 
 // The sequence whose rows hold row t (called by a whole warp, the same t in every lane): the
@@ -59,6 +60,13 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
     return (((int64_t)page * kv.H) << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
 }
 
+// The page table of sequence (kPrefix: group) `seq`.
+template <KvMode kMode>
+__device__ __forceinline__ const int32_t *kv_table(const KvBatchDev &b, const KvShareDev &share, int seq)
+{
+    return b.table + (int64_t)(kMode == kPrefix ? share.groups[seq].x : seq) * b.table_stride;
+}
+
 // x / G for 0 <= x < 2^31 (KvAttn::g_mul, g_shift).
 __device__ __forceinline__ int div_g(const KvAttn &a, int x)
 {
@@ -75,11 +83,12 @@ __device__ __forceinline__ int div_g(const KvAttn &a, int x)
 // sequence by sequence, tile by tile, head by head; CTA c of `grid` takes units [c total / grid,
 // (c + 1) total / grid). Every member but next() is called by whole warps, which all
 // compute the same. Sequences with n G outside min_rows..max_rows are left out.
-template <int R, int kUnit, int kHead>
+template <int R, int kUnit, int kHead, KvMode kMode = kPlain>
 struct KvWork {
     const KvDev &kv;
     const KvBatchDev &b;
     const KvAttn &a;
+    const KvShareDev &share;
     const int G, window, min_rows, max_rows, lane;
     int64_t total = 0;           // units of all items
     int64_t grid = 0, u_end = 0;
@@ -88,11 +97,12 @@ struct KvWork {
     int64_t tile0 = 0;           // first unit of the tile's first head
     int seq = -1, tile = 0, tiles = 0, nu = 0, head = 0, lo = 0, hi = 0;
     int j0 = 0, j1 = 0;          // units of tokens: [j0, j1) of the item's nu - kHead
-    KvSeq sh{0, 0, 0};
+    KvSeq sh{0, 0, 0, 0};
 
-    __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, const KvAttn &a_, int min_rows_,
-                                      int max_rows_, int lane_)
-        : kv(kv_), b(b_), a(a_), G(a_.G), window(a_.window), min_rows(min_rows_), max_rows(max_rows_), lane(lane_)
+    __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, const KvAttn &a_, const KvShareDev &share_,
+                                      int min_rows_, int max_rows_, int lane_)
+        : kv(kv_), b(b_), a(a_), share(share_), G(a_.G), window(kMode == kPlain ? a_.window : 0), min_rows(min_rows_),
+          max_rows(max_rows_), lane(lane_)
     {
         for (int s0 = 0; s0 < b.n_seqs; s0 += 32) {
             const int64_t v = units_of_32(s0);
@@ -178,19 +188,36 @@ private:
         return true;
     }
 
+    __device__ __forceinline__ KvSeq seq_at(int i) const
+    {
+        if (kMode == kPrefix) {
+            const int4 g = share.groups[i];
+            return KvSeq{g.z, g.w, g.y, 0};
+        }
+        KvSeq s = kv_seq(b, kv.page_shift, i, kv.err);
+        if (kMode == kOwn) s.lo = share.lo[i];
+        return s;
+    }
     __device__ __forceinline__ int tiles_of(const KvSeq &s) const
     {
         const int64_t rows = (int64_t)s.n * G;
+        if (kMode == kPrefix && s.L == 0) return 0;
         return rows >= min_rows && rows <= max_rows ? (int)((rows + R - 1) / R) : 0;
     }
     __device__ __forceinline__ void range(const KvSeq &s, int t, int *lo_, int *hi_) const
     {
+        if (kMode == kPrefix) {
+            *lo_ = 0;
+            *hi_ = s.L;
+            return;
+        }
         // (n G < 2^31, and the last tile's last row may pass it)
         const int r1 = min(t * R + (R - 1u), s.n * (uint32_t)G - 1u);
         const int i0 = div_g(a, t * R), i1 = div_g(a, r1);
         const int p0 = s.L - s.n + i0, p1 = s.L - s.n + i1;
         *hi_ = max(0, p1 + 1);
         *lo_ = min((window > 0 ? max(0, p0 - window + 1) : 0) & ~15, *hi_);
+        if (kMode == kOwn) *lo_ = min(s.lo, *hi_);
     }
     __device__ __forceinline__ int units(const KvSeq &s, int t) const
     {
@@ -202,15 +229,16 @@ private:
     // of many is counted by all lanes together.
     __device__ __forceinline__ int64_t units_of_32(int s0) const
     {
-        KvSeq s{0, 0, 0};
-        if (s0 + lane < b.n_seqs) s = kv_seq(b, kv.page_shift, s0 + lane, kv.err);
+        KvSeq s{0, 0, 0, 0};
+        if (s0 + lane < b.n_seqs) s = seq_at(s0 + lane);
         const int n = tiles_of(s);
         int64_t v = 0;
         if (n <= 8)
             for (int t = 0; t < n; ++t) v += units(s, t);
         for (uint32_t todo = __ballot_sync(0xffffffffu, n > 8); todo; todo &= todo - 1) {
             const int k = __ffs(todo) - 1;
-            const KvSeq q{0, __shfl_sync(0xffffffffu, s.n, k), __shfl_sync(0xffffffffu, s.L, k)};
+            const KvSeq q{0, __shfl_sync(0xffffffffu, s.n, k), __shfl_sync(0xffffffffu, s.L, k),
+                          kMode == kOwn ? __shfl_sync(0xffffffffu, s.lo, k) : 0};
             const int m = __shfl_sync(0xffffffffu, n, k);
             int64_t part = 0;
             for (int t = lane; t < m; t += 32) part += units(q, t);
@@ -222,7 +250,7 @@ private:
     __device__ __forceinline__ void set_seq(int s)
     {
         seq = s;
-        sh = kv_seq(b, kv.page_shift, s, kv.err);
+        sh = seq_at(s);
         tiles = tiles_of(sh);
     }
     __device__ __forceinline__ void set_tile(int t)

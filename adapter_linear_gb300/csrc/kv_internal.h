@@ -55,6 +55,21 @@ struct KvAttn {
     float scale;
 };
 
+// Attention over a prefix that the sequences of a group share (kv_shared.cu) runs the attention kernels in two
+// more modes.
+//   kPrefix: the "sequences" are groups: all rows of one see all tokens of its prefix, in the pages of its first
+//     sequence with rows. O and lse (in units of log2) go to the arrays below, fp32; the group of an empty
+//     prefix is left out.
+//   kOwn: sequence b starts at token lo[b] (a multiple of the page's tokens); where that is above 0 its rows
+//     are joined with what the first mode left there.
+enum KvMode { kPlain = 0, kPrefix = 1, kOwn = 2 };
+struct KvShareDev {
+    int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
+    int32_t *lo;   // [n_seqs]
+    float *O;      // [T][Hq][D]
+    float *lse2;   // [T][Hq]
+};
+
 // The kernel for short chunks. It takes the sequences of at most max_rows rows (new tokens times
 // G); max_new is the caller's bound on the new tokens of one. part, count: scratch of
 // kv_decode_part_floats floats and kv_decode_grid ints (zero between calls), used by one call at a
@@ -70,5 +85,16 @@ int kv_prefill_grid(int num_sms);
 size_t kv_prefill_part_floats(int D, int num_sms);
 cudaError_t launch_kv_prefill(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int min_rows,
                               float *part, int *count, int num_sms, cudaStream_t stream);
+
+// Both for groups that share prefixes. plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
+// one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).
+cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
+                                 const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream);
+cudaError_t launch_kv_decode_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
+                                    const KvShareDev &share, int max_new, int max_rows, float *part, int *count,
+                                    int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_prefill_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
+                                     const KvShareDev &share, int min_rows, float *part, int *count, int num_sms,
+                                     cudaStream_t stream);
 
 }  // namespace lora

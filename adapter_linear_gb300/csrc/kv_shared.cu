@@ -1,0 +1,74 @@
+// kv_shared.cu -- attention of groups of sequences that share a prefix's pages.
+//
+// The softmax over a row's keys splits into any sets of them: with (O1, lse1) over the prefix and (O2, lse2) over
+// the sequence's own tokens,
+//   O = (w1 O1 + w2 O2) / (w1 + w2),  lse = log(w1 + w2) + max(lse1, lse2),  w = exp(lse - max(lse1, lse2)).
+// So a group's rows attend to its prefix together, as one chunk that sees all of it: the prefix is read once for
+// all of them, and many rows fill the tcgen05 kernel's tiles where each sequence alone would read it again for
+// a handful of rows. Then every sequence attends to its own tokens, and the kernel that does this joins the two
+// where it writes its result. O1 is kept in fp32.
+#include "kv_prefill_kernel.cuh"
+
+namespace lora {
+namespace {
+
+// A group's prefix: what is asked for, but no further than the new tokens of any of its sequences, in
+// whole pages. A group of one sequence, or one with a sequence whose start or length is bad, has none.
+__global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDev b, const int32_t *seq_start,
+                                                             const int32_t *prefix_len, int n_groups, KvShareDev share)
+{
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) share.lo[i] = 0;
+    bool ordered = true;
+    for (int g = threadIdx.x; g < n_groups; g += blockDim.x)
+        ordered = ordered && seq_start[g] >= 0 && seq_start[g] <= seq_start[g + 1] && seq_start[g + 1] <= b.n_seqs;
+    ordered = __syncthreads_and(ordered);
+    if (!ordered && threadIdx.x == 0) kv_flag_range(kv.err);
+    for (int g = threadIdx.x >> 5; g < n_groups; g += blockDim.x >> 5) {
+        const int s0 = ordered ? seq_start[g] : 0, s1 = ordered ? seq_start[g + 1] : 0;
+        int before = INT32_MAX, first = INT32_MAX, rows = 0, with_rows = 0;
+        bool ok = true;
+        for (int i = s0 + lane; i < s1; i += 32) {
+            const KvSeq s = kv_seq(b, kv.page_shift, i, kv.err);
+            ok = ok && s.n == b.start[i + 1] - b.start[i];
+            if (s.n > 0) {
+                before = min(before, s.L - s.n);
+                first = min(first, i);
+                rows += s.n;
+                ++with_rows;
+            }
+        }
+        before = __reduce_min_sync(0xffffffffu, before);
+        first = __reduce_min_sync(0xffffffffu, first);
+        rows = __reduce_add_sync(0xffffffffu, rows);
+        with_rows = __reduce_add_sync(0xffffffffu, with_rows);
+        ok = __all_sync(0xffffffffu, ok) && with_rows > 1;
+        int e = ok ? max(0, min(before, prefix_len[g])) : 0;
+        e = e >> kv.page_shift << kv.page_shift;
+        if (lane == 0) share.groups[g] = e > 0 ? make_int4(first, e, b.start[first], rows) : make_int4(0, 0, 0, 0);
+        if (e > 0)
+            for (int i = s0 + lane; i < s1; i += 32) share.lo[i] = e;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
+                                 const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream)
+{
+    const cudaError_t e = ensure_smem_attr((const void *)kv_share_plan_kernel, 0);
+    if (e != cudaSuccess) return e;
+    kv_share_plan_kernel<<<1, 1024, 0, stream>>>(kv, b, seq_start, prefix_len, n_groups, share);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_prefill_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
+                                     const KvShareDev &share, int min_rows, float *part, int *count, int num_sms,
+                                     cudaStream_t stream)
+{
+    return mode == kPrefix
+               ? launch_kv_prefill_mode<kPrefix>(kv, int8, b, a, share, min_rows, part, count, num_sms, stream)
+               : launch_kv_prefill_mode<kOwn>(kv, int8, b, a, share, min_rows, part, count, num_sms, stream);
+}
+
+}  // namespace lora

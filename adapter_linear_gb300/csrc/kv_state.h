@@ -26,6 +26,11 @@ struct lora_kv {
     // the attention's scratch, used by one call at a time; attn_ev: the attention calls so far
     cudaEvent_t attn_ev = nullptr;
     float *dec_part = nullptr, *pre_part = nullptr;  // pre_part: from the first call or reserve
+    // what the attention over shared prefixes keeps between its kernels: share_bytes of it. Blocks that a larger
+    // one has replaced stay, captured graphs may name them
+    void *share = nullptr;
+    size_t share_bytes = 0;
+    std::vector<void *> share_old;
     int *count = nullptr;                            // the short-chunk kernel's, then the other's
     cudaStream_t ctl_stream = nullptr;         // error-word reads
 };

@@ -22,6 +22,11 @@ class _BatchStruct(ctypes.Structure):
                 ("max_new", ctypes.c_int32)]
 
 
+class _GroupsStruct(ctypes.Structure):
+    _fields_ = [("seq_start", ctypes.c_void_p), ("prefix_len", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
+                ("max_tokens", ctypes.c_int32)]
+
+
 def _clamped(x: int) -> int:
     """x as the library's int takes it: ctypes would drop high bits; above 2^30 nothing differs, and
     any negative number is refused."""
@@ -50,6 +55,28 @@ class KvBatch:
         self.tensors = (page_table, start, kv_len)
         self.struct = _BatchStruct(page_table.data_ptr(), start.data_ptr(), kv_len.data_ptr(),
                                    page_table.shape[1], n, T, _clamped(max_new))
+        self.ref = ctypes.byref(self.struct)
+
+
+class KvGroups:
+    """Groups of a batch's sequences that share a prefix: sequences seq_start[g]..seq_start[g+1] hold the same
+    first prefix_len[g] tokens, in the same pages as far as these are whole.
+
+    seq_start int32 [n_groups + 1] and prefix_len int32 [n_groups] are device tensors (kept alive here, read
+    when the kernels run), max_tokens a bound on the rows of one group."""
+
+    def __init__(self, seq_start, prefix_len, max_tokens: int):
+        for t in (seq_start, prefix_len):
+            if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+                raise LoraError(LORA_ERR_ARG, "KvGroups: seq_start and prefix_len are contiguous int32")
+        n = prefix_len.shape[0]
+        if seq_start.shape[0] != n + 1:
+            raise LoraError(LORA_ERR_SHAPE, "KvGroups: seq_start has n_groups + 1 entries")
+        self.device = seq_start.get_device()
+        if self.device < 0 or prefix_len.get_device() != self.device:
+            raise LoraError(LORA_ERR_ARG, "KvGroups: seq_start and prefix_len are on one GPU")
+        self.tensors = (seq_start, prefix_len)
+        self.struct = _GroupsStruct(seq_start.data_ptr(), prefix_len.data_ptr(), n, _clamped(max_tokens))
         self.ref = ctypes.byref(self.struct)
 
 
@@ -202,27 +229,44 @@ class KvCache:
                   stream=None):
         """Attention of the batch's tokens over the cache, which already holds them.
         Q bf16 [T, n_heads, head_dim]; returns O (as Q) and lse fp32 [T, n_heads]."""
+        Q, qs, O, os_, lse, scale = self._attention_args("lora_kv_attention", Q, batch, scale, O, lse, stream)
+        st = self._stream(stream, batch, Q, O, lse)
+        _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Q.shape[1], batch.ref, scale, _clamped(window),
+                                           O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention")
+        return O, lse
+
+    def reserve_shared(self, max_tokens: int, n_heads: int, max_seqs: int):
+        _check(self._lib.lora_kv_reserve_shared(self.handle, max_tokens, n_heads, max_seqs), "lora_kv_reserve_shared")
+
+    def attention_shared(self, Q, batch: KvBatch, groups: KvGroups, scale: Optional[float] = None, O=None, lse=None,
+                         stream=None):
+        """attention() without a window, for a batch whose groups of sequences share prefixes: each group's
+        prefix is read once."""
+        Q, qs, O, os_, lse, scale = self._attention_args("lora_kv_attention_shared", Q, batch, scale, O, lse, stream)
+        if groups.device != self._device:
+            raise LoraError(LORA_ERR_ARG, "lora_kv_attention_shared: the tensors of a call are on the cache's GPU")
+        st = self._stream(stream, batch, Q, O, lse, *groups.tensors)
+        _check(self._lib.lora_kv_attention_shared(self.handle, Q.data_ptr(), qs, Q.shape[1], batch.ref, groups.ref, scale,
+                                                  O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention_shared")
+        return O, lse
+
+    def _attention_args(self, what, Q, batch, scale, O, lse, stream):
         if Q.dim() != 3:
-            raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention: Q is [T, n_heads, head_dim]")
+            raise LoraError(LORA_ERR_SHAPE, f"{what}: Q is [T, n_heads, head_dim]")
         T, Hq, _ = Q.shape
-        qs = self._rows(Q, Hq, batch, "lora_kv_attention Q")
+        qs = self._rows(Q, Hq, batch, what + " Q")
         if O is None:
             O = self._empty((T, Hq, self.head_dim), torch.bfloat16, stream)
             os_ = Hq * self.head_dim
         else:
-            os_ = self._rows(O, Hq, batch, "lora_kv_attention O")
+            os_ = self._rows(O, Hq, batch, what + " O")
         if lse is None:
             lse = self._empty((T, Hq), torch.float32, stream)
         elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous():
-            raise LoraError(LORA_ERR_SHAPE, "lora_kv_attention lse: contiguous float32 [T, n_heads] expected")
+            raise LoraError(LORA_ERR_SHAPE, f"{what} lse: contiguous float32 [T, n_heads] expected")
         elif lse.get_device() != self._device:
-            raise LoraError(LORA_ERR_ARG, "lora_kv_attention lse: the tensors of a call are on the cache's GPU")
-        if scale is None:
-            scale = 1.0 / math.sqrt(self.head_dim)
-        st = self._stream(stream, batch, Q, O, lse)
-        _check(self._lib.lora_kv_attention(self.handle, Q.data_ptr(), qs, Hq, batch.ref, scale, _clamped(window),
-                                           O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention")
-        return O, lse
+            raise LoraError(LORA_ERR_ARG, f"{what} lse: the tensors of a call are on the cache's GPU")
+        return Q, qs, O, os_, lse, 1.0 / math.sqrt(self.head_dim) if scale is None else scale
 
     def copy(self, pages: "KvPages", stream=None):
         """Make the copies that the last update or compaction of `pages` asks for."""

@@ -217,6 +217,34 @@ lora_status lora_kv_attention(lora_kv_t kv, const void *Q, int64_t q_stride, int
                               const lora_kv_batch *batch, float scale, int window, void *O,
                               int64_t o_stride, float *lse, lora_stream_t stream);
 
+/* The batch's groups of sequences that share a prefix. Sequences seq_start[g] .. seq_start[g+1] - 1 of the batch
+ * (no group: those before the first and behind the last) hold the same first prefix_len[g] tokens, in the same
+ * pages as far as these are whole: lora_kv_pages_update makes such tables. */
+typedef struct lora_kv_groups {
+    const int32_t *seq_start;   /* device [n_groups + 1], not decreasing                */
+    const int32_t *prefix_len;  /* device [n_groups]                                    */
+    int32_t n_groups;           /* at most the batch's n_seqs                           */
+    int32_t max_tokens;         /* a bound on the rows of one group (the sum of its n_b): only chooses
+                                   between kernels                                      */
+} lora_kv_groups;
+
+/* As lora_kv_reserve, for lora_kv_attention_shared: the first call of a size allocates what it needs
+ * (T * n_heads * (D + 1) floats and the above; what a larger call replaces is freed with the handle). */
+lora_status lora_kv_reserve_shared(lora_kv_t kv, int max_tokens, int n_heads, int max_seqs);
+
+/*
+ * lora_kv_attention without a window, for a batch whose sequences share prefixes: every group's prefix is read
+ * once, through the pages of its first sequence with rows. Same O and lse, but for the order of the sums: O of
+ * the two parts is joined in fp32. What is shared is the largest number of whole pages that holds at most
+ * prefix_len[g] tokens and, for each of the group's sequences with rows, none of its new tokens; the rest is
+ * read per sequence. A group of one sequence shares nothing. seq_start out of order or outside 0..n_seqs sets
+ * the error word (LORA_ERR_RANGE), and nothing is shared. groups may be NULL (nothing is shared).
+ * Asynchronous on `stream`. Errors: ARG, SHAPE (n_heads), OOM (scratch), CUDA.
+ */
+lora_status lora_kv_attention_shared(lora_kv_t kv, const void *Q, int64_t q_stride, int n_heads,
+                                     const lora_kv_batch *batch, const lora_kv_groups *groups, float scale, void *O,
+                                     int64_t o_stride, float *lse, lora_stream_t stream);
+
 /* Wait for the calls enqueued on the cache, then read and clear its error word: LORA_OK,
  * LORA_ERR_RANGE or LORA_ERR_TIMEOUT, LORA_ERR_CUDA if the device reported an error. After
  * LORA_ERR_TIMEOUT (a kernel's bounded wait ran out) the outputs of the attention calls since the
