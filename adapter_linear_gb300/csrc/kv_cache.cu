@@ -368,12 +368,15 @@ lora_status ensure_pre_part(lora_kv *p)
 // The attention over shared prefixes keeps between its kernels, one behind the other (16-byte pieces): O and lse
 // of the prefixes, the groups, and where each sequence's own tokens begin.
 struct ShareSizes {
-    size_t O, lse2, groups, total;
+    size_t O, lse2, groups, items, part, total;
     ShareSizes(const lora_kv *p, int64_t T, int n_heads, int64_t n_seqs)
     {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
-        O = 0;
-        lse2 = up((size_t)T * n_heads * p->D * sizeof(float));
+        // what does not depend on the call's size first
+        part = 0;
+        items = up(sizeof(float) * kv_share_part_floats(p->D, p->num_sms));
+        O = items + up(sizeof(KvShareItem) * (size_t)kv_prefill_grid(p->num_sms));
+        lse2 = O + up((size_t)T * n_heads * p->D * sizeof(float));
         groups = lse2 + up((size_t)T * n_heads * sizeof(float));
         total = groups + (size_t)n_seqs * (sizeof(int4) + sizeof(int32_t));
     }
@@ -720,6 +723,8 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     if ((st = ensure_share(p, sizes.total)) != LORA_OK) return st;
     char *const block = static_cast<char *>(p->share);
     KvShareDev share;
+    share.part = reinterpret_cast<float *>(block + sizes.part);
+    share.items = reinterpret_cast<KvShareItem *>(block + sizes.items);
     share.O = reinterpret_cast<float *>(block + sizes.O);
     share.lse2 = reinterpret_cast<float *>(block + sizes.lse2);
     share.groups = reinterpret_cast<int4 *>(block + sizes.groups);
@@ -738,6 +743,7 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
                                             stream)
                  : launch_kv_decode_shared(kPrefix, kv, p->int8, bg, a, share, max_tokens, INT_MAX, p->dec_part,
                                            p->count, p->num_sms, stream);
+    if (wide && e == cudaSuccess) e = launch_kv_share_join(kv, p->int8, a, share, p->num_sms, stream);
     if (decode && e == cudaSuccess)
         e = launch_kv_decode_shared(kOwn, kv, p->int8, bd, a, share, max_new, prefill ? kDecodeRows : INT_MAX,
                                     p->dec_part, p->count, p->num_sms, stream);

@@ -63,7 +63,15 @@ struct KvAttn {
 //   kOwn: sequence b starts at token lo[b] (a multiple of the page's tokens); where that is above 0 its rows
 //     are joined with what the first mode left there.
 enum KvMode { kPlain = 0, kPrefix = 1, kOwn = 2 };
+//     The tcgen05 kernel leaves the pieces of an item that several CTAs share in `part` (row major), and what
+//     they are pieces of in items[first CTA]; a kernel behind it joins them.
+struct KvShareItem {
+    int last, row0, head, rows;  // last CTA with a piece (-1: nothing to join), the first token's row, kv head, rows
+    int first_row, pad[3];       // the first row's number among the group's rows
+};
 struct KvShareDev {
+    float *part;         // [2 grid][256][D], then (m, l) [2 grid][256][2]
+    KvShareItem *items;  // [grid]
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]
     float *O;      // [T][Hq][D]
@@ -85,6 +93,11 @@ int kv_prefill_grid(int num_sms);
 size_t kv_prefill_part_floats(int D, int num_sms);
 cudaError_t launch_kv_prefill(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a, int min_rows,
                               float *part, int *count, int num_sms, cudaStream_t stream);
+
+// The pieces that launch_kv_prefill_shared(kPrefix) left, joined into share.O and share.lse2.
+size_t kv_share_part_floats(int D, int num_sms);
+cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, const KvShareDev &share, int num_sms,
+                                 cudaStream_t stream);
 
 // Both for groups that share prefixes. plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
 // one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).

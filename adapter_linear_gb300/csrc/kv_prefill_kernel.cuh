@@ -695,9 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             segment_done(seg);
             // a warp's rows of a piece: [D / 4][32][4], so that the warp writes 512 bytes at a time
-            float *const part = plan.part + ((int64_t)slot * 8 + warp) * 32 * D + lane * 4;
+            // (kPrefix: row by row, as the kernel behind reads them)
+            constexpr int kPartStep = kMode == kPrefix ? 1 : 32;
+            float *const all_parts = kMode == kPrefix ? share.part : plan.part;
+            float *const part = all_parts + ((int64_t)slot * 8 + warp) * 32 * D + lane * (kMode == kPrefix ? D : 4);
             float2 *const part_ml =
-                reinterpret_cast<float2 *>(plan.part + (int64_t)2 * gridDim.x * kBlockRows * D) + warp * 32 + lane;
+                reinterpret_cast<float2 *>(all_parts + (int64_t)2 * gridDim.x * kBlockRows * D) + warp * 32 + lane;
             uint8_t *const out = smem + C::kOut + warp * 32 * kOutPitch;
             uint16_t *to[4];  // through shared memory (see below): the rows this lane writes a piece of
             bool to_on[4];
@@ -758,13 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (on) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(part + (x + e) * 32) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        *reinterpret_cast<uint4 *>(part + (x + e) * kPartStep) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
                 __syncwarp();  // the next load is the whole warp's
             }
             tc_fence_before_sync();
             if (whole) {
                 if (on) put_lse(m, l);
+            } else if constexpr (kMode == kPrefix) {
+                if (on) part_ml[slot * kBlockRows] = make_float2(m, l);
             } else {
                 if (on) part_ml[slot * kBlockRows] = make_float2(m, l);
                 __threadfence();
@@ -817,15 +822,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 acc[y] *= back;
                             }
                         }
-                        if constexpr (kMode == kPrefix) {
-                            float *const to = share.O + shared_row * D + d;
-                            *reinterpret_cast<float4 *>(to) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                            *reinterpret_cast<float4 *>(to + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-                        } else {
-                            *reinterpret_cast<uint4 *>(dst + d) =
-                                make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                           pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
-                        }
+                        *reinterpret_cast<uint4 *>(dst + d) =
+                            make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                       pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
                     }
                     put_lse(M, sum);
                 }
@@ -1143,6 +1142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------- the share, segment by segment
             KvWork<kBlockRows, kKeys, kHeadUnits, kMode> w(kv, b, a, share, plan.min_rows, INT32_MAX, lane);
             bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
+            KvShareItem begun{-1, 0, 0, 0, 0, {0, 0, 0}};  // kPrefix: the item that begins here and ends elsewhere
             for (int seg = 0;; ++seg) {
                 if (!warp_wait(&bars.seg_empty[seg % kSegments], ((uint32_t)(seg / kSegments) & 1u) ^ 1u, &abort_flag,
                                kv.err))
@@ -1165,6 +1165,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     g.c0 = w.first_cta();
                     g.c1 = w.last_cta();
                     g.first = w.sh.lo;
+                    if (kMode == kPrefix && !g.whole && w.first())
+                        begun = KvShareItem{g.c1, g.row0, g.head, min(kBlockRows, g.n * G - g.tile * kBlockRows),
+                                            g.tile * kBlockRows, {0, 0, 0}};
                 }
                 if (lane == 0) {
                     segs[seg % kSegments] = g;
@@ -1173,6 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (!more) break;
             }
+            if (kMode == kPrefix && lane == 0) share.items[blockIdx.x] = begun;
         }
     }
     tc_fence_before_sync();

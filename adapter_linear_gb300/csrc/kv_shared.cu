@@ -51,7 +51,84 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
     }
 }
 
+// The pieces of the items that several CTAs of the prefix's kernel share: with few groups an item is cut into
+// dozens. A block takes kJoinRows rows of the item that begins in CTA blockIdx.x.
+constexpr int kJoinRows = 8, kJoinThreads = 256, kMaxPieces = 256;
+
+template <int D, bool kInt8>
+__global__ void __launch_bounds__(kJoinThreads) kv_share_join_kernel(KvAttn a, KvShareDev share, int grid)
+{
+    __shared__ float weight[kJoinRows][kMaxPieces];
+    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+    const KvShareItem item = share.items[c0];
+    const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, item.rows - r0);
+    if (item.last < 0 || rows <= 0) return;
+    const int n = item.last - c0 + 1;
+    auto slot = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
+    auto out_row = [&](int r) {
+        const int row = item.first_row + r0 + r;
+        return (int64_t)(item.row0 + row / a.G) * a.Hq + item.head * a.G + row % a.G;
+    };
+    const float2 *const ml = reinterpret_cast<const float2 *>(share.part + (int64_t)2 * grid * kBlockRows * D);
+    // a row's maximum, sum and weights by one warp
+    for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
+        float M = -INFINITY, sum = 0.0f;
+        for (int x = lane; x < n; x += 32) {
+            const float m = ml[slot(x) * kBlockRows + r0 + r].x;
+            weight[r][x] = m;
+            M = fmaxf(M, m);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        const float ref = M == -INFINITY ? 0.0f : M;
+        for (int x = lane; x < n; x += 32) {
+            const float w = fast_exp2(weight[r][x] - ref);
+            sum += w * ml[slot(x) * kBlockRows + r0 + r].y;
+            weight[r][x] = w;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int x = lane; x < n; x += 32) weight[r][x] *= inv;
+        if (lane == 0) share.lse2[out_row(r)] = sum == 0.0f ? -INFINITY : M + log2f(sum);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        const float *const src = share.part + (int64_t)(r0 + r) * D + d;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int x = 0; x < n; ++x) {
+            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)slot(x) * kBlockRows * D);
+            const float w = weight[r][x];
+            acc.x = add_piece<kInt8>(w, v.x, acc.x);
+            acc.y = add_piece<kInt8>(w, v.y, acc.y);
+            acc.z = add_piece<kInt8>(w, v.z, acc.z);
+            acc.w = add_piece<kInt8>(w, v.w, acc.w);
+        }
+        *reinterpret_cast<float4 *>(share.O + out_row(r) * D + d) = acc;
+    }
+}
+
 }  // namespace
+
+size_t kv_share_part_floats(int D, int num_sms)
+{
+    return (size_t)2 * kv_prefill_grid(num_sms) * kBlockRows * (D + 2);
+}
+
+cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, const KvShareDev &share, int num_sms,
+                                 cudaStream_t stream)
+{
+    auto fn = kv.D == 128 ? (int8 ? kv_share_join_kernel<128, true> : kv_share_join_kernel<128, false>)
+                          : (int8 ? kv_share_join_kernel<64, true> : kv_share_join_kernel<64, false>);
+    const int grid = kv_prefill_grid(num_sms);
+    if (grid > kMaxPieces) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
+    if (e != cudaSuccess) return e;
+    fn<<<dim3(grid, kBlockRows / kJoinRows), kJoinThreads, 0, stream>>>(a, share, grid);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
                                  const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream)
