@@ -15,20 +15,23 @@ using namespace lora;
 namespace {
 
 // The tables are some hundred kilobytes, in L2, and the work on them a handful of steps that each need all of
-// the one before (who names a page, which pages are free, who gets them), so latency bounds it: one cluster
-// of kCtas CTAs does all steps, a cluster barrier between them.
+// the one before (who names a page, which pages are free, who gets them), so the latency of L2 (0.3 us) and of
+// the steps' ends bounds it: one cluster of kCtas CTAs does all steps, a cluster barrier between them, and what all
+// of them need of the slots is in every CTA's shared memory.
 constexpr int kCtas = 8, kThreads = 1024;
-constexpr int kUnit = 128;  // table entries a warp takes at a time, four a lane
+constexpr int kUnit = 128;       // table entries a warp takes at a time, four a lane
+constexpr int kTile = 4 * kThreads;  // pages a CTA scans at a time, four a thread
+constexpr int kSlotsHere = 2048; // slots that fit the shared memory; of more the numbers lie in scratch
 
 struct PagesDev {
     int32_t *table, *kv_len, *refs;
     int P, S, W, shift;        // pages, slots, entries a slot, log2 of a page's tokens
-    int32_t *old_table;        // [S][W] the table before the call, where it is used
-    int32_t *kept, *src;       // [S] tokens kept, and of which slot (-1: none)
+    int4 *slots;               // [S], where they do not fit the shared memory
+    int32_t *stash;            // [S][W] entries that slots take over from others
+    int32_t *last;             // [S] the page that a slot's kept tokens end inside
     int32_t *base;             // [S] the first new page of a slot among all, 2 x + (keeps the page it ends in)
-    int32_t *held;             // [S] entries used before
     int32_t *count, *claim;    // [P] slots that have all of a page; the first that ends inside (kNone: none)
-    int32_t *fresh;            // [P] new pages, in order
+    int32_t *list;             // [P] free pages, in order, of each CTA's part of the pages
     int32_t *moves;            // [3][cap]: page, page, rows
     int32_t *moves_n;          // [1]
     int cap;
@@ -37,34 +40,30 @@ struct PagesDev {
 
 constexpr int kNone = INT_MAX;
 
-// What the CTAs of the cluster tell each other, in the first one's shared memory.
-struct Common {
-    int bad[2];            // error bits of the first two steps, each looked at behind its step's barrier
-    int found[kCtas];      // free (update) or used (compaction) pages of each CTA's part
-    int need, copies;      // new pages and copies in all
-    int below;             // compaction: used pages below n
+// A slot: tokens kept, of which slot (-1: none), tokens afterwards, entries used before.
+__device__ __forceinline__ int kept_of(const int4 &s) { return s.x; }
+__device__ __forceinline__ int from_of(const int4 &s) { return s.y; }
+__device__ __forceinline__ int total_of(const int4 &s) { return s.z; }
+__device__ __forceinline__ int held_of(const int4 &s) { return s.w; }
+
+// What a CTA tells the others: they read it behind a cluster barrier.
+struct Told {
+    int bad[2];        // error bits of the first two steps
+    int found;         // pages it found
+    int need, copies;  // the first CTA: new pages and copies in all
 };
 
 __device__ __forceinline__ int entries(int tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
 
 // Sum over a block of v, in every thread. sm: 33 values.
-template <class T>
-__device__ __forceinline__ T block_sum(T v, T *sm)
+__device__ __forceinline__ int block_sum(int v, int *sm)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    v = __reduce_add_sync(0xffffffffu, v);
     __syncthreads();
     if (lane == 0) sm[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        T s = sm[lane];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (lane == 0) sm[32] = s;
-    }
-    __syncthreads();
-    return sm[32];
+    return __reduce_add_sync(0xffffffffu, sm[lane]);
 }
 
 // Exclusive prefix of v over a block; *all: the sum.
@@ -81,119 +80,169 @@ __device__ __forceinline__ T block_scan(T v, T *sm, T *all)
     __syncthreads();
     if (lane == 31) sm[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        T x = sm[lane], y = x;
+    T x = sm[lane], y = x;  // every warp: the warps' sums
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const T o = __shfl_up_sync(0xffffffffu, y, d);
-            if (lane >= d) y += o;
-        }
-        sm[lane] = y - x;
-        if (lane == 31) sm[32] = y;
+    for (int d = 1; d < 32; d <<= 1) {
+        const T o = __shfl_up_sync(0xffffffffu, y, d);
+        if (lane >= d) y += o;
     }
-    __syncthreads();
-    *all = sm[32];
-    return sm[warp] + s - v;
+    *all = __shfl_sync(0xffffffffu, y, 31);
+    return __shfl_sync(0xffffffffu, y - x, warp) + s - v;
 }
 
-// Calls fn(slot, entry) for the entries below used(slot) of all slots, spread over the cluster's warps.
-template <class Used, class Fn>
-__device__ __forceinline__ void each_entry(const PagesDev &p, int cta, Used used, Fn fn)
+// Calls fn(slot, entry) for the entries begin(slot) .. end(slot) - 1 of all slots, spread over the cluster's warps.
+template <class Begin, class End, class Fn>
+__device__ __forceinline__ void each_entry(const PagesDev &p, int cta, Begin begin, End end, Fn fn)
 {
     const int lane = threadIdx.x & 31;
-    const int per = (p.W + kUnit - 1) / kUnit;
-    for (int64_t u = cta * (kThreads / 32) + (threadIdx.x >> 5); u < (int64_t)p.S * per; u += kCtas * (kThreads / 32)) {
-        const int s = (int)(u / per), j0 = (int)(u % per) * kUnit;
-        const int n = used(s);
+    const int per = (p.W + kUnit - 1) / kUnit;  // S W is below 2^31
+    for (uint32_t u = cta * (kThreads / 32) + (threadIdx.x >> 5); u < (uint32_t)p.S * per; u += kCtas * (kThreads / 32)) {
+        const int s = u / per, j0 = u % per * kUnit;
+        const int n = end(s);
+        if (j0 >= n || j0 + kUnit <= begin(s)) continue;
 #pragma unroll
-        for (int k = 0; k < kUnit / 32; ++k)
-            if (j0 + k * 32 + lane < n) fn(s, j0 + k * 32 + lane);
+        for (int k = 0; k < kUnit / 32; ++k) {
+            const int j = j0 + k * 32 + lane;
+            if (j < n && j >= begin(s)) fn(s, j);
+        }
     }
+}
+
+// value(told) of every CTA of the cluster into out[kCtas]; behind a cluster barrier, called by all threads.
+template <class Value>
+__device__ __forceinline__ void gather(cg::cluster_group &cluster, Told *mine, int *out, Value value)
+{
+    __syncthreads();
+    if (threadIdx.x < kCtas) out[threadIdx.x] = value(*cluster.map_shared_rank(mine, threadIdx.x));
+    __syncthreads();
 }
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     kv_pages_update_kernel(PagesDev p, const int32_t *parent, const int32_t *keep, const int32_t *room)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ Common mine;
+    __shared__ Told mine;
+    __shared__ int4 slots_here[kSlotsHere];
     __shared__ int64_t sm[33];
+    __shared__ int others[kCtas];
     int *const sm32 = reinterpret_cast<int *>(sm);
     const int cta = blockIdx.x, tid = cta * kThreads + threadIdx.x;
-    Common *const all = cluster.map_shared_rank(&mine, 0);
+    const bool here = p.S <= kSlotsHere;
+    int4 *const slots = here ? slots_here : p.slots;
+    const bool counted = !parent && !keep;  // every slot keeps what it has: refs are the counts
     if (threadIdx.x < 2) mine.bad[threadIdx.x] = 0;
-    cluster.sync();
+    __syncthreads();
 
-    // ---- 1: what is asked for; the counts start from zero; the table as it is
+    // ---- 1: what is asked for (all slots in every CTA where they fit); the counts start from zero
     const int capacity = (int)min((int64_t)p.W << p.shift, (int64_t)INT_MAX);
-    for (int i = tid; i < p.S; i += kCtas * kThreads) {
-        const int from = parent ? parent[i] : i, here = p.kv_len[i];
-        const int extra = room ? room[i] : 0;
-        bool wrong = from < -1 || from >= p.S || extra < 0 || here < 0 || here > capacity;
+    for (int i = here ? threadIdx.x : tid; i < p.S; i += here ? kThreads : kCtas * kThreads) {
+        const int from = parent ? parent[i] : i, now = p.kv_len[i];
+        const int extra = room ? room[i] : 0, most = keep ? max(0, keep[i]) : INT_MAX;
+        bool wrong = from < -1 || from >= p.S || extra < 0 || now < 0 || now > capacity;
         int n = 0;
         if (!wrong && from >= 0) {
-            n = p.kv_len[from];
+            n = from == i ? now : p.kv_len[from];
             wrong = n < 0 || n > capacity;
-            if (keep) n = min(n, max(0, keep[i]));
+            n = min(n, most);
         }
         wrong = wrong || (int64_t)n + extra > capacity;
-        if (wrong) atomicOr(&all->bad[0], kErrRangeBit);
-        p.kept[i] = wrong ? 0 : n;
-        p.src[i] = wrong ? -1 : from;
-        p.held[i] = wrong ? 0 : entries(here, p.shift);
+        if (wrong) mine.bad[0] = kErrRangeBit;
+        slots[i] = wrong ? make_int4(0, -1, 0, 0) : make_int4(n, from, n + extra, entries(now, p.shift));
     }
-    for (int x = tid; x < p.P; x += kCtas * kThreads) {
-        p.count[x] = 0;
-        p.claim[x] = kNone;
-    }
-    each_entry(p, cta, [&](int s) { return min(p.W, max(0, entries(min(p.kv_len[s], capacity), p.shift))); },
-               [&](int s, int j) { p.old_table[(int64_t)s * p.W + j] = p.table[(int64_t)s * p.W + j]; });
+    if (!counted)
+        for (int x = tid; x < p.P; x += kCtas * kThreads) {
+            p.count[x] = 0;
+            p.claim[x] = kNone;
+        }
     cluster.sync();
-    int bad = all->bad[0];
+    int bad = 0;
+    gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
+    for (int c = 0; c < kCtas; ++c) bad |= others[c];
     if (bad) goto refuse;
 
     // ---- 2: who has a page, who ends inside one
-    each_entry(p, cta, [&](int s) { return entries(__ldcg(p.kept + s), p.shift); },
-               [&](int s, int j) {
-                   const int x = __ldcg(p.old_table + (int64_t)__ldcg(p.src + s) * p.W + j);
-                   if (x < 0 || x >= p.P) {
-                       atomicOr(&all->bad[1], kErrRangeBit);
-                   } else if (j < __ldcg(p.kept + s) >> p.shift) {
-                       atomicAdd(p.count + x, 1);
-                   } else {
-                       atomicMin(p.claim + x, s + (__ldcg(p.src + s) == s ? 0 : p.S));
-                   }
-               });
-    cluster.sync();
-    bad = all->bad[1];
-    if (bad) goto refuse;
+    if (counted) {  // known: the entries are only looked at (the result is asked for behind the next barrier)
+        each_entry(p, cta, [&](int) { return 0; }, [&](int s) { return held_of(slots[s]); },
+                   [&](int s, int j) {
+                       const int x = p.table[(int64_t)s * p.W + j];
+                       if (x < 0 || x >= p.P) mine.bad[1] = kErrRangeBit;
+                   });
+    } else {
+        each_entry(p, cta, [&](int) { return 0; }, [&](int s) { return entries(kept_of(slots[s]), p.shift); },
+                   [&](int s, int j) {
+                       const int from = from_of(slots[s]), x = p.table[(int64_t)from * p.W + j];
+                       if (x < 0 || x >= p.P) {
+                           mine.bad[1] = kErrRangeBit;
+                           return;
+                       }
+                       if (from != s) p.stash[(int64_t)s * p.W + j] = x;
+                       if (j < kept_of(slots[s]) >> p.shift) {
+                           atomicAdd(p.count + x, 1);
+                       } else {
+                           atomicMin(p.claim + x, s + (from == s ? 0 : p.S));
+                           p.last[s] = x;
+                       }
+                   });
+        cluster.sync();
+        gather(cluster, &mine, others, [](const Told &t) { return t.bad[1]; });
+        for (int c = 0; c < kCtas; ++c) bad |= others[c];
+        if (bad) goto refuse;
+    }
 
     {
-        // ---- 3: free pages of this CTA's part (a page that someone ends inside and nobody has stays with the
-        // first who asked); the first CTA: the new pages and copies of every slot
-        const int part = (p.P + kCtas - 1) / kCtas, x0 = min(p.P, cta * part), x1 = min(p.P, x0 + part);
-        int free = 0;
-        for (int x = x0 + threadIdx.x; x < x1; x += kThreads)
-            free += __ldcg(p.count + x) == 0 && __ldcg(p.claim + x) == kNone;
-        free = block_sum(free, sm32);
-        if (threadIdx.x == 0) all->found[cta] = free;
-        if (cta == 0) {
+        // ---- 3: the free pages of this CTA's part (a page that someone ends inside and nobody has stays with the
+        // first who asked), in order; the last CTA, which has no part: the new pages and copies of every slot
+        const int part = ((p.P + kCtas - 2) / (kCtas - 1) + 3) & ~3;
+        const int x0 = min(p.P, cta * part), x1 = cta == kCtas - 1 ? x0 : min(p.P, x0 + part);
+        auto pages4 = [&](int x, int (&c)[4], int (&cl)[4]) {  // counts and claims of pages x .. x + 3 below x1
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                c[e] = 1;
+                cl[e] = kNone;
+                if (x + e < x1) {
+                    c[e] = counted ? p.refs[x + e] : __ldcg(p.count + x + e);
+                    if (!counted) cl[e] = __ldcg(p.claim + x + e);
+                }
+            }
+        };
+        int found = 0;
+        for (int y0 = x0; y0 < x1; y0 += kTile) {
+            const int x = y0 + 4 * threadIdx.x;
+            int c[4], cl[4], v = 0, sum;
+            pages4(x, c, cl);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v += c[e] == 0 && cl[e] == kNone;
+            int at = found + block_scan(v, sm32, &sum);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c[e] == 0 && cl[e] == kNone) {
+                    p.list[x0 + at] = x + e;
+                    if (!counted) p.count[x + e] = -1 - at;  // free: its place in the list
+                    ++at;
+                }
+            found += sum;
+        }
+        if (threadIdx.x == 0) mine.found = found;
+        if (cta == kCtas - 1) {
             int64_t before = 0;  // new pages, and in the upper half copies
             for (int s0 = 0; s0 < p.S; s0 += kThreads) {
                 const int s = s0 + threadIdx.x;
-                int64_t v = 0;
-                int stays = 0, n = 0, old = -1, to = -1;
+                int64_t v = 0, sum;
+                int stays = 0, n = 0, old = -1;
                 if (s < p.S) {
-                    n = __ldcg(p.kept + s);
-                    const int total = n + (room ? room[s] : 0), full = n >> p.shift;
+                    n = kept_of(slots[s]);
                     if (n & ((1 << p.shift) - 1)) {
-                        to = __ldcg(p.src + s);
-                        old = __ldcg(p.old_table + (int64_t)to * p.W + full);
-                        stays = __ldcg(p.claim + old) == s + (to == s ? 0 : p.S) && __ldcg(p.count + old) == 0;
+                        if (counted) {
+                            stays = 1;
+                        } else {
+                            old = __ldcg(p.last + s);
+                            const int count = __ldcg(p.count + old);  // (a page that someone asked for is not in a list)
+                            stays = __ldcg(p.claim + old) == s + (from_of(slots[s]) == s ? 0 : p.S) && count == 0;
+                        }
                         if (!stays) v = 1ll << 32;
                     }
-                    v += entries(total, p.shift) - full - stays;
+                    v += entries(total_of(slots[s]), p.shift) - (n >> p.shift) - stays;
                 }
-                int64_t sum;
                 const int64_t at = before + block_scan(v, sm, &sum);
                 if (s < p.S) {
                     p.base[s] = 2 * (int)(uint32_t)at + stays;
@@ -207,61 +256,67 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                 before += sum;
             }
             if (threadIdx.x == 0) {
-                mine.need = (int)(uint32_t)before;
+                mine.need = (int)min((int64_t)(uint32_t)before, (int64_t)INT_MAX);
                 mine.copies = (int)(before >> 32);
             }
         }
         cluster.sync();
 
-        // ---- 4: the lowest free pages, as many as are needed
-        const int need = all->need;
-        int before = 0, there = 0;
+        // ---- 4: the new state
+        if (counted) {
+            gather(cluster, &mine, others, [](const Told &t) { return t.bad[1]; });
+            for (int c = 0; c < kCtas; ++c) bad |= others[c];
+            if (bad) goto refuse;
+        }
+        gather(cluster, &mine, others, [](const Told &t) { return t.found; });
+        const Told *const last_told = cluster.map_shared_rank(&mine, kCtas - 1);
+        const int need = last_told->need, copies = last_told->copies;
+        int there = 0, before = 0;
         for (int c = 0; c < kCtas; ++c) {
-            if (c < cta) before += all->found[c];
-            there += all->found[c];
+            if (c < cta) before += others[c];
+            there += others[c];
         }
         if (need > there) {
             bad = kErrPagesBit;
             goto refuse;
         }
-        for (int y0 = x0; y0 < x1 && before < need; y0 += kThreads) {
-            const int x = y0 + threadIdx.x;
-            const int v = x < x1 && __ldcg(p.count + x) == 0 && __ldcg(p.claim + x) == kNone;
-            int sum;
-            const int at = before + block_scan(v, sm32, &sum);
-            if (v && at < need) {
-                p.fresh[at] = x;
-                p.count[x] = 1;
+        auto new_page = [&](int i) {  // the i-th of all free pages
+            int c = 0;
+            for (; c < kCtas - 2 && i >= others[c]; ++c) i -= others[c];
+            return __ldcg(p.list + c * part + i);
+        };
+        if (!counted)
+            for (int y0 = x0; y0 < x1; y0 += kTile) {
+                const int x = y0 + 4 * threadIdx.x;
+                int c[4], cl[4];
+                pages4(x, c, cl);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (x + e < x1)
+                        p.refs[x + e] = c[e] < 0 ? before - 1 - c[e] < need : c[e] == 0 && cl[e] != kNone ? 1 : c[e];
             }
-            before += sum;
-        }
-        cluster.sync();
-
-        // ---- 5: the new state
-        for (int x = tid; x < p.P; x += kCtas * kThreads) {
-            const int c = __ldcg(p.count + x);
-            p.refs[x] = c == 0 && __ldcg(p.claim + x) != kNone ? 1 : c;
-        }
         each_entry(p, cta,
-                   [&](int s) {
-                       return max(__ldcg(p.held + s), entries(__ldcg(p.kept + s) + (room ? room[s] : 0), p.shift));
-                   },
+                   [&](int s) { return from_of(slots[s]) == s ? kept_of(slots[s]) >> p.shift : 0; },
+                   [&](int s) { return max(held_of(slots[s]), entries(total_of(slots[s]), p.shift)); },
                    [&](int s, int j) {
-                       const int n = __ldcg(p.kept + s), b = __ldcg(p.base + s);
-                       const int old = (n >> p.shift) + (b & 1);  // entries that stay
-                       int x = -1;
-                       if (j < old)
-                           x = __ldcg(p.old_table + (int64_t)__ldcg(p.src + s) * p.W + j);
-                       else if (j < entries(n + (room ? room[s] : 0), p.shift))
-                           x = __ldcg(p.fresh + (b >> 1) + j - old);
-                       p.table[(int64_t)s * p.W + j] = x;
+                       const int4 me = slots[s];
+                       const int b = __ldcg(p.base + s);
+                       const int old = (kept_of(me) >> p.shift) + (b & 1);  // entries that stay
+                       int32_t *const to = p.table + (int64_t)s * p.W + j;
+                       if (j < old) {
+                           if (from_of(me) != s) *to = __ldcg(p.stash + (int64_t)s * p.W + j);
+                       } else if (j < entries(total_of(me), p.shift)) {
+                           const int x = new_page((b >> 1) + j - old);
+                           *to = x;
+                           if (counted) p.refs[x] = 1;
+                       } else {
+                           *to = -1;
+                       }
                    });
-        for (int s = tid; s < p.S; s += kCtas * kThreads) p.kv_len[s] = __ldcg(p.kept + s) + (room ? room[s] : 0);
-        const int copies = all->copies;
-        for (int k = tid; k < copies; k += kCtas * kThreads)
-            p.moves[p.cap + k] = __ldcg(p.fresh + __ldcg(p.moves + p.cap + k));
+        for (int s = tid; s < p.S; s += kCtas * kThreads) p.kv_len[s] = total_of(slots[s]);
+        for (int k = tid; k < copies; k += kCtas * kThreads) p.moves[p.cap + k] = new_page(__ldcg(p.moves + p.cap + k));
         if (tid == 0) *p.moves_n = copies;
-        cluster.sync();  // the first CTA's shared memory is still read
+        cluster.sync();  // the CTAs' shared memory is still read
         return;
     }
 
@@ -273,86 +328,107 @@ refuse:
     cluster.sync();
 }
 
+// n pages are used. The used page x >= n with d used pages above it moves to the (moved - 1 - d)-th free page below n.
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     kv_pages_compact_kernel(PagesDev p, int32_t *table_out, int32_t *refs_out)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ Common mine;
-    __shared__ int sm[33];
+    __shared__ Told mine;
+    __shared__ int sm[33], others[kCtas];
     const int cta = blockIdx.x, tid = cta * kThreads + threadIdx.x;
-    Common *const all = cluster.map_shared_rank(&mine, 0);
-    const int part = (p.P + kCtas - 1) / kCtas, x0 = min(p.P, cta * part), x1 = min(p.P, x0 + part);
-    cluster.sync();  // all have started
+    const int part = ((p.P + kCtas - 1) / kCtas + 3) & ~3;
+    const int x0 = min(p.P, cta * part), x1 = min(p.P, x0 + part);
+    auto refs4 = [&](int x, int (&r)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = x + e < x1 ? p.refs[x + e] : 0;
+    };
 
     int used = 0;
-    for (int x = x0 + threadIdx.x; x < x1; x += kThreads) used += p.refs[x] > 0;
+    for (int y0 = x0; y0 < x1; y0 += kTile) {
+        int r[4];
+        refs4(y0 + 4 * threadIdx.x, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) used += r[e] > 0;
+    }
     used = block_sum(used, sm);
-    if (threadIdx.x == 0) all->found[cta] = used;
+    if (threadIdx.x == 0) mine.found = used;
     cluster.sync();
+    gather(cluster, &mine, others, [](const Told &t) { return t.found; });
     int n = 0, before = 0;
     for (int c = 0; c < kCtas; ++c) {
-        if (c < cta) before += all->found[c];
-        n += all->found[c];
+        if (c < cta) before += others[c];
+        n += others[c];
     }
-    // used pages below n: counted by the CTA whose part n is in
-    if (n >= x0 && (n < x1 || (x1 == p.P && n == p.P && x0 < x1))) {
-        int v = 0;
-        for (int x = x0 + threadIdx.x; x < min(n, x1); x += kThreads) v += p.refs[x] > 0;
-        v = block_sum(v, sm);
-        if (threadIdx.x == 0) all->below = before + v;
-    }
-    cluster.sync();
-    const int below = all->below, moved = n - below;
-    // the k-th used page from n on, the k-th free one below n
-    for (int y0 = x0; y0 < x1; y0 += kThreads) {
-        const int x = y0 + threadIdx.x;
-        const int r = x < x1 ? p.refs[x] : 0;
-        int sum;
-        const int at = before + block_scan((int)(r > 0), sm, &sum);
-        if (x < x1 && x >= n && r > 0) {
-            p.moves[at - below] = x;
-            p.moves[2 * p.cap + at - below] = 1 << p.shift;
-            p.count[x] = at - below;  // its move
-            p.claim[at - below] = r;
+    // the used pages from n on, from the last; the free ones below n, from the first
+    int holes = 0;
+    for (int y0 = x0; y0 < x1; y0 += kTile) {
+        const int x = y0 + 4 * threadIdx.x;
+        int r[4], v = 0, sum;
+        refs4(x, r);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v += r[e] > 0;
+        int at = before + block_scan(v, sm, &sum);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int y = x + e;
+            if (y < x1 && r[e] > 0) {
+                if (y >= n) {
+                    const int d = n - 1 - at;
+                    p.list[d] = y;
+                    p.count[y] = d;
+                    p.claim[d] = r[e];
+                }
+                ++at;
+            } else if (y < x1 && y < n) {
+                p.moves[p.cap + y - at] = y;
+                ++holes;
+            }
         }
-        if (x < x1 && x < n && r == 0) p.moves[p.cap + x - at] = x;
         before += sum;
     }
+    holes = block_sum(holes, sm);
+    if (threadIdx.x == 0) mine.need = holes;
     cluster.sync();
+    gather(cluster, &mine, others, [](const Told &t) { return t.need; });
+    int moved = 0;
+    for (int c = 0; c < kCtas; ++c) moved += others[c];
 
+    for (int k = tid; k < moved; k += kCtas * kThreads) {
+        const int d = moved - 1 - k;
+        p.moves[k] = __ldcg(p.list + d);
+        p.moves[2 * p.cap + k] = 1 << p.shift;
+        refs_out[__ldcg(p.moves + p.cap + k)] = __ldcg(p.claim + d);
+    }
     for (int x = tid; x < p.P; x += kCtas * kThreads) {
-        const int r = p.refs[x];
         if (x >= n)
             refs_out[x] = 0;
-        else if (r > 0 && refs_out != p.refs)
-            refs_out[x] = r;
+        else if (refs_out != p.refs) {
+            const int r = p.refs[x];
+            if (r > 0) refs_out[x] = r;
+        }
     }
-    for (int k = tid; k < moved; k += kCtas * kThreads) refs_out[__ldcg(p.moves + p.cap + k)] = __ldcg(p.claim + k);
     const int capacity = (int)min((int64_t)p.W << p.shift, (int64_t)INT_MAX);
-    each_entry(p, cta,
-               [&](int s) {
-                   if (table_out != p.table) return p.W;
-                   return max(0, entries(min(p.kv_len[s], capacity), p.shift));
-               },
+    const bool copy = table_out != p.table;
+    each_entry(p, cta, [&](int) { return 0; },
+               [&](int s) { return copy ? p.W : max(0, entries(min(p.kv_len[s], capacity), p.shift)); },
                [&](int s, int j) {
                    const int64_t e = (int64_t)s * p.W + j;
                    const int x = p.table[e];
-                   const bool inside = j < entries(max(0, min(p.kv_len[s], capacity)), p.shift);
-                   const bool bad = inside && (x < 0 || x >= p.P);
-                   if (bad) atomicOr(p.err, kErrRangeBit);
-                   // (a page that refs does not count has no move)
+                   const bool inside = !copy || j < entries(max(0, min(p.kv_len[s], capacity)), p.shift);
                    int to = x;
-                   if (inside && !bad && x >= n && x < p.P) {
-                       const int k = __ldcg(p.count + x);
-                       if (k >= 0 && k < moved && __ldcg(p.moves + k) == x)
-                           to = __ldcg(p.moves + p.cap + k);
-                       else
+                   if (inside && (x < 0 || x >= p.P)) {
+                       atomicOr(p.err, kErrRangeBit);
+                   } else if (inside && x >= n) {
+                       const int d = __ldcg(p.count + x);
+                       if (d >= 0 && d < moved && __ldcg(p.list + d) == x)
+                           to = __ldcg(p.moves + p.cap + moved - 1 - d);
+                       else  // a page that refs does not count has no move
                            atomicOr(p.err, kErrRangeBit);
                    }
-                   if (to != x || table_out != p.table) table_out[e] = to;
+                   if (to != x || copy) table_out[e] = to;
                });
     if (tid == 0) *p.moves_n = moved;
-    cluster.sync();  // the first CTA's shared memory is still read
+    cluster.sync();  // the CTAs' shared memory is still read
 }
 
 __global__ void __launch_bounds__(kThreads) kv_pages_used_kernel(const int32_t *refs, int P, int *out)
@@ -461,14 +537,13 @@ PagesDev pages_view(const lora_kv_pages *p)
         at += n;
         return x;
     };
-    v.old_table = take(S * (size_t)p->stride);
-    v.kept = take(S);
-    v.src = take(S);
+    v.slots = reinterpret_cast<int4 *>(take(4 * S));  // (cudaMalloc's alignment)
+    v.stash = take(S * (size_t)p->stride);
+    v.last = take(S);
     v.base = take(S);
-    v.held = take(S);
     v.count = take(P);
     v.claim = take(P);
-    v.fresh = take(P);
+    v.list = take(P + 4 * kCtas);
     v.cap = p->cap();
     v.moves = take(3 * (size_t)p->cap());
     v.moves_n = take(1);
@@ -541,8 +616,8 @@ lora_status lora_kv_pages_create(int num_pages, int page_tokens, int max_seqs, i
     p->table = page_table;
     p->kv_len = kv_len;
     p->refs = refs;
-    const size_t ints = (size_t)max_seqs * table_stride + 4 * (size_t)max_seqs + 3 * (size_t)num_pages +
-                        3 * (size_t)p->cap() + 1;
+    const size_t ints = (size_t)max_seqs * table_stride + 6 * (size_t)max_seqs + 3 * (size_t)num_pages +
+                        4 * kCtas + 3 * (size_t)p->cap() + 1;
     if (cudaMalloc((void **)&p->d_err, 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc((void **)&p->scratch, sizeof(int32_t) * ints) != cudaSuccess ||
         cudaHostAlloc((void **)&p->h_err, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
