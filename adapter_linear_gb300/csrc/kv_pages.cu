@@ -16,12 +16,12 @@ namespace {
 
 // The tables are some hundred kilobytes, in L2, and the work on them a handful of steps that each need all of
 // the one before (who names a page, which pages are free, who gets them), so the latency of L2 (0.3 us) and of
-// the steps' ends bounds it: one cluster of kCtas CTAs does all steps, a cluster barrier between them, and what all
-// of them need of the slots is in every CTA's shared memory.
+// the steps' ends bounds it (a hop to L2 0.5 us, a cluster barrier 0.6): one cluster of kCtas CTAs does all
+// steps, a cluster barrier between them, and what all of them need of the slots is in every CTA's shared memory.
 constexpr int kCtas = 8, kThreads = 1024;
 constexpr int kUnit = 128;       // table entries a warp takes at a time, four a lane
 constexpr int kTile = 4 * kThreads;  // pages a CTA scans at a time, four a thread
-constexpr int kSlotsHere = 2048; // slots that fit the shared memory; of more the numbers lie in scratch
+constexpr int kSlotsHere = 1024; // slots that fit the shared memory; of more the numbers lie in scratch
 
 struct PagesDev {
     int32_t *table, *kv_len, *refs;
@@ -30,15 +30,17 @@ struct PagesDev {
     int32_t *stash;            // [S][W] entries that slots take over from others
     int32_t *last;             // [S] the page that a slot's kept tokens end inside
     int32_t *base;             // [S] the first new page of a slot among all, 2 x + (keeps the page it ends in)
-    int32_t *count, *claim;    // [P] slots that have all of a page; the first that ends inside (kNone: none)
+    int32_t *count, *claim;    // [P] slots that have all of a page; the first that ends inside (kNone: none);
+                               // 0 and kNone between calls
     int32_t *list;             // [P] free pages, in order, of each CTA's part of the pages
+    int32_t *place, *named;    // compaction: [P] a page's place in the list, [P / 2 + 1] refs of those in the list
     int32_t *moves;            // [3][cap]: page, page, rows
     int32_t *moves_n;          // [1]
     int cap;
     int *err;
 };
 
-constexpr int kNone = INT_MAX;
+constexpr int kNone = 0x7F7F7F7F;  // (bytes that are all the same)
 
 // A slot: tokens kept, of which slot (-1: none), tokens afterwards, entries used before.
 __device__ __forceinline__ int kept_of(const int4 &s) { return s.x; }
@@ -90,23 +92,39 @@ __device__ __forceinline__ T block_scan(T v, T *sm, T *all)
     return __shfl_sync(0xffffffffu, y - x, warp) + s - v;
 }
 
-// Calls fn(slot, entry) for the entries begin(slot) .. end(slot) - 1 of all slots, spread over the cluster's warps.
-template <class Begin, class End, class Fn>
-__device__ __forceinline__ void each_entry(const PagesDev &p, int cta, Begin begin, End end, Fn fn)
+// The cluster's warps share out pieces of kUnit entries of all slots: piece(slot, its first entry).
+template <class Piece>
+__device__ __forceinline__ void each_piece(const PagesDev &p, int cta, Piece piece)
+{
+    const uint32_t per = (p.W + kUnit - 1) / kUnit;  // S W is below 2^31
+#pragma unroll 1
+    for (uint32_t u = (threadIdx.x >> 5) * kCtas + cta; u < p.S * per; u += kCtas * (kThreads / 32))
+        piece((int)(u / per), (int)(u % per) * kUnit);
+}
+
+// For the entries begin(slot) .. end(slot) - 1 of all slots: use(slot, entry, *at(slot, entry)). A lane's four
+// loads are made whether they are needed or not (of some entry), behind no branch: all at once.
+template <class Begin, class End, class At, class Use>
+__device__ __forceinline__ void each_entry(const PagesDev &p, int cta, Begin begin, End end, At at, Use use)
 {
     const int lane = threadIdx.x & 31;
-    const int per = (p.W + kUnit - 1) / kUnit;  // S W is below 2^31
-    for (uint32_t u = cta * (kThreads / 32) + (threadIdx.x >> 5); u < (uint32_t)p.S * per; u += kCtas * (kThreads / 32)) {
-        const int s = u / per, j0 = u % per * kUnit;
-        const int n = end(s);
-        if (j0 >= n || j0 + kUnit <= begin(s)) continue;
+    each_piece(p, cta, [&](int s, int first) {
+        const int from = begin(s), n = end(s);
+        if (first >= n || first + kUnit <= from) return;
+        int x[kUnit / 32];
+#pragma unroll
+        for (int k = 0; k < kUnit / 32; ++k) x[k] = __ldcg(at(s, min(max(first + lane + k * 32, from), n - 1)));
 #pragma unroll
         for (int k = 0; k < kUnit / 32; ++k) {
-            const int j = j0 + k * 32 + lane;
-            if (j < n && j >= begin(s)) fn(s, j);
+            const int j = first + lane + k * 32;
+            if (j >= from && j < n) use(s, j, x[k]);
         }
-    }
+    });
 }
+
+// The end of a kernel whose CTAs read each other's shared memory: arrive when this one has, wait before it goes.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 // value(told) of every CTA of the cluster into out[kCtas]; behind a cluster barrier, called by all threads.
 template <class Value>
@@ -123,18 +141,25 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Told mine;
     __shared__ int4 slots_here[kSlotsHere];
+    __shared__ int kids[kSlotsHere], least[kSlotsHere];  // slots that go on from a slot, the fewest whole pages of them
+    __shared__ int last_here[kSlotsHere], base_here[kSlotsHere];  // the last CTA's: PagesDev::last, base
     __shared__ int64_t sm[33];
     __shared__ int others[kCtas];
     int *const sm32 = reinterpret_cast<int *>(sm);
-    const int cta = blockIdx.x, tid = cta * kThreads + threadIdx.x;
+    const int cta = blockIdx.x, tid = cta * kThreads + threadIdx.x, mask = (1 << p.shift) - 1;
     const bool here = p.S <= kSlotsHere;
     int4 *const slots = here ? slots_here : p.slots;
     const bool counted = !parent && !keep;  // every slot keeps what it has: refs are the counts
     if (threadIdx.x < 2) mine.bad[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < kSlotsHere; i += kThreads) {
+        kids[i] = 0;
+        least[i] = INT_MAX;
+    }
     __syncthreads();
 
-    // ---- 1: what is asked for (all slots in every CTA where they fit); the counts start from zero
+    // ---- 1: what is asked for (all slots in every CTA where they fit)
     const int capacity = (int)min((int64_t)p.W << p.shift, (int64_t)INT_MAX);
+    bool any_wrong = false;
     for (int i = here ? threadIdx.x : tid; i < p.S; i += here ? kThreads : kCtas * kThreads) {
         const int from = parent ? parent[i] : i, now = p.kv_len[i];
         const int extra = room ? room[i] : 0, most = keep ? max(0, keep[i]) : INT_MAX;
@@ -146,186 +171,231 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
             n = min(n, most);
         }
         wrong = wrong || (int64_t)n + extra > capacity;
-        if (wrong) mine.bad[0] = kErrRangeBit;
+        any_wrong = any_wrong || wrong;
         slots[i] = wrong ? make_int4(0, -1, 0, 0) : make_int4(n, from, n + extra, entries(now, p.shift));
-    }
-    if (!counted)
-        for (int x = tid; x < p.P; x += kCtas * kThreads) {
-            p.count[x] = 0;
-            p.claim[x] = kNone;
+        if (here && !wrong && from >= 0) {
+            atomicAdd(kids + from, 1);
+            atomicMin(least + from, n >> p.shift);
         }
-    cluster.sync();
+    }
     int bad = 0;
-    gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
-    for (int c = 0; c < kCtas; ++c) bad |= others[c];
-    if (bad) goto refuse;
+    if (here) {  // every CTA has looked at all of them
+        if (__syncthreads_or(any_wrong)) {
+            if (tid == 0) {
+                atomicOr(p.err, kErrRangeBit);
+                *p.moves_n = 0;
+            }
+            return;
+        }
+        cluster_arrive_relaxed();  // all have started, before the first reaches into another's shared memory
+        cluster_wait();
+    } else {
+        if (any_wrong) mine.bad[0] = kErrRangeBit;
+        cluster.sync();
+        gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
+        for (int c = 0; c < kCtas; ++c) bad |= others[c];
+        if (bad) {
+            cluster_arrive_relaxed();
+            if (tid == 0) {
+                atomicOr(p.err, bad);
+                *p.moves_n = 0;
+            }
+            cluster_wait();
+            return;
+        }
+    }
+    int *const last = here ? cluster.map_shared_rank(last_here, kCtas - 1) : p.last;
+    int *const base = here ? cluster.map_shared_rank(base_here, kCtas - 1) : p.base;
 
-    // ---- 2: who has a page, who ends inside one
+    // ---- 2: who has a page, who ends inside one. The pages that all slots that go on from one have are
+    // counted once for all of them: an SM's atomics go 1.6 cycles a lane.
     if (counted) {  // known: the entries are only looked at (the result is asked for behind the next barrier)
         each_entry(p, cta, [&](int) { return 0; }, [&](int s) { return held_of(slots[s]); },
-                   [&](int s, int j) {
-                       const int x = p.table[(int64_t)s * p.W + j];
+                   [&](int s, int j) { return p.table + (int64_t)s * p.W + j; },
+                   [&](int, int, int x) {
                        if (x < 0 || x >= p.P) mine.bad[1] = kErrRangeBit;
                    });
     } else {
-        each_entry(p, cta, [&](int) { return 0; }, [&](int s) { return entries(kept_of(slots[s]), p.shift); },
-                   [&](int s, int j) {
-                       const int from = from_of(slots[s]), x = p.table[(int64_t)from * p.W + j];
-                       if (x < 0 || x >= p.P) {
-                           mine.bad[1] = kErrRangeBit;
-                           return;
-                       }
-                       if (from != s) p.stash[(int64_t)s * p.W + j] = x;
-                       if (j < kept_of(slots[s]) >> p.shift) {
-                           atomicAdd(p.count + x, 1);
-                       } else {
-                           atomicMin(p.claim + x, s + (from == s ? 0 : p.S));
-                           p.last[s] = x;
-                       }
-                   });
+        each_piece(p, cta, [&](int s, int first) {
+            const int4 me = slots[s];
+            const int from = from_of(me), n = entries(kept_of(me), p.shift), whole = kept_of(me) >> p.shift;
+            const int to = here && kids[s] > 0 ? least[s] : 0;     // entries of this row that all its kids have
+            const int since = here && from >= 0 ? least[from] : 0; // entries of the other row that are counted here
+            if (first >= max(n, to)) return;
+            const int32_t *const mine_row = p.table + (int64_t)s * p.W;
+            const int32_t *const row = from >= 0 ? p.table + (int64_t)from * p.W : mine_row;
+            int x[kUnit / 32], y[kUnit / 32];
+#pragma unroll
+            for (int k = 0; k < kUnit / 32; ++k) {
+                const int j = first + (threadIdx.x & 31) + k * 32;
+                x[k] = __ldcg(mine_row + min(j, p.W - 1));
+                y[k] = __ldcg(row + min(j, p.W - 1));
+            }
+#pragma unroll
+            for (int k = 0; k < kUnit / 32; ++k) {
+                const int j = first + (threadIdx.x & 31) + k * 32;
+                if (j < to) {
+                    if (x[k] >= 0 && x[k] < p.P)
+                        atomicAdd(p.count + x[k], kids[s]);
+                    else
+                        mine.bad[1] = kErrRangeBit;
+                }
+                if (j >= n) continue;
+                const bool ok = y[k] >= 0 && y[k] < p.P;
+                if (!ok) mine.bad[1] = kErrRangeBit;
+                if (from != s) p.stash[(int64_t)s * p.W + j] = y[k];
+                if (j == whole) {  // ends inside
+                    if (ok) atomicMin(p.claim + y[k], s + (from == s ? 0 : p.S));
+                    last[s] = ok ? y[k] : 0;
+                } else if (j >= since && ok) {
+                    atomicAdd(p.count + y[k], 1);
+                }
+            }
+        });
         cluster.sync();
-        gather(cluster, &mine, others, [](const Told &t) { return t.bad[1]; });
-        for (int c = 0; c < kCtas; ++c) bad |= others[c];
-        if (bad) goto refuse;
     }
 
-    {
-        // ---- 3: the free pages of this CTA's part (a page that someone ends inside and nobody has stays with the
-        // first who asked), in order; the last CTA, which has no part: the new pages and copies of every slot
-        const int part = ((p.P + kCtas - 2) / (kCtas - 1) + 3) & ~3;
-        const int x0 = min(p.P, cta * part), x1 = cta == kCtas - 1 ? x0 : min(p.P, x0 + part);
-        auto pages4 = [&](int x, int (&c)[4], int (&cl)[4]) {  // counts and claims of pages x .. x + 3 below x1
+    // ---- 3: the free pages of this CTA's part (a page that someone ends inside and nobody has stays with the
+    // first who asked), in order; the last CTA, which has no part: the new pages and copies of every slot
+    const int part = ((p.P + kCtas - 2) / (kCtas - 1) + 3) & ~3;
+    const int x0 = min(p.P, cta * part), x1 = cta == kCtas - 1 ? x0 : min(p.P, x0 + part);
+    auto pages4 = [&](int x, int (&c)[4], int (&cl)[4]) {  // counts and claims of pages x .. x + 3 below x1
+        const int32_t *const from = counted ? p.refs : p.count;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                c[e] = 1;
-                cl[e] = kNone;
-                if (x + e < x1) {
-                    c[e] = counted ? p.refs[x + e] : __ldcg(p.count + x + e);
-                    if (!counted) cl[e] = __ldcg(p.claim + x + e);
-                }
-            }
-        };
-        int found = 0;
-        for (int y0 = x0; y0 < x1; y0 += kTile) {
-            const int x = y0 + 4 * threadIdx.x;
-            int c[4], cl[4], v = 0, sum;
-            pages4(x, c, cl);
+        for (int e = 0; e < 4; ++e) {
+            const int y = min(x + e, x1 - 1);
+            c[e] = __ldcg(from + y);
+            cl[e] = __ldcg((counted ? p.refs : p.claim) + y);
+        }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v += c[e] == 0 && cl[e] == kNone;
-            int at = found + block_scan(v, sm32, &sum);
+        for (int e = 0; e < 4; ++e) {
+            if (x + e >= x1) c[e] = 1;
+            if (counted) cl[e] = kNone;
+        }
+    };
+    int found = 0;
+    for (int y0 = x0; y0 < x1; y0 += kTile) {
+        const int x = y0 + 4 * threadIdx.x;
+        int c[4], cl[4], v = 0, sum;
+        pages4(x, c, cl);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c[e] == 0 && cl[e] == kNone) {
-                    p.list[x0 + at] = x + e;
-                    if (!counted) p.count[x + e] = -1 - at;  // free: its place in the list
-                    ++at;
-                }
-            found += sum;
-        }
-        if (threadIdx.x == 0) mine.found = found;
-        if (cta == kCtas - 1) {
-            int64_t before = 0;  // new pages, and in the upper half copies
-            for (int s0 = 0; s0 < p.S; s0 += kThreads) {
-                const int s = s0 + threadIdx.x;
-                int64_t v = 0, sum;
-                int stays = 0, n = 0, old = -1;
-                if (s < p.S) {
-                    n = kept_of(slots[s]);
-                    if (n & ((1 << p.shift) - 1)) {
-                        if (counted) {
-                            stays = 1;
-                        } else {
-                            old = __ldcg(p.last + s);
-                            const int count = __ldcg(p.count + old);  // (a page that someone asked for is not in a list)
-                            stays = __ldcg(p.claim + old) == s + (from_of(slots[s]) == s ? 0 : p.S) && count == 0;
-                        }
-                        if (!stays) v = 1ll << 32;
-                    }
-                    v += entries(total_of(slots[s]), p.shift) - (n >> p.shift) - stays;
-                }
-                const int64_t at = before + block_scan(v, sm, &sum);
-                if (s < p.S) {
-                    p.base[s] = 2 * (int)(uint32_t)at + stays;
-                    if (v >> 32) {
-                        const int k = (int)(at >> 32);
-                        p.moves[k] = old;
-                        p.moves[p.cap + k] = (int)(uint32_t)at;  // (which new page: its number below)
-                        p.moves[2 * p.cap + k] = n & ((1 << p.shift) - 1);
-                    }
-                }
-                before += sum;
-            }
-            if (threadIdx.x == 0) {
-                mine.need = (int)min((int64_t)(uint32_t)before, (int64_t)INT_MAX);
-                mine.copies = (int)(before >> 32);
-            }
-        }
-        cluster.sync();
-
-        // ---- 4: the new state
-        if (counted) {
-            gather(cluster, &mine, others, [](const Told &t) { return t.bad[1]; });
-            for (int c = 0; c < kCtas; ++c) bad |= others[c];
-            if (bad) goto refuse;
-        }
-        gather(cluster, &mine, others, [](const Told &t) { return t.found; });
-        const Told *const last_told = cluster.map_shared_rank(&mine, kCtas - 1);
-        const int need = last_told->need, copies = last_told->copies;
-        int there = 0, before = 0;
-        for (int c = 0; c < kCtas; ++c) {
-            if (c < cta) before += others[c];
-            there += others[c];
-        }
-        if (need > there) {
-            bad = kErrPagesBit;
-            goto refuse;
-        }
-        auto new_page = [&](int i) {  // the i-th of all free pages
-            int c = 0;
-            for (; c < kCtas - 2 && i >= others[c]; ++c) i -= others[c];
-            return __ldcg(p.list + c * part + i);
-        };
-        if (!counted)
-            for (int y0 = x0; y0 < x1; y0 += kTile) {
-                const int x = y0 + 4 * threadIdx.x;
-                int c[4], cl[4];
-                pages4(x, c, cl);
+        for (int e = 0; e < 4; ++e) v += c[e] == 0 && cl[e] == kNone;
+        int at = found + block_scan(v, sm32, &sum);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (x + e < x1)
-                        p.refs[x + e] = c[e] < 0 ? before - 1 - c[e] < need : c[e] == 0 && cl[e] != kNone ? 1 : c[e];
+        for (int e = 0; e < 4; ++e)
+            if (c[e] == 0 && cl[e] == kNone) {
+                p.list[x0 + at] = x + e;
+                if (!counted) p.count[x + e] = -1 - at;  // free: its place in the list
+                ++at;
             }
-        each_entry(p, cta,
-                   [&](int s) { return from_of(slots[s]) == s ? kept_of(slots[s]) >> p.shift : 0; },
-                   [&](int s) { return max(held_of(slots[s]), entries(total_of(slots[s]), p.shift)); },
-                   [&](int s, int j) {
-                       const int4 me = slots[s];
-                       const int b = __ldcg(p.base + s);
-                       const int old = (kept_of(me) >> p.shift) + (b & 1);  // entries that stay
-                       int32_t *const to = p.table + (int64_t)s * p.W + j;
-                       if (j < old) {
-                           if (from_of(me) != s) *to = __ldcg(p.stash + (int64_t)s * p.W + j);
-                       } else if (j < entries(total_of(me), p.shift)) {
-                           const int x = new_page((b >> 1) + j - old);
-                           *to = x;
-                           if (counted) p.refs[x] = 1;
-                       } else {
-                           *to = -1;
-                       }
-                   });
-        for (int s = tid; s < p.S; s += kCtas * kThreads) p.kv_len[s] = total_of(slots[s]);
-        for (int k = tid; k < copies; k += kCtas * kThreads) p.moves[p.cap + k] = new_page(__ldcg(p.moves + p.cap + k));
-        if (tid == 0) *p.moves_n = copies;
-        cluster.sync();  // the CTAs' shared memory is still read
-        return;
+        found += sum;
     }
-
-refuse:
-    if (tid == 0) {
-        atomicOr(p.err, bad);
-        *p.moves_n = 0;
+    if (threadIdx.x == 0) mine.found = found;
+    if (cta == kCtas - 1) {
+        int64_t before = 0;  // new pages, and in the upper half copies
+        for (int s0 = 0; s0 < p.S; s0 += kThreads) {
+            const int s = s0 + threadIdx.x;
+            int64_t v = 0, sum;
+            int stays = 0, n = 0, old = -1;
+            if (s < p.S) {
+                n = kept_of(slots[s]);
+                if (n & mask) {
+                    if (counted) {
+                        stays = 1;
+                    } else {
+                        old = last[s];
+                        const int count = __ldcg(p.count + old);  // (a page that someone asked for is not in a list)
+                        stays = __ldcg(p.claim + old) == s + (from_of(slots[s]) == s ? 0 : p.S) && count == 0;
+                    }
+                    if (!stays) v = 1ll << 32;
+                }
+                v += entries(total_of(slots[s]), p.shift) - (n >> p.shift) - stays;
+            }
+            const int64_t at = before + block_scan(v, sm, &sum);
+            if (s < p.S) {
+                base[s] = 2 * (int)(uint32_t)at + stays;
+                if (v >> 32) {
+                    const int k = (int)(at >> 32);
+                    p.moves[k] = old;
+                    p.moves[p.cap + k] = (int)(uint32_t)at;  // (which new page: its number below)
+                    p.moves[2 * p.cap + k] = n & mask;
+                }
+            }
+            before += sum;
+        }
+        if (threadIdx.x == 0) {
+            mine.need = (int)min((int64_t)(uint32_t)before, (int64_t)INT_MAX);
+            mine.copies = (int)(before >> 32);
+        }
     }
     cluster.sync();
+
+    // ---- 4: the new state
+    gather(cluster, &mine, others, [](const Told &t) { return t.found | (t.bad[1] ? INT_MIN : 0); });
+    const Told *const last_told = cluster.map_shared_rank(&mine, kCtas - 1);
+    const int need = last_told->need, copies = last_told->copies;
+    int there = 0, before = 0;
+    for (int c = 0; c < kCtas; ++c) {
+        const int f = others[c] & INT_MAX;
+        bad |= others[c] < 0 ? kErrRangeBit : 0;
+        if (c < cta) before += f;
+        there += f;
+    }
+    if (!bad && need > there) bad = kErrPagesBit;
+    if (!counted)
+        for (int y0 = x0; y0 < x1; y0 += kTile) {
+            const int x = y0 + 4 * threadIdx.x;
+            int c[4], cl[4];
+            pages4(x, c, cl);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (x + e < x1) {
+                    if (!bad)
+                        p.refs[x + e] = c[e] < 0 ? before - 1 - c[e] < need : c[e] == 0 && cl[e] != kNone ? 1 : c[e];
+                    p.count[x + e] = 0;  // for the next call
+                    p.claim[x + e] = kNone;
+                }
+        }
+    if (bad) {
+        cluster_arrive_relaxed();
+        if (tid == 0) {
+            atomicOr(p.err, bad);
+            *p.moves_n = 0;
+        }
+        cluster_wait();
+        return;
+    }
+    auto new_page = [&](int i) {  // where the i-th of all free pages is listed
+        int c = 0;
+#pragma unroll
+        for (int y = 0; y < kCtas - 2; ++y)
+            if (c == y && i >= others[y]) {
+                i -= others[y];
+                ++c;
+            }
+        return p.list + c * part + i;
+    };
+    each_entry(p, cta,
+               [&](int s) { return from_of(slots[s]) == s ? kept_of(slots[s]) >> p.shift : 0; },
+               [&](int s) { return max(held_of(slots[s]), entries(total_of(slots[s]), p.shift)); },
+               [&](int s, int j) -> const int32_t * {
+                   const int4 me = slots[s];
+                   const int b = base[s];
+                   const int old = (kept_of(me) >> p.shift) + (b & 1);  // entries that stay
+                   const int32_t *const there = (from_of(me) == s ? p.table : p.stash) + (int64_t)s * p.W + j;
+                   return j < old || j >= entries(total_of(me), p.shift) ? there : new_page((b >> 1) + j - old);
+               },
+               [&](int s, int j, int x) {
+                   const int4 me = slots[s];
+                   const bool used = j < entries(total_of(me), p.shift);
+                   p.table[(int64_t)s * p.W + j] = used ? x : -1;
+                   if (counted && used && j >= entries(kept_of(me), p.shift)) p.refs[x] = 1;
+               });
+    cluster_arrive_relaxed();  // nothing more of another CTA's shared memory
+    for (int s = tid; s < p.S; s += kCtas * kThreads) p.kv_len[s] = total_of(slots[s]);
+    for (int k = tid; k < copies; k += kCtas * kThreads) p.moves[p.cap + k] = __ldcg(new_page(__ldcg(p.moves + p.cap + k)));
+    if (tid == 0) *p.moves_n = copies;
+    cluster_wait();
 }
 
 // n pages are used. The used page x >= n with d used pages above it moves to the (moved - 1 - d)-th free page below n.
@@ -340,7 +410,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     const int x0 = min(p.P, cta * part), x1 = min(p.P, x0 + part);
     auto refs4 = [&](int x, int (&r)[4]) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = x + e < x1 ? p.refs[x + e] : 0;
+        for (int e = 0; e < 4; ++e) r[e] = __ldcg(p.refs + min(x + e, x1 - 1));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (x + e >= x1) r[e] = 0;
     };
 
     int used = 0;
@@ -375,8 +448,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                 if (y >= n) {
                     const int d = n - 1 - at;
                     p.list[d] = y;
-                    p.count[y] = d;
-                    p.claim[d] = r[e];
+                    p.place[y] = d;
+                    p.named[d] = r[e];
                 }
                 ++at;
             } else if (y < x1 && y < n) {
@@ -390,6 +463,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) mine.need = holes;
     cluster.sync();
     gather(cluster, &mine, others, [](const Told &t) { return t.need; });
+    cluster_arrive_relaxed();  // nothing more of another CTA's shared memory
     int moved = 0;
     for (int c = 0; c < kCtas; ++c) moved += others[c];
 
@@ -397,7 +471,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
         const int d = moved - 1 - k;
         p.moves[k] = __ldcg(p.list + d);
         p.moves[2 * p.cap + k] = 1 << p.shift;
-        refs_out[__ldcg(p.moves + p.cap + k)] = __ldcg(p.claim + d);
+        refs_out[__ldcg(p.moves + p.cap + k)] = __ldcg(p.named + d);
     }
     for (int x = tid; x < p.P; x += kCtas * kThreads) {
         if (x >= n)
@@ -411,15 +485,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     const bool copy = table_out != p.table;
     each_entry(p, cta, [&](int) { return 0; },
                [&](int s) { return copy ? p.W : max(0, entries(min(p.kv_len[s], capacity), p.shift)); },
-               [&](int s, int j) {
+               [&](int s, int j) { return p.table + (int64_t)s * p.W + j; },
+               [&](int s, int j, int x) {
                    const int64_t e = (int64_t)s * p.W + j;
-                   const int x = p.table[e];
                    const bool inside = !copy || j < entries(max(0, min(p.kv_len[s], capacity)), p.shift);
                    int to = x;
                    if (inside && (x < 0 || x >= p.P)) {
                        atomicOr(p.err, kErrRangeBit);
                    } else if (inside && x >= n) {
-                       const int d = __ldcg(p.count + x);
+                       const int d = __ldcg(p.place + x);
                        if (d >= 0 && d < moved && __ldcg(p.list + d) == x)
                            to = __ldcg(p.moves + p.cap + moved - 1 - d);
                        else  // a page that refs does not count has no move
@@ -428,7 +502,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                    if (to != x || copy) table_out[e] = to;
                });
     if (tid == 0) *p.moves_n = moved;
-    cluster.sync();  // the CTAs' shared memory is still read
+    cluster_wait();
 }
 
 __global__ void __launch_bounds__(kThreads) kv_pages_used_kernel(const int32_t *refs, int P, int *out)
@@ -544,6 +618,8 @@ PagesDev pages_view(const lora_kv_pages *p)
     v.count = take(P);
     v.claim = take(P);
     v.list = take(P + 4 * kCtas);
+    v.place = take(P);
+    v.named = take(P / 2 + 1);
     v.cap = p->cap();
     v.moves = take(3 * (size_t)p->cap());
     v.moves_n = take(1);
@@ -616,8 +692,8 @@ lora_status lora_kv_pages_create(int num_pages, int page_tokens, int max_seqs, i
     p->table = page_table;
     p->kv_len = kv_len;
     p->refs = refs;
-    const size_t ints = (size_t)max_seqs * table_stride + 6 * (size_t)max_seqs + 3 * (size_t)num_pages +
-                        4 * kCtas + 3 * (size_t)p->cap() + 1;
+    const size_t ints = (size_t)max_seqs * table_stride + 6 * (size_t)max_seqs + 4 * (size_t)num_pages +
+                        (size_t)num_pages / 2 + 1 + 4 * kCtas + 3 * (size_t)p->cap() + 1;
     if (cudaMalloc((void **)&p->d_err, 3 * sizeof(int)) != cudaSuccess ||
         cudaMalloc((void **)&p->scratch, sizeof(int32_t) * ints) != cudaSuccess ||
         cudaHostAlloc((void **)&p->h_err, sizeof(int), cudaHostAllocDefault) != cudaSuccess) {
@@ -627,6 +703,8 @@ lora_status lora_kv_pages_create(int num_pages, int page_tokens, int max_seqs, i
     }
     if (cudaMemset(p->d_err, 0, 3 * sizeof(int)) != cudaSuccess ||
         cudaMemset(pages_view(p).moves_n, 0, sizeof(int)) != cudaSuccess ||
+        cudaMemset(pages_view(p).count, 0, sizeof(int32_t) * (size_t)num_pages) != cudaSuccess ||
+        cudaMemset(pages_view(p).claim, kNone & 0xff, sizeof(int32_t) * (size_t)num_pages) != cudaSuccess ||
         cudaStreamCreateWithFlags(&p->ctl_stream, cudaStreamNonBlocking) != cudaSuccess ||
         cudaEventCreateWithFlags(&p->ev, cudaEventDisableTiming) != cudaSuccess ||
         ensure_smem_attr((const void *)kv_pages_update_kernel, 0) != cudaSuccess ||
