@@ -742,11 +742,11 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
         e = wide ? launch_kv_prefill_shared(kPrefix, kv, p->int8, bg, a, share, 0, p->pre_part, pre_count, p->num_sms,
                                             stream)
                  : launch_kv_decode_shared(kPrefix, kv, p->int8, bg, a, share, max_tokens, INT_MAX, p->dec_part,
-                                           p->count, p->num_sms, stream);
+                                           p->count, p->num_sms, false, stream);
     if (wide && e == cudaSuccess) e = launch_kv_share_join(kv, p->int8, a, share, p->num_sms, stream);
     if (decode && e == cudaSuccess)
         e = launch_kv_decode_shared(kOwn, kv, p->int8, bd, a, share, max_new, prefill ? kDecodeRows : INT_MAX,
-                                    p->dec_part, p->count, p->num_sms, stream);
+                                    p->dec_part, p->count, p->num_sms, wide, stream);
     if (prefill && e == cudaSuccess)
         e = launch_kv_prefill_shared(kOwn, kv, p->int8, bd, a, share, decode ? kDecodeRows + 1 : 0, p->pre_part,
                                      pre_count, p->num_sms, stream);

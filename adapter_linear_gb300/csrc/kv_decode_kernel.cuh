@@ -442,7 +442,10 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
     KvWork<R, kUnit, kHeadUnits, kMode> w(kv, b, a, share, 0, plan.max_rows, lane);
     // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
     // they save
-    if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits))) return;
+    if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits))) {
+        if (kMode == kOwn) pdl_wait_prior();  // (a kernel behind this one counts on the ones ahead having ended)
+        return;
+    }
 
     const uint32_t base = kv_opaque(0x43004300u);
     uint8_t *const ring = smem + warp * C::kRing;
@@ -580,6 +583,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
             run(std::integral_constant<int, 1>());
         else
             run(std::integral_constant<int, kN>());
+        if (kMode == kOwn) pdl_wait_prior();  // the prefix's O and lse
         __syncthreads();
         const bool whole = w.whole();
         // row r of the item in [T][Hq] arrays
@@ -742,15 +746,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
 template <KvMode kMode>
 cudaError_t launch_kv_decode_mode(const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
                                   const KvShareDev &share, int max_new, int max_rows, float *part, int *count,
-                                  int num_sms, cudaStream_t stream)
+                                  int num_sms, bool early, cudaStream_t stream)
 {
     auto launch = [&](auto cfg, auto *fn) {
         using C = decltype(cfg);
         const cudaError_t e = ensure_smem_attr((const void *)fn, C::kSmem);
         if (e != cudaSuccess) return e;
         const Plan plan{max_rows, a.scale * 1.4426950408889634f, part, count};
-        fn<<<min(C::kCtas * num_sms, C::kMaxGrid), kWarps * 32, C::kSmem, stream>>>(kv, b, a, share, plan);
-        return cudaGetLastError();
+        return kv_launch(early, fn, dim3(min(C::kCtas * num_sms, C::kMaxGrid)), kWarps * 32, C::kSmem, stream, kv, b, a,
+                         share, plan);
     };
     const int64_t rows = (int64_t)max_new * a.G;
     auto pick = [&](auto d, auto i8) {

@@ -4,10 +4,31 @@
 
 #include <cuda_fp16.h>
 
+#include <utility>
+
 #include "device_common.cuh"
 #include "kv_internal.h"
 
 namespace lora {
+
+// Launch with or without leave to start before the kernel ahead of it in the stream has ended (which it then
+// waits for itself: griddep_wait).
+template <class... Params, class... Args>
+cudaError_t kv_launch(bool early, void (*fn)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                      Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...);
+}
 
 __device__ __forceinline__ void kv_flag_range(int *err) { atomicOr(err, kErrRangeBit); }
 

@@ -99,13 +99,14 @@ size_t kv_share_part_floats(int D, int num_sms);
 cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, const KvShareDev &share, int num_sms,
                                  cudaStream_t stream);
 
-// Both for groups that share prefixes. plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
+// Both for groups that share prefixes. early: the kernel may start before the one ahead of it has ended
+// (kOwn, behind the join: it waits before it reads the prefixes' results). plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
 // one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
                                  const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream);
 cudaError_t launch_kv_decode_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
                                     const KvShareDev &share, int max_new, int max_rows, float *part, int *count,
-                                    int num_sms, cudaStream_t stream);
+                                    int num_sms, bool early, cudaStream_t stream);
 cudaError_t launch_kv_prefill_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
                                      const KvShareDev &share, int min_rows, float *part, int *count, int num_sms,
                                      cudaStream_t stream);

@@ -519,6 +519,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
     }
+    if constexpr (kMode == kPrefix) {
+        // The groups are known once the kernel ahead has ended. Those behind may start then, so that they
+        // too find what it wrote.
+        pdl_wait_prior();
+        pdl_launch_dependents();
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
@@ -1197,8 +1203,8 @@ cudaError_t launch_kv_prefill_mode(const KvDev &kv, bool int8, const KvBatchDev 
         if (e != cudaSuccess) return e;
         const Plan plan{min_rows, fabsf(a.scale) * 1.4426950408889634f, signbit(a.scale) ? 0x80008000u : 0u, part,
                         count};
-        fn<<<kv_prefill_grid(num_sms), kThreads, smem, stream>>>(kv, b, a, share, plan);
-        return cudaGetLastError();
+        return kv_launch(kMode == kPrefix, fn, dim3(kv_prefill_grid(num_sms)), kThreads, smem, stream, kv, b, a, share,
+                         plan);
     };
     if (kv.D == 128)
         return int8 ? launch(Cfg<128>::kSmem, kv_prefill_kernel<128, true, kMode>)

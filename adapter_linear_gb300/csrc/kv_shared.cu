@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
                                                              const int32_t *prefix_len, int n_groups, KvShareDev share)
 {
     const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
     for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) share.lo[i] = 0;
     bool ordered = true;
     for (int g = threadIdx.x; g < n_groups; g += blockDim.x)
@@ -52,61 +53,84 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
 }
 
 // The pieces of the items that several CTAs of the prefix's kernel share: with few groups an item is cut into
-// dozens. A block takes kJoinRows rows of the item that begins in CTA blockIdx.x.
+// dozens. A unit of work is kJoinRows rows of one item; the blocks, all resident, take turns.
 constexpr int kJoinRows = 8, kJoinThreads = 256, kMaxPieces = 256;
+static_assert(kMaxPieces == kJoinThreads, "an item a thread");
 
 template <int D, bool kInt8>
 __global__ void __launch_bounds__(kJoinThreads) kv_share_join_kernel(KvAttn a, KvShareDev share, int grid)
 {
     __shared__ float weight[kJoinRows][kMaxPieces];
-    const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-    const KvShareItem item = share.items[c0];
-    const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, item.rows - r0);
-    if (item.last < 0 || rows <= 0) return;
-    const int n = item.last - c0 + 1;
-    auto slot = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
-    auto out_row = [&](int r) {
-        const int row = item.first_row + r0 + r;
-        return (int64_t)(item.row0 + row / a.G) * a.Hq + item.head * a.G + row % a.G;
-    };
-    const float2 *const ml = reinterpret_cast<const float2 *>(share.part + (int64_t)2 * grid * kBlockRows * D);
-    // a row's maximum, sum and weights by one warp
-    for (int r = threadIdx.x >> 5; r < rows; r += kJoinThreads / 32) {
-        float M = -INFINITY, sum = 0.0f;
-        for (int x = lane; x < n; x += 32) {
-            const float m = ml[slot(x) * kBlockRows + r0 + r].x;
-            weight[r][x] = m;
-            M = fmaxf(M, m);
-        }
+    __shared__ int units_to[kMaxPieces], sums[kJoinThreads / 32];  // units of the items up to each
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    pdl_wait_prior();
+    int n = 0;
+    if (threadIdx.x < grid && share.items[threadIdx.x].last >= 0)
+        n = (share.items[threadIdx.x].rows + kJoinRows - 1) / kJoinRows;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        const float ref = M == -INFINITY ? 0.0f : M;
-        for (int x = lane; x < n; x += 32) {
-            const float w = fast_exp2(weight[r][x] - ref);
-            sum += w * ml[slot(x) * kBlockRows + r0 + r].y;
-            weight[r][x] = w;
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        for (int x = lane; x < n; x += 32) weight[r][x] *= inv;
-        if (lane == 0) share.lse2[out_row(r)] = sum == 0.0f ? -INFINITY : M + log2f(sum);
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, n, d);
+        if (lane >= d) n += o;
     }
+    if (lane == 31) sums[warp] = n;
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        const float *const src = share.part + (int64_t)(r0 + r) * D + d;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int x = 0; x < n; ++x) {
-            const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)slot(x) * kBlockRows * D);
-            const float w = weight[r][x];
-            acc.x = add_piece<kInt8>(w, v.x, acc.x);
-            acc.y = add_piece<kInt8>(w, v.y, acc.y);
-            acc.z = add_piece<kInt8>(w, v.z, acc.z);
-            acc.w = add_piece<kInt8>(w, v.w, acc.w);
+    for (int x = 0; x < warp; ++x) n += sums[x];
+    units_to[threadIdx.x] = n;
+    __syncthreads();
+    const float2 *const ml = reinterpret_cast<const float2 *>(share.part + (int64_t)2 * grid * kBlockRows * D);
+    for (int u = blockIdx.x; u < units_to[kMaxPieces - 1]; u += gridDim.x) {
+        int c0 = 0;  // the first item whose units go beyond u
+#pragma unroll
+        for (int step = kMaxPieces / 2; step > 0; step >>= 1)
+            if (units_to[c0 + step - 1] <= u) c0 += step;
+        const KvShareItem item = share.items[c0];
+        const int r0 = (u - (c0 > 0 ? units_to[c0 - 1] : 0)) * kJoinRows, rows = min(kJoinRows, item.rows - r0);
+        const int pieces = item.last - c0 + 1;
+        auto slot = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
+        auto out_row = [&](int r) {
+            const int row = item.first_row + r0 + r;
+            return (int64_t)(item.row0 + row / a.G) * a.Hq + item.head * a.G + row % a.G;
+        };
+        // a row's maximum, sum and weights by one warp
+        for (int r = warp; r < rows; r += kJoinThreads / 32) {
+            float M = -INFINITY, sum = 0.0f;
+            for (int x = lane; x < pieces; x += 32) {
+                const float m = ml[slot(x) * kBlockRows + r0 + r].x;
+                weight[r][x] = m;
+                M = fmaxf(M, m);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            const float ref = M == -INFINITY ? 0.0f : M;
+            for (int x = lane; x < pieces; x += 32) {
+                const float w = fast_exp2(weight[r][x] - ref);
+                sum += w * ml[slot(x) * kBlockRows + r0 + r].y;
+                weight[r][x] = w;
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            for (int x = lane; x < pieces; x += 32) weight[r][x] *= inv;
+            if (lane == 0) share.lse2[out_row(r)] = sum == 0.0f ? -INFINITY : M + log2f(sum);
         }
-        *reinterpret_cast<float4 *>(share.O + out_row(r) * D + d) = acc;
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
+            const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+            const float *const src = share.part + (int64_t)(r0 + r) * D + d;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int x = 0; x < pieces; ++x) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + (int64_t)slot(x) * kBlockRows * D);
+                const float w = weight[r][x];
+                acc.x = add_piece<kInt8>(w, v.x, acc.x);
+                acc.y = add_piece<kInt8>(w, v.y, acc.y);
+                acc.z = add_piece<kInt8>(w, v.z, acc.z);
+                acc.w = add_piece<kInt8>(w, v.w, acc.w);
+            }
+            *reinterpret_cast<float4 *>(share.O + out_row(r) * D + d) = acc;
+        }
+        __syncthreads();  // the weights are free again
     }
 }
 
@@ -126,8 +150,7 @@ cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, co
     if (grid > kMaxPieces) return cudaErrorInvalidConfiguration;
     const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
     if (e != cudaSuccess) return e;
-    fn<<<dim3(grid, kBlockRows / kJoinRows), kJoinThreads, 0, stream>>>(a, share, grid);
-    return cudaGetLastError();
+    return kv_launch(true, fn, dim3(2 * num_sms), kJoinThreads, 0, stream, a, share, grid);
 }
 
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,

@@ -1,5 +1,6 @@
 // rotary.cu -- rotary positions: frequencies (host), and the kernel that rotates tensors of tokens.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "pool_state.h"
@@ -182,12 +183,20 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
     }
     if (T == 0) return LORA_OK;
     if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3)) return LORA_ERR_ARG;
-    int dev = 0, major = 0, minor = 0, sms = 0;
+    int dev = 0;
     CUDA_TRY(cudaGetDevice(&dev));
-    CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-    CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-    CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    if (major != 10 || minor != 3) return LORA_ERR_UNSUPPORTED;
+    // multiprocessors of the devices asked about so far; -1: not a device of ours
+    static std::atomic<int> known[64];
+    int sms = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
+        int major = 0, minor = 0;
+        CUDA_TRY(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
+        CUDA_TRY(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
+        CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        if (major != 10 || minor != 3) sms = -1;
+        if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    }
+    if (sms < 0) return LORA_ERR_UNSUPPORTED;
     CUDA_TRY(ensure_smem_attr((const void *)rotary_kernel, 0));
     const int per = 32 / (head_dim / 16);
     const int64_t all = (rows + per - 1) / per;  // blocks of a token

@@ -154,22 +154,22 @@ class KvCache:
 
     def _empty(self, shape, dtype, stream):
         """An output, allocated for the stream that will write it."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self._torch_device)
+        if stream is None:  # (sizes one by one: a tuple takes torch 1 us more)
+            return torch.empty(*shape, dtype=dtype, device=self._torch_device)
         with torch.cuda.stream(self._stream_object(stream)):
-            return torch.empty(shape, dtype=dtype, device=self._torch_device)
+            return torch.empty(*shape, dtype=dtype, device=self._torch_device)
 
     def _rows(self, x, heads: int, batch: KvBatch, what: str) -> int:
         """The token stride of x, a bf16 [T, heads, head_dim] tensor with contiguous heads."""
         T, D = batch.T, self.head_dim
-        if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[0] != T or x.shape[1] != heads or x.shape[2] != D:
+        if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape != (T, heads, D):
             raise LoraError(LORA_ERR_SHAPE, f"{what}: bfloat16 [{T}, {heads}, {D}] expected")
         if x.get_device() != self._device or batch.device != self._device:
             raise LoraError(LORA_ERR_ARG, f"{what}: the tensors of a call are on the cache's GPU")
-        s = x.stride()
-        if (s[2] != 1 and D > 1) or (s[1] != D and heads > 1):
+        st, sh, sd = x.stride()
+        if (sd != 1 and D > 1) or (sh != D and heads > 1):
             raise LoraError(LORA_ERR_ARG, f"{what}: the heads of a token must be contiguous")
-        return s[0] if T > 1 else heads * D
+        return st if T > 1 else heads * D
 
     def reserve(self, max_tokens: int, n_heads: int, max_seqs: int):
         _check(self._lib.lora_kv_reserve(self.handle, max_tokens, n_heads, max_seqs), "lora_kv_reserve")

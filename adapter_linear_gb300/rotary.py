@@ -6,6 +6,7 @@ tensors of tokens; ``KvCache.write_rotary`` rotates keys on their way into the c
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -23,9 +24,8 @@ class _RotaryStruct(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * (LORA_ROTARY_MAX_DIM // 2))]
 
 
-class _TensorStruct(ctypes.Structure):
-    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
-                ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+# n lora_rotary_tensor in a row: two addresses, two strides, heads, reserved
+_TENSORS = [struct.Struct("PPqqii" * n) for n in range(LORA_ROTARY_MAX_TENSORS + 1)]
 
 
 class Rotary:
@@ -71,50 +71,54 @@ class Rotary:
         `tensors` themselves: in place); by default new ones, returned as a tuple. inverse: the other
         way round (the gradient). Runs on the current stream or on `stream`."""
         xs = tuple(tensors)
-        if not 1 <= len(xs) <= LORA_ROTARY_MAX_TENSORS:
+        n = len(xs)
+        if not 1 <= n <= LORA_ROTARY_MAX_TENSORS:
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: one to four tensors")
         if positions.dtype != torch.int32 or positions.dim() != 1 or not positions.is_contiguous():
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: positions are contiguous int32 [T]")
-        T, D = positions.shape[0], xs[0].shape[-1] if xs[0].dim() == 3 else 0
-        device = positions.get_device()
-        for x in xs:
-            self._token_stride(x, T, x.shape[1] if x.dim() == 3 else 0, D, device)
-        if device != torch.cuda.current_device():
+        T, D, device = positions.shape[0], xs[0].shape[-1], positions.get_device()
+        given = [self._rows(x, None, T, D, device) for x in xs]
+        if device < 0 or device != torch._C._cuda_getDevice():
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the tensors are on the current GPU")
-        current = torch._C._cuda_getCurrentRawStream(device)
-        handle = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        handle = current = torch._C._cuda_getCurrentRawStream(device)
         other = None
-        if handle != current:
-            other = torch.cuda.ExternalStream(stream, xs[0].device) if isinstance(stream, int) else stream
+        if stream is not None:
+            handle = stream if isinstance(stream, int) else stream.cuda_stream
+            if handle != current:
+                other = torch.cuda.ExternalStream(stream, xs[0].device) if isinstance(stream, int) else stream
         if out is None:
             if other is None:
-                out = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs)
+                out = tuple([torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs])
             else:
                 with torch.cuda.stream(other):  # they belong to the stream that writes them
-                    out = tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs)
+                    out = tuple([torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs])
+            results = [(y.data_ptr(), h * D, h) for y, (_, _, h) in zip(out, given)]
         else:
             out = tuple(out)
-            if len(out) != len(xs):
+            if len(out) != n:
                 raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: as many results as tensors")
-        arr = (_TensorStruct * len(xs))()
-        for a, x, y in zip(arr, xs, out):
-            a.inp, a.out, a.heads = x.data_ptr(), y.data_ptr(), x.shape[1]
-            a.in_stride = self._token_stride(x, T, x.shape[1], D, device)
-            a.out_stride = self._token_stride(y, T, x.shape[1], D, device)
+            results = [self._rows(y, h, T, D, device) for y, (_, _, h) in zip(out, given)]
+        fields = []
+        for (a, sa, h), (b, sb, _) in zip(given, results):
+            fields += (a, b, sa, sb, h, 0)
         if other is not None:
             for t in xs + out + (positions,):
                 t.record_stream(other)
-        _check(self._lib.lora_rotary_apply(self.ref, len(xs), arr, D, positions.data_ptr(), T, int(inverse), handle),
-               "lora_rotary_apply")
+        _check(self._lib.lora_rotary_apply(self.ref, n, _TENSORS[n].pack(*fields), D, positions.data_ptr(), T, inverse,
+                                           handle), "lora_rotary_apply")
         return out
 
     @staticmethod
-    def _token_stride(x, T, heads, D, device) -> int:
-        if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[0] != T or x.shape[1] != heads or x.shape[2] != D:
+    def _rows(x, heads, T, D, device):
+        """Address, token stride and heads of x, a bf16 [T, heads, D] tensor with contiguous heads."""
+        if x.dim() != 3 or x.dtype != torch.bfloat16:
             raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, heads, {D}] expected")
-        if device < 0 or x.get_device() != device:
+        t, h, d = x.shape
+        if t != T or d != D or (heads is not None and h != heads):
+            raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, {heads or 'heads'}, {D}] expected")
+        if x.get_device() != device:
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the tensors of a call are on one GPU")
-        s = x.stride()
-        if (s[2] != 1 and D > 1) or (s[1] != D and heads > 1):
+        st, sh, sd = x.stride()
+        if (sd != 1 and D > 1) or (sh != D and h > 1):
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the heads of a token must be contiguous")
-        return s[0] if T > 1 else heads * D
+        return x.data_ptr(), st if T > 1 else h * D, h

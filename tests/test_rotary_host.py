@@ -95,11 +95,11 @@ def test_refusals(lib):
 
 
 def test_apply_refuses_before_touching_the_device(lib):
-    from adapter_linear_gb300.rotary import _TensorStruct
+    from adapter_linear_gb300.rotary import _TENSORS
     r = Rotary(32)
 
     def call(n=1, head_dim=64, pos=64, T=3, rot=None, inp=64, out=128, stride=128, out_stride=128, heads=2):
-        arr = (_TensorStruct * 5)(*[_TensorStruct(inp, out, stride, out_stride, heads, 0)] * 5)
+        arr = _TENSORS[1].pack(inp or 0, out or 0, stride, out_stride, heads, 0) * 5
         return lib.lora_rotary_apply(rot or r.ref, n, arr, head_dim, pos, T, 0, None)
 
     for n in (0, 5):
