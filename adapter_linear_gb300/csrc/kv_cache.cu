@@ -343,8 +343,9 @@ KvDev kv_view(const lora_kv *p)
     return v;
 }
 
-// Arrival counters of both attention kernels.
-int count_ints(const lora_kv *p) { return kv_decode_grid(p->num_sms) + 8 * kv_prefill_grid(p->num_sms); }
+// Arrival counters of both attention kernels, and of the short-chunk kernel behind a shared prefix (which may run
+// beside the one of the prefix).
+int count_ints(const lora_kv *p) { return 2 * kv_decode_grid(p->num_sms) + 8 * kv_prefill_grid(p->num_sms); }
 
 // Rows (query heads of new tokens) of a kv head up to which the short-chunk kernel takes a sequence: 32
 // requests of 6 tokens on 4 query heads (24 rows) take 82 us there, 161 on the tcgen05 kernel, of
@@ -368,16 +369,18 @@ lora_status ensure_pre_part(lora_kv *p)
 // The attention over shared prefixes keeps between its kernels, one behind the other (16-byte pieces): O and lse
 // of the prefixes, the groups, and where each sequence's own tokens begin.
 struct ShareSizes {
-    size_t O, lse2, groups, items, part, total;
+    size_t O, lse2, where, groups, items, own_part, part, total;
     ShareSizes(const lora_kv *p, int64_t T, int n_heads, int64_t n_seqs)
     {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
         // what does not depend on the call's size first
         part = 0;
         items = up(sizeof(float) * kv_share_part_floats(p->D, p->num_sms));
-        O = items + up(sizeof(KvShareItem) * (size_t)kv_prefill_grid(p->num_sms));
+        own_part = items + up(sizeof(KvShareItem) * (size_t)kv_prefill_grid(p->num_sms));
+        O = own_part + up(sizeof(float) * kv_decode_part_floats(p->D, p->num_sms));
         lse2 = O + up((size_t)T * n_heads * p->D * sizeof(float));
-        groups = lse2 + up((size_t)T * n_heads * sizeof(float));
+        where = lse2 + up((size_t)T * n_heads * sizeof(float));
+        groups = where + up((size_t)T * n_heads * sizeof(uint2));
         total = groups + (size_t)n_seqs * (sizeof(int4) + sizeof(int32_t));
     }
 };
@@ -712,8 +715,10 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     const int64_t row = (int64_t)n_heads * p->D;
     if (!tensor_ok(Q, q_stride, row) || !tensor_ok(O, o_stride, row)) return LORA_ERR_ARG;
     const KvAttn a = attention_view(p, Q, q_stride, n_heads, scale, 0, O, o_stride, lse);
-    // the kernels of the sequences' own tokens: as for lora_kv_attention; of the prefixes: the short-chunk one
-    // where no group has more rows than it takes
+    // The kernels of the sequences' own tokens: as for lora_kv_attention; of the prefixes: the short-chunk one
+    // where no group has more rows than one tile of it. (It would take more in several tiles, reading the prefix again
+    // from L2 for each: one group of 32 rows over 1000, 4000, 16000 8-bit 22, 31, 47 us, the tcgen05 kernel 20, 29,
+    // 44; 8 groups 44, 71, 173 and 44, 75, 190; 64 rows 65, 96, 248 and 54, 83, 198; bf16 the more so.)
     const int max_new = std::min(batch->max_new, batch->T), max_tokens = std::min(groups->max_tokens, batch->T);
     const bool prefill = (int64_t)max_new * a.G > kDecodeRows;
     const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
@@ -727,7 +732,12 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     share.items = reinterpret_cast<KvShareItem *>(block + sizes.items);
     share.O = reinterpret_cast<float *>(block + sizes.O);
     share.lse2 = reinterpret_cast<float *>(block + sizes.lse2);
+    share.where = reinterpret_cast<uint2 *>(block + sizes.where);
     share.groups = reinterpret_cast<int4 *>(block + sizes.groups);
+    share.ml_at = (int64_t)2 * kv_prefill_grid(p->num_sms) * kShareRows * p->D;
+    // The short-chunk kernel, a few rows a CTA, reads the pieces of the prefix's output itself. The other, a thread a
+    // row, would take 40 us for 20 of them: then they are joined first.
+    share.pieces = wide && !prefill;
     share.lo = reinterpret_cast<int32_t *>(share.groups + batch->n_seqs);
     const bool tracked = !capturing(stream, &st);  // the scratch belongs to one call at a time
     if (st != LORA_OK) return st;
@@ -742,11 +752,12 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
         e = wide ? launch_kv_prefill_shared(kPrefix, kv, p->int8, bg, a, share, 0, p->pre_part, pre_count, p->num_sms,
                                             stream)
                  : launch_kv_decode_shared(kPrefix, kv, p->int8, bg, a, share, max_tokens, INT_MAX, p->dec_part,
-                                           p->count, p->num_sms, false, stream);
-    if (wide && e == cudaSuccess) e = launch_kv_share_join(kv, p->int8, a, share, p->num_sms, stream);
+                                           p->count, p->num_sms, true, stream);
+    if (wide && prefill && e == cudaSuccess) e = launch_kv_share_join(kv, p->int8, a, share, p->num_sms, stream);
     if (decode && e == cudaSuccess)
         e = launch_kv_decode_shared(kOwn, kv, p->int8, bd, a, share, max_new, prefill ? kDecodeRows : INT_MAX,
-                                    p->dec_part, p->count, p->num_sms, wide, stream);
+                                    reinterpret_cast<float *>(block + sizes.own_part),
+                                    pre_count + 8 * kv_prefill_grid(p->num_sms), p->num_sms, true, stream);
     if (prefill && e == cudaSuccess)
         e = launch_kv_prefill_shared(kOwn, kv, p->int8, bd, a, share, decode ? kDecodeRows + 1 : 0, p->pre_part,
                                      pre_count, p->num_sms, stream);

@@ -49,8 +49,12 @@ constexpr int kMaxCtas = 4;    // CTAs an SM, of any variant
 constexpr int kPartRows = 48;  // and the rows that those of one SM hold
 
 // kN: tiles of 8 rows (a row: one query head of one new token) an item holds.
-template <int D, bool kInt8, int kN>
+template <int D, bool kInt8, int kN, KvMode kMode = kPlain>
 struct Cfg {
+    // Two warps may take an item by themselves (kOwn), or one where it is one row tile: teams that work on items of
+    // their own, each with room for its rows' Q and numbers. (With more tiles and teams that room would leave
+    // an SM one CTA.)
+    static constexpr int kTeams = kMode == kOwn ? (kN == 1 ? kWarps : 2) : 1;
     static constexpr int kRows = 8 * kN;
     static constexpr int kRowBytes = D * (kInt8 ? 1 : 2);
     static constexpr int kTile = kStep * kRowBytes;              // K or V of a step
@@ -60,8 +64,8 @@ struct Cfg {
     // spill at 3: 104 us against 81 for 32 drafts; rows of 256 bytes: 2 of 98 KB): 100 to
     // 150 KB in flight beside the stages in use. (Two row tiles of an 8-bit cache, D = 128: 16 bytes a thread
     // spill; the others none.)
-    static constexpr int kStages = kWide || kN == 1 ? 3 : 4;
-    static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 ? 4 : 3;
+    static constexpr int kStages = kWide || kN == 1 || (kN == 2 && kMode == kOwn) ? 3 : 4;
+    static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 && kMode != kOwn ? 4 : 3;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kSmem = kWarps * kRing;
     static constexpr int kLdO = D + 4;                           // fp32 row of O in shared memory
@@ -118,16 +122,16 @@ struct Plan {
     int *count;          // [grid] arrivals at the item that starts in that CTA and ends in another
 };
 
-// A warp's steps of an item, nk of them from token `tok`, for the first kT tiles of its rows, and
-// then their O into the ring and (m, l) into sm_m and sm_l. issue() starts the copy of the next step.
+// A warp's steps of an item, nk of them from token `tok`, every ways-th of the item's, for the first kT tiles of its
+// rows, and then their O into the ring and (m, l) into sm_m and sm_l. issue() starts the copy of the next step.
 // v_row(j): V of token j < tok_end, which the table names (for an unquantised cache's bad values).
-template <int D, bool kInt8, int kN, int kT, class Issue, class Row>
-__device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int tok, int tok_end, int window, int rows,
+template <int D, bool kInt8, int kN, int kT, KvMode kMode, class Issue, class Row>
+__device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int tok, int ways, int tok_end, int window, int rows,
                                           int pos_min, int pos_max, uint32_t base, uint8_t *ring,
                                           const uint4 (&sm_q)[kN][D / 32][32], const float *sm_back, const int *sm_pos,
                                           float *sm_m, float *sm_l)
 {
-    using C = Cfg<D, kInt8, kN>;
+    using C = Cfg<D, kInt8, kN, kMode>;
     constexpr int kM = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     // of the rows this lane has scores of: 8 t + 2 c, + 1
@@ -152,7 +156,7 @@ __device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int 
     bool bad = false;  // V had an infinity or a NaN that was left out of the product
     int stage = 0;
     const int tok_first = tok;
-    for (int k = 0; k < nk; ++k, tok += kStep * kWarps) {
+    for (int k = 0; k < nk; ++k, tok += kStep * ways) {
         cp_wait<C::kStages - 2>();
         __syncwarp();
         const uint8_t *st = ring + stage * C::kStage;
@@ -371,7 +375,7 @@ __device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int 
             for (int pass = 0; pass < 2; ++pass)
 #pragma unroll 1
                 for (int y = 0; y < nk * kStep; ++y) {
-                    const int j = tok_first + y % kStep + y / kStep * (kStep * kWarps);
+                    const int j = tok_first + y % kStep + y / kStep * (kStep * ways);
                     if (j >= tok_end) break;
                     const uint16_t *const row = v_row(j);
 #pragma unroll
@@ -421,28 +425,76 @@ __device__ __forceinline__ void run_steps(Issue &issue, Row &v_row, int nk, int 
 }
 
 template <int D, bool kInt8, int kN, KvMode kMode>
-__global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
     kv_decode_kernel(KvDev kv, KvBatchDev b, KvAttn a, KvShareDev share, Plan plan)
 {
-    using C = Cfg<D, kInt8, kN>;
+    using C = Cfg<D, kInt8, kN, kMode>;
     constexpr int R = C::kRows;
     constexpr int kM = D / 16;                    // MMAs of 16 dimensions
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_w[kWarps][R], sm_lse[R];
-    __shared__ float sm_back[R];
-    __shared__ int sm_pos[R];
-    __shared__ uint4 sm_q[kN][kM / 2][32];  // [tile][pair of MMAs][lane]: the same for all warps
-    __shared__ float sm_prior[kMode == kOwn ? R : 1];  // weight of the prefix's O
+    __shared__ float sm_m[kWarps][R], sm_l[kWarps][R], sm_w[kWarps][R], sm_lses[C::kTeams][R];
+    __shared__ float sm_backs[C::kTeams][R];
+    __shared__ int sm_poss[C::kTeams][R];
+    __shared__ uint4 sm_qs[C::kTeams][kN][kM / 2][32];  // [tile][pair of MMAs][lane]: the same for all warps of a team
+    // the prefix's weight, the maximum its pieces' weights are relative to, where it is
+    constexpr int kOwnRows = kMode == kOwn ? R : 1;
+    __shared__ float sm_priors[C::kTeams][kOwnRows], sm_tops[C::kTeams][kOwnRows];
+    __shared__ uint2 sm_wheres[C::kTeams][kOwnRows];
     __shared__ int sm_last;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, c = lane & 3;
     const int G = a.G;
 
+    if (kMode == kPrefix) {  // the groups are known once the kernel ahead has ended; those behind may start then
+        pdl_wait_prior();
+        pdl_launch_dependents();
+    }
     KvWork<R, kUnit, kHeadUnits, kMode> w(kv, b, a, share, 0, plan.max_rows, lane);
     // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
     // they save
-    if (!w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits))) {
+    // kOwn: what is behind a prefix is short, and there is much of it: cutting items into equal shares costs a
+    // second item's start and end in most CTAs, and where there are many items their starts and ends one
+    // after the other are most of the time. So items may go whole to teams of 4, 2 or 1 warps. The time of
+    // each, in units (64 tokens by 4 warps), with kEnds for an item's start and end:
+    int ways = kWarps;  // warps that work on an item
+    if constexpr (kMode == kOwn) {
+        constexpr int kEnds = 12;
+        const int64_t items = max(w.items, (int64_t)1), avg = w.total / items - kHeadUnits + 1;
+        int64_t best = w.total / gridDim.x + 3 * kEnds;  // cut
+#pragma unroll
+        for (int teams = 1; teams <= C::kTeams; teams *= 2) {
+            const int64_t n = (int64_t)gridDim.x * teams, turns = (items + n - 1) / n;
+            const int64_t time = teams * max((int64_t)w.most, turns * avg) + turns * kEnds;
+            if (time < best) {
+                best = time;
+                ways = -kWarps / teams;
+            }
+        }
+        if (ways < 0) {
+            w.by_items();
+            ways = -ways;
+        }
+    }
+    const int team = C::kTeams > 1 ? warp / ways : 0, first_warp = team * ways, in_team = warp - first_warp;
+    const int tt = threadIdx.x - first_warp * 32, team_threads = ways * 32;
+    auto team_sync = [&]() {
+        if (C::kTeams > 1 && ways == 1)
+            __syncwarp();
+        else if (C::kTeams > 1 && ways == 2 && team == 0)
+            asm volatile("bar.sync 1, 64;" ::: "memory");  // (numbers the compiler knows: an SM has 64 barriers)
+        else if (C::kTeams > 1 && ways == 2)
+            asm volatile("bar.sync 2, 64;" ::: "memory");
+        else
+            __syncthreads();
+    };
+    float *const sm_lse = sm_lses[team], *const sm_back = sm_backs[team], *const sm_prior = sm_priors[team], *const sm_top = sm_tops[team];
+    uint2 *const sm_where = sm_wheres[team];
+    int *const sm_pos = sm_poss[team];
+    uint4(&sm_q)[kN][kM / 2][32] = sm_qs[team];
+    const int64_t teams = (int64_t)gridDim.x * (C::kTeams > 1 ? kWarps / ways : 1);
+    const int64_t want = !w.cuts() ? w.total : (w.total + kMinUnits - 1) / kMinUnits;
+    if (!w.take_share((int64_t)team * gridDim.x + blockIdx.x, min(teams, want))) {
         if (kMode == kOwn) pdl_wait_prior();  // (a kernel behind this one counts on the ones ahead having ended)
         return;
     }
@@ -464,7 +516,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         const int rows = min(R, sh.n * G - tile * R);
 
         // ---- this warp's steps: tokens tok0 + 16 (warp + 4 k)
-        const int nk = max(0, (tok1 - tok0 + kStep - 1) / kStep - warp + kWarps - 1) / kWarps;
+        const int nk = max(0, (tok1 - tok0 + kStep - 1) / kStep - in_team + ways - 1) / ways;
         int page_cache = 0;  // lane i: the page of step (k & ~31) + i
         const int32_t *table = kv_table<kMode>(b, share, seq);
         int fill_k = 0, fill_stage = 0;  // the next step to copy and its stage
@@ -474,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 if ((k & 31) == 0) {
                     page_cache = 0;
                     if (k + lane < nk) {
-                        page_cache = table[(tok0 + kStep * (warp + kWarps * (k + lane))) >> kv.page_shift];
+                        page_cache = table[(tok0 + kStep * (in_team + ways * (k + lane))) >> kv.page_shift];
                         if (page_cache < 0 || page_cache >= kv.num_pages) {
                             kv_flag_range(kv.err);
                             page_cache = 0;
@@ -482,7 +534,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                     }
                 }
                 const int page = __shfl_sync(0xffffffffu, page_cache, k & 31);
-                const int tok = tok0 + kStep * (warp + kWarps * k);
+                const int tok = tok0 + kStep * (in_team + ways * k);
                 const int64_t row = (((int64_t)page * kv.H + head) << kv.page_shift) +
                                     (tok & ((1 << kv.page_shift) - 1));
                 const uint32_t st = fill_stage * C::kStage;
@@ -523,9 +575,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         // Q as the 8-column operand, a tile a warp: lane (g, c) holds row g of it; its dims of MMA i
         // are those its K words hold (8-bit: 64-dim blocks of 16 dims a lane; bf16: 32-dim blocks of 8)
         static_assert(kN <= kWarps, "a tile a warp");
-        if (warp < kN) {
-            const int row = tile * R + 8 * warp + g;
-            const bool on = 8 * warp + g < rows;
+        for (int t = in_team; t < kN; t += ways) {
+            const int row = tile * R + 8 * t + g;
+            const bool on = 8 * t + g < rows;
             const int i = row / G;
             const uint16_t *src = a.Q + (int64_t)(sh.row0 + i) * a.q_stride + (int64_t)(head * G + row % G) * D;
             constexpr int kBlock = kInt8 ? 64 : 32, kLane = kBlock / 4;
@@ -561,20 +613,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 for (int x = 0; x < kM / 2; ++x) q[x] = make_uint4(f16(q[x].x), f16(q[x].y), f16(q[x].z), f16(q[x].w));
             }
 #pragma unroll
-            for (int x = 0; x < kM / 2; ++x) sm_q[warp][x][lane] = q[x];
+            for (int x = 0; x < kM / 2; ++x) sm_q[t][x][lane] = q[x];
             if (c == 0) {
-                sm_back[8 * warp + g] = back * plan.scale_log2;  // to units of log2
+                sm_back[8 * t + g] = back * plan.scale_log2;  // to units of log2
                 // rows beyond the tile: any position, not written
-                sm_pos[8 * warp + g] = on && kMode != kPrefix ? sh.L - sh.n + i : sh.L - 1;
+                sm_pos[8 * t + g] = on && kMode != kPrefix ? sh.L - sh.n + i : sh.L - 1;
             }
         }
-        __syncthreads();
+        team_sync();
         const int pos_min = kMode == kPrefix ? sh.L - 1 : sh.L - sh.n + tile * R / G;
         const int pos_max = kMode == kPrefix ? sh.L - 1 : sh.L - sh.n + (tile * R + rows - 1) / G;
         // one tile where the item's rows fit it (40 requests of 7 heads, 37 of them of one token: 99 us
         // with all tiles, 93 with one)
         auto run = [&](auto tiles) {
-            run_steps<D, kInt8, kN, decltype(tiles)::value>(issue, v_row, nk, tok0 + kStep * warp, tok1,
+            run_steps<D, kInt8, kN, decltype(tiles)::value, kMode>(issue, v_row, nk, tok0 + kStep * in_team, ways, tok1,
                                                             kMode == kPlain ? a.window : 0, rows,
                                                             pos_min, pos_max, base, ring, sm_q, sm_back, sm_pos,
                                                             sm_m[warp], sm_l[warp]);
@@ -584,7 +636,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         else
             run(std::integral_constant<int, kN>());
         if (kMode == kOwn) pdl_wait_prior();  // the prefix's O and lse
-        __syncthreads();
+        team_sync();
         const bool whole = w.whole();
         // row r of the item in [T][Hq] arrays
         auto out_row = [&](int r) {
@@ -596,11 +648,33 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         auto finish = [&](int r, float M, float sum) {
             float own = 1.0f;
             if constexpr (kMode == kOwn) {
-                const float P = sh.lo > 0 && r < rows ? share.lse2[out_row(r)] : -INFINITY;
+                // the prefix: one O with its lse, or pieces with a maximum and a sum each
+                float P = -INFINITY, l1 = 1.0f;
+                uint2 at = make_uint2(kJoined, 0);
+                if (sh.lo > 0 && r < rows) {
+                    if (share.pieces) at = share.where[out_row(r)];
+                    if (at.x == kJoined) {
+                        P = share.lse2[out_row(r)];
+                    } else {
+                        const int c0 = at.x & 0xFFFF, n = (int)(at.x >> 16) - c0 + 1;
+                        const float2 *const ml = reinterpret_cast<const float2 *>(share.part + share.ml_at) + at.y;
+#pragma unroll 8
+                        for (int x = 0; x < n; ++x) P = fmaxf(P, ml[kv_slot(c0, x) * kShareRows].x);
+                        const float ref = P == -INFINITY ? 0.0f : P;
+                        l1 = 0.0f;
+#pragma unroll 8
+                        for (int x = 0; x < n; ++x) {
+                            const float2 e = ml[kv_slot(c0, x) * kShareRows];
+                            l1 += fast_exp2(e.x - ref) * e.y;
+                        }
+                    }
+                }
+                sm_where[r] = at;
+                sm_top[r] = P == -INFINITY ? 0.0f : P;
                 const float top = fmaxf(M, P), ref = top == -INFINITY ? 0.0f : top;
                 const float prior = fast_exp2(P - ref);
                 own = fast_exp2(M - ref);
-                sum = fmaf(sum, own, prior);
+                sum = fmaf(sum, own, prior * l1);
                 M = top;
                 sm_prior[r] = sum == 0.0f ? 0.0f : prior / sum;
             }
@@ -618,13 +692,25 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 if (d == 0) share.lse2[t * a.Hq + h] = sm_lse[r];
             } else {
                 if constexpr (kMode == kOwn) {
-                    if (sh.lo > 0) {
-                        const float4 v = *reinterpret_cast<const float4 *>(share.O + (t * a.Hq + h) * D + d);
-                        const float wt = sm_prior[r];
+                    auto add = [&](float wt, const float *from) {
+                        const float4 v = *reinterpret_cast<const float4 *>(from);
                         acc.x = add_piece<kInt8>(wt, v.x, acc.x);
                         acc.y = add_piece<kInt8>(wt, v.y, acc.y);
                         acc.z = add_piece<kInt8>(wt, v.z, acc.z);
                         acc.w = add_piece<kInt8>(wt, v.w, acc.w);
+                    };
+                    const uint2 at = sm_where[r];
+                    if (sh.lo > 0 && at.x == kJoined) {
+                        add(sm_prior[r], share.O + (t * a.Hq + h) * D + d);
+                    } else if (sh.lo > 0) {
+                        const int c0 = at.x & 0xFFFF, n = (int)(at.x >> 16) - c0 + 1;
+                        const float2 *const ml = reinterpret_cast<const float2 *>(share.part + share.ml_at) + at.y;
+                        const float *const from = share.part + (int64_t)at.y * D + d;
+#pragma unroll 4
+                        for (int x = 0; x < n; ++x) {
+                            const int sl = kv_slot(c0, x);
+                            add(sm_prior[r] * fast_exp2(ml[sl * kShareRows].x - sm_top[r]), from + (int64_t)sl * kShareRows * D);
+                        }
                     }
                 }
                 *reinterpret_cast<uint2 *>(a.O + t * a.o_stride + (int64_t)h * D + d) =
@@ -635,36 +721,40 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
         const int slot = 2 * blockIdx.x + (w.first() ? 1 : 0);
         float *part_o = plan.part + (int64_t)slot * R * D;
         float *part_ml = plan.part + (int64_t)2 * gridDim.x * R * D + slot * 2 * R;
-        if (threadIdx.x < R) {
-            const int r = threadIdx.x;
+        if (tt < R) {
+            const int r = tt;
             float M = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int x = 0; x < kWarps; ++x) M = fmaxf(M, sm_m[x][r]);
+            for (int x = 0; x < kWarps; ++x)
+                if (x < ways) M = fmaxf(M, sm_m[first_warp + x][r]);
             const float Mx = M == -INFINITY ? 0.0f : M;
 #pragma unroll
             for (int x = 0; x < kWarps; ++x) {
-                const float wt = fast_exp2(sm_m[x][r] - Mx);
-                sm_w[x][r] = wt;
-                sum += wt * sm_l[x][r];
+                if (x >= ways) break;
+                const float wt = fast_exp2(sm_m[first_warp + x][r] - Mx);
+                sm_w[first_warp + x][r] = wt;
+                sum += wt * sm_l[first_warp + x][r];
             }
             if (whole) {
                 const float inv = finish(r, M, sum);
 #pragma unroll
-                for (int x = 0; x < kWarps; ++x) sm_w[x][r] *= inv;
+                for (int x = 0; x < kWarps; ++x)
+                    if (x < ways) sm_w[first_warp + x][r] *= inv;
             } else {
                 part_ml[2 * r] = M;
                 part_ml[2 * r + 1] = sum;
             }
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kWarps * 32) {
+        team_sync();
+        for (int i = tt; i < rows * (D / 4); i += team_threads) {
             const int r = i / (D / 4), d = (i % (D / 4)) * 4;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int x = 0; x < kWarps; ++x) {
+                if (x >= ways) break;
                 const float4 v = *reinterpret_cast<const float4 *>(
-                    reinterpret_cast<const float *>(smem + x * C::kRing) + r * C::kLdO + d);
-                const float wt = sm_w[x][r];
+                    reinterpret_cast<const float *>(smem + (first_warp + x) * C::kRing) + r * C::kLdO + d);
+                const float wt = sm_w[first_warp + x][r];
                 acc.x = add_piece<kInt8>(wt, v.x, acc.x);
                 acc.y = add_piece<kInt8>(wt, v.y, acc.y);
                 acc.z = add_piece<kInt8>(wt, v.z, acc.z);
@@ -739,7 +829,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN>::kCtas)
                 }
             }
         }
-        __syncthreads();  // the rings and the small arrays are free again
+        team_sync();  // the rings and the small arrays are free again
     }
 }
 
@@ -760,9 +850,9 @@ cudaError_t launch_kv_decode_mode(const KvDev &kv, bool int8, const KvBatchDev &
     auto pick = [&](auto d, auto i8) {
         constexpr int D = decltype(d)::value;
         constexpr bool kInt8 = decltype(i8)::value;
-        if (rows <= 8) return launch(Cfg<D, kInt8, 1>(), kv_decode_kernel<D, kInt8, 1, kMode>);
-        if (rows <= 16) return launch(Cfg<D, kInt8, 2>(), kv_decode_kernel<D, kInt8, 2, kMode>);
-        return launch(Cfg<D, kInt8, 3>(), kv_decode_kernel<D, kInt8, 3, kMode>);
+        if (rows <= 8) return launch(Cfg<D, kInt8, 1, kMode>(), kv_decode_kernel<D, kInt8, 1, kMode>);
+        if (rows <= 16) return launch(Cfg<D, kInt8, 2, kMode>(), kv_decode_kernel<D, kInt8, 2, kMode>);
+        return launch(Cfg<D, kInt8, 3, kMode>(), kv_decode_kernel<D, kInt8, 3, kMode>);
     };
     using std::integral_constant;
     if (kv.D == 128)

@@ -81,6 +81,10 @@ __device__ __forceinline__ int64_t kv_row(const KvDev &kv, const KvBatchDev &b, 
     return (((int64_t)page * kv.H) << kv.page_shift) + (pos & ((1 << kv.page_shift) - 1));
 }
 
+// The scratch slot of an item's x-th piece, the first of which CTA c0 has: a CTA's two slots are its last segment's
+// and its first one's.
+__device__ __forceinline__ int kv_slot(int c0, int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); }
+
 // The page table of sequence (kPrefix: group) `seq`.
 template <KvMode kMode>
 __device__ __forceinline__ const int32_t *kv_table(const KvBatchDev &b, const KvShareDev &share, int seq)
@@ -118,6 +122,8 @@ struct KvWork {
     int64_t tile0 = 0;           // first unit of the tile's first head
     int seq = -1, tile = 0, tiles = 0, nu = 0, head = 0, lo = 0, hi = 0;
     int j0 = 0, j1 = 0;          // units of tokens: [j0, j1) of the item's nu - kHead
+    int64_t items = 0;           // kOwn: items, and the most units of tokens of one
+    int most = 0;
     KvSeq sh{0, 0, 0, 0};
 
     __device__ __forceinline__ KvWork(const KvDev &kv_, const KvBatchDev &b_, const KvAttn &a_, const KvShareDev &share_,
@@ -131,6 +137,18 @@ struct KvWork {
             total += v;
         }
         total = sum(total);
+        if (kMode == kOwn) {
+            items = sum(items) * kv.H;
+            most = __reduce_max_sync(0xffffffffu, most) - kHead;
+        }
+    }
+
+    // From now on shares are equal numbers of items, none of which is cut (kOwn).
+    __device__ __forceinline__ void by_items()
+    {
+        by_items_ = true;
+        total = items;
+        first_ = units_of_32(0);
     }
 
     // Take share c of n; false: it is empty.
@@ -170,6 +188,12 @@ struct KvWork {
     // The share's next segment that has tokens' units; false at its end.
     __device__ __forceinline__ bool next()
     {
+        if (kMode == kOwn && by_items_) {
+            if (!next_any()) return false;
+            j0 = 0;
+            j1 = units_of(sh, tile) - kHead;
+            return true;
+        }
         do {
             if (!next_any()) return false;
             j0 = max(0, (int)(u - item0) - kHead);
@@ -179,7 +203,8 @@ struct KvWork {
     }
 
     __device__ __forceinline__ bool first() const { return j0 == 0; }
-    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nu - kHead; }
+    __device__ __forceinline__ bool cuts() const { return !(kMode == kOwn && by_items_); }  // items into pieces
+    __device__ __forceinline__ bool whole() const { return !cuts() || (j0 == 0 && j1 == nu - kHead); }
     // The CTAs that have the item's first and last tokens' units (total >= grid: no share is
     // empty).
     __device__ __forceinline__ int first_cta() const { return cta_of(item0 + kHead); }
@@ -187,6 +212,7 @@ struct KvWork {
 
 private:
     int64_t first_ = 0;  // the units of sequence `lane`
+    bool by_items_ = false;
 
     __device__ __forceinline__ int cta_of(int64_t x) const { return (int)(((x + 1) * grid - 1) / total); }
     __device__ __forceinline__ bool next_any()
@@ -242,18 +268,26 @@ private:
     }
     __device__ __forceinline__ int units(const KvSeq &s, int t) const
     {
+        return kMode == kOwn && by_items_ ? 1 : units_of(s, t);
+    }
+    __device__ __forceinline__ int units_of(const KvSeq &s, int t) const
+    {
         int l, h;
         range(s, t, &l, &h);
         return kHead + max(1, (h - l + kUnit - 1) / kUnit);
     }
     // Units of sequence s0 + lane (0 past the last). Few tiles: a lane counts its own; a sequence
     // of many is counted by all lanes together.
-    __device__ __forceinline__ int64_t units_of_32(int s0) const
+    __device__ __forceinline__ int64_t units_of_32(int s0)
     {
         KvSeq s{0, 0, 0, 0};
         if (s0 + lane < b.n_seqs) s = seq_at(s0 + lane);
         const int n = tiles_of(s);
         int64_t v = 0;
+        if (kMode == kOwn && !by_items_ && n > 0) {  // (later tiles see more tokens)
+            items += n;
+            most = max(most, units(s, n - 1));
+        }
         if (n <= 8)
             for (int t = 0; t < n; ++t) v += units(s, t);
         for (uint32_t todo = __ballot_sync(0xffffffffu, n > 8); todo; todo &= todo - 1) {

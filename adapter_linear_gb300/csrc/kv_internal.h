@@ -63,8 +63,11 @@ struct KvAttn {
 //   kOwn: sequence b starts at token lo[b] (a multiple of the page's tokens); where that is above 0 its rows
 //     are joined with what the first mode left there.
 enum KvMode { kPlain = 0, kPrefix = 1, kOwn = 2 };
-//     The tcgen05 kernel leaves the pieces of an item that several CTAs share in `part` (row major), and what
-//     they are pieces of in items[first CTA]; a kernel behind it joins them.
+//     The tcgen05 kernel leaves the pieces of an item that several CTAs share in `part` (row major). What they
+//     are pieces of is in items[first CTA], for a kernel that joins them, and in where[row], for one that
+//     reads the pieces themselves (pieces).
+constexpr int kShareRows = 256;  // rows of a slot of `part`
+constexpr uint32_t kJoined = 0xFFFFFFFFu;
 struct KvShareItem {
     int last, row0, head, rows;  // last CTA with a piece (-1: nothing to join), the first token's row, kv head, rows
     int first_row, pad[3];       // the first row's number among the group's rows
@@ -72,6 +75,10 @@ struct KvShareItem {
 struct KvShareDev {
     float *part;         // [2 grid][256][D], then (m, l) [2 grid][256][2]
     KvShareItem *items;  // [grid]
+    uint2 *where;        // [T][Hq] last and first CTA with a piece of the row, 16 bits each, and its row in their blocks;
+                         // x == kJoined: none, O and lse2 are there
+    bool pieces;         // read the pieces; else all are joined
+    int64_t ml_at;       // where in part (m, l) begin
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]
     float *O;      // [T][Hq][D]

@@ -52,7 +52,7 @@
 namespace lora {
 namespace {
 
-constexpr int kBlockRows = 256, kTileRows = 128, kKeys = 128, kHalf = 64, kPart = 32;
+constexpr int kBlockRows = kShareRows, kTileRows = 128, kKeys = 128, kHalf = 64, kPart = 32;
 constexpr int kSoftWarps = 8, kLoadWarps = 4;
 constexpr int kThreads = (kSoftWarps + kLoadWarps + 4) * 32;  // two MMA warps, one that hands out the work, one idle
 // Registers a thread of the softmax warps, the loading warps and the MMA warps' group: a block of
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t out_t = w->row0 + i;
             const int h = w->head * G + (on ? row % G : 0);
             uint16_t *const dst = a.O + out_t * a.o_stride + (int64_t)h * D;
-            const int first_own = w->first;
+            const int first_own = w->first, w_tile = w->tile;
             const int64_t shared_row = out_t * a.Hq + h;  // of the prefix's arrays
             // the prefix's lse, kOwn
             const float P = kMode == kOwn && on && first_own > 0 ? share.lse2[shared_row] : -INFINITY;
@@ -773,9 +773,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before_sync();
             if (whole) {
-                if (on) put_lse(m, l);
+                if (on) {
+                    put_lse(m, l);
+                    if constexpr (kMode == kPrefix) share.where[shared_row].x = kJoined;
+                }
             } else if constexpr (kMode == kPrefix) {
-                if (on) part_ml[slot * kBlockRows] = make_float2(m, l);
+                if (on) {
+                    part_ml[slot * kBlockRows] = make_float2(m, l);
+                    if (slot & 1)  // the first piece
+                        share.where[shared_row] = make_uint2((uint32_t)c1 << 16 | (uint32_t)c0, row - w_tile * kBlockRows);
+                }
             } else {
                 if (on) part_ml[slot * kBlockRows] = make_float2(m, l);
                 __threadfence();

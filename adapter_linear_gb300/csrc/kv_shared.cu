@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_share_join_kernel(KvAttn a, K
     for (int x = 0; x < warp; ++x) n += sums[x];
     units_to[threadIdx.x] = n;
     __syncthreads();
-    const float2 *const ml = reinterpret_cast<const float2 *>(share.part + (int64_t)2 * grid * kBlockRows * D);
+    const float2 *const ml = reinterpret_cast<const float2 *>(share.part + share.ml_at);
     for (int u = blockIdx.x; u < units_to[kMaxPieces - 1]; u += gridDim.x) {
         int c0 = 0;  // the first item whose units go beyond u
 #pragma unroll
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_share_join_kernel(KvAttn a, K
         const KvShareItem item = share.items[c0];
         const int r0 = (u - (c0 > 0 ? units_to[c0 - 1] : 0)) * kJoinRows, rows = min(kJoinRows, item.rows - r0);
         const int pieces = item.last - c0 + 1;
-        auto slot = [&](int x) { return 2 * (c0 + x) + (x == 0 ? 1 : 0); };
+        auto slot = [&](int x) { return kv_slot(c0, x); };
         auto out_row = [&](int r) {
             const int row = item.first_row + r0 + r;
             return (int64_t)(item.row0 + row / a.G) * a.Hq + item.head * a.G + row % a.G;

@@ -229,7 +229,7 @@ typedef struct lora_kv_groups {
 } lora_kv_groups;
 
 /* As lora_kv_reserve, for lora_kv_attention_shared: the first call of a size allocates what it needs
- * (40 MB, T * n_heads * (D + 1) floats and lora_kv_reserve's; what a larger call replaces is freed with the handle). */
+ * (50 MB, T * n_heads * (D + 3) floats and lora_kv_reserve's; what a larger call replaces is freed with the handle). */
 lora_status lora_kv_reserve_shared(lora_kv_t kv, int max_tokens, int n_heads, int max_seqs);
 
 /*
