@@ -162,7 +162,7 @@ class KvCache:
     def _rows(self, x, heads: int, batch: KvBatch, what: str) -> int:
         """The token stride of x, a bf16 [T, heads, head_dim] tensor with contiguous heads."""
         T, D = batch.T, self.head_dim
-        if x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape != (T, heads, D):
+        if x.dtype is not torch.bfloat16 or x.shape != (T, heads, D):
             raise LoraError(LORA_ERR_SHAPE, f"{what}: bfloat16 [{T}, {heads}, {D}] expected")
         if x.get_device() != self._device or batch.device != self._device:
             raise LoraError(LORA_ERR_ARG, f"{what}: the tensors of a call are on the cache's GPU")

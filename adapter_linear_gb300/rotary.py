@@ -70,55 +70,53 @@ class Rotary:
         Heads of a token are contiguous, tokens may be strided. out: tensors for the results (those of
         `tensors` themselves: in place); by default new ones, returned as a tuple. inverse: the other
         way round (the gradient). Runs on the current stream or on `stream`."""
-        xs = tuple(tensors)
-        n = len(xs)
-        if not 1 <= n <= LORA_ROTARY_MAX_TENSORS:
-            raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: one to four tensors")
-        if positions.dtype != torch.int32 or positions.dim() != 1 or not positions.is_contiguous():
+        if positions.dtype is not torch.int32 or positions.dim() != 1 or not positions.is_contiguous():
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: positions are contiguous int32 [T]")
-        T, D, device = positions.shape[0], xs[0].shape[-1], positions.get_device()
+        xs = tuple(tensors)
+        n, device, T = len(xs), positions.get_device(), positions.shape[0]
+        if not 1 <= n <= LORA_ROTARY_MAX_TENSORS or (out is not None and len(out) != n):
+            raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: one to four tensors, as many results")
+        D = xs[0].shape[-1]
         given = [self._rows(x, None, T, D, device) for x in xs]
         if device < 0 or device != torch._C._cuda_getDevice():
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the tensors are on the current GPU")
-        handle = current = torch._C._cuda_getCurrentRawStream(device)
-        other = None
+        handle, other = torch._C._cuda_getCurrentRawStream(device), None
         if stream is not None:
-            handle = stream if isinstance(stream, int) else stream.cuda_stream
-            if handle != current:
-                other = torch.cuda.ExternalStream(stream, xs[0].device) if isinstance(stream, int) else stream
-        if out is None:
-            if other is None:
-                out = tuple([torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs])
+            where = stream if isinstance(stream, int) else stream.cuda_stream
+            if where != handle:
+                other = torch.cuda.ExternalStream(stream, positions.device) if isinstance(stream, int) else stream
+            handle = where
+        fields, results = [], []
+        for x, (at, stride, heads) in zip(xs, given):
+            if out is not None:
+                y = out[len(results)]
+                to, to_stride, _ = self._rows(y, heads, T, D, device)
             else:
-                with torch.cuda.stream(other):  # they belong to the stream that writes them
-                    out = tuple([torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs])
-            results = [(y.data_ptr(), h * D, h) for y, (_, _, h) in zip(out, given)]
-        else:
-            out = tuple(out)
-            if len(out) != n:
-                raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: as many results as tensors")
-            results = [self._rows(y, h, T, D, device) for y, (_, _, h) in zip(out, given)]
-        fields = []
-        for (a, sa, h), (b, sb, _) in zip(given, results):
-            fields += (a, b, sa, sb, h, 0)
+                if other is None:
+                    y = torch.empty_like(x, memory_format=torch.contiguous_format)
+                else:
+                    with torch.cuda.stream(other):  # it belongs to the stream that writes it
+                        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+                to, to_stride = y.data_ptr(), heads * D
+            results.append(y)
+            fields += (at, to, stride, to_stride, heads, 0)
         if other is not None:
-            for t in xs + out + (positions,):
+            for t in (*xs, *results, positions):
                 t.record_stream(other)
         _check(self._lib.lora_rotary_apply(self.ref, n, _TENSORS[n].pack(*fields), D, positions.data_ptr(), T, inverse,
                                            handle), "lora_rotary_apply")
-        return out
+        return tuple(results)
 
     @staticmethod
     def _rows(x, heads, T, D, device):
         """Address, token stride and heads of x, a bf16 [T, heads, D] tensor with contiguous heads."""
-        if x.dim() != 3 or x.dtype != torch.bfloat16:
+        if x.dim() != 3 or x.dtype is not torch.bfloat16:
             raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, heads, {D}] expected")
-        t, h, d = x.shape
+        (t, h, d), (st, sh, sd) = x.shape, x.stride()
         if t != T or d != D or (heads is not None and h != heads):
             raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, {heads or 'heads'}, {D}] expected")
         if x.get_device() != device:
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the tensors of a call are on one GPU")
-        st, sh, sd = x.stride()
         if (sd != 1 and D > 1) or (sh != D and h > 1):
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the heads of a token must be contiguous")
         return x.data_ptr(), st if T > 1 else h * D, h
