@@ -8,6 +8,7 @@
 
 #include "kv_pages_state.h"
 #include "kv_state.h"
+#include "launch_stream.h"
 
 namespace cg = cooperative_groups;
 using namespace lora;
@@ -634,14 +635,12 @@ namespace lora {
 cudaError_t launch_kv_copy(const KvDev &kv, bool int8, const int32_t *src, const int32_t *dst, const int32_t *rows,
                            const int32_t *n_dev, int n, int num_sms, cudaStream_t stream)
 {
-    const cudaError_t e = ensure_smem_attr((const void *)kv_copy_kernel, 0);
-    if (e != cudaSuccess) return e;
     const int row_bytes = kv.D * (int8 ? 1 : 2);
     const int64_t slices = (((int64_t)row_bytes << kv.page_shift) + kSlice - 1) / kSlice;
     const int64_t units = (int64_t)n * 2 * kv.H * slices;
     const int64_t ctas = std::min<int64_t>((units + 7) / 8, 8 * (int64_t)num_sms);
-    kv_copy_kernel<<<(unsigned)ctas, 256, 0, stream>>>(kv, row_bytes, CopyList{src, dst, rows, n_dev, n});
-    return cudaGetLastError();
+    return launch_stream(true, kv_copy_kernel, (unsigned)ctas, 256, stream, kv, row_bytes,
+                         CopyList{src, dst, rows, n_dev, n});
 }
 
 // The moves of the last update or compaction of `p`.

@@ -1,14 +1,14 @@
 // kv_rotary.cu -- the paged cache's write with rotary positions on the way: K rotated (and quantised) into
 // its pages, V as it is, Q rotated beside it, in one pass over the three.
-#include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include "kv_device.cuh"
+#include "launch_stream.h"
 #include "rotary_device.cuh"
 
 namespace lora {
 namespace {
-
-constexpr int kBatch = 4;  // blocks of rows loaded before any is stored
 
 // Scale and codes of the 16 fp32 values of this lane; the row's kLanes lanes take part. As the write of bf16
 // rows quantises (kv_cache.cu), of which a bf16 x is a case: y = x (1 / s) is rounded to a multiple of 2^-11
@@ -45,97 +45,125 @@ __device__ __forceinline__ uint4 quantise16f(const float (&x)[16], uint16_t *sca
     return make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// A row is one head of one token: Hq of Q, H of K, H of V. D / 16 lanes hold one. A warp takes `blocks` blocks
-// of 512 / D rows of one token, which is looked up once and whose angles (8 a lane) serve all of them.
-template <int D, bool kInt8>
-__global__ void __launch_bounds__(256) kv_write_rotary_kernel(KvDev kv, KvBatchDev b, const __grid_constant__ RotaryDev rot,
-                                                              KvRotaryArgs a, int parts, int blocks)
+constexpr int kBatch = 4;  // blocks loaded before any is stored
+
+// A row is one head of one token: Hq of Q, H of K, H of V. D / 16 lanes hold one, a block is the 512 / D rows of one
+// of them that a warp holds at a time. A warp takes a chunk of consecutive tokens, or a part of one token's
+// blocks; the tokens are looked up 32 at a time, a lane a token, and a lane's eight angles serve all its
+// rows of a token.
+template <int D, bool kInt8, bool kHalf>
+__global__ void __launch_bounds__(RotaryGrid::kWarps * 32, RotaryGrid::kCtas)
+    kv_write_rotary_kernel(KvDev kv, KvBatchDev b, const __grid_constant__ RotaryDev rot, KvRotaryArgs a, int parts)
 {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes;
     const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t64 = w / parts;
-    if (t64 >= b.T) return;
-    const int t = (int)t64;
     const int sub = lane / kLanes, c = lane % kLanes;
-    const int rows = a.Hq + 2 * kv.H;
-    const int first = (int)(w - t64 * parts) * blocks * kRows, last = min(rows, first + blocks * kRows);
+    const int q_blocks = (a.Hq + kRows - 1) / kRows, h_blocks = (kv.H + kRows - 1) / kRows, all = q_blocks + 2 * h_blocks;
+    const RotaryShare me(b.T, all, parts);
+    const int b0 = me.b0, b1 = me.b1;
     int d0, d1;
-    rotary_runs(rot, c, &d0, &d1);
-
-    // rows of the tensors, from this lane's in the block that starts at r0
-    uint4 x[kBatch][2];
-    auto load = [&](int r0) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kRows + sub;
-            x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
-            if (r >= last) continue;
-            const uint16_t *src = r < a.Hq          ? a.Q + (int64_t)t * a.q_stride + r * D
-                                  : r < a.Hq + kv.H ? a.K + (int64_t)t * a.k_stride + (r - a.Hq) * D
-                                                    : a.V + (int64_t)t * a.v_stride + (r - a.Hq - kv.H) * D;
-            x[i][0] = *reinterpret_cast<const uint4 *>(src + d0);
-            x[i][1] = *reinterpret_cast<const uint4 *>(src + d1);
-        }
-    };
-    load(first);  // on their way while the token is looked up
-
-    // the token's sequence, position and cache row (-1: none)
-    int seq = kv_find_seq(b, t, lane);
-    KvSeq s{0, 0, 0};
-    bool there = seq >= 0;
-    if (there) {
-        for (;; ++seq) {  // (among bad starts the search may stop before t's sequence)
-            if (seq >= b.n_seqs) {
-                there = false;
-                break;
-            }
-            s = kv_seq(b, kv.page_shift, seq, kv.err);
-            if (t < s.row0) there = false;
-            if (!there || t - s.row0 < s.n) break;
-        }
-    }
-    if (!there) return;  // padding, or a bad sequence
-    const int pos = s.L - s.n + (t - s.row0);
-    const int64_t cache_row = pos >= 0 && last > a.Hq ? kv_row(kv, b, seq, pos) : -1;
+    rotary_runs(rot, D, c, &d0, &d1);
     const bool turns = 16 * c < rot.dim;
-    Turn8 turn;
-    if (turns) turn = rotary_turn(rot, c, pos, false);
 
-    for (int r0 = first; r0 < last; r0 += kBatch * kRows) {
-        if (r0 > first) load(r0);
+    // Of the warp's token number 32 y + lane: its position, and its cache row for head 0 (-1: none); kNowhere: padding
+    // behind the last sequence, or a bad sequence.
+    constexpr int kNowhere = INT_MIN;
+    int my_pos = kNowhere;
+    int64_t my_row = -1;
+    auto look_up = [&](int first) {
+        int seq = max(0, kv_find_seq(b, first, lane));
+        my_pos = kNowhere;
+        my_row = -1;
+        const int t = first + lane * me.step;
+        if (t >= me.t1) return;
+        KvSeq s;
+        for (;; ++seq) {  // (a chunk may end in a later sequence; among bad starts the search may stop early)
+            if (seq >= b.n_seqs) return;
+            s = kv_seq(b, kv.page_shift, seq, kv.err);
+            if (t < s.row0) return;
+            if (t - s.row0 < s.n) break;
+        }
+        my_pos = s.L - s.n + (t - s.row0);
+        if (my_pos >= 0 && b1 > q_blocks) my_row = kv_row(kv, b, seq, my_pos);
+    };
+
+#pragma unroll 1
+    for (int t = me.t0, i = 0; t < me.t1; t += me.step, ++i) {
+        if ((i & 31) == 0) look_up(t);
+        const int pos = __shfl_sync(0xffffffffu, my_pos, i & 31);
+        const int64_t cache_row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        if (pos == kNowhere) continue;
+        Turn8 turn;
+        if (turns) turn = rotary_turn<kHalf>(rot, c, pos, false);
+
+        // Q's blocks of this warp
+        {
+            const uint16_t *const src = a.Q + (int64_t)t * a.q_stride + sub * D;
+            uint16_t *const dst = a.Q_out + (int64_t)t * a.qo_stride + sub * D;
+            const int end = min(b1 * kRows, a.Hq) - sub;
+#pragma unroll 1
+            for (int r0 = b0 * kRows; r0 < end; r0 += kBatch * kRows) {
+                uint4 v[kBatch][2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * kRows + sub;
-            if (r0 + i * kRows >= last) break;
-            float f[16];
-            unpack8(x[i][0], f);
-            unpack8(x[i][1], f + 8);
-            if (turns && r < a.Hq + kv.H) rotary_pairs(rot.half, turn, f);
-            const bool is_v = r >= a.Hq + kv.H;
-            const int64_t row = cache_row + ((int64_t)(r - a.Hq - (is_v ? kv.H : 0)) << kv.page_shift);
-            if constexpr (kInt8) {
-                if (r0 + (i + 1) * kRows > a.Hq) {  // some of the block's rows go to the cache
+                for (int i = 0; i < kBatch; ++i)
+                    if (r0 + i * kRows < end) {
+                        v[i][0] = *reinterpret_cast<const uint4 *>(src + (r0 + i * kRows) * D + d0);
+                        v[i][1] = *reinterpret_cast<const uint4 *>(src + (r0 + i * kRows) * D + d1);
+                    }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (r0 + i * kRows < end) {
+                        if (turns) {
+                            float f[16];
+                            unpack16(v[i], f);
+                            rotary_pairs<kHalf>(turn, f);
+                            v[i][0] = pack8(f);
+                            v[i][1] = pack8(f + 8);
+                        }
+                        if (pos < 0) v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(dst + (r0 + i * kRows) * D + d0) = v[i][0];
+                        *reinterpret_cast<uint4 *>(dst + (r0 + i * kRows) * D + d1) = v[i][1];
+                    }
+            }
+        }
+        // K's and V's
+        if (cache_row < 0) continue;
+#pragma unroll 1
+        for (int blk = max(b0, q_blocks); blk < b1; blk += kBatch) {
+            uint4 v[kBatch][2];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+                const bool is_v = blk + i - q_blocks >= h_blocks;
+                const int h = (blk + i - q_blocks - (is_v ? h_blocks : 0)) * kRows + sub;
+                if (blk + i >= b1 || h >= kv.H) continue;
+                const uint16_t *const src = (is_v ? a.V + (int64_t)t * a.v_stride : a.K + (int64_t)t * a.k_stride) + h * D;
+                v[i][0] = *reinterpret_cast<const uint4 *>(src + d0);
+                v[i][1] = *reinterpret_cast<const uint4 *>(src + d1);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (blk + i >= b1) break;
+                const bool is_v = blk + i - q_blocks >= h_blocks;
+                const int h = (blk + i - q_blocks - (is_v ? h_blocks : 0)) * kRows + sub;
+                const int64_t row = cache_row + ((int64_t)h << kv.page_shift);
+                float f[16];
+                unpack16(v[i], f);
+                if (turns && !is_v) rotary_pairs<kHalf>(turn, f);
+                if constexpr (kInt8) {
                     uint16_t scale;
                     const uint4 q = quantise16f<kLanes>(f, &scale);
-                    if (r >= a.Hq && r < last && cache_row >= 0) {
+                    if (h < kv.H) {
                         uint8_t *const to = static_cast<uint8_t *>(is_v ? kv.v : kv.k) + row * D;
                         *reinterpret_cast<uint2 *>(to + d0) = make_uint2(q.x, q.y);
                         *reinterpret_cast<uint2 *>(to + d1) = make_uint2(q.z, q.w);
                         if (c == 0) (is_v ? kv.vs : kv.ks)[row] = scale;
                     }
+                } else if (h < kv.H) {
+                    uint16_t *const to = static_cast<uint16_t *>(is_v ? kv.v : kv.k) + row * D;
+                    *reinterpret_cast<uint4 *>(to + d0) = pack8(f);
+                    *reinterpret_cast<uint4 *>(to + d1) = pack8(f + 8);
                 }
-            } else if (r >= a.Hq && r < last && cache_row >= 0) {
-                uint16_t *const to = static_cast<uint16_t *>(is_v ? kv.v : kv.k) + row * D;
-                *reinterpret_cast<uint4 *>(to + d0) = pack8(f);
-                *reinterpret_cast<uint4 *>(to + d1) = pack8(f + 8);
-            }
-            if (r < a.Hq && r < last) {
-                uint16_t *const to = a.Q_out + (int64_t)t * a.qo_stride + r * D;
-                const bool zero = pos < 0;
-                const uint4 none = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(to + d0) = zero ? none : pack8(f);
-                *reinterpret_cast<uint4 *>(to + d1) = zero ? none : pack8(f + 8);
             }
         }
     }
@@ -146,16 +174,15 @@ __global__ void __launch_bounds__(256) kv_write_rotary_kernel(KvDev kv, KvBatchD
 cudaError_t launch_kv_write_rotary(const KvDev &kv, bool int8, const KvBatchDev &b, const lora_rotary *rotary,
                                    const KvRotaryArgs &a, int num_sms, cudaStream_t stream)
 {
-    auto fn = kv.D == 128 ? (int8 ? kv_write_rotary_kernel<128, true> : kv_write_rotary_kernel<128, false>)
-                          : (int8 ? kv_write_rotary_kernel<64, true> : kv_write_rotary_kernel<64, false>);
-    const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
-    if (e != cudaSuccess) return e;
+    auto pick = [&](auto half) {
+        constexpr bool kHalf = decltype(half)::value;
+        return kv.D == 128 ? (int8 ? kv_write_rotary_kernel<128, true, kHalf> : kv_write_rotary_kernel<128, false, kHalf>)
+                           : (int8 ? kv_write_rotary_kernel<64, true, kHalf> : kv_write_rotary_kernel<64, false, kHalf>);
+    };
+    auto fn = rotary->layout == LORA_ROTARY_HALF ? pick(std::true_type()) : pick(std::false_type());
     const int per = 512 / kv.D;
-    const int64_t all = (a.Hq + 2 * kv.H + per - 1) / per;  // blocks of a token
-    const int64_t blocks = std::min(all, std::max<int64_t>(1, b.T * all / (16 * (int64_t)num_sms)));
-    const int64_t parts = (all + blocks - 1) / blocks;
-    fn<<<(unsigned)((b.T * parts + 7) / 8), 256, 0, stream>>>(kv, b, rotary_view(rotary), a, (int)parts, (int)blocks);
-    return cudaGetLastError();
+    const RotaryGrid g(b.T, (a.Hq + per - 1) / per + 2 * ((kv.H + per - 1) / per), num_sms);
+    return launch_stream(g.streams, fn, g.ctas, RotaryGrid::kWarps * 32, stream, kv, b, rotary_view(rotary), a, g.parts);
 }
 
 }  // namespace lora

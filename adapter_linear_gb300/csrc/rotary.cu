@@ -4,6 +4,7 @@
 #include <cmath>
 
 #include "pool_state.h"
+#include "launch_stream.h"
 #include "rotary_device.cuh"
 
 using namespace lora;
@@ -14,69 +15,68 @@ struct Tensors {
     const uint16_t *in[LORA_ROTARY_MAX_TENSORS];
     uint16_t *out[LORA_ROTARY_MAX_TENSORS];
     int64_t in_stride[LORA_ROTARY_MAX_TENSORS], out_stride[LORA_ROTARY_MAX_TENSORS];
-    int end[LORA_ROTARY_MAX_TENSORS];  // heads of the tensors up to this one (those past the last: the same)
+    int heads[LORA_ROTARY_MAX_TENSORS];
+    int n;
 };
 
-constexpr int kBatch = 4;  // blocks of rows loaded before any is stored
+constexpr int kBatch = 4;  // blocks loaded before any is stored
 
-// A row is one head of one token, of any tensor; head_dim / 16 lanes hold one. A warp takes `blocks`
-// blocks of 32 / (head_dim / 16) rows of one token, so that its lanes' eight angles each serve all of them.
-__global__ void __launch_bounds__(256) rotary_kernel(const __grid_constant__ RotaryDev rot, Tensors x, int head_dim,
-                                                     const int32_t *__restrict__ positions, int T, int inverse,
-                                                     int parts, int blocks)
+// A row is one head of one token; head_dim / 16 lanes hold one, a block is the 32 / (head_dim / 16) rows of one
+// tensor that a warp holds at a time. A warp takes a chunk of tokens, or a part of one token's blocks; its lanes'
+// eight angles serve all its rows of a token.
+template <bool kHalf>
+__global__ void __launch_bounds__(RotaryGrid::kWarps * 32, RotaryGrid::kCtas)
+    rotary_kernel(const __grid_constant__ RotaryDev rot, const __grid_constant__ Tensors x, int head_dim,
+                  const int32_t *__restrict__ positions, int T, int inverse, int parts)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int64_t t64 = w / parts;
-    if (t64 >= T) return;
-    const int t = (int)t64;
     const int lanes = head_dim / 16, per = 32 / lanes;  // lanes of a row, rows of a block
     const int sub = lane / lanes, c = lane - sub * lanes;
-    const int rows = x.end[LORA_ROTARY_MAX_TENSORS - 1];
-    const int first = (int)(w - t64 * parts) * blocks * per + sub;
-    const int last = sub < per ? min(rows, first - sub + blocks * per) : 0;
+    int all = 0;
+    for (int k = 0; k < x.n; ++k) all += (x.heads[k] + per - 1) / per;
+    const RotaryShare me(T, all, parts);
     int d0, d1;
-    rotary_runs(rot, c, &d0, &d1);
+    rotary_runs(rot, head_dim, c, &d0, &d1);
     const bool turns = 16 * c < rot.dim;
-    Turn8 turn;
-    if (turns) turn = rotary_turn(rot, c, positions[t], inverse);
-    for (int r0 = first; r0 < last; r0 += kBatch * per) {
-        uint4 v[kBatch][2];
-        uint16_t *to[kBatch];
+#pragma unroll 1
+    for (int t = me.t0; t < me.t1; t += me.step) {
+        Turn8 turn;
+        if (turns) turn = rotary_turn<kHalf>(rot, c, positions[t], inverse);
+        int first = 0;  // the tensor's first block
+#pragma unroll 1
+        for (int k = 0; k < x.n; ++k) {
+            const int heads = x.heads[k], blocks = (heads + per - 1) / per;
+            const int from = max(me.b0 - first, 0) * per, to = min((me.b1 - first) * per, heads);
+            first += blocks;
+            // (in place: what is not rotated is there)
+            const uint16_t *const src = x.in[k] + (int64_t)t * x.in_stride[k];
+            uint16_t *const dst = x.out[k] + (int64_t)t * x.out_stride[k];
+            const bool on = sub < per && (turns || src != dst);
+#pragma unroll 1
+            for (int r0 = from + sub; r0 < to; r0 += kBatch * per) {
+                uint4 v[kBatch][2];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i * per;
-            to[i] = nullptr;
-            if (r >= last) continue;
-            int k = 0, begin = 0;
-#pragma unroll
-            for (int y = 0; y < LORA_ROTARY_MAX_TENSORS - 1; ++y)
-                if (r >= x.end[y]) {
-                    k = y + 1;
-                    begin = x.end[y];
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at = (r0 + i * per) * head_dim;
+                    if (!on || r0 + i * per >= to) continue;
+                    v[i][0] = *reinterpret_cast<const uint4 *>(src + at + d0);
+                    v[i][1] = *reinterpret_cast<const uint4 *>(src + at + d1);
                 }
-            const uint16_t *const src = x.in[k] + (int64_t)t * x.in_stride[k] + (int64_t)(r - begin) * head_dim;
-            to[i] = x.out[k] + (int64_t)t * x.out_stride[k] + (int64_t)(r - begin) * head_dim;
-            if (!turns && to[i] == src) {  // in place: what is not rotated is there
-                to[i] = nullptr;
-                continue;
-            }
-            v[i][0] = *reinterpret_cast<const uint4 *>(src + d0);
-            v[i][1] = *reinterpret_cast<const uint4 *>(src + d1);
-        }
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (!to[i]) continue;
-            if (turns) {
-                float f[16];
-                unpack8(v[i][0], f);
-                unpack8(v[i][1], f + 8);
-                rotary_pairs(rot.half, turn, f);
-                v[i][0] = pack8(f);
-                v[i][1] = pack8(f + 8);
+                for (int i = 0; i < kBatch; ++i) {
+                    const int at = (r0 + i * per) * head_dim;
+                    if (!on || r0 + i * per >= to) continue;
+                    if (turns) {
+                        float f[16];
+                        unpack16(v[i], f);
+                        rotary_pairs<kHalf>(turn, f);
+                        v[i][0] = pack8(f);
+                        v[i][1] = pack8(f + 8);
+                    }
+                    *reinterpret_cast<uint4 *>(dst + at + d0) = v[i][0];
+                    *reinterpret_cast<uint4 *>(dst + at + d1) = v[i][1];
+                }
             }
-            *reinterpret_cast<uint4 *>(to[i] + d0) = v[i][0];
-            *reinterpret_cast<uint4 *>(to[i] + d1) = v[i][1];
         }
     }
 }
@@ -162,7 +162,6 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
         return LORA_ERR_ARG;
     if (head_dim < rotary->rotary_dim || head_dim > LORA_ROTARY_MAX_DIM || head_dim % 16 != 0) return LORA_ERR_SHAPE;
     Tensors x = {};
-    int64_t rows = 0;
     for (int i = 0; i < LORA_ROTARY_MAX_TENSORS; ++i) {
         if (i < n) {
             const lora_rotary_tensor &a = tensors[i];
@@ -177,10 +176,10 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
             x.out[i] = static_cast<uint16_t *>(a.out);
             x.in_stride[i] = a.in_stride;
             x.out_stride[i] = a.out_stride;
-            rows += a.heads;
+            x.heads[i] = a.heads;
         }
-        x.end[i] = (int)rows;
     }
+    x.n = n;
     if (T == 0) return LORA_OK;
     if (!positions || (reinterpret_cast<uintptr_t>(positions) & 3)) return LORA_ERR_ARG;
     int dev = 0;
@@ -197,17 +196,13 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
         if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
     }
     if (sms < 0) return LORA_ERR_UNSUPPORTED;
-    CUDA_TRY(ensure_smem_attr((const void *)rotary_kernel, 0));
+    auto *const fn = rotary->layout == LORA_ROTARY_HALF ? rotary_kernel<true> : rotary_kernel<false>;
     const int per = 32 / (head_dim / 16);
-    const int64_t all = (rows + per - 1) / per;  // blocks of a token
-    // one block a warp until four warps a scheduler have one, then up to all of a token's
-    const int64_t blocks = std::min(all, std::max<int64_t>(1, (int64_t)T * all / (16 * (int64_t)sms)));
-    const int64_t parts = (all + blocks - 1) / blocks;
-    const int64_t ctas = ((int64_t)T * parts + 7) / 8;
-    if (ctas > 0x7FFFFFFF) return LORA_ERR_ARG;
-    rotary_kernel<<<(unsigned)ctas, 256, 0, stream>>>(rotary_view(rotary), x, head_dim, positions, T, inverse != 0,
-                                                      (int)parts, (int)blocks);
-    CUDA_TRY(cudaGetLastError());
+    int64_t all = 0;  // blocks of a token
+    for (int i = 0; i < n; ++i) all += (x.heads[i] + per - 1) / per;
+    const RotaryGrid g(T, all, sms);
+    CUDA_TRY(launch_stream(g.streams, fn, g.ctas, RotaryGrid::kWarps * 32, stream, rotary_view(rotary), x, head_dim,
+                           positions, T, (int)(inverse != 0), g.parts));
     return LORA_OK;
 }
 
