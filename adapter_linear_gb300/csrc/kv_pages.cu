@@ -16,8 +16,8 @@ using namespace lora;
 namespace {
 
 // The tables are some hundred kilobytes, in L2, and the work on them a handful of steps that each need all of
-// the one before (who names a page, which pages are free, who gets them), so the latency of L2 (0.3 us) and of
-// the steps' ends bounds it (a hop to L2 0.5 us, a cluster barrier 0.6): one cluster of kCtas CTAs does all
+// the one before (who names a page, which pages are free, who gets them), so the latency of L2 and of the steps'
+// ends bounds it (a hop to L2 0.5 us, a cluster barrier 0.6): one cluster of kCtas CTAs does all
 // steps, a cluster barrier between them, and what all of them need of the slots is in every CTA's shared memory.
 constexpr int kCtas = 8, kThreads = 1024;
 constexpr int kUnit = 128;       // table entries a warp takes at a time, four a lane
@@ -53,7 +53,7 @@ __device__ __forceinline__ int held_of(const int4 &s) { return s.w; }
 struct Told {
     int bad[2];        // error bits of the first two steps
     int found;         // pages it found
-    int need, copies;  // the first CTA: new pages and copies in all
+    int need, copies;  // the last CTA: new pages and copies in all
 };
 
 __device__ __forceinline__ int entries(int tokens, int shift) { return (tokens + (1 << shift) - 1) >> shift; }
@@ -156,12 +156,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
         kids[i] = 0;
         least[i] = INT_MAX;
     }
-    __syncthreads();
+    cluster_arrive_relaxed();  // all have started, before the first reaches into another's shared memory
+    cluster_wait();
 
-    // ---- 1: what is asked for (all slots in every CTA where they fit)
+    // ---- 1: what is asked for. Each slot is read once, by one thread, which tells all CTAs where the slots fit
+    // (so that they agree, whatever else may write what they read).
     const int capacity = (int)min((int64_t)p.W << p.shift, (int64_t)INT_MAX);
-    bool any_wrong = false;
-    for (int i = here ? threadIdx.x : tid; i < p.S; i += here ? kThreads : kCtas * kThreads) {
+    for (int i = threadIdx.x * kCtas + cta; i < p.S; i += kCtas * kThreads) {
         const int from = parent ? parent[i] : i, now = p.kv_len[i];
         const int extra = room ? room[i] : 0, most = keep ? max(0, keep[i]) : INT_MAX;
         bool wrong = from < -1 || from >= p.S || extra < 0 || now < 0 || now > capacity;
@@ -172,38 +173,34 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
             n = min(n, most);
         }
         wrong = wrong || (int64_t)n + extra > capacity;
-        any_wrong = any_wrong || wrong;
-        slots[i] = wrong ? make_int4(0, -1, 0, 0) : make_int4(n, from, n + extra, entries(now, p.shift));
-        if (here && !wrong && from >= 0) {
-            atomicAdd(kids + from, 1);
-            atomicMin(least + from, n >> p.shift);
-        }
+        if (wrong) mine.bad[0] = kErrRangeBit;
+        const int4 slot = wrong ? make_int4(0, -1, 0, 0) : make_int4(n, from, n + extra, entries(now, p.shift));
+        if (here)
+#pragma unroll
+            for (int c = 0; c < kCtas; ++c) cluster.map_shared_rank(slots_here, c)[i] = slot;
+        else
+            slots[i] = slot;
     }
+    cluster.sync();
     int bad = 0;
-    if (here) {  // every CTA has looked at all of them
-        if (__syncthreads_or(any_wrong)) {
-            if (tid == 0) {
-                atomicOr(p.err, kErrRangeBit);
-                *p.moves_n = 0;
-            }
-            return;
+    gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
+    for (int c = 0; c < kCtas; ++c) bad |= others[c];
+    if (bad) {
+        cluster_arrive_relaxed();
+        if (tid == 0) {
+            atomicOr(p.err, bad);
+            *p.moves_n = 0;
         }
-        cluster_arrive_relaxed();  // all have started, before the first reaches into another's shared memory
         cluster_wait();
-    } else {
-        if (any_wrong) mine.bad[0] = kErrRangeBit;
-        cluster.sync();
-        gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
-        for (int c = 0; c < kCtas; ++c) bad |= others[c];
-        if (bad) {
-            cluster_arrive_relaxed();
-            if (tid == 0) {
-                atomicOr(p.err, bad);
-                *p.moves_n = 0;
+        return;
+    }
+    if (here && !counted) {
+        for (int i = threadIdx.x; i < p.S; i += kThreads)
+            if (from_of(slots_here[i]) >= 0) {
+                atomicAdd(kids + from_of(slots_here[i]), 1);
+                atomicMin(least + from_of(slots_here[i]), kept_of(slots_here[i]) >> p.shift);
             }
-            cluster_wait();
-            return;
-        }
+        __syncthreads();
     }
     int *const last = here ? cluster.map_shared_rank(last_here, kCtas - 1) : p.last;
     int *const base = here ? cluster.map_shared_rank(base_here, kCtas - 1) : p.base;
@@ -213,8 +210,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     if (counted) {  // known: the entries are only looked at (the result is asked for behind the next barrier)
         each_entry(p, cta, [&](int) { return 0; }, [&](int s) { return held_of(slots[s]); },
                    [&](int s, int j) { return p.table + (int64_t)s * p.W + j; },
-                   [&](int, int, int x) {
-                       if (x < 0 || x >= p.P) mine.bad[1] = kErrRangeBit;
+                   [&](int s, int j, int x) {
+                       // (a page that a slot ends inside is its own, unless the caller's tables have it otherwise)
+                       if (x < 0 || x >= p.P || (j == kept_of(slots[s]) >> p.shift && p.refs[x] != 1))
+                           mine.bad[1] = kErrRangeBit;
                    });
     } else {
         each_piece(p, cta, [&](int s, int first) {
@@ -446,14 +445,14 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e) {
             const int y = x + e;
             if (y < x1 && r[e] > 0) {
-                if (y >= n) {
-                    const int d = n - 1 - at;
+                const int d = n - 1 - at;
+                if (y >= n && d >= 0 && d < p.P / 2 + 1) {  // (as it is, unless refs change meanwhile)
                     p.list[d] = y;
                     p.place[y] = d;
                     p.named[d] = r[e];
                 }
                 ++at;
-            } else if (y < x1 && y < n) {
+            } else if (y < x1 && y < n && y - at < p.cap) {
                 p.moves[p.cap + y - at] = y;
                 ++holes;
             }
@@ -467,6 +466,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_arrive_relaxed();  // nothing more of another CTA's shared memory
     int moved = 0;
     for (int c = 0; c < kCtas; ++c) moved += others[c];
+    moved = min(moved, p.P / 2 + 1);
 
     for (int k = tid; k < moved; k += kCtas * kThreads) {
         const int d = moved - 1 - k;
@@ -722,12 +722,15 @@ lora_status lora_kv_pages_create(int num_pages, int page_tokens, int max_seqs, i
 lora_status lora_kv_pages_destroy(lora_kv_pages_t p)
 {
     if (!p) return LORA_ERR_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev != p->device) cudaSetDevice(p->device);
     cudaDeviceSynchronize();
     if (p->ctl_stream) cudaStreamDestroy(p->ctl_stream);
     if (p->ev) cudaEventDestroy(p->ev);
     if (p->scratch) cudaFree(p->scratch);
     if (p->d_err) cudaFree(p->d_err);
     if (p->h_err) cudaFreeHost(p->h_err);
+    if (dev >= 0 && dev != p->device) cudaSetDevice(dev);
     delete p;
     return LORA_OK;
 }
@@ -775,6 +778,8 @@ lora_status lora_kv_pages_used(lora_kv_pages_t p, int *used)
 lora_status lora_kv_pages_check_errors(lora_kv_pages_t p)
 {
     if (!p) return LORA_ERR_ARG;
+    const lora_status st = on_device(p->device);
+    if (st != LORA_OK) return st;
     CUDA_TRY(cudaStreamWaitEvent(p->ctl_stream, p->ev, 0));
     kv_pages_read_clear_kernel<<<1, 1, 0, p->ctl_stream>>>(p->d_err);
     if (cudaGetLastError() != cudaSuccess ||

@@ -1177,7 +1177,12 @@ cudaError_t ensure_smem_attr(const void *kernel, size_t bytes)
                              cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess && bytes > 0)
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) done.push_back({kernel, dev, bytes});
+    if (e == cudaSuccess) {
+        try {
+            done.push_back({kernel, dev, bytes});
+        } catch (...) {  // asked for again next time: nothing may be thrown through the C calls
+        }
+    }
     return e;
 }
 

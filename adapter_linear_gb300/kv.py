@@ -238,15 +238,16 @@ class KvCache:
     def reserve_shared(self, max_tokens: int, n_heads: int, max_seqs: int):
         _check(self._lib.lora_kv_reserve_shared(self.handle, max_tokens, n_heads, max_seqs), "lora_kv_reserve_shared")
 
-    def attention_shared(self, Q, batch: KvBatch, groups: KvGroups, scale: Optional[float] = None, O=None, lse=None,
+    def attention_shared(self, Q, batch: KvBatch, groups: Optional[KvGroups], scale: Optional[float] = None, O=None, lse=None,
                          stream=None):
-        """attention() without a window, for a batch whose groups of sequences share prefixes: each group's
-        prefix is read once."""
+        """attention() without a window, for a batch whose groups of sequences share prefixes (None: no groups):
+        each group's prefix is read once."""
         Q, qs, O, os_, lse, scale = self._attention_args("lora_kv_attention_shared", Q, batch, scale, O, lse, stream)
-        if groups.device != self._device:
+        if groups is not None and groups.device != self._device:
             raise LoraError(LORA_ERR_ARG, "lora_kv_attention_shared: the tensors of a call are on the cache's GPU")
-        st = self._stream(stream, batch, Q, O, lse, *groups.tensors)
-        _check(self._lib.lora_kv_attention_shared(self.handle, Q.data_ptr(), qs, Q.shape[1], batch.ref, groups.ref, scale,
+        st = self._stream(stream, batch, Q, O, lse, *(groups.tensors if groups is not None else ()))
+        _check(self._lib.lora_kv_attention_shared(self.handle, Q.data_ptr(), qs, Q.shape[1], batch.ref,
+                                                  groups.ref if groups is not None else None, scale,
                                                   O.data_ptr(), os_, lse.data_ptr(), st), "lora_kv_attention_shared")
         return O, lse
 

@@ -164,7 +164,9 @@ lora_status lora_kv_pages_destroy(lora_kv_pages_t pages);
  * longer uses become -1.
  *
  * Where the pages do not suffice (LORA_ERR_OOM from lora_kv_pages_check_errors), or a parent, a room, a length or
- * an entry is out of range (LORA_ERR_RANGE), nothing changes and nothing is to be copied.
+ * an entry is out of range (LORA_ERR_RANGE), nothing changes and nothing is to be copied. With room alone
+ * (parent and keep NULL) the call takes refs at its word, and a page that a slot ends inside and refs does not
+ * count once (these calls make no such tables) is LORA_ERR_RANGE, too.
  * Asynchronous on `stream`. Errors: ARG, CUDA.
  */
 lora_status lora_kv_pages_update(lora_kv_pages_t pages, const int32_t *parent, const int32_t *keep, const int32_t *room,

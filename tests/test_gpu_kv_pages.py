@@ -185,6 +185,42 @@ def test_bad_tables_are_reported_and_left():
     t.check()
 
 
+def test_what_cannot_be_done_with_many_slots():
+    t = Pair(3000, 16, 1500, 4, ((BF16, 1, 64),))
+    t.update(room=[17 + i % 3 for i in range(1500)])
+    bad = list(range(1500))
+    bad[1400] = 1500
+    assert t.update(parent=bad) == "range"
+    assert t.update(room=[0] * 1499 + [64]) == "range"
+    assert t.update(parent=[i // 2 for i in range(1500)], room=[32] * 1500) == "oom"
+    t.update(parent=[i // 2 for i in range(1500)])
+
+
+def test_a_shared_page_that_slots_end_inside():
+    """Tables of the caller's own making: with room alone the call says so, with a parent it mends them."""
+    t = Pair(20, 16, 3, 8)
+    t.update(room=[20, 0, 0])
+    t.pages.table[1] = t.pages.table[0]
+    t.pages.kv_len[1] = 20
+    t.pages.refs[:2] = 2
+    t.model.table[1], t.model.len[1] = t.model.table[0][:], 20
+    assert t.model.refs() == t.pages.refs.tolist()
+    t.pages.update(room=ints([1, 1, 0]))
+    assert t.pages.check_errors() == al.LORA_ERR_RANGE
+    t.check()
+    assert [m[2] for m in t.update(parent=[0, 1, 2], room=[1, 1, 0])] == [4]
+    t.update(room=[1, 1, 1])
+
+
+def test_the_tables_own_arrays_as_arguments():
+    t = Pair(60, 16, 3, 8)
+    t.update(room=[20, 5, 33])
+    t.pages.update(keep=t.pages.kv_len, room=t.pages.kv_len)
+    t.caches[0].copy(t.pages)
+    assert t.model.update(keep=[20, 5, 33], room=[20, 5, 33]) == []
+    t.check()
+
+
 def test_compaction_into_other_tables():
     t = Pair(30, 16, 5, 6)
     t.update(room=[60, 33, 16, 80, 1])

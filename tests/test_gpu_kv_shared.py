@@ -244,9 +244,19 @@ def test_bad_groups_share_nothing_and_are_reported():
 def test_no_groups_is_the_plain_attention():
     p = Shared(INT8, 2, 64, 16, [(64, [(9, 1), (20, 1)])], seed=1)
     Q = p.queries(4)
-    none = al.KvGroups(ints([0]), ints([]), 0)
-    for a, b in zip(p.cache.attention_shared(Q, p.batch, none), p.cache.attention(Q, p.batch)):
-        assert torch.equal(a, b)
+    for none in (al.KvGroups(ints([0]), ints([]), 0), None):
+        for a, b in zip(p.cache.attention_shared(Q, p.batch, none), p.cache.attention(Q, p.batch)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bound", [0, 1, 10 ** 9])
+def test_a_wrong_bound_on_a_groups_rows_costs_time_only(bound):
+    p = Shared(INT8, 2, 64, 16, [(64, [(9, 1)] * 20), (32, [(40, 30), (6, 1)])], [(90, 3)], seed=1)
+    Q = p.queries(8)
+    groups = al.KvGroups(ints(p.seq_start), ints(p.prefix), bound)
+    for max_new in (0, 1, 30, 10 ** 6):
+        batch = al.KvBatch(p.table, p.batch.start, p.batch.kv_len, p.T, max_new)
+        R.check_attention(*p.cache.attention_shared(Q, batch, groups), R.attention(Q, p, 0.125), f"{bound} {max_new}")
 
 
 def test_refusals():
