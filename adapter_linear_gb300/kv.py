@@ -152,6 +152,13 @@ class KvCache:
     def _stream_object(self, stream):
         return torch.cuda.ExternalStream(stream, self._torch_device) if isinstance(stream, int) else stream
 
+    def _empty_like(self, x, stream):
+        """An output of x's shape, as _empty (torch takes 1 us less)."""
+        if stream is None:
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
+        with torch.cuda.stream(self._stream_object(stream)):
+            return torch.empty_like(x, memory_format=torch.contiguous_format)
+
     def _empty(self, shape, dtype, stream):
         """An output, allocated for the stream that will write it."""
         if stream is None:  # (sizes one by one: a tuple takes torch 1 us more)
@@ -166,6 +173,8 @@ class KvCache:
             raise LoraError(LORA_ERR_SHAPE, f"{what}: bfloat16 [{T}, {heads}, {D}] expected")
         if x.get_device() != self._device or batch.device != self._device:
             raise LoraError(LORA_ERR_ARG, f"{what}: the tensors of a call are on the cache's GPU")
+        if x.is_contiguous():
+            return heads * D
         st, sh, sd = x.stride()
         if (sd != 1 and D > 1) or (sh != D and heads > 1):
             raise LoraError(LORA_ERR_ARG, f"{what}: the heads of a token must be contiguous")
@@ -195,7 +204,7 @@ class KvCache:
             heads = Q.shape[1]
             qs = self._rows(Q, heads, batch, what + " Q")
             if Q_out is None:
-                Q_out = self._empty((batch.T, heads, self.head_dim), torch.bfloat16, stream)
+                Q_out = self._empty_like(Q, stream)
                 os_ = heads * self.head_dim
             else:
                 os_ = self._rows(Q_out, heads, batch, what + " Q_out")
@@ -257,7 +266,7 @@ class KvCache:
         T, Hq, _ = Q.shape
         qs = self._rows(Q, Hq, batch, what + " Q")
         if O is None:
-            O = self._empty((T, Hq, self.head_dim), torch.bfloat16, stream)
+            O = self._empty_like(Q, stream)
             os_ = Hq * self.head_dim
         else:
             os_ = self._rows(O, Hq, batch, what + " O")
