@@ -381,7 +381,7 @@ struct ShareSizes {
         lse2 = O + up((size_t)T * n_heads * p->D * sizeof(float));
         where = lse2 + up((size_t)T * n_heads * sizeof(float));
         groups = where + up((size_t)T * n_heads * sizeof(uint2));
-        total = groups + (size_t)n_seqs * (sizeof(int4) + sizeof(int32_t));
+        total = groups + ((size_t)n_seqs + 1) * (sizeof(int4) + 2 * sizeof(int32_t));
     }
 };
 lora_status ensure_share(lora_kv *p, size_t bytes)
@@ -738,7 +738,9 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     // The short-chunk kernel, a few rows a CTA, reads the pieces of the prefix's output itself. The other, a thread a
     // row, would take 40 us for 20 of them: then they are joined first.
     share.pieces = wide && !prefill;
-    share.lo = reinterpret_cast<int32_t *>(share.groups + batch->n_seqs);
+    share.own_sums = share.groups + batch->n_seqs;
+    share.lo = reinterpret_cast<int32_t *>(share.own_sums + 1);
+    share.own_first = share.lo + batch->n_seqs;
     const bool tracked = !capturing(stream, &st);  // the scratch belongs to one call at a time
     if (st != LORA_OK) return st;
     if (tracked) CUDA_TRY(cudaStreamWaitEvent(stream, p->attn_ev, 0));
@@ -747,7 +749,9 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     KvBatchDev bg = bd;
     bg.n_seqs = groups->n_groups;
     int *const pre_count = p->count + kv_decode_grid(p->num_sms);
-    cudaError_t e = launch_kv_share_plan(kv, bd, groups->seq_start, groups->prefix_len, groups->n_groups, share, stream);
+    cudaError_t e = launch_kv_share_plan(kv, bd, groups->seq_start, groups->prefix_len, groups->n_groups, a.G,
+                                         kv_decode_rows((int64_t)max_new * a.G), prefill ? kDecodeRows : INT_MAX, share,
+                                         stream);
     if (e == cudaSuccess)
         e = wide ? launch_kv_prefill_shared(kPrefix, kv, p->int8, bg, a, share, 0, p->pre_part, pre_count, p->num_sms,
                                             stream)

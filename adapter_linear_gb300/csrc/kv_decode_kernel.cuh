@@ -40,9 +40,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kStep = 16;            // tokens per warp step: never crosses a page (pages hold 16 k)
 constexpr int kUnit = kWarps * kStep;
+static_assert(kUnit == kDecodeUnit, "what the plan of shared prefixes counts in");
 // An item's cost beside its units, in units: 32 8-bit drafts 85 us at 2, 81 at 3, 79 at 4, 64 requests of
 // one token 99 at each.
-constexpr int kHeadUnits = 4;
+constexpr int kHeadUnits = kDecodeHeadUnits;
 constexpr int kMinUnits = 2;         // one request, one token: 11.2 us at 1, 11.0 at 2, 11.6 at 4
 
 constexpr int kMaxCtas = 4;    // CTAs an SM, of any variant
@@ -450,31 +451,33 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
         pdl_wait_prior();
         pdl_launch_dependents();
     }
-    KvWork<R, kUnit, kHeadUnits, kMode> w(kv, b, a, share, 0, plan.max_rows, lane);
-    // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than
-    // they save
+    KvWork<R, kUnit, kHeadUnits, kMode> w(kv, b, a, share, 0, plan.max_rows, lane, kMode != kOwn);
     // kOwn: what is behind a prefix is short, and there is much of it: cutting items into equal shares costs a
     // second item's start and end in most CTAs, and where there are many items their starts and ends one
     // after the other are most of the time. So items may go whole to teams of 4, 2 or 1 warps. The time of
     // each, in units (64 tokens by 4 warps), with kEnds for an item's start and end:
     int ways = kWarps;  // warps that work on an item
+    int own_items = 0;  // items that go whole
     if constexpr (kMode == kOwn) {
         constexpr int kEnds = 12;
-        const int64_t items = max(w.items, (int64_t)1), avg = w.total / items - kHeadUnits + 1;
-        int64_t best = w.total / gridDim.x + 3 * kEnds;  // cut
+        const int4 sums = *share.own_sums;
+        const int64_t items = max(sums.x, 1), total = (int64_t)((uint64_t)(uint32_t)sums.w << 32 | (uint32_t)sums.z);
+        const int64_t avg = total / items - kHeadUnits + 1;
+        int64_t best = total / gridDim.x + 3 * kEnds;  // cut
 #pragma unroll
         for (int teams = 1; teams <= C::kTeams; teams *= 2) {
             const int64_t n = (int64_t)gridDim.x * teams, turns = (items + n - 1) / n;
-            const int64_t time = teams * max((int64_t)w.most, turns * avg) + turns * kEnds;
+            const int64_t time = teams * max((int64_t)sums.y, turns * avg) + turns * kEnds;
             if (time < best) {
                 best = time;
                 ways = -kWarps / teams;
             }
         }
-        if (ways < 0) {
-            w.by_items();
+        own_items = ways < 0 ? sums.x : 0;
+        if (ways < 0)
             ways = -ways;
-        }
+        else
+            w.count();
     }
     const int team = C::kTeams > 1 ? warp / ways : 0, first_warp = team * ways, in_team = warp - first_warp;
     const int tt = threadIdx.x - first_warp * 32, team_threads = ways * 32;
@@ -492,9 +495,15 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
     uint2 *const sm_where = sm_wheres[team];
     int *const sm_pos = sm_poss[team];
     uint4(&sm_q)[kN][kM / 2][32] = sm_qs[team];
-    const int64_t teams = (int64_t)gridDim.x * (C::kTeams > 1 ? kWarps / ways : 1);
-    const int64_t want = !w.cuts() ? w.total : (w.total + kMinUnits - 1) / kMinUnits;
-    if (!w.take_share((int64_t)team * gridDim.x + blockIdx.x, min(teams, want))) {
+    bool some;
+    if (kMode == kOwn && own_items > 0) {
+        const int64_t teams = (int64_t)gridDim.x * (C::kTeams > 1 ? kWarps / ways : 1);
+        some = w.take_items((int64_t)team * gridDim.x + blockIdx.x, min(teams, (int64_t)own_items), share.own_first, own_items);
+    } else {
+        // a CTA takes kMinUnits units at least: more pieces of an item cost more to join than they save
+        some = w.take_share(blockIdx.x, min((int64_t)gridDim.x, (w.total + kMinUnits - 1) / kMinUnits));
+    }
+    if (!some) {
         if (kMode == kOwn) pdl_wait_prior();  // (a kernel behind this one counts on the ones ahead having ended)
         return;
     }
@@ -643,6 +652,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
             const int row = tile * R + r;
             return (int64_t)(sh.row0 + row / G) * a.Hq + head * G + row % G;
         };
+        constexpr int kBatch = 8;  // pieces of the prefix read at once
         // A row's maximum (units of log2), sum and what its O is to be multiplied by: the prefix joined in
         // (kOwn), its lse for `out`.
         auto finish = [&](int r, float M, float sum) {
@@ -658,14 +668,20 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
                     } else {
                         const int c0 = at.x & 0xFFFF, n = (int)(at.x >> 16) - c0 + 1;
                         const float2 *const ml = reinterpret_cast<const float2 *>(share.part + share.ml_at) + at.y;
-#pragma unroll 8
-                        for (int x = 0; x < n; ++x) P = fmaxf(P, ml[kv_slot(c0, x) * kShareRows].x);
-                        const float ref = P == -INFINITY ? 0.0f : P;
                         l1 = 0.0f;
-#pragma unroll 8
-                        for (int x = 0; x < n; ++x) {
-                            const float2 e = ml[kv_slot(c0, x) * kShareRows];
-                            l1 += fast_exp2(e.x - ref) * e.y;
+                        for (int x0 = 0; x0 < n; x0 += kBatch) {
+                            float2 e[kBatch];
+                            float top = P;
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y) {
+                                e[y] = x0 + y < n ? ml[kv_slot(c0, x0 + y) * kShareRows] : make_float2(-INFINITY, 0.0f);
+                                top = fmaxf(top, e[y].x);
+                            }
+                            const float ref = top == -INFINITY ? 0.0f : top;
+                            l1 *= fast_exp2(P - ref);
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y) l1 += fast_exp2(e[y].x - ref) * e[y].y;
+                            P = top;
                         }
                     }
                 }
@@ -692,8 +708,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
                 if (d == 0) share.lse2[t * a.Hq + h] = sm_lse[r];
             } else {
                 if constexpr (kMode == kOwn) {
-                    auto add = [&](float wt, const float *from) {
-                        const float4 v = *reinterpret_cast<const float4 *>(from);
+                    auto add = [&](float wt, const float4 &v) {
                         acc.x = add_piece<kInt8>(wt, v.x, acc.x);
                         acc.y = add_piece<kInt8>(wt, v.y, acc.y);
                         acc.z = add_piece<kInt8>(wt, v.z, acc.z);
@@ -701,15 +716,24 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
                     };
                     const uint2 at = sm_where[r];
                     if (sh.lo > 0 && at.x == kJoined) {
-                        add(sm_prior[r], share.O + (t * a.Hq + h) * D + d);
+                        add(sm_prior[r], *reinterpret_cast<const float4 *>(share.O + (t * a.Hq + h) * D + d));
                     } else if (sh.lo > 0) {
                         const int c0 = at.x & 0xFFFF, n = (int)(at.x >> 16) - c0 + 1;
                         const float2 *const ml = reinterpret_cast<const float2 *>(share.part + share.ml_at) + at.y;
                         const float *const from = share.part + (int64_t)at.y * D + d;
-#pragma unroll 4
-                        for (int x = 0; x < n; ++x) {
-                            const int sl = kv_slot(c0, x);
-                            add(sm_prior[r] * fast_exp2(ml[sl * kShareRows].x - sm_top[r]), from + (int64_t)sl * kShareRows * D);
+                        for (int x0 = 0; x0 < n; x0 += kBatch) {
+                            float4 v[kBatch];
+                            float wt[kBatch];
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y) {
+                                const int sl = kv_slot(c0, x0 + y);
+                                const bool is = x0 + y < n;
+                                wt[y] = is ? ml[sl * kShareRows].x : -INFINITY;
+                                v[y] = is ? *reinterpret_cast<const float4 *>(from + (int64_t)sl * kShareRows * D)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            }
+#pragma unroll
+                            for (int y = 0; y < kBatch; ++y) add(sm_prior[r] * fast_exp2(wt[y] - sm_top[r]), v[y]);
                         }
                     }
                 }

@@ -81,6 +81,10 @@ struct KvShareDev {
     int64_t ml_at;       // where in part (m, l) begin
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]
+    // Work of the short-chunk kernel on the sequences' own tokens: the first item of each sequence [n_seqs + 1],
+    // and of all {items, the most units of one, units (64 bits, the lower half first)}.
+    int32_t *own_first;
+    int4 *own_sums;
     float *O;      // [T][Hq][D]
     float *lse2;   // [T][Hq]
 };
@@ -109,8 +113,13 @@ cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, co
 // Both for groups that share prefixes. early: the kernel may start before the one ahead of it has ended
 // (kOwn, behind the join: it waits before it reads the prefixes' results). plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
 // one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).
+// own_rows: rows of an item of launch_kv_decode_shared(kOwn), kv_decode_rows(max_new * G); it takes sequences of up to
+// max_rows.
+constexpr int kDecodeUnit = 64, kDecodeHeadUnits = 4;
+inline int kv_decode_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 24; }
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
-                                 const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream);
+                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows,
+                                 const KvShareDev &share, cudaStream_t stream);
 cudaError_t launch_kv_decode_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
                                     const KvShareDev &share, int max_new, int max_rows, float *part, int *count,
                                     int num_sms, bool early, cudaStream_t stream);

@@ -15,9 +15,12 @@ namespace {
 // A group's prefix: what is asked for, but no further than the new tokens of any of its sequences, in
 // whole pages. A group of one sequence, or one with a sequence whose start or length is bad, has none.
 __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDev b, const int32_t *seq_start,
-                                                             const int32_t *prefix_len, int n_groups, KvShareDev share)
+                                                             const int32_t *prefix_len, int n_groups, int G, int own_rows,
+                                                             int max_rows, KvShareDev share)
 {
-    const int lane = threadIdx.x & 31;
+    __shared__ int sm_items[32], sm_most[32];
+    __shared__ unsigned long long sm_units;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     pdl_launch_dependents();
     for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) share.lo[i] = 0;
     bool ordered = true;
@@ -49,6 +52,56 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
         if (lane == 0) share.groups[g] = e > 0 ? make_int4(first, e, b.start[first], rows) : make_int4(0, 0, 0, 0);
         if (e > 0)
             for (int i = s0 + lane; i < s1; i += 32) share.lo[i] = e;
+    }
+
+    // the items of what is behind, a sequence a thread
+    if (threadIdx.x == 0) sm_units = 0;
+    __syncthreads();
+    int before = 0, most = 0;
+    unsigned long long units = 0;
+    for (int i0 = 0; i0 < b.n_seqs; i0 += blockDim.x) {
+        const int i = i0 + threadIdx.x;
+        int tiles = 0;
+        if (i < b.n_seqs) {
+            const KvSeq s = kv_seq(b, kv.page_shift, i, kv.err);
+            const int64_t rows = (int64_t)s.n * G;
+            if (rows <= max_rows) tiles = (int)((rows + own_rows - 1) / own_rows);
+            const int lo = share.lo[i];
+            for (int t = 0; t < tiles; ++t) {
+                const int last = (int)min((int64_t)(t + 1) * own_rows, rows) - 1;
+                const int hi = max(0, s.L - s.n + last / G + 1);
+                const int n = max(1, (hi - min(lo, hi) + kDecodeUnit - 1) / kDecodeUnit);
+                units += kDecodeHeadUnits + n;
+                most = max(most, n);
+            }
+        }
+        int x = tiles * kv.H;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += o;
+        }
+        __syncthreads();
+        if (lane == 31) sm_items[warp] = x;
+        __syncthreads();
+        const int w = lane < warps ? sm_items[lane] : 0;
+        x += __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+        if (i < b.n_seqs) share.own_first[i] = before + x - tiles * kv.H;
+        before += __reduce_add_sync(0xffffffffu, w);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) sm_most[warp] = most;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) units += __shfl_xor_sync(0xffffffffu, units, d);
+    if (lane == 0) atomicAdd(&sm_units, units);
+    __syncthreads();
+    if (warp == 0) {
+        most = __reduce_max_sync(0xffffffffu, lane < warps ? sm_most[lane] : 0);
+        if (lane == 0) {
+            units = sm_units * kv.H;
+            share.own_first[b.n_seqs] = before;
+            *share.own_sums = make_int4(before, most, (int)(uint32_t)units, (int)(units >> 32));
+        }
     }
 }
 
@@ -154,11 +207,15 @@ cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, co
 }
 
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
-                                 const int32_t *prefix_len, int n_groups, const KvShareDev &share, cudaStream_t stream)
+                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows,
+                                 const KvShareDev &share, cudaStream_t stream)
 {
     const cudaError_t e = ensure_smem_attr((const void *)kv_share_plan_kernel, 0);
     if (e != cudaSuccess) return e;
-    kv_share_plan_kernel<<<1, 1024, 0, stream>>>(kv, b, seq_start, prefix_len, n_groups, share);
+    // a sequence a thread, a group a warp
+    const int threads = (int)std::min<int64_t>(1024, 32 * (int64_t)std::max((b.n_seqs + 31) / 32, std::max(n_groups, 1)));
+    kv_share_plan_kernel<<<1, threads, 0, stream>>>(kv, b, seq_start, prefix_len, n_groups, G, own_rows, max_rows,
+                                                 share);
     return cudaGetLastError();
 }
 
