@@ -369,19 +369,20 @@ lora_status ensure_pre_part(lora_kv *p)
 // The attention over shared prefixes keeps between its kernels, one behind the other (16-byte pieces): O and lse
 // of the prefixes, the groups, and where each sequence's own tokens begin.
 struct ShareSizes {
-    size_t O, lse2, where, groups, items, own_part, part, total;
+    size_t O, lse2, where, groups, items, begins, own_part, part, total;
     ShareSizes(const lora_kv *p, int64_t T, int n_heads, int64_t n_seqs)
     {
         auto up = [](size_t n) { return (n + 15) / 16 * 16; };
         // what does not depend on the call's size first
         part = 0;
         items = up(sizeof(float) * kv_share_part_floats(p->D, p->num_sms));
-        own_part = items + up(sizeof(KvShareItem) * (size_t)kv_prefill_grid(p->num_sms));
+        begins = items + up(sizeof(KvShareItem) * (size_t)kv_prefill_grid(p->num_sms));
+        own_part = begins + up(sizeof(KvShareBegin) * (size_t)kv_prefill_grid(p->num_sms));
         O = own_part + up(sizeof(float) * kv_decode_part_floats(p->D, p->num_sms));
         lse2 = O + up((size_t)T * n_heads * p->D * sizeof(float));
         where = lse2 + up((size_t)T * n_heads * sizeof(float));
         groups = where + up((size_t)T * n_heads * sizeof(uint2));
-        total = groups + ((size_t)n_seqs + 1) * (sizeof(int4) + 2 * sizeof(int32_t));
+        total = groups + ((size_t)n_seqs + 1) * (sizeof(int4) + sizeof(int64_t) + 2 * sizeof(int32_t));
     }
 };
 lora_status ensure_share(lora_kv *p, size_t bytes)
@@ -730,6 +731,7 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     KvShareDev share;
     share.part = reinterpret_cast<float *>(block + sizes.part);
     share.items = reinterpret_cast<KvShareItem *>(block + sizes.items);
+    share.begins = reinterpret_cast<KvShareBegin *>(block + sizes.begins);
     share.O = reinterpret_cast<float *>(block + sizes.O);
     share.lse2 = reinterpret_cast<float *>(block + sizes.lse2);
     share.where = reinterpret_cast<uint2 *>(block + sizes.where);
@@ -739,7 +741,8 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     // row, would take 40 us for 20 of them: then they are joined first.
     share.pieces = wide && !prefill;
     share.own_sums = share.groups + batch->n_seqs;
-    share.lo = reinterpret_cast<int32_t *>(share.own_sums + 1);
+    share.group_at = reinterpret_cast<int64_t *>(share.own_sums + 1);
+    share.lo = reinterpret_cast<int32_t *>(share.group_at + batch->n_seqs);
     share.own_first = share.lo + batch->n_seqs;
     const bool tracked = !capturing(stream, &st);  // the scratch belongs to one call at a time
     if (st != LORA_OK) return st;
@@ -750,8 +753,8 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     bg.n_seqs = groups->n_groups;
     int *const pre_count = p->count + kv_decode_grid(p->num_sms);
     cudaError_t e = launch_kv_share_plan(kv, bd, groups->seq_start, groups->prefix_len, groups->n_groups, a.G,
-                                         kv_decode_rows((int64_t)max_new * a.G), prefill ? kDecodeRows : INT_MAX, share,
-                                         stream);
+                                         kv_decode_rows((int64_t)max_new * a.G), prefill ? kDecodeRows : INT_MAX,
+                                         wide ? kv_prefill_grid(p->num_sms) : 0, share, stream);
     if (e == cudaSuccess)
         e = wide ? launch_kv_prefill_shared(kPrefix, kv, p->int8, bg, a, share, 0, p->pre_part, pre_count, p->num_sms,
                                             stream)

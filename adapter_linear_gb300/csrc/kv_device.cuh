@@ -160,6 +160,22 @@ struct KvWork {
         return true;
     }
 
+    // In place of count() and take_share(): the share that the plan gave this CTA (kPrefix).
+    __device__ __forceinline__ bool take_begin(const KvShareBegin &x)
+    {
+        total = x.total;
+        grid = x.shares;
+        seg_end = x.u;
+        u_end = x.u_end;
+        tile0 = x.tile0;
+        if (seg_end >= u_end) return false;
+        seq = x.seq;
+        sh = KvSeq{x.group.z, x.group.w, x.group.y, x.group.x};
+        tiles = tiles_of(sh);
+        set_tile(x.tile);
+        return true;
+    }
+
     // Take share c of n; false: it is empty.
     __device__ __forceinline__ bool take_share(int64_t c, int64_t n)
     {
@@ -248,7 +264,7 @@ private:
     {
         if (kMode == kPrefix) {
             const int4 g = share.groups[i];
-            return KvSeq{g.z, g.w, g.y, 0};
+            return KvSeq{g.z, g.w, g.y, g.x};  // (lo, which is not used: whose pages)
         }
         KvSeq s = kv_seq(b, kv.page_shift, i, kv.err);
         if (kMode == kOwn) s.lo = share.lo[i];

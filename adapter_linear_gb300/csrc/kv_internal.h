@@ -72,7 +72,17 @@ struct KvShareItem {
     int last, row0, head, rows;  // last CTA with a piece (-1: nothing to join), the first token's row, kv head, rows
     int first_row, pad[3];       // the first row's number among the group's rows
 };
+// Where a CTA's share of the prefixes' work begins, from the plan: the item's group (as in groups), its number and
+// tile of rows, and in the tcgen05 kernel's units the share [u, u_end), the tile's first one, and all of them.
+struct KvShareBegin {
+    int4 group;
+    int64_t u, u_end, tile0, total;
+    int seq, tile, shares, pad;
+};
+static_assert(sizeof(KvShareBegin) == 64, "read as four pieces");
 struct KvShareDev {
+    KvShareBegin *begins;  // [grid of the tcgen05 kernel]
+    int64_t *group_at;     // [n_groups] the plan's own
     float *part;         // [2 grid][256][D], then (m, l) [2 grid][256][2]
     KvShareItem *items;  // [grid]
     uint2 *where;        // [T][Hq] last and first CTA with a piece of the row, 16 bits each, and its row in their blocks;
@@ -114,11 +124,11 @@ cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, co
 // (kOwn, behind the join: it waits before it reads the prefixes' results). plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
 // one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).
 // own_rows: rows of an item of launch_kv_decode_shared(kOwn), kv_decode_rows(max_new * G); it takes sequences of up to
-// max_rows.
+// max_rows. shares: kv_prefill_grid where launch_kv_prefill_shared(kPrefix) is next, else 0.
 constexpr int kDecodeUnit = 64, kDecodeHeadUnits = 4;
 inline int kv_decode_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 24; }
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
-                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows,
+                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows, int shares,
                                  const KvShareDev &share, cudaStream_t stream);
 cudaError_t launch_kv_decode_shared(KvMode mode, const KvDev &kv, bool int8, const KvBatchDev &b, const KvAttn &a,
                                     const KvShareDev &share, int max_new, int max_rows, float *part, int *count,

@@ -88,7 +88,7 @@ struct Cfg {
 
 // One segment of the CTA's share, as the warp that walks the share hands it to the others.
 struct Segment {
-    int seq, row0, n, L;    // the sequence (row0: its first row of the call's tensors)
+    int seq, row0, n, L;    // the sequence whose pages are read (row0: its first row of the call's tensors)
     int tile, head;         // block of 256 rows, kv head
     int lo, hi;             // its visible tokens
     int j0, j1;             // key tiles [j0, j1) of them; j1 == 0: no more segments
@@ -416,11 +416,11 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const uint4 (&v)[D / 3
 // position, -1: no row; finite: the row's weights are. A block of 8 columns where O is finite lacks
 // what the loading warps took out; one where it is not is worked out from all tokens again.
 template <int D, KvMode kMode>
-__device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const KvShareDev &share, const Segment *w,
+__device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, const Segment *w,
                                         int G, int window, int pos, bool finite, uint32_t tO)
 {
     const int lane = threadIdx.x & 31;
-    const int32_t *const table = kv_table<kMode>(b, share, w->seq);
+    const int32_t *const table = b.table + (int64_t)w->seq * b.table_stride;
     const int2 seen = seen_by_all<kMode>(w, G, window);
     const int end = min(w->hi, w->lo + w->j1 * kKeys);
 #pragma unroll 1
@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool odd = on && l == l && (zero[0] + zero[1]) + (zero[2] + zero[3]) != 0.0f;
                 if (__any_sync(0xffffffffu, odd || *const_cast<const volatile int *>(&w->bad)))
-                    add_bad<D, kMode>(kv, b, share, w, G, window, on ? pos : -1, on && l == l, tO);
+                    add_bad<D, kMode>(kv, b, w, G, window, on ? pos : -1, on && l == l, tO);
             }
             segment_done(seg);
             // a warp's rows of a piece: [D / 4][32][4], so that the warp writes 512 bytes at a time
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!w) break;
             const int j0 = w->j0, j1 = w->j1, rows = w->n * G, head = w->head, hi = w->hi;
             const int lo = w->lo + (lw & 1) * 64;
-            const int32_t *table = kv_table<kMode>(b, share, w->seq);
+            const int32_t *table = b.table + (int64_t)w->seq * b.table_stride;
             // cache row of the first token of the warp's group x of key tile j, and how many of the 16
             // there are
             auto group = [&](int j, int x, int *count) -> int64_t {
@@ -1153,8 +1153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (t == 2) {
             // ------------------------------------------- the share, segment by segment
-            KvWork<kBlockRows, kKeys, kHeadUnits, kMode> w(kv, b, a, share, plan.min_rows, INT32_MAX, lane);
-            bool more = w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
+            KvWork<kBlockRows, kKeys, kHeadUnits, kMode> w(kv, b, a, share, plan.min_rows, INT32_MAX, lane,
+                                                           kMode != kPrefix);
+            bool more = kMode == kPrefix ? w.take_begin(share.begins[blockIdx.x])
+                                         : w.take_share(blockIdx.x, min((int64_t)gridDim.x, w.total));
             KvShareItem begun{-1, 0, 0, 0, 0, {0, 0, 0}};  // kPrefix: the item that begins here and ends elsewhere
             for (int seg = 0;; ++seg) {
                 if (!warp_wait(&bars.seg_empty[seg % kSegments], ((uint32_t)(seg / kSegments) & 1u) ^ 1u, &abort_flag,
@@ -1163,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 more = more && w.next();
                 Segment g{};
                 if (more) {
-                    g.seq = w.seq;
+                    g.seq = kMode == kPrefix ? w.sh.lo : w.seq;
                     g.row0 = w.sh.row0;
                     g.n = w.sh.n;
                     g.L = w.sh.L;

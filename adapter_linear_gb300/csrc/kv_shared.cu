@@ -7,27 +7,46 @@
 // all of them, and many rows fill the tcgen05 kernel's tiles where each sequence alone would read it again for
 // a handful of rows. Then every sequence attends to its own tokens, and the kernel that does this joins the two
 // where it writes its result. O1 is kept in fp32.
+#include <algorithm>
+
 #include "kv_prefill_kernel.cuh"
 
 namespace lora {
 namespace {
 
+// x / y, not negative
+__device__ __forceinline__ int64_t plan_div(int64_t x, int64_t y)
+{
+    return (x | y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // A group's prefix: what is asked for, but no further than the new tokens of any of its sequences, in
 // whole pages. A group of one sequence, or one with a sequence whose start or length is bad, has none.
+//
+// Then the kernels' work is counted here, once, not by every CTA of theirs, whose code and loads are cold (7 of the
+// 20 us of 8 sequences over 1000 tokens, 9 us of 256 sequences' own tokens). Two CTAs at the same time: the first
+// writes the groups and shares out the prefixes' units (begins), the second writes lo and numbers the items of
+// the own tokens.
+constexpr int kPlanGroups = 1024;  // whose sums shared memory holds
 __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDev b, const int32_t *seq_start,
                                                              const int32_t *prefix_len, int n_groups, int G, int own_rows,
-                                                             int max_rows, KvShareDev share)
+                                                             int max_rows, int shares, KvShareDev share)
 {
+    __shared__ int64_t sm_at[kPlanGroups], sm_sums[32];
     __shared__ int sm_items[32], sm_most[32];
     __shared__ unsigned long long sm_units;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const bool prefixes = blockIdx.x == 0;
+    int64_t *const at = n_groups <= kPlanGroups ? sm_at : share.group_at;
     pdl_launch_dependents();
-    for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) share.lo[i] = 0;
+    if (!prefixes)
+        for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) share.lo[i] = 0;
     bool ordered = true;
     for (int g = threadIdx.x; g < n_groups; g += blockDim.x)
         ordered = ordered && seq_start[g] >= 0 && seq_start[g] <= seq_start[g + 1] && seq_start[g + 1] <= b.n_seqs;
     ordered = __syncthreads_and(ordered);
     if (!ordered && threadIdx.x == 0) kv_flag_range(kv.err);
+    auto item_units = [&](int e) { return kHeadUnits + max(1, (e + kKeys - 1) / kKeys); };  // e tokens, a head, a tile
     for (int g = threadIdx.x >> 5; g < n_groups; g += blockDim.x >> 5) {
         const int s0 = ordered ? seq_start[g] : 0, s1 = ordered ? seq_start[g + 1] : 0;
         int before = INT32_MAX, first = INT32_MAX, rows = 0, with_rows = 0;
@@ -49,14 +68,70 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
         ok = __all_sync(0xffffffffu, ok) && with_rows > 1;
         int e = ok ? max(0, min(before, prefix_len[g])) : 0;
         e = e >> kv.page_shift << kv.page_shift;
-        if (lane == 0) share.groups[g] = e > 0 ? make_int4(first, e, b.start[first], rows) : make_int4(0, 0, 0, 0);
-        if (e > 0)
+        if (prefixes) {
+            if (lane == 0) {
+                share.groups[g] = e > 0 ? make_int4(first, e, b.start[first], rows) : make_int4(0, 0, 0, 0);
+                const int64_t tiles = ((int64_t)rows * G + kBlockRows - 1) / kBlockRows;
+                if (shares > 0) at[g] = e > 0 ? tiles * kv.H * item_units(e) : 0;
+            }
+        } else if (e > 0) {
             for (int i = s0 + lane; i < s1; i += 32) share.lo[i] = e;
+        }
+    }
+    __syncthreads();
+
+    if (prefixes) {
+        if (shares == 0) return;
+        int64_t total = 0;  // at[g]: from its units to those of the groups before it
+        for (int g0 = 0; g0 < n_groups; g0 += blockDim.x) {
+            const int g = g0 + threadIdx.x;
+            const int64_t mine = g < n_groups ? at[g] : 0;
+            int64_t x = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += o;
+            }
+            __syncthreads();
+            if (lane == 31) sm_sums[warp] = x;
+            __syncthreads();
+            x += total;
+            for (int y = 0; y < warps; ++y) {
+                total += sm_sums[y];
+                if (y < warp) x += sm_sums[y];
+            }
+            if (g < n_groups) at[g] = x - mine;
+        }
+        __syncthreads();
+        const int64_t n = min((int64_t)shares, total), q = n > 0 ? plan_div(total, n) : 0, r = total - q * n;
+        for (int c = threadIdx.x; c < shares; c += blockDim.x) {
+            KvShareBegin begin{};
+            if (c < n) {
+                begin.u = c * q + c * (int)r / (int)n;  // c total / n
+                begin.u_end = (c + 1) * q + (c + 1) * (int)r / (int)n;
+                int g = 0;
+                for (int hi = n_groups - 1; g < hi;) {  // the last whose units begin at u or before
+                    const int mid = (g + hi + 1) >> 1;
+                    if (at[mid] <= begin.u)
+                        g = mid;
+                    else
+                        hi = mid - 1;
+                }
+                begin.group = share.groups[g];
+                begin.seq = g;
+                const int64_t tile = (int64_t)item_units(begin.group.y) * kv.H;
+                begin.tile = (int)plan_div(begin.u - at[g], tile);
+                begin.tile0 = at[g] + begin.tile * tile;
+                begin.total = total;
+                begin.shares = (int)n;
+            }
+            share.begins[c] = begin;
+        }
+        return;
     }
 
     // the items of what is behind, a sequence a thread
     if (threadIdx.x == 0) sm_units = 0;
-    __syncthreads();
     int before = 0, most = 0;
     unsigned long long units = 0;
     for (int i0 = 0; i0 < b.n_seqs; i0 += blockDim.x) {
@@ -81,7 +156,7 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
             const int o = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += o;
         }
-        __syncthreads();
+        __syncthreads();  // (sm_units, too)
         if (lane == 31) sm_items[warp] = x;
         __syncthreads();
         const int w = lane < warps ? sm_items[lane] : 0;
@@ -207,15 +282,16 @@ cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, co
 }
 
 cudaError_t launch_kv_share_plan(const KvDev &kv, const KvBatchDev &b, const int32_t *seq_start,
-                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows,
+                                 const int32_t *prefix_len, int n_groups, int G, int own_rows, int max_rows, int shares,
                                  const KvShareDev &share, cudaStream_t stream)
 {
     const cudaError_t e = ensure_smem_attr((const void *)kv_share_plan_kernel, 0);
     if (e != cudaSuccess) return e;
-    // a sequence a thread, a group a warp
-    const int threads = (int)std::min<int64_t>(1024, 32 * (int64_t)std::max((b.n_seqs + 31) / 32, std::max(n_groups, 1)));
-    kv_share_plan_kernel<<<1, threads, 0, stream>>>(kv, b, seq_start, prefix_len, n_groups, G, own_rows, max_rows,
-                                                 share);
+    // a sequence a thread, a group a warp, a share a thread
+    const int64_t most = std::max<int64_t>({1, b.n_seqs, 32 * (int64_t)n_groups, shares});
+    const int threads = (int)std::min<int64_t>(1024, (most + 31) / 32 * 32);
+    kv_share_plan_kernel<<<2, threads, 0, stream>>>(kv, b, seq_start, prefix_len, n_groups, G, own_rows, max_rows, shares,
+                                                    share);
     return cudaGetLastError();
 }
 
