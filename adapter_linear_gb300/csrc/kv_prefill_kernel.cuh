@@ -472,6 +472,44 @@ __device__ __forceinline__ void add_bad(const KvDev &kv, const KvBatchDev &b, co
     tmem_st_wait();
 }
 
+// Tile t of a segment's rows of Q on their way into shared memory, by 128 threads; rows past the chunk's last
+// become zeros.
+template <int D>
+__device__ __forceinline__ void copy_q(const KvAttn &a, const Segment *w, int t, int tid, uint8_t *dst)
+{
+    constexpr int kLanes = D / 8, kRows = kTileRows / kLanes;
+    const int G = a.G, rows = w->n * G, r = tid / kLanes, c = tid % kLanes;
+    int q = w->tile * kBlockRows + t * kTileRows + r, i = div_g(a, q), g = q - i * G;  // row, its token and head
+    const int step_i = div_g(a, kRows), step_g = kRows - step_i * G;
+    const uint16_t *const src = a.Q + (int64_t)w->row0 * a.q_stride + (int64_t)w->head * G * D + c * 8;
+#pragma unroll 4
+    for (int x = 0; x < kTileRows / kRows; ++x) {
+        const bool on = q < rows;
+        cp_async16(smem_u32(dst + tile_off(r + x * kRows, c)), src + (on ? (int64_t)i * a.q_stride + g * D : 0),
+                   on ? 16u : 0u);
+        q += kRows;
+        i += step_i;
+        g += step_g;
+        if (g >= G) {
+            g -= G;
+            ++i;
+        }
+    }
+}
+// The same threads' values with their signs as the scale's (sign: of a pair).
+template <int D>
+__device__ __forceinline__ void sign_q(int tid, uint8_t *tile, uint32_t sign)
+{
+    constexpr int kLanes = D / 8;
+    if (sign == 0) return;
+#pragma unroll 1
+    for (int r = tid / kLanes; r < kTileRows; r += kTileRows / kLanes) {
+        uint4 *const at = reinterpret_cast<uint4 *>(tile + tile_off(r, tid % kLanes));
+        const uint4 u = *at;
+        *at = make_uint4(u.x ^ sign, u.y ^ sign, u.z ^ sign, u.w ^ sign);
+    }
+}
+
 template <int D, bool kInt8, KvMode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     kv_prefill_kernel(KvDev kv, KvBatchDev b, KvAttn a, KvShareDev share, Plan plan)
@@ -562,6 +600,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it += j1 - j0;
                 segment_done(seg);
                 continue;
+            }
+            if (seg == 0) {
+                uint8_t *const dst = smem + C::kQ + t * C::kTileBytes;
+                copy_q<D>(a, w, t, row_in_tile, dst);
+                cp_commit();
+                cp_wait<0>();
+                sign_q<D>(row_in_tile, dst, plan.q_sign);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_full[t]);
             }
             const int row = row_t + row_in_tile;
             const bool on = row < rows;
@@ -959,29 +1007,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             // Q: copies of both tiles' rows first, so that they cost one latency
-            constexpr int kLanesQ = D / 8, kRowsQ = kLoadWarps * 32 / kLanesQ;
-            const int qr = tid / kLanesQ, qc = tid % kLanesQ;
+            // (the first segment's come by the softmax warps, which have nothing else to do then)
             const int nt = w->tile * kBlockRows + kTileRows < rows ? 2 : 1;
-            int q = w->tile * kBlockRows + qr, qi = q / G, qg = q - qi * G;  // row, its token and head
-            const int step_i = kRowsQ / G, step_g = kRowsQ - step_i * G;
-            const uint16_t *const q_src = a.Q + (int64_t)w->row0 * a.q_stride + (int64_t)head * G * D + qc * 8;
             for (int t = 0; t < nt && ok; ++t) {
-                ok = warp_wait(&bars.q_empty[t], (nq[t]++ & 1u) ^ 1u, &abort_flag, kv.err);
-                if (!ok) break;
-#pragma unroll 4
-                for (int x = 0; x < kTileRows / kRowsQ; ++x) {
-                    // rows past the chunk's last become zeros
-                    const bool on = q < rows;
-                    cp_async16(smem_u32(smem + C::kQ + t * C::kTileBytes + tile_off(qr + x * kRowsQ, qc)),
-                               q_src + (on ? (int64_t)qi * a.q_stride + qg * D : 0), on ? 16u : 0u);
-                    q += kRowsQ;
-                    qi += step_i;
-                    qg += step_g;
-                    if (qg >= G) {
-                        qg -= G;
-                        ++qi;
-                    }
-                }
+                const uint32_t phase = nq[t]++;
+                if (seg == 0) continue;
+                ok = warp_wait(&bars.q_empty[t], (phase & 1u) ^ 1u, &abort_flag, kv.err);
+                if (ok) copy_q<D>(a, w, t, tid, smem + C::kQ + t * C::kTileBytes);
             }
             cp_commit();
             if (!ok) {
@@ -993,17 +1025,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 drop_bad(stages + (it % C::kStages) * C::kTileBytes, j0);
                 arrive(full[it % C::kStages]);
             }
-            cp_wait<0>();
-            for (int t = 0; t < nt; ++t) {
-                if (plan.q_sign) {
-#pragma unroll 1
-                    for (int r = qr; r < kTileRows; r += kRowsQ) {
-                        uint4 *const at = reinterpret_cast<uint4 *>(smem + C::kQ + t * C::kTileBytes + tile_off(r, qc));
-                        const uint4 u = *at;
-                        *at = make_uint4(u.x ^ plan.q_sign, u.y ^ plan.q_sign, u.z ^ plan.q_sign, u.w ^ plan.q_sign);
-                    }
+            if (seg > 0) {
+                cp_wait<0>();
+                for (int t = 0; t < nt; ++t) {
+                    sign_q<D>(tid, smem + C::kQ + t * C::kTileBytes, plan.q_sign);
+                    arrive(bars.q_full[t]);
                 }
-                arrive(bars.q_full[t]);
             }
             segment_done(seg);
             if (!ok) break;
