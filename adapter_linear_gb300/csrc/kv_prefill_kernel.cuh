@@ -526,6 +526,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.G, window = kMode == kPlain ? a.window : 0;
     Segment *const segs = reinterpret_cast<Segment *>(smem + C::kSegs);
+    // The first segment's Q comes by the softmax warps, which have nothing else to do then, while the loading warps
+    // convert the first tokens' codes: 64 requests with one 8-bit prefix 56 us, not 58. (An unquantised cache's have
+    // nothing to convert: 16 prompts of 16 answers 109 either way. In longer chunks what it does to the code costs
+    // more: 512 tokens over 32000 8-bit 375, not 359.)
+    constexpr bool kSoftQ = kMode == kPrefix && kInt8;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 segment_done(seg);
                 continue;
             }
-            if (seg == 0) {
+            if (kSoftQ && seg == 0) {
                 uint8_t *const dst = smem + C::kQ + t * C::kTileBytes;
                 copy_q<D>(a, w, t, row_in_tile, dst);
                 cp_commit();
@@ -1007,11 +1012,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             // Q: copies of both tiles' rows first, so that they cost one latency
-            // (the first segment's come by the softmax warps, which have nothing else to do then)
             const int nt = w->tile * kBlockRows + kTileRows < rows ? 2 : 1;
             for (int t = 0; t < nt && ok; ++t) {
                 const uint32_t phase = nq[t]++;
-                if (seg == 0) continue;
+                if (kSoftQ && seg == 0) continue;
                 ok = warp_wait(&bars.q_empty[t], (phase & 1u) ^ 1u, &abort_flag, kv.err);
                 if (ok) copy_q<D>(a, w, t, tid, smem + C::kQ + t * C::kTileBytes);
             }
@@ -1025,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 drop_bad(stages + (it % C::kStages) * C::kTileBytes, j0);
                 arrive(full[it % C::kStages]);
             }
-            if (seg > 0) {
+            if (!kSoftQ || seg > 0) {
                 cp_wait<0>();
                 for (int t = 0; t < nt; ++t) {
                     sign_q<D>(tid, smem + C::kQ + t * C::kTileBytes, plan.q_sign);
