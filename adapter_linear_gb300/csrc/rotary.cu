@@ -1,4 +1,13 @@
 // rotary.cu -- rotary positions: frequencies (host), and the kernel that rotates tensors of tokens.
+//
+// Pair i of a head at position p turns by the angle p f_i: (x, y) -> g (x cos - y sin, x sin + y cos), g the scaling's
+// factor; the other way round (inverse) with -sin. In fp32, each result rounded once to bf16.
+//
+// What bounds it: many tokens, HBM: a value is read and written once, and a token's angles are worked out once for all
+// its heads by the lanes that hold them. Few tokens: a launch and two loads that depend on nothing but the
+// position. Measured: 30011 tokens of 24 + 8 heads of 128 values, 64 of them rotated, out of a fused projection, 82 to
+// 84 us (5.9 TB/s, 87 % of the copy bandwidth; before lanes' runs filled sectors and L1 was given room 95); 64 tokens
+// of 32 + 8 heads 3.5 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
