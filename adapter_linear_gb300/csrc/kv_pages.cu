@@ -14,6 +14,7 @@
 
 #include <cooperative_groups.h>
 
+#include "device_common.cuh"
 #include "kv_pages_state.h"
 #include "kv_state.h"
 #include "launch_stream.h"
@@ -147,6 +148,7 @@ __device__ __forceinline__ void gather(cg::cluster_group &cluster, Told *mine, i
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     kv_pages_update_kernel(PagesDev p, const int32_t *parent, const int32_t *keep, const int32_t *room)
 {
+    pdl_launch_dependents();  // (the copies' kernel)
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Told mine;
     __shared__ int4 slots_here[kSlotsHere];
@@ -410,6 +412,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     kv_pages_compact_kernel(PagesDev p, int32_t *table_out, int32_t *refs_out)
 {
+    pdl_launch_dependents();  // (the copies' kernel)
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Told mine;
     __shared__ int sm[33], others[kCtas];
@@ -537,6 +540,7 @@ struct CopyList {
 
 __global__ void __launch_bounds__(256) kv_copy_kernel(KvDev kv, int row_bytes, CopyList list)
 {
+    pdl_wait_prior();  // (what is to be copied: the update's or compaction's kernel, which lets this one start)
     const int lane = threadIdx.x & 31;
     const int n = list.n_dev ? min(*list.n_dev, list.n) : list.n;
     const int tokens = 1 << kv.page_shift;
@@ -647,7 +651,7 @@ cudaError_t launch_kv_copy(const KvDev &kv, bool int8, const int32_t *src, const
     const int64_t slices = (((int64_t)row_bytes << kv.page_shift) + kSlice - 1) / kSlice;
     const int64_t units = (int64_t)n * 2 * kv.H * slices;
     const int64_t ctas = std::min<int64_t>((units + 7) / 8, 8 * (int64_t)num_sms);
-    return launch_stream(true, kv_copy_kernel, (unsigned)ctas, 256, stream, kv, row_bytes,
+    return launch_stream(true, true, kv_copy_kernel, (unsigned)ctas, 256, stream, kv, row_bytes,
                          CopyList{src, dst, rows, n_dev, n});
 }
 

@@ -190,7 +190,7 @@ cudaError_t launch_kv_write_rotary(const KvDev &kv, bool int8, const KvBatchDev 
     auto fn = rotary->layout == LORA_ROTARY_HALF ? pick(std::true_type()) : pick(std::false_type());
     const int per = 512 / kv.D;
     const RotaryGrid g(b.T, (a.Hq + per - 1) / per + 2 * ((kv.H + per - 1) / per), num_sms);
-    return launch_stream(g.streams, fn, g.ctas, RotaryGrid::kWarps * 32, stream, kv, b, rotary_view(rotary), a, g.parts);
+    return launch_stream(g.streams, false, fn, g.ctas, RotaryGrid::kWarps * 32, stream, kv, b, rotary_view(rotary), a, g.parts);
 }
 
 }  // namespace lora

@@ -9,9 +9,10 @@ namespace lora {
 
 // The library's kernels ask for the largest shared memory, so that an SM need not be emptied between two of them.
 // That leaves L1 28 KB, and loads wait for room in it: a kernel that streams (large calls) asks for L1 instead
-// (pages of a compaction, 778 MB: 143 us, so 125).
+// (pages of a compaction, 778 MB: 143 us, so 125). early: the kernel waits by itself for the one ahead of it.
 template <class... Params, class... Args>
-cudaError_t launch_stream(bool streams, void (*fn)(Params...), unsigned ctas, int threads, cudaStream_t stream, Args &&...args)
+cudaError_t launch_stream(bool streams, bool early, void (*fn)(Params...), unsigned ctas, int threads, cudaStream_t stream,
+                          Args &&...args)
 {
     const cudaError_t e = ensure_smem_attr((const void *)fn, 0);
     if (e != cudaSuccess) return e;
@@ -19,11 +20,18 @@ cudaError_t launch_stream(bool streams, void (*fn)(Params...), unsigned ctas, in
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(threads);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
-    attr[0].val.sharedMemCarveout = cudaSharedmemCarveoutMaxL1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (streams) {
+        attr[n].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+        attr[n++].val.sharedMemCarveout = cudaSharedmemCarveoutMaxL1;
+    }
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = streams ? 1 : 0;
+    cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, fn, std::forward<Args>(args)...);
 }
 

@@ -210,7 +210,7 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
     int64_t all = 0;  // blocks of a token
     for (int i = 0; i < n; ++i) all += (x.heads[i] + per - 1) / per;
     const RotaryGrid g(T, all, sms);
-    CUDA_TRY(launch_stream(g.streams, fn, g.ctas, RotaryGrid::kWarps * 32, stream, rotary_view(rotary), x, head_dim,
+    CUDA_TRY(launch_stream(g.streams, false, fn, g.ctas, RotaryGrid::kWarps * 32, stream, rotary_view(rotary), x, head_dim,
                            positions, T, (int)(inverse != 0), g.parts));
     return LORA_OK;
 }
