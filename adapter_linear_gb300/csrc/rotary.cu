@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(RotaryGrid::kWarps * 32, RotaryGrid::kCtas)
     rotary_kernel(const __grid_constant__ RotaryDev rot, const __grid_constant__ Tensors x, int head_dim,
                   const int32_t *__restrict__ positions, int T, int inverse, int parts)
 {
+    pdl_wait_prior();  // (its start overlaps the end of the kernel ahead: many tokens, call after call, 84 us, so 81.5)
     const int lane = threadIdx.x & 31;
     const int lanes = head_dim / 16, per = 32 / lanes;  // lanes of a row, rows of a block
     const int sub = lane / lanes, c = lane - sub * lanes;
@@ -210,7 +211,7 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, int n, const lora_rotar
     int64_t all = 0;  // blocks of a token
     for (int i = 0; i < n; ++i) all += (x.heads[i] + per - 1) / per;
     const RotaryGrid g(T, all, sms);
-    CUDA_TRY(launch_stream(g.streams, false, fn, g.ctas, RotaryGrid::kWarps * 32, stream, rotary_view(rotary), x, head_dim,
+    CUDA_TRY(launch_stream(g.streams, true, fn, g.ctas, RotaryGrid::kWarps * 32, stream, rotary_view(rotary), x, head_dim,
                            positions, T, (int)(inverse != 0), g.parts));
     return LORA_OK;
 }
