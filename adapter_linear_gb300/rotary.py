@@ -72,7 +72,7 @@ class Rotary:
         way round (the gradient). Runs on the current stream or on `stream`."""
         if positions.dtype is not torch.int32 or positions.dim() != 1 or not positions.is_contiguous():
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: positions are contiguous int32 [T]")
-        xs = tuple(tensors)
+        xs = tensors if type(tensors) is tuple else tuple(tensors)
         n, device, T = len(xs), positions.get_device(), positions.shape[0]
         if not 1 <= n <= LORA_ROTARY_MAX_TENSORS or (out is not None and len(out) != n):
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: one to four tensors, as many results")
@@ -87,19 +87,20 @@ class Rotary:
                 other = torch.cuda.ExternalStream(stream, positions.device) if isinstance(stream, int) else stream
             handle = where
         fields, results = [], []
-        for x, (at, stride, heads) in zip(xs, given):
+        for i, x in enumerate(xs):
+            stride, heads = given[i]
             if out is not None:
-                y = out[len(results)]
-                to, to_stride, _ = self._rows(y, heads, T, D, device)
+                y = out[i]
+                to_stride, _ = self._rows(y, heads, T, D, device)
             else:
                 if other is None:
                     y = torch.empty_like(x, memory_format=torch.contiguous_format)
                 else:
                     with torch.cuda.stream(other):  # it belongs to the stream that writes it
                         y = torch.empty_like(x, memory_format=torch.contiguous_format)
-                to, to_stride = y.data_ptr(), heads * D
+                to_stride = heads * D
             results.append(y)
-            fields += (at, to, stride, to_stride, heads, 0)
+            fields += (x.data_ptr(), y.data_ptr(), stride, to_stride, heads, 0)
         if other is not None:
             for t in (*xs, *results, positions):
                 t.record_stream(other)
@@ -109,14 +110,17 @@ class Rotary:
 
     @staticmethod
     def _rows(x, heads, T, D, device):
-        """Address, token stride and heads of x, a bf16 [T, heads, D] tensor with contiguous heads."""
-        if x.dim() != 3 or x.dtype is not torch.bfloat16:
+        """Token stride and heads of x, a bf16 [T, heads, D] tensor with contiguous heads."""
+        if x.dtype is not torch.bfloat16 or x.dim() != 3:
             raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, heads, {D}] expected")
-        (t, h, d), (st, sh, sd) = x.shape, x.stride()
+        t, h, d = x.shape
         if t != T or d != D or (heads is not None and h != heads):
             raise LoraError(LORA_ERR_SHAPE, f"lora_rotary_apply: bfloat16 [{T}, {heads or 'heads'}, {D}] expected")
         if x.get_device() != device:
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the tensors of a call are on one GPU")
+        if x.is_contiguous():
+            return h * D, h
+        st, sh, sd = x.stride()
         if (sd != 1 and D > 1) or (sh != D and h > 1):
             raise LoraError(LORA_ERR_ARG, "lora_rotary_apply: the heads of a token must be contiguous")
-        return x.data_ptr(), st if T > 1 else h * D, h
+        return st if T > 1 else h * D, h
