@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
         const int64_t avg = total / items - kHeadUnits + 1;
         int64_t best = total / gridDim.x + 3 * kEnds;  // cut
 #pragma unroll
-        for (int teams = 1; teams <= C::kTeams; teams *= 2) {
+        for (int teams = 1; teams <= C::kTeams && sums.x >= 0; teams *= 2) {
             const int64_t n = (int64_t)gridDim.x * teams, turns = (items + n - 1) / n;
             const int64_t time = teams * max((int64_t)sums.y, turns * avg) + turns * kEnds;
             if (time < best) {

@@ -92,7 +92,7 @@ struct KvShareDev {
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]
     // Work of the short-chunk kernel on the sequences' own tokens: the first item of each sequence [n_seqs + 1],
-    // and of all {items, the most units of one, units (64 bits, the lower half first)}.
+    // and of all {items (-1: too many to be numbered), the most units of one, units (64 bits, the lower half first)}.
     int32_t *own_first;
     int4 *own_sums;
     float *O;      // [T][Hq][D]

@@ -18,6 +18,7 @@
 // own, bf16, 109 us (365 MB: 3.4 TB/s); 3 groups of 16 over 9000 to 16000 with 3 to 6 new tokens, 8-bit, 148 us
 // (0.32 PFLOP/s).
 #include <algorithm>
+#include <climits>
 
 #include "kv_prefill_kernel.cuh"
 
@@ -43,7 +44,7 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
                                                              int max_rows, int shares, KvShareDev share)
 {
     __shared__ int64_t sm_at[kPlanGroups], sm_sums[32];
-    __shared__ int sm_items[32], sm_most[32];
+    __shared__ int sm_most[32];
     __shared__ unsigned long long sm_units;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const bool prefixes = blockIdx.x == 0;
@@ -90,27 +91,31 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
     }
     __syncthreads();
 
+    // total plus `mine` of the threads before this one; then all of the block's are in total, too
+    auto before_me = [&](int64_t mine, int64_t &total) {
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += o;
+        }
+        __syncthreads();
+        if (lane == 31) sm_sums[warp] = x;
+        __syncthreads();
+        x += total - mine;
+        for (int y = 0; y < warps; ++y) {
+            total += sm_sums[y];
+            if (y < warp) x += sm_sums[y];
+        }
+        return x;
+    };
     if (prefixes) {
         if (shares == 0) return;
         int64_t total = 0;  // at[g]: from its units to those of the groups before it
         for (int g0 = 0; g0 < n_groups; g0 += blockDim.x) {
             const int g = g0 + threadIdx.x;
-            const int64_t mine = g < n_groups ? at[g] : 0;
-            int64_t x = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += o;
-            }
-            __syncthreads();
-            if (lane == 31) sm_sums[warp] = x;
-            __syncthreads();
-            x += total;
-            for (int y = 0; y < warps; ++y) {
-                total += sm_sums[y];
-                if (y < warp) x += sm_sums[y];
-            }
-            if (g < n_groups) at[g] = x - mine;
+            const int64_t x = before_me(g < n_groups ? at[g] : 0, total);
+            if (g < n_groups) at[g] = x;
         }
         __syncthreads();
         const int64_t n = min((int64_t)shares, total), q = n > 0 ? plan_div(total, n) : 0, r = total - q * n;
@@ -140,9 +145,11 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
         return;
     }
 
-    // the items of what is behind, a sequence a thread
+    // the items of what is behind, a sequence a thread (starts that decrease may make more than 2^31: then they have
+    // no numbers)
     if (threadIdx.x == 0) sm_units = 0;
-    int before = 0, most = 0;
+    int64_t before = 0;
+    int most = 0;
     unsigned long long units = 0;
     for (int i0 = 0; i0 < b.n_seqs; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
@@ -160,19 +167,8 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
                 most = max(most, n);
             }
         }
-        int x = tiles * kv.H;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += o;
-        }
-        __syncthreads();  // (sm_units, too)
-        if (lane == 31) sm_items[warp] = x;
-        __syncthreads();
-        const int w = lane < warps ? sm_items[lane] : 0;
-        x += __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
-        if (i < b.n_seqs) share.own_first[i] = before + x - tiles * kv.H;
-        before += __reduce_add_sync(0xffffffffu, w);
+        const int64_t x = before_me((int64_t)tiles * kv.H, before);  // (its barriers are sm_units', too)
+        if (i < b.n_seqs) share.own_first[i] = (int)x;
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 0) sm_most[warp] = most;
@@ -184,8 +180,8 @@ __global__ void __launch_bounds__(1024) kv_share_plan_kernel(KvDev kv, KvBatchDe
         most = __reduce_max_sync(0xffffffffu, lane < warps ? sm_most[lane] : 0);
         if (lane == 0) {
             units = sm_units * kv.H;
-            share.own_first[b.n_seqs] = before;
-            *share.own_sums = make_int4(before, most, (int)(uint32_t)units, (int)(units >> 32));
+            share.own_first[b.n_seqs] = (int)before;
+            *share.own_sums = make_int4(before <= INT_MAX ? (int)before : -1, most, (int)(uint32_t)units, (int)(units >> 32));
         }
     }
 }
