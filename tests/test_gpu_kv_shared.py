@@ -241,6 +241,30 @@ def test_bad_groups_share_nothing_and_are_reported():
     R.check_attention(O[:2], lse[:2], [x[:2] for x in want])
 
 
+@pytest.mark.parametrize("start", [-1, 0, 4, 10 ** 9])
+def test_bad_starts_are_reported_and_not_followed(start):
+    p = Shared(INT8, 2, 64, 16, [(64, [(9, 1), (20, 1)]), (32, [(5, 1), (6, 1), (7, 1)])], seed=1)
+    Q = p.queries(4)
+    want = R.attention(Q, p, 0.125)
+    starts = p.batch.start.clone()
+    starts[2] = start   # of sequences 1 and 2: one of them, or both, have none of the rows
+    batch = al.KvBatch(p.table, starts, p.batch.kv_len, p.T, 1)
+    O, lse = p.cache.attention_shared(Q, batch, p.groups, scale=0.125)
+    assert p.cache.check_errors() == al.LORA_ERR_RANGE
+    keep = {0: [3, 4], 4: [0, 4]}.get(start, [0, 3, 4])   # (rows that no other sequence has, too)
+    R.check_attention(O[keep], lse[keep], [x[keep] for x in want])
+
+
+@pytest.mark.parametrize("heads", [4, 8])   # the last group's rows: a short chunk's, or the tcgen05 kernel's
+def test_more_groups_and_sequences_than_a_block_has_threads(heads):
+    groups = [(16 * (1 + i % 3), [(1 + i % 5, 1), (2, 1)]) for i in range(1100)] + [(400, [(3 + i, 1) for i in range(5)])]
+    p = Shared(BF16, 1, 64, 16, groups, [(20, 1)], seed=2)
+    Q = p.queries(heads)
+    O, lse = p.cache.attention_shared(Q, p.batch, p.groups)
+    assert p.cache.check_errors() == al.LORA_OK
+    R.check_attention(O, lse, R.attention(Q, p, 0.125))
+
+
 def test_no_groups_is_the_plain_attention():
     p = Shared(INT8, 2, 64, 16, [(64, [(9, 1), (20, 1)])], seed=1)
     Q = p.queries(4)
