@@ -5,9 +5,9 @@
 //
 // What bounds it: many tokens, HBM: a value is read and written once, and a token's angles are worked out once for all
 // its heads by the lanes that hold them. Few tokens: a launch and two loads that depend on nothing but the
-// position. Measured: 30011 tokens of 24 + 8 heads of 128 values, 64 of them rotated, out of a fused projection, 82 to
-// 84 us (5.9 TB/s, 87 % of the copy bandwidth; before lanes' runs filled sectors and L1 was given room 95); 64 tokens
-// of 32 + 8 heads 3.5 us.
+// position. Measured: 30011 tokens of 24 + 8 heads of 128 values, 64 of them rotated, out of a fused projection, 81 us
+// (6.0 TB/s, 89 % of the copy bandwidth; before lanes' runs filled sectors and L1 was given room 95); 64 tokens
+// of 32 + 8 heads 3.3 us.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
