@@ -740,6 +740,7 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     // The short-chunk kernel, a few rows a CTA, reads the pieces of the prefix's output itself. The other, a thread a
     // row, would take 40 us for 20 of them: then they are joined first.
     share.pieces = wide && !prefill;
+    share.pieces_grid = kv_prefill_grid(p->num_sms);
     share.own_sums = share.groups + batch->n_seqs;
     share.group_at = reinterpret_cast<int64_t *>(share.own_sums + 1);
     share.lo = reinterpret_cast<int32_t *>(share.group_at + batch->n_seqs);

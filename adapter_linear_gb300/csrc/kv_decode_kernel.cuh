@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D, kInt8, kN, kMode>::kCtas)
                 float P = -INFINITY, l1 = 1.0f;
                 uint2 at = make_uint2(kJoined, 0);
                 if (sh.lo > 0 && r < rows) {
-                    if (share.pieces) at = share.where[out_row(r)];
+                    if (share.pieces) at = kv_where(share.where[out_row(r)], share.pieces_grid);
                     if (at.x == kJoined) {
                         P = share.lse2[out_row(r)];
                     } else {

@@ -80,6 +80,15 @@ struct KvShareBegin {
     int seq, tile, shares, pad;
 };
 static_assert(sizeof(KvShareBegin) == 64, "read as four pieces");
+// What where[row] says of the pieces [c0, c0 + n) of a row's prefix. After a wait of the prefix's kernel has run
+// out a row has none, and the word there is what the memory held before: then kJoined, whose O and lse2 are the row's own
+// places, so that nothing outside the scratch is read (grid: of the prefix's kernel).
+__host__ __device__ inline uint2 kv_where(uint2 w, int grid)
+{
+    const uint32_t c0 = w.x & 0xFFFFu, c1 = w.x >> 16;
+    if (w.x != kJoined && !(c0 <= c1 && c1 < (uint32_t)grid && w.y < (uint32_t)kShareRows)) w.x = kJoined;
+    return w;
+}
 struct KvShareDev {
     KvShareBegin *begins;  // [grid of the tcgen05 kernel]
     int64_t *group_at;     // [n_groups] the plan's own
@@ -88,6 +97,7 @@ struct KvShareDev {
     uint2 *where;        // [T][Hq] last and first CTA with a piece of the row, 16 bits each, and its row in their blocks;
                          // x == kJoined: none, O and lse2 are there
     bool pieces;         // read the pieces; else all are joined
+    int pieces_grid;     // the grid of the kernel that left them
     int64_t ml_at;       // where in part (m, l) begin
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]
