@@ -132,8 +132,15 @@ __device__ __forceinline__ void each_entry(const PagesDev &p, int cta, Begin beg
     });
 }
 
-// The end of a kernel whose CTAs read each other's shared memory: arrive when this one has, wait before it goes.
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed;"); }
+// A cluster barrier in two halves, which orders no memory beyond the CTA's own: the block's barrier ahead of it has
+// every thread's reads of another CTA's shared memory done, and what the threads wrote into their own there for each other.
+// The start of a kernel (all CTAs have started before the first reaches into another), and its end (arrive when
+// this CTA has read, wait before it goes).
+__device__ __forceinline__ void cluster_arrive()
+{
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 // value(told) of every CTA of the cluster into out[kCtas]; behind a cluster barrier, called by all threads.
@@ -166,7 +173,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
         kids[i] = 0;
         least[i] = INT_MAX;
     }
-    cluster_arrive_relaxed();  // all have started, before the first reaches into another's shared memory
+    cluster_arrive();  // all have started, before the first reaches into another's shared memory
     cluster_wait();
 
     // ---- 1: what is asked for. Each slot is read once, by one thread, which tells all CTAs where the slots fit
@@ -196,7 +203,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     gather(cluster, &mine, others, [](const Told &t) { return t.bad[0]; });
     for (int c = 0; c < kCtas; ++c) bad |= others[c];
     if (bad) {
-        cluster_arrive_relaxed();
+        cluster_arrive();
         if (tid == 0) {
             atomicOr(p.err, bad);
             *p.moves_n = 0;
@@ -367,7 +374,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                 }
         }
     if (bad) {
-        cluster_arrive_relaxed();
+        cluster_arrive();
         if (tid == 0) {
             atomicOr(p.err, bad);
             *p.moves_n = 0;
@@ -401,7 +408,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
                    p.table[(int64_t)s * p.W + j] = used ? x : -1;
                    if (counted && used && j >= entries(kept_of(me), p.shift)) p.refs[x] = 1;
                });
-    cluster_arrive_relaxed();  // nothing more of another CTA's shared memory
+    cluster_arrive();  // nothing more of another CTA's shared memory
     for (int s = tid; s < p.S; s += kCtas * kThreads) p.kv_len[s] = total_of(slots[s]);
     for (int k = tid; k < copies; k += kCtas * kThreads) p.moves[p.cap + k] = __ldcg(new_page(__ldcg(p.moves + p.cap + k)));
     if (tid == 0) *p.moves_n = copies;
@@ -474,7 +481,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) mine.need = holes;
     cluster.sync();
     gather(cluster, &mine, others, [](const Told &t) { return t.need; });
-    cluster_arrive_relaxed();  // nothing more of another CTA's shared memory
+    cluster_arrive();  // nothing more of another CTA's shared memory
     int moved = 0;
     for (int c = 0; c < kCtas; ++c) moved += others[c];
     moved = min(moved, p.P / 2 + 1);

@@ -196,6 +196,28 @@ def test_what_cannot_be_done_with_many_slots():
     t.update(parent=[i // 2 for i in range(1500)])
 
 
+@pytest.mark.parametrize("S", [256, 1024, 1030])
+def test_one_bad_slot_is_always_reported(S):
+    """Whichever of them it is, and so whichever thread of whichever CTA finds it, call after call: a CTA's error word
+    is cleared by other threads than those that set it."""
+    t = Pair(2 * S, 16, S, 2, ((BF16, 1, 64),))
+    t.update(room=[17] * S)
+    parent, room = ints(list(range(S))), ints([0] * S)
+    for i in sorted({0, 1, 2, 7, 8, 9, 63, 64, 255, S // 2, S - 9, S - 8, S - 2, S - 1} & set(range(S))):
+        for _ in range(8):
+            room[i] = 16                                           # one token more than its row of the table holds
+            t.pages.update(room=room)
+            assert t.pages.check_errors() == al.LORA_ERR_RANGE, i
+            room[i] = 0
+            parent[i] = S
+            t.pages.update(parent, None, room)
+            assert t.pages.check_errors() == al.LORA_ERR_RANGE, i
+            parent[i] = i
+    t.pages.update(parent, None, room)
+    assert t.pages.check_errors() == al.LORA_OK
+    t.check()
+
+
 def test_a_shared_page_that_slots_end_inside():
     """Tables of the caller's own making: with room alone the call says so, with a parent it mends them."""
     t = Pair(20, 16, 3, 8)
