@@ -36,9 +36,12 @@ constexpr int kBatch = 4;  // blocks loaded before any is stored
 template <bool kHalf>
 __global__ void __launch_bounds__(RotaryGrid::kWarps * 32, RotaryGrid::kCtas)
     rotary_kernel(const __grid_constant__ RotaryDev rot, const __grid_constant__ Tensors x, int head_dim,
-                  const int32_t *__restrict__ positions, int T, int inverse, int parts)
+                  const int32_t *positions, int T, int inverse, int parts)
 {
-    pdl_wait_prior();  // (its start overlaps the end of the kernel ahead: many tokens, call after call, 84 us, so 81.5)
+    // Its start overlaps the end of the kernel ahead (many tokens, call after call, 84 us, so 81.5), whose results are there
+    // from here on. They may be the positions, so these are not __restrict__: that would let them be read as memory that
+    // nothing writes while this kernel runs.
+    pdl_wait_prior();
     const int lane = threadIdx.x & 31;
     const int lanes = head_dim / 16, per = 32 / lanes;  // lanes of a row, rows of a block
     const int sub = lane / lanes, c = lane - sub * lanes;

@@ -156,6 +156,37 @@ def test_streams_and_graph():
     assert torch.equal(out, rot.apply((x,), pos)[0])
 
 
+@pytest.mark.parametrize("T", [64, 20000])
+def test_positions_that_the_kernel_ahead_writes(T):
+    """A call's kernel may start while the one ahead of it still runs: it turns by the positions that one leaves. Page
+    tables' updates let it start at once, call after call, and so from a graph; lengths are the positions."""
+    rot, S = al.Rotary(64), T
+    pages = al.KvPages(S, 16, S, 1)
+    x, room = rows(T, 2, 64, 1), torch.ones(S, dtype=torch.int32, device="cuda")
+
+    def three():
+        got = []
+        for _ in range(3):
+            pages.update(room=room)
+            got.append(rot.apply((x,), pages.kv_len)[0])
+        return got
+
+    first = three()
+    want = [rot.apply((x,), torch.full((T,), n, dtype=torch.int32, device="cuda"))[0] for n in range(1, 10)]
+    for n, y in enumerate(first):
+        assert torch.equal(y, want[n])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = three()
+    for n in (3, 6):
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, y in enumerate(got):
+            assert torch.equal(y, want[n + i])
+    assert pages.check_errors() == al.LORA_OK
+
+
 @pytest.mark.parametrize("fmt,Hq,H,D,page,lens,new,n,layout", [
     (INT8, 32, 8, 128, 16, [1, 17, 16, 400], [1, 5, 0, 203], 128, "half"),
     (INT8, 3, 1, 64, 32, [33, 1, 90], [33, 1, 7], 32, "interleaved"),
