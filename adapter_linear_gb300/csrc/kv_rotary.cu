@@ -18,10 +18,11 @@
 namespace lora {
 namespace {
 
-// Scale and codes of the 16 fp32 values of this lane; the row's kLanes lanes take part. As the write of bf16
-// rows quantises (kv_cache.cu), of which a bf16 x is a case: y = x (1 / s) is rounded to a multiple of 2^-11
-// and then to a whole number, so a code is off by at most 1/2 + 2^-12 + 2^-16 of a step, and a bf16 row's
-// codes are those of exact arithmetic.
+// Scale and codes of the 16 fp32 values of this lane; the row's kLanes lanes take part. y = x (1 / s) is corrected by what
+// it leaves of x, (x - y s) (1 / s) (Markstein 1990): x / s to half a step of fp32, and exactly where it is a number of
+// fp32, as ties are. So a code is within 1/2 + 2^-18 of a step of x, and a bf16 row's codes are those of exact arithmetic.
+// (The write of bf16 rows, kv_cache.cu, does with a rounding of y to a multiple of 2^-11 ahead of the one to a whole
+// number, which moves codes of fp32 values that lie 2^-12 beside a tie.)
 template <int kLanes>
 __device__ __forceinline__ uint4 quantise16f(const float (&x)[16], uint16_t *scale_bits)
 {
@@ -36,7 +37,7 @@ __device__ __forceinline__ uint4 quantise16f(const float (&x)[16], uint16_t *sca
     *scale_bits = finite ? (uint16_t)(__float_as_uint(s) >> 16) : (uint16_t)0x7FC0;
     const float inv = __frcp_rn(s);
     const uint64_t inv2 = pack2(inv, inv);
-    const uint64_t grid = pack2(6144.0f, 6144.0f), back = pack2(-6144.0f, -6144.0f);  // 1.5 2^12: multiples of 2^-11
+    const uint64_t neg = pack2(-s, -s);
     const uint64_t whole = pack2(12582912.0f, 12582912.0f);  // 1.5 2^23: the code in the low byte
     uint32_t c[4];
 #pragma unroll
@@ -44,8 +45,9 @@ __device__ __forceinline__ uint4 quantise16f(const float (&x)[16], uint16_t *sca
         uint32_t v[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+            const uint64_t xs = pack2(x[4 * q + 2 * e], x[4 * q + 2 * e + 1]), y = mul2(xs, inv2);
             float lo, hi;
-            unpack2(add2(add2(fma2(pack2(x[4 * q + 2 * e], x[4 * q + 2 * e + 1]), inv2, grid), back), whole), &lo, &hi);
+            unpack2(add2(fma2(fma2(y, neg, xs), inv2, y), whole), &lo, &hi);
             v[e] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x0040);
         }
         c[q] = finite ? __byte_perm(v[0], v[1], 0x5410) : 0u;

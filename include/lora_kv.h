@@ -107,7 +107,7 @@ lora_status lora_kv_write(lora_kv_t kv, const void *K, int64_t k_stride, const v
  * in fp32 and written (rounded once to bf16, or quantised from fp32 as above), V's are written as they are,
  * and, where n_heads > 0, Q ([T][n_heads][D]) is rotated into Q_out (rounded once), in one pass.
  * Scales and codes of V are those of lora_kv_write. K's come from fp32 values that are off by their
- * arithmetic (2^-21 of the pair's length): a code is within 1/2 + 2^-10 of a step of the exact
+ * arithmetic (2^-21 of the pair's length, factor included): a code is within 1/2 + 2^-13 of a step of the exact
  * value; a rotated value beyond the largest bf16 counts as an infinity. Q_out == Q (and its stride) rotates in
  * place; otherwise the two do not overlap. Rows of Q_out at positions below zero become zeros; those at
  * and after start[n_seqs] and those of a bad sequence are not written (Q's and K's are loaded).

@@ -239,6 +239,32 @@ def test_write_rotary(fmt, Hq, H, D, page, lens, new, n, layout):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("D,n", [(128, 128), (64, 64), (128, 32)])
+def test_codes_of_fp32_keys_are_rounded_once(D, n):
+    """Without an angle a key is fp32(x factor), what its code comes from is known: rint(that / scale), to even at a tie,
+    but for 2^-17 of a step beside a tie (the quotient in fp32: half of its 2^-17 below 128, twice that allowed). Keys
+    that are not rotated are bf16: exactly rint."""
+    H, L = 8, 3000
+    p = R.Paged(al, INT8, [L], [L], H, D, 16, seed=3)
+    K, V = rows(L, H, D, 5), rows(L, H, D, 6)
+    factor = torch.tensor(1.0123457, dtype=torch.float32)
+    p.cache.write_rotary(al.Rotary(n, freq=[0.0] * (n // 2), factor=float(factor)), K, V, p.batch)
+    assert p.cache.check_errors() == al.LORA_OK
+    pages, offs = p.where(0, torch.arange(L, device="cuda"))
+    x = K.float()
+    x[..., :n] *= factor.cuda()
+    s, code = p.cache.k_scales[pages, :, offs].double(), p.cache.k[pages, :, offs].double()
+    assert torch.equal(s.to(torch.bfloat16), R.bf16_of_f64((x.abs().amax(-1) / torch.full_like(x[..., 0], 127)).double()))
+    y = x.double() / s[..., None]
+    beside = (y - torch.floor(y) - 0.5).abs()
+    sure = (beside > 2.0 ** -17) | (torch.arange(D, device="cuda") >= n)
+    assert torch.equal(code[sure], torch.round(y)[sure])
+    # what a rounding to a multiple of 2^-11 ahead would have moved is among them
+    assert int((sure & (beside < 2.0 ** -12)).sum()) > 300
+    want, _ = R.quantise(V)
+    assert torch.equal(p.cache.v[pages, :, offs].double(), want)
+
+
 def test_write_rotary_strided_in_place_padded():
     p = R.Paged(al, INT8, [20, 7], [13, 2], 2, 64, 16, seed=9)
     rot = al.Rotary(64)
