@@ -315,7 +315,7 @@ class _Tensors:
 class KvPages:
     """The page tables of max_seqs sequences over num_pages pages of page_tokens tokens: `table` int32 [max_seqs,
     max_entries], `kv_len` int32 [max_seqs] and `refs` int32 [num_pages] (table entries that name a page),
-    device tensors that a KvBatch may name. tensors: (table, kv_len, refs) to use in place of new, empty ones.
+    tensors on the current GPU that a KvBatch may name. tensors: (table, kv_len, refs) to use in place of new, empty ones.
 
     Calls run on the current stream or on `stream`. They change the tables; KvCache.copy then makes the copies
     they ask for, in each cache."""
@@ -334,6 +334,8 @@ class KvPages:
         self._device = table.get_device()
         self._state(table, refs, "KvPages")
         self._slots(kv_len, "KvPages: kv_len")
+        if self._device != torch._C._cuda_getDevice():  # (the handle would be the current one's)
+            raise LoraError(LORA_ERR_ARG, "KvPages: the tensors are on the current GPU")
         self.table, self.kv_len, self.refs = table, kv_len, refs
         self.tensors = (table, kv_len, refs)
         h = ctypes.c_void_p()

@@ -62,6 +62,29 @@ def test_host_tensors_are_refused():
     assert e.value.status == al.LORA_ERR_SHAPE
 
 
+@pytest.mark.parametrize("current", [0, 1])
+def test_tensors_of_another_gpu_than_the_current_one_are_refused(current, monkeypatch):
+    """(The handle belongs to the current GPU, the calls' streams to the tensors'.)"""
+    from adapter_linear_gb300 import kv
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or al.LORA_OK
+
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    monkeypatch.setattr(kv, "load_library", Library)
+    tensors = (torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32))
+    if current == 1:
+        al.KvPages(8, 16, 2, 4, tensors=tensors)
+        assert calls == ["lora_kv_pages_create"]
+        return
+    with pytest.raises(al.LoraError) as e:
+        al.KvPages(8, 16, 2, 4, tensors=tensors)
+    assert e.value.status == al.LORA_ERR_ARG and calls == []
+
+
 def test_the_model():
     t = Tables(8, 16, 3, 4)
     assert t.update(room=[20, 16, 0]) == []
