@@ -81,7 +81,7 @@ class KvGroups:
 
 
 class KvCache:
-    """A paged cache of num_pages pages of page_tokens tokens for kv_heads heads of head_dim
+    """A paged cache on the current GPU, of num_pages pages of page_tokens tokens for kv_heads heads of head_dim
     values, bf16 or int8 with a bf16 scale per row. arenas: the tensors (k, v, k_scales,
     v_scales; the scales None for bf16) to use in place of newly allocated ones.
 
@@ -111,6 +111,8 @@ class KvCache:
         self._torch_device, self._device = k.device, k.get_device()
         if self._device < 0 or any(t is not None and t.get_device() != self._device for t in (v, ks, vs)):
             raise LoraError(LORA_ERR_ARG, "KvCache: the arenas are on one GPU")
+        if self._device != torch._C._cuda_getDevice():  # (the handle would be the current one's)
+            raise LoraError(LORA_ERR_ARG, "KvCache: the arenas are on the current GPU")
         self.k, self.v, self.k_scales, self.v_scales = k, v, ks, vs
         h = ctypes.c_void_p()
         _check(load_library().lora_kv_create(num_pages, page_tokens, kv_heads, head_dim, fmt, _ptr(k), _ptr(v),

@@ -85,6 +85,28 @@ def test_tensors_of_another_gpu_than_the_current_one_are_refused(current, monkey
     assert e.value.status == al.LORA_ERR_ARG and calls == []
 
 
+@pytest.mark.parametrize("current", [0, 1])
+def test_arenas_on_another_gpu_than_the_current_one_are_refused(current, monkeypatch):
+    from adapter_linear_gb300 import kv
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append(name) or al.LORA_OK
+
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current, raising=False)
+    monkeypatch.setattr(kv, "load_library", Library)
+    arenas = (*(torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16) for _ in "kv"), None, None)
+    if current == 1:
+        al.KvCache(4, 16, 2, 64, al.LORA_KV_BF16, arenas=arenas)
+        assert calls == ["lora_kv_create"]
+        return
+    with pytest.raises(al.LoraError) as e:
+        al.KvCache(4, 16, 2, 64, al.LORA_KV_BF16, arenas=arenas)
+    assert e.value.status == al.LORA_ERR_ARG and calls == []
+
+
 def test_the_model():
     t = Tables(8, 16, 3, 4)
     assert t.update(room=[20, 16, 0]) == []
