@@ -385,23 +385,25 @@ struct ShareSizes {
         total = groups + ((size_t)n_seqs + 1) * (sizeof(int4) + sizeof(int64_t) + 2 * sizeof(int32_t));
     }
 };
-lora_status ensure_share(lora_kv *p, size_t bytes)
+// most: of the block, where there is room for it (bytes do otherwise).
+lora_status ensure_share(lora_kv *p, size_t bytes, size_t most)
 {
     if (bytes <= p->share_bytes) return LORA_OK;
-    bytes = std::max(bytes, 2 * p->share_bytes);
     try {
         p->share_old.reserve(p->share_old.size() + 1);
     } catch (...) {
         return LORA_ERR_OOM;
     }
+    size_t size = std::max(bytes, most);
     void *block = nullptr;
-    if (cudaMalloc(&block, bytes) != cudaSuccess) {
+    while (cudaMalloc(&block, size) != cudaSuccess) {
         cudaGetLastError();
-        return LORA_ERR_OOM;
+        if (size == bytes) return LORA_ERR_OOM;
+        size = bytes;
     }
     if (p->share) p->share_old.push_back(p->share);
     p->share = block;
-    p->share_bytes = bytes;
+    p->share_bytes = size;
     return LORA_OK;
 }
 
@@ -695,7 +697,7 @@ lora_status lora_kv_reserve_shared(lora_kv_t p, int max_tokens, int n_heads, int
     if (n_heads < 1 || n_heads > 1024 || n_heads % p->H != 0) return LORA_ERR_SHAPE;
     if ((int64_t)max_tokens * n_heads > INT_MAX) return LORA_ERR_ARG;
     const lora_status st = lora_kv_reserve(p, max_tokens, n_heads, max_seqs);
-    return st == LORA_OK ? ensure_share(p, ShareSizes(p, max_tokens, n_heads, max_seqs).total) : st;
+    return st == LORA_OK ? ensure_share(p, ShareSizes(p, max_tokens, n_heads, max_seqs).total, 0) : st;
 }
 
 lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_stride, int n_heads,
@@ -726,7 +728,8 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     const bool wide = (int64_t)max_tokens * a.G > kDecodeRows;
     const ShareSizes sizes(p, batch->T, n_heads, batch->n_seqs);
     if ((prefill || wide) && (st = ensure_pre_part(p)) != LORA_OK) return st;
-    if ((st = ensure_share(p, sizes.total)) != LORA_OK) return st;
+    // (blocks that grow step by step stay few: a call that needs more than all before it takes twice what they had)
+    if ((st = ensure_share(p, sizes.total, 2 * p->share_bytes)) != LORA_OK) return st;
     char *const block = static_cast<char *>(p->share);
     KvShareDev share;
     share.part = reinterpret_cast<float *>(block + sizes.part);

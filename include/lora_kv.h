@@ -230,8 +230,10 @@ typedef struct lora_kv_groups {
                                    between kernels                                      */
 } lora_kv_groups;
 
-/* As lora_kv_reserve, for lora_kv_attention_shared: the first call of a size allocates what it needs
- * (50 MB, T * n_heads * (D + 3) floats and lora_kv_reserve's; what a larger call replaces is freed with the handle). */
+/* As lora_kv_reserve, for lora_kv_attention_shared: 50 MB, T * n_heads * (D + 3) floats and lora_kv_reserve's. A call
+ * that needs more than the handle has allocates it, and twice what the handle had where that is more and there is room;
+ * this allocates no more than its size needs. What a larger block replaces is freed with the handle (a captured
+ * graph may name it). */
 lora_status lora_kv_reserve_shared(lora_kv_t kv, int max_tokens, int n_heads, int max_seqs);
 
 /*

@@ -203,6 +203,30 @@ def test_scratch_that_grows_leaves_captured_calls_theirs():
     assert torch.equal(O, want)
 
 
+def test_a_reservation_takes_what_its_size_needs():
+    """And not twice what an earlier one took; a call of that size then takes nothing."""
+    p = Shared(BF16, 1, 64, 16, [(64, [(9, 1)] * 8)], seed=8)
+
+    def taken(call):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        call()
+        torch.cuda.synchronize()
+        return before - torch.cuda.mem_get_info()[0]
+
+    taken(lambda: p.cache.reserve_shared(10, 4, 8))                # (and lora_kv_reserve's 40 MB)
+    for tokens in (200000, 230000, 240000):
+        # O, lse and a place of 8 bytes a row and head; pieces of 256 and 48 rows an SM twice; whole 2 MB from the driver
+        sms = torch.cuda.get_device_properties(0).multi_processor_count
+        need = tokens * 4 * (64 + 3) * 4 + 2 * sms * (256 + 48) * (64 + 2) * 4
+        assert need <= taken(lambda: p.cache.reserve_shared(tokens, 4, 8)) <= need + 8e6
+    assert taken(lambda: p.cache.reserve_shared(240000, 4, 8)) == 0
+    Q = p.queries(4)
+    O, lse = torch.empty_like(Q), torch.empty(p.T, 4, device="cuda")
+    assert taken(lambda: p.cache.attention_shared(Q, p.batch, p.groups, O=O, lse=lse)) < 4e6   # (code that is loaded)
+    R.check_attention(O, lse, R.attention(Q, p, 0.125))
+
+
 def test_calls_on_two_streams():
     p = Shared(INT8, 8, 128, 16, [(3000, [(40 + i, 1) for i in range(64)])], seed=8)
     a, b = p.queries(32, 1), p.queries(32, 2)
