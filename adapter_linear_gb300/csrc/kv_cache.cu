@@ -727,7 +727,7 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
     const bool wide = (int64_t)max_tokens * a.G > kDecodeRows;
     const ShareSizes sizes(p, batch->T, n_heads, batch->n_seqs);
-    if ((prefill || wide) && (st = ensure_pre_part(p)) != LORA_OK) return st;
+    if (prefill && (st = ensure_pre_part(p)) != LORA_OK) return st;  // (the prefix's pieces are in the shared scratch)
     // (blocks that grow step by step stay few: a call that needs more than all before it takes twice what they had)
     if ((st = ensure_share(p, sizes.total, 2 * p->share_bytes)) != LORA_OK) return st;
     char *const block = static_cast<char *>(p->share);

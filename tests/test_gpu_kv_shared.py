@@ -227,6 +227,24 @@ def test_a_reservation_takes_what_its_size_needs():
     R.check_attention(O, lse, R.attention(Q, p, 0.125))
 
 
+def test_short_chunks_behind_a_wide_prefix_take_no_other_scratch():
+    """The tcgen05 kernel leaves a prefix's pieces in the shared scratch, not in the 40 MB of its own."""
+    taken = []
+    for cache in range(2):                                         # (the first call's kernels are loaded)
+        p = Shared(INT8, 1, 128, 16, [(2000, [(9, 1)] * 40)], seed=8)
+        Q = p.queries(4)
+        O, lse = torch.empty_like(Q), torch.empty(p.T, 4, device="cuda")
+        want = R.attention(Q, p, 128 ** -0.5)
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        p.cache.attention_shared(Q, p.batch, p.groups, O=O, lse=lse)
+        torch.cuda.synchronize()
+        taken.append(before - torch.cuda.mem_get_info()[0])
+        R.check_attention(O, lse, want)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert taken[1] <= 2 * sms * (256 + 48) * (128 + 2) * 4 + 8e6
+
+
 def test_calls_on_two_streams():
     p = Shared(INT8, 8, 128, 16, [(3000, [(40 + i, 1) for i in range(64)])], seed=8)
     a, b = p.queries(32, 1), p.queries(32, 2)
