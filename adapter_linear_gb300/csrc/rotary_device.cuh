@@ -6,12 +6,12 @@
 
 namespace lora {
 
-// The rotation as the kernels see it (a kernel parameter: lanes read their own entries of `step`).
+// The rotation as the kernels see it (a kernel parameter: lanes read their own entries of `step`). Its layout, pairs
+// (i, i + dim / 2) or else (2 i, 2 i + 1), is the kernels' kHalf.
 struct RotaryDev {
     uint64_t step[LORA_ROTARY_MAX_DIM / 2];  // of a pair: turns from one position to the next, times 2^64
     float factor;
     int dim;    // values of a head that are rotated, a multiple of 16
-    int half;   // pairs (i, i + dim / 2), else (2 i, 2 i + 1): the kernels' kHalf
 };
 
 // A lane holds 16 values of a head as two runs of 8, one of each half of the rotated values (or of the others), so that
@@ -128,7 +128,6 @@ inline RotaryDev rotary_view(const lora_rotary *r)
     for (int i = 0; i < LORA_ROTARY_MAX_DIM / 2; ++i) v.step[i] = r->step[i];
     v.factor = r->factor;
     v.dim = r->rotary_dim;
-    v.half = r->layout == LORA_ROTARY_HALF;
     return v;
 }
 
