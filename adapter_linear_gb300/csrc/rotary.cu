@@ -160,9 +160,11 @@ lora_status lora_rotary_init(int rotary_dim, int layout, const double *freq, dou
     r.layout = layout;
     r.factor = (float)factor;
     for (int i = 0; i < rotary_dim / 2; ++i) {
-        double turns = freq[i] / kTwoPi;
-        turns -= std::floor(turns);                       // in [0, 1], 1 by rounding
-        r.step[i] = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
+        // (of the magnitude, whose fraction is exact: that of a small negative number would lose its last bits beside 1)
+        double turns = std::fabs(freq[i]) / kTwoPi;
+        turns -= std::floor(turns);
+        const uint64_t step = (uint64_t)std::ldexp(turns, 64);
+        r.step[i] = freq[i] < 0.0 ? 0 - step : step;
     }
     *out = r;
     return LORA_OK;

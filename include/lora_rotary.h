@@ -11,8 +11,8 @@
  *
  * The angle is reduced in fixed point: freq[i] / 2 pi is held as a fraction of 2^64 turns, so p times it
  * modulo one turn is exact, and a far position costs no precision: an angle is off by less than 2^-22
- * (plus |p| times what the fp64 freq[i] is off by). Sine, cosine and the products are fp32, and a
- * result is rounded once.
+ * (plus 2^-51 |p freq[i]|, the roundings of freq[i] and of its quotient in fp64). Sine, cosine and the
+ * products are fp32, and a result is rounded once.
  */
 #ifndef LORA_ROTARY_H
 #define LORA_ROTARY_H

@@ -1,5 +1,6 @@
 """Rotary positions without a GPU: the frequencies of every scaling, the fixed-point steps, refusals."""
 import ctypes
+import fractions
 import math
 
 import pytest
@@ -69,6 +70,18 @@ def test_steps_are_the_frequencies_in_turns():
         # fp64's rounding of the quotient and of its fraction
         assert abs((got - turns + 0.5) % 1.0 - 0.5) <= 2.0 ** -52 * max(1.0, abs(turns))
     assert list(r.struct.step[8:]) == [0] * 120 and r.struct.factor == 2.0
+
+
+def test_negative_frequencies_turn_back_as_far():
+    freq = [0.25, 1e-3, 1e-7, 1e-12, 3.0, 2 * math.pi, 7.5, 1.0]
+    there, back = (Rotary(16, freq=[sign * f for f in freq]).struct.step[:8] for sign in (1, -1))
+    assert [(a + b) % 2 ** 64 for a, b in zip(there, back)] == [0] * 8
+    # against pi to 40 digits: the quotient's rounding and 2 pi's, 2^-52 of it together, and what 2^-64 cuts off
+    two_pi = 2 * fractions.Fraction("3.1415926535897932384626433832795028841972")
+    for f, step in zip(freq, back):
+        turns = fractions.Fraction(f) / two_pi
+        off = (fractions.Fraction(step, 2 ** 64) + turns) % 1
+        assert min(off, 1 - off) <= turns / 2 ** 52 + fractions.Fraction(1, 2 ** 64), f
 
 
 def test_refusals(lib):
