@@ -805,8 +805,12 @@ lora_status lora_kv_check_errors(lora_kv_t p)
 lora_status lora_kv_selftest_timeout(lora_kv_t p, lora_stream_t stream)
 {
     if (!p) return LORA_ERR_ARG;
+    CUDA_TRY(cudaStreamWaitEvent(stream, p->attn_ev, 0));
     kv_abandon_kernel<<<1, 256, 0, stream>>>(p->d_err, p->count, count_ints(p));
     CUDA_TRY(cudaGetLastError());
+    // what a shared prefix's kernel has not written there is anything: large numbers, as floats, too
+    if (p->share) CUDA_TRY(cudaMemsetAsync(p->share, 0x7f, p->share_bytes, stream));
+    CUDA_TRY(cudaEventRecord(p->attn_ev, stream));
     return note_kv_call(p, stream);
 }
 

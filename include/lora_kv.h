@@ -256,8 +256,9 @@ lora_status lora_kv_attention_shared(lora_kv_t kv, const void *Q, int64_t q_stri
  * synchronise their stream first.) */
 lora_status lora_kv_check_errors(lora_kv_t kv);
 
-/* Test hook: leave the cache as attention calls do whose bounded waits ran out (the error word, and
- * pieces of a split sequence that others wait to join). Nothing waits or fails on the device. */
+/* Test hook: leave the cache as attention calls do whose bounded waits ran out (the error word, pieces of a
+ * split sequence that others wait to join, and anything in the scratch of shared prefixes). Nothing waits or fails on
+ * the device. Not inside a capture. */
 lora_status lora_kv_selftest_timeout(lora_kv_t kv, lora_stream_t stream);
 
 #ifdef __cplusplus

@@ -245,6 +245,29 @@ def test_short_chunks_behind_a_wide_prefix_take_no_other_scratch():
     assert taken[1] <= 2 * sms * (256 + 48) * (128 + 2) * 4 + 8e6
 
 
+@pytest.mark.parametrize("fmt", [INT8, BF16])
+@pytest.mark.parametrize("groups", [
+    [(3000, [(9, 1), (2000, 1)])],                                 # the short-chunk kernel, twice
+    [(3000, [(40 + i, 1) for i in range(30)]), (500, [(9, 2)] * 9)],  # the tcgen05 kernel, its pieces read behind it
+    [(3000, [(90, 70), (300, 200), (5, 1)])],                      # its pieces joined, long chunks
+])
+def test_the_cache_works_again_after_a_timeout(groups, fmt):
+    """Which a hook stands in for: it leaves arrivals of pieces that no call waits for any more, and numbers in the
+    scratch that name no CTA and no row."""
+    p = Shared(fmt, 2, 128, 16, groups, seed=8)
+    Q = p.queries(8)
+    want = R.attention(Q, p, 128 ** -0.5)
+    first = p.cache.attention_shared(Q, p.batch, p.groups)
+    R.check_attention(*first, want)
+    p.cache.selftest_timeout()
+    assert p.cache.check_errors() == al.LORA_ERR_TIMEOUT and p.cache.check_errors() == al.LORA_OK
+    for _ in range(3):
+        O, lse = torch.full_like(Q, float("nan")), torch.full((p.T, 8), float("nan"), device="cuda")
+        p.cache.attention_shared(Q, p.batch, p.groups, O=O, lse=lse)
+        assert torch.equal(O, first[0]) and torch.equal(lse, first[1])
+    assert p.cache.check_errors() == al.LORA_OK
+
+
 def test_calls_on_two_streams():
     p = Shared(INT8, 8, 128, 16, [(3000, [(40 + i, 1) for i in range(64)])], seed=8)
     a, b = p.queries(32, 1), p.queries(32, 2)
