@@ -744,6 +744,9 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     // row, would take 40 us for 20 of them: then they are joined first.
     share.pieces = wide && !prefill;
     share.pieces_grid = kv_prefill_grid(p->num_sms);
+    // As precise as lora_kv_attention: a short chunk's weights have 16 bits there, a longer one's need not. (8 prompts of
+    // 300 tokens behind 2000 8-bit 206 us with, 192 without, bf16 183 and 165.)
+    share.two_parts = decode;
     share.own_sums = share.groups + batch->n_seqs;
     share.group_at = reinterpret_cast<int64_t *>(share.own_sums + 1);
     share.lo = reinterpret_cast<int32_t *>(share.group_at + batch->n_seqs);

@@ -98,6 +98,7 @@ struct KvShareDev {
                          // x == kJoined: none, O and lse2 are there
     bool pieces;         // read the pieces; else all are joined
     int pieces_grid;     // the grid of the kernel that left them
+    bool two_parts;      // the tcgen05 kernel gives every weight of a prefix two bf16 parts
     int64_t ml_at;       // where in part (m, l) begin
     int4 *groups;  // a group's sequence whose pages are read, tokens of its prefix, first row, rows
     int32_t *lo;   // [n_seqs]

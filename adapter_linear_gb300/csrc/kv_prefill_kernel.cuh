@@ -38,10 +38,10 @@
 // A weight rounded to bf16 is off by up to 2^-8 of it, which averages out over many keys but shows
 // where one key holds much of a row's weight. So where a key may hold more than a quarter of
 // what its row has so far, the half's weights go to the product in two bf16 parts, the second with
-// the rest (a second product for that half: a piece's first keys, then rarely). A prefix that sequences share (kPrefix)
-// has all its weights in two parts, as the short-chunk kernel has, which each of the sequences alone would have gone to:
-// 64 requests over 8192 tokens 8-bit 57 us, 56 with the rule; 16 prompts of 16 answers bf16 114.5 and 109; 48 drafts
-// over 9000 to 16000 8-bit 163 and 150.
+// the rest (a second product for that half: a piece's first keys, then rarely). A prefix that short chunks share
+// (KvShareDev::two_parts) has all its weights in two parts, as the short-chunk kernel has, which each of them alone would
+// have gone to: 64 requests over 8192 tokens 8-bit 57 us, 56 with the rule; 16 prompts of 16 answers bf16 114.5 and 109;
+// 48 drafts over 9000 to 16000 8-bit 163 and 150.
 //
 // Work is shared out like the short-chunk kernel's: the grid's CTAs (one an SM) take equal
 // contiguous runs of 128-token units over all items, pieces of an item go to scratch as
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // nothing to convert: 16 prompts of 16 answers 109 either way. In longer chunks what it does to the code costs
     // more: 512 tokens over 32000 8-bit 375, not 359.)
     constexpr bool kSoftQ = kMode == kPrefix && kInt8;
-    constexpr bool kTwoParts = kMode == kPrefix;  // of every weight
+    const bool two_parts = kMode == kPrefix && share.two_parts;  // of every weight
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -685,10 +685,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int y = 0; y < kPart; y += 8) scale_p(tS + k0 - kPart + y, down);
                     }
                     const float mn = m == -INFINITY ? 0.0f : m;
-                    l += kInt8 && mask ? part_weights<kInt8, kInt8>(z, tS + k0, sc + k0, mn, kTwoParts || rest)
-                                       : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, kTwoParts || rest);
+                    l += kInt8 && mask ? part_weights<kInt8, kInt8>(z, tS + k0, sc + k0, mn, two_parts || rest)
+                                       : part_weights<kInt8, false>(z, tS + k0, sc + k0, mn, two_parts || rest);
                     thr = mn + fminf(fast_log2(l) - 1.58496f, 16.0f);  // a third of what the row has
-                    rest_half |= kTwoParts || rest;
+                    rest_half |= two_parts || rest;
                     if (x & 1) {
                         if (lane == 0)
                             reinterpret_cast<volatile uint8_t *>(&rest_flags[t][x >> 1])[warp & 3] = rest_half;

@@ -239,7 +239,8 @@ lora_status lora_kv_reserve_shared(lora_kv_t kv, int max_tokens, int n_heads, in
 /*
  * lora_kv_attention without a window, for a batch whose sequences share prefixes: every group's prefix is read
  * once, through the pages of its first sequence with rows. Same O and lse, but for the order of the sums: O of
- * the two parts is joined in fp32, and the prefix's weights are sums of two bf16 numbers however many rows there are. What is shared is the largest number of whole pages that holds at most
+ * the two parts is joined in fp32, and where the batch has sequences of up to 24 rows of a kv head (or max_new and T
+ * leave room for them) every weight of a prefix is the sum of two bf16 numbers. What is shared is the largest number of whole pages that holds at most
  * prefix_len[g] tokens and, for each of the group's sequences with rows, none of its new tokens; the rest is
  * read per sequence. A group of one sequence shares nothing. seq_start out of order or outside 0..n_seqs sets
  * the error word (LORA_ERR_RANGE), and nothing is shared. groups may be NULL (nothing is shared).

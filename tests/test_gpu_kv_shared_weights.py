@@ -1,5 +1,5 @@
 """The precision of the weights of a shared prefix: 16 bits or more each, as in the attention of every sequence by
-itself, however many rows share it."""
+itself, however many rows share it; in longer chunks, as there, those of keys that hold much of a row's weight."""
 import pytest
 import torch
 
@@ -16,7 +16,8 @@ CASES = [
     (32, 8, 128, 16, 1104, 40, 1),     # the tcgen05 kernel, one tile
     (8, 1, 64, 32, 3000, 100, 2),      # several blocks of rows, items in pieces
     (4, 4, 128, 64, 1300, 70, 3),
-    (16, 2, 64, 16, 2000, 3, 40),      # long chunks of their own
+    (16, 2, 64, 16, 2000, 3, 40),      # long chunks of their own: one part will do
+    (4, 2, 128, 32, 1500, 5, [30, 1]), # beside short ones
 ]
 
 
@@ -24,10 +25,10 @@ CASES = [
 @pytest.mark.parametrize("case", range(len(CASES)))
 def test_weights_of_a_prefix_keep_their_bits(case, fmt):
     Hq, H, D, page, pre, members, n = CASES[case]
-    pre = pre // page * page
-    p = R.Paged(al, fmt, [pre + n] * members, [n] * members, H, D, page, seed=410 + case)
+    pre, new = pre // page * page, [n] * members if isinstance(n, int) else (n * members)[:members]
+    p = R.Paged(al, fmt, [pre + x for x in new], new, H, D, page, seed=410 + case)
     p.table[1:, :pre // page] = p.table[0, :pre // page]
-    K, V, Q = E.rows_on_eight_keys(members * n, pre, members * n, Hq, H, D, 400 + case, "cuda")
+    K, V, Q = E.rows_on_eight_keys(p.T, pre, p.T, Hq, H, D, 400 + case, "cuda")
 
     def ints(*x):
         return torch.tensor(x, dtype=torch.int32, device="cuda")
@@ -36,15 +37,17 @@ def test_weights_of_a_prefix_keep_their_bits(case, fmt):
     p.cache.write(K[pre:], V[pre:], p.batch)
     if fmt == al.LORA_KV_INT8:
         K, V = (q * s[..., None] for q, s in map(R.quantise, (K, V)))
-    groups = al.KvGroups(ints(0, members), ints(pre), members * n)
+    groups = al.KvGroups(ints(0, members), ints(pre), p.T)
     got, _ = p.cache.attention_shared(Q, p.batch, groups, scale=1.0)
     assert p.cache.check_errors() == al.LORA_OK
-    for b in range(members):
-        own = slice(pre + b * n, pre + (b + 1) * n)
+    long = min(new) * Hq // H > 24
+    for b, n in enumerate(new):
+        rows = slice(p.start[b], p.start[b] + n)
+        own = slice(pre + p.start[b], pre + p.start[b] + n)
         k, v = (torch.cat((x[:pre], x[own])) for x in (K, V))
-        O, A, S, _ = W.exact(Q[b * n:(b + 1) * n], k, v, torch.arange(pre + 1, pre + n + 1, device="cuda"))
+        O, A, S, A_rest = W.exact(Q[rows], k, v, torch.arange(pre + 1, pre + n + 1, device="cuda"))
         # the own keys score 0, 11 and more below the others: of a row's weight they hold n 2^-15 at most, which one
         # bf16 part may miss by 2^-8 of that, times the largest value
-        rest = n * 2.0 ** -15 * v[pre:].double().abs().amax()
-        over = (got[b * n:(b + 1) * n].double() - O).abs() / W.bound(O, A, S, rest, pre + n)
+        rest = A_rest if long else n * 2.0 ** -15 * v[pre:].double().abs().amax()
+        over = (got[rows].double() - O).abs() / W.bound(O, A, S, rest, pre + n)
         assert (over <= 1).all(), f"{CASES[case]}: {float(over.max()):.3g} of the bound"
