@@ -147,6 +147,32 @@ def test_infinities_of_the_prefix(members, n, bad):
     assert ((lse - lse2).abs() <= 1e-4).all()
 
 
+@pytest.mark.parametrize("bad", [(float("inf"),), (float("nan"),), (float("inf"), float("-inf"))])
+@pytest.mark.parametrize("spread", [1.0, 30.0])
+def test_infinities_of_a_prefix_that_many_short_chunks_share(bad, spread):
+    """There every weight has two parts, the second zero or negative as often as not; with scores far apart most
+    weights are 0."""
+    p = Shared(BF16, 2, 64, 16, [(400, [(1 + i, 1) for i in range(40)]), (64, [(1, 1)] * 30)], seed=6)
+    for i, x in enumerate(bad):
+        pages, rows = p.where(0, torch.tensor([7 + 300 * i], device="cuda"))
+        p.cache.v[pages, 1, rows, 5] = x
+        p.cache.v[pages, 0, rows, 63 - i] = x
+    Q = p.queries(4)
+    O, lse = p.cache.attention_shared(Q, p.batch, p.groups, scale=0.125 * spread)
+    want, _ = p.cache.attention(Q, p.batch, scale=0.125 * spread)
+    assert not torch.isfinite(want[:40]).all() and torch.isfinite(want[40:]).all()
+    for f in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(f(O), f(want))
+    # the values beside them (whose V the reference has): a rounding of the output, 2^-8 of it, of each weight, 2^-16, and
+    # scores off by dz, as in check_attention
+    ref, lse64, A, S = R.attention(Q, p, 0.125 * spread)
+    dz = 2.0 ** -17 * S + 2.0 ** -20
+    bound = A * (2.0 ** -8 + 2.0 ** -16 + 2 * dz[..., None]) + 2.0 ** -100
+    good = torch.isfinite(want)
+    assert ((O.double() - ref).abs()[good] <= bound[good]).all()
+    assert ((lse.double() - lse64).abs() <= dz + 2.0 ** -20 * (1 + lse64.abs())).all()
+
+
 def test_queries_that_are_not_finite_reach_their_rows_only():
     p = Shared(INT8, 2, 128, 16, [(160, [(9, 1)] * 9)], seed=6)
     Q = p.queries(4)
