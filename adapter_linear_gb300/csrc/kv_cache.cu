@@ -720,8 +720,8 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     const KvAttn a = attention_view(p, Q, q_stride, n_heads, scale, 0, O, o_stride, lse);
     // The kernels of the sequences' own tokens: as for lora_kv_attention; of the prefixes: the short-chunk one
     // where no group has more rows than one tile of it. (It would take more in several tiles, reading the prefix again
-    // from L2 for each: one group of 32 rows over 1000, 4000, 16000 8-bit 22, 31, 47 us, the tcgen05 kernel 20, 29,
-    // 44; 8 groups 44, 71, 173 and 44, 75, 190; 64 rows 65, 96, 248 and 54, 83, 198; bf16 the more so.)
+    // from L2 for each: one group of 32 rows over 1000, 4000, 16000 8-bit 24, 33, 46 us, with the tcgen05 kernel 19, 24,
+    // 38; 8 groups 39, 68, 170 and 37, 68, 187; 64 rows 55, 88, 240 and 40, 72, 193; bf16 60, 94, 261 and 41, 65, 154.)
     const int max_new = std::min(batch->max_new, batch->T), max_tokens = std::min(groups->max_tokens, batch->T);
     const bool prefill = (int64_t)max_new * a.G > kDecodeRows;
     const bool decode = !prefill || batch->T < (int64_t)batch->n_seqs * max_new;
@@ -745,7 +745,7 @@ lora_status lora_kv_attention_shared(lora_kv_t p, const void *Q, int64_t q_strid
     share.pieces = wide && !prefill;
     share.pieces_grid = kv_prefill_grid(p->num_sms);
     // As precise as lora_kv_attention: a short chunk's weights have 16 bits there, a longer one's need not. (8 prompts of
-    // 300 tokens behind 2000 8-bit 206 us with, 192 without, bf16 183 and 165.)
+    // 300 tokens behind 2000 8-bit 206 us with, 194 without, bf16 183 and 167.)
     share.two_parts = decode;
     share.own_sums = share.groups + batch->n_seqs;
     share.group_at = reinterpret_cast<int64_t *>(share.own_sums + 1);

@@ -63,8 +63,9 @@ struct Cfg {
     static constexpr bool kWide = kRowBytes == 256;
     // 4 CTAs of 50 KB an SM (3 of 66 KB where two row tiles take the registers, 2 for three, which
     // spill at 3: 104 us against 81 for 32 drafts; rows of 256 bytes: 2 of 98 KB): 100 to
-    // 150 KB in flight beside the stages in use. (Two row tiles of an 8-bit cache, D = 128: 16 bytes a thread
-    // spill; the others none.)
+    // 150 KB in flight beside the stages in use. (Spills, bytes a thread: two row tiles of an 8-bit cache, D = 128, 16,
+    // over a prefix 8, behind one 36; behind a prefix also two tiles bf16, D = 64, 52, three bf16, D = 128, 56; the others
+    // none.)
     static constexpr int kStages = kWide || kN == 1 || (kN == 2 && kMode == kOwn) ? 3 : 4;
     static constexpr int kCtas = kWide || kN == 3 ? 2 : kN == 1 && kMode != kOwn ? 4 : 3;
     static constexpr int kRing = kStages * kStage;

@@ -131,9 +131,9 @@ size_t kv_share_part_floats(int D, int num_sms);
 cudaError_t launch_kv_share_join(const KvDev &kv, bool int8, const KvAttn &a, const KvShareDev &share, int num_sms,
                                  cudaStream_t stream);
 
-// Both for groups that share prefixes. early: the kernel may start before the one ahead of it has ended
-// (kOwn, behind the join: it waits before it reads the prefixes' results). plan fills share.groups and share.lo; the prefix's kernel is the short-chunk
-// one where no group has more than max_rows of that (max_tokens: bound of a group's tokens).
+// Both for groups that share prefixes. early: the kernel may start before the one ahead of it has ended; it waits for
+// that one itself, kPrefix before it reads the plan, kOwn before it reads the prefixes' results. The plan fills
+// share.groups and share.lo.
 // own_rows: rows of an item of launch_kv_decode_shared(kOwn), kv_decode_rows(max_new * G); it takes sequences of up to
 // max_rows. shares: kv_prefill_grid where launch_kv_prefill_shared(kPrefix) is next, else 0.
 constexpr int kDecodeUnit = 64, kDecodeHeadUnits = 4;

@@ -5,9 +5,11 @@
 // more. Whole pages are shared: refs[x] is the number of entries that name page x, and a page is free when that is 0.
 // A page that n_i ends inside stays with one slot (the lowest that ends there, if no other has all of it),
 // the others get a copy; new pages are the lowest free ones in order of slot and entry, so equal calls
-// give equal tables. Measured (tables of 16-token pages): 64 slots of up to 4000 tokens that keep theirs and get 5
-// more 12.4 us; 4 prompts of up to 6000 tokens forked into 256 slots 18.5 us; 300 slots over 24000 pages, 55 % used,
-// compacted, and 5900 pages of 64 KB copied, 136 us (5.7 TB/s).
+// give equal tables. Measured on the GPU (tables of 16-token pages): 64 slots of up to 4000 tokens that keep a number of
+// theirs and get 5 more 12.5 us; 4 prompts of up to 6000 tokens forked into 256 slots, and the copies, 18.5 us; room alone,
+// one token more for each of 64 slots of 2000 tokens 7.6 us, 256 of 1000 10.2, 1024 of 400 34, and the copies' kernel,
+// with nothing to do, 1.2 us more; the same trimmed to what they held before and extended 13, 18 and 74; 300 slots over
+// 24000 pages, 55 % used, compacted, and 5900 pages of 64 KB copied, 135 us (5.8 TB/s).
 #include <algorithm>
 #include <climits>
 #include <new>

@@ -4,10 +4,10 @@
 // The rotation is rotary.cu's; what it gives goes to the quantisation in fp32 (of the 8-bit formats: scale =
 // max(bf16(amax / 127), 2^-126), code = x / scale to the nearest), so that a key is rounded once. What bounds it:
 // HBM, and with an 8-bit cache nearly as much the instructions (40 % of the issue slots at 16 warps an SM, which 128
-// registers a thread allow): the quantisation's 16 values a lane wait for the row's maximum. Measured, 32 query heads
-// and 8 kv heads of 128 values: 8 prompts of 2048 tokens 8-bit 84 us (5.2 TB/s; the rotation and the write
-// one after the other read and write 1.3 times as much); 64 requests of one token 7 us (start, length, page
-// and row are loads that depend on one another).
+// registers a thread allow): the quantisation's 16 values a lane wait for the row's maximum. Measured on the GPU, 32 query
+// heads and 8 kv heads of 128 values: 8 prompts of 2048 tokens 8-bit 62 us (370 MB, 6.0 TB/s; the rotation and
+// the write one after the other read and write 1.3 times as much), bf16 66 us (403 MB, 6.1 TB/s; 4 bytes a thread
+// spill); 64 requests of one token 3.9 and 4.0 us (start, length, page and row are loads that depend on one another).
 #include <climits>
 #include <type_traits>
 

@@ -8,15 +8,18 @@
 // a handful of rows. Then every sequence attends to its own tokens, and the kernel that does this joins the two
 // where it writes its result. O1 is kept in fp32.
 //
-// What bounds it: the prefix's kernel takes 3500 (bf16) or 6200 (8-bit) cycles a key tile for two tiles of 128 rows
-// and hardly less for one, the softmax's as in kv_prefill_kernel.cuh, and 9 us of each call go by before its first
+// What bounds it: the prefix's kernel takes 4500 (bf16) or 7200 (8-bit) cycles a key tile of one or two tiles of 128
+// rows, the softmax's as in kv_prefill_kernel.cuh with both parts of every weight, and 9 us of each call go by before its first
 // scores: the plan 2, the share's first segment, tokens and Q 4, cold code of each role the rest. The own
 // tokens' kernel starts while it ends and waits for it only before its epilogue, which reads the prefix's pieces (19
 // of an item where one group's heads are all there is). Measured on the GPU, 32 query heads on 8 kv heads of 128
-// values: 8 sequences over one prefix of 1000, 8-bit, 18.5 us; 64 over 8192 with up to 500 of their own, 8-bit,
-// 56 us (prefix's kernel 33, own tokens' 30, overlapping); 16 groups of 16 over 500 to 4000 with up to 400 of their
-// own, bf16, 109 us (365 MB: 3.4 TB/s); 3 groups of 16 over 9000 to 16000 with 3 to 6 new tokens, 8-bit, 148 us
-// (0.32 PFLOP/s).
+// values: 8 sequences over one prefix of 1000, 8-bit, 19 us; 64 over 8192 with up to 500 of their own, 8-bit,
+// 58 us (prefix's kernel 34, own tokens' 30, overlapping); 16 groups of 16 over 500 to 4000 with up to 400 of their
+// own, bf16, 115 us (365 MB: 3.2 TB/s); 3 groups of 16 over 9000 to 16000 with 3 to 6 new tokens, 8-bit, 165 us
+// (0.29 PFLOP/s); 8 prompts of 300 behind 2000, 8-bit 194 us, bf16 167. Every sequence by itself
+// (lora_kv_attention, whose reads of common pages come from L2), 30 tokens of its own, 8-bit, and shared: 8 sequences
+// over 1000, 4000, 16000 tokens 14, 22, 49 us and 19, 24, 38; 64 sequences 33, 92, 316 and 30, 36, 55; the 8 prompts 155 and
+// 194. So it takes many short chunks over a long prefix to pay; long chunks did not in any case measured.
 #include <algorithm>
 #include <climits>
 

@@ -108,8 +108,8 @@ lora_status lora_kv_write(lora_kv_t kv, const void *K, int64_t k_stride, const v
  * and, where n_heads > 0, Q ([T][n_heads][D]) is rotated into Q_out (rounded once), in one pass.
  * Scales and codes of V are those of lora_kv_write. K's come from fp32 values that are off by their
  * arithmetic (2^-21 of the pair's length, factor included): a code is within 1/2 + 2^-13 of a step of the exact
- * value; a rotated value beyond the largest bf16 counts as an infinity. Q_out == Q (and its stride) rotates in
- * place; otherwise the two do not overlap. Rows of Q_out at positions below zero become zeros; those at
+ * value. A rotated value beyond fp32 is an infinity, in a bf16 cache and in Q_out also one that rounds beyond bf16.
+ * Q_out == Q (and its stride) rotates in place; otherwise the two do not overlap. Rows of Q_out at positions below zero become zeros; those at
  * and after start[n_seqs] and those of a bad sequence are not written (Q's and K's are loaded).
  * rotary: HOST, rotary_dim at most the cache's head_dim. n_heads: 0..1024.
  * Asynchronous on `stream`. Errors: ARG, SHAPE (rotary_dim, n_heads), CUDA.
@@ -240,9 +240,12 @@ lora_status lora_kv_reserve_shared(lora_kv_t kv, int max_tokens, int n_heads, in
  * lora_kv_attention without a window, for a batch whose sequences share prefixes: every group's prefix is read
  * once, through the pages of its first sequence with rows. Same O and lse, but for the order of the sums: O of
  * the two parts is joined in fp32, and where the batch has sequences of up to 24 rows of a kv head (or max_new and T
- * leave room for them) every weight of a prefix is the sum of two bf16 numbers. What is shared is the largest number of whole pages that holds at most
- * prefix_len[g] tokens and, for each of the group's sequences with rows, none of its new tokens; the rest is
- * read per sequence. A group of one sequence shares nothing. seq_start out of order or outside 0..n_seqs sets
+ * leave room for them) every weight of a prefix is the sum of two bf16 numbers. What is shared is the largest number
+ * of whole pages that holds at most prefix_len[g] tokens and, for each of the group's sequences with rows, none of its new
+ * tokens; the rest is read per sequence. It pays for many short chunks over a long prefix (one group of single tokens, 32
+ * heads on 8: from 16 sequences over 4000 tokens, or 8 over 16000; 64 over 1000 gain a tenth); for few rows, short
+ * prefixes and chunks of more than 24 rows a kv head lora_kv_attention is quicker (kv_shared.cu has both
+ * times). A group of one sequence shares nothing. seq_start out of order or outside 0..n_seqs sets
  * the error word (LORA_ERR_RANGE), and nothing is shared. groups may be NULL (nothing is shared).
  * Asynchronous on `stream`. Errors: ARG, SHAPE (n_heads), OOM (scratch), CUDA.
  */
