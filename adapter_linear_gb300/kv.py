@@ -252,7 +252,7 @@ class KvCache:
     def attention_shared(self, Q, batch: KvBatch, groups: Optional[KvGroups], scale: Optional[float] = None, O=None, lse=None,
                          stream=None):
         """attention() without a window, for a batch whose groups of sequences share prefixes (None: no groups):
-        each group's prefix is read once."""
+        each group's prefix is read once, which pays for many short chunks over a long prefix."""
         Q, qs, O, os_, lse, scale = self._attention_args("lora_kv_attention_shared", Q, batch, scale, O, lse, stream)
         if groups is not None and groups.device != self._device:
             raise LoraError(LORA_ERR_ARG, "lora_kv_attention_shared: the tensors of a call are on the cache's GPU")

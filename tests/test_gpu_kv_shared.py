@@ -240,16 +240,17 @@ def test_a_reservation_takes_what_its_size_needs():
         torch.cuda.synchronize()
         return before - torch.cuda.mem_get_info()[0]
 
-    taken(lambda: p.cache.reserve_shared(10, 4, 8))                # (and lora_kv_reserve's 40 MB)
+    Q = p.queries(4)
+    p.cache.attention_shared(Q, p.batch, p.groups)                 # (its kernels are loaded)
+    taken(lambda: p.cache.reserve_shared(10, 4, 8))                # (and lora_kv_reserve's 20 MB)
     for tokens in (200000, 230000, 240000):
         # O, lse and a place of 8 bytes a row and head; pieces of 256 and 48 rows an SM twice; whole 2 MB from the driver
         sms = torch.cuda.get_device_properties(0).multi_processor_count
         need = tokens * 4 * (64 + 3) * 4 + 2 * sms * (256 + 48) * (64 + 2) * 4
         assert need <= taken(lambda: p.cache.reserve_shared(tokens, 4, 8)) <= need + 8e6
     assert taken(lambda: p.cache.reserve_shared(240000, 4, 8)) == 0
-    Q = p.queries(4)
     O, lse = torch.empty_like(Q), torch.empty(p.T, 4, device="cuda")
-    assert taken(lambda: p.cache.attention_shared(Q, p.batch, p.groups, O=O, lse=lse)) < 4e6   # (code that is loaded)
+    assert taken(lambda: p.cache.attention_shared(Q, p.batch, p.groups, O=O, lse=lse)) == 0
     R.check_attention(O, lse, R.attention(Q, p, 0.125))
 
 
